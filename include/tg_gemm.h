@@ -252,6 +252,143 @@ TG_API tg_status tg_gemm_sp24_bf16(int64_t M, int64_t N, int64_t K,
                             int epilogue, void *stream);
 
 /*
+ * 8-bit linear layers.
+ *
+ * tg_quant_i8 -- rows of 16-bit values to signed 8-bit integers with one
+ * scale per row (the activations of tg_gemm_w8a8, one scale per token):
+ *
+ *     top = max_k |X[m][k]|,  scales[m] = top / 127,
+ *     Q[m][k] = X[m][k] * 127 / top rounded to the nearest integer, ties to even
+ *
+ * Q is exactly what the formula gives in real arithmetic.  A row of zeros gets scale 0 and
+ * Q = 0; a row that holds an infinity or a NaN gets scale NaN and Q = 0, so
+ * that its products are NaN.
+ *   X: M x K values of `type` (TG_TYPE_F16 or TG_TYPE_BF16), row pitch ldx
+ *      (elements, % 8 == 0);  Q: M x K, row pitch ldq (% 16 == 0);  scales: M
+ *      floats, 4-byte aligned.  K == 0 writes scales of 0.
+ *
+ * tg_gemm_w8a8 -- C = epi( (sum_k A[m][k] * W[k][n]) * row_scales[m] * col_scales[n] )
+ *   A: M x K signed 8-bit, row pitch lda;  W: K x N signed 8-bit in B, row
+ *   pitch ldb >= N, or with trans_b = 1 stored N x K, ldb >= K (both % 16 ==
+ *   0);  row_scales: M floats, col_scales: N floats, 4-byte aligned;  C: M x N of
+ *   `type`, row pitch ldc (% 8 == 0).
+ * The sum is an exact 32-bit integer (K above 131071, where 128 * 128 * K
+ * could leave its range -> TG_ERR_UNSUPPORTED); it is rounded to fp32 and
+ * multiplied by row_scales[m], then by col_scales[n], in fp32, and rounded once to C's
+ * type after epi.
+ */
+enum { TG_TYPE_F16 = 0, TG_TYPE_BF16 = 1 };
+
+TG_API tg_status tg_quant_i8(int64_t M, int64_t K, const void *X, int64_t ldx, int type,
+                             int8_t *Q, int64_t ldq, float *scales, void *stream);
+
+TG_API tg_status tg_gemm_w8a8(int64_t M, int64_t N, int64_t K,
+                              const int8_t *A, int64_t lda, const float *row_scales,
+                              const int8_t *B, int64_t ldb, int trans_b, const float *col_scales,
+                              void *C, int64_t ldc, int type, int epilogue, void *stream);
+
+/*
+ * Experts' products (the linear layers of a mixture of experts).
+ *
+ * The rows of A are sorted into E groups: group e is the rows
+ * [offsets[e], offsets[e + 1]).  offsets is E + 1 int32 in DEVICE memory,
+ * non-decreasing, offsets[0] = 0, offsets[E] <= M (tg_expert_sort writes it);
+ * no host needs to know the group sizes.  Values outside 0..M and decreasing
+ * ones are clamped (never read or written out of bounds, but then the result
+ * is unspecified).  1 <= E <= 1024 (more -> TG_ERR_UNSUPPORTED); a group may
+ * be empty.
+ *
+ * tg_gemm_grouped_f16 / _bf16 -- C[r][:] = epi( A[r][:] . W_e ), e the group of row r
+ *   A: M x K, row pitch lda;  W_e: K x N at B + e * plane_b elements, row pitch
+ *   ldb >= N, or with trans_b = 1 stored N x K, ldb >= K;  C: M x N, row pitch
+ *   ldc.  Pitches and plane_b % 8 == 0.  The rows of C from offsets[E] to M are written
+ *   as zero.
+ *
+ * tg_gemm_grouped_wgrad_f16 / _bf16 -- C_e[k][n] = sum over the rows r of group e
+ *   of A[r][k] * G[r][n], the gradient of W_e for the gradient G of the
+ *   product's rows.  A: M x K, row pitch lda;  G: M x N, row pitch ldg;  C_e: K x N
+ *   at C + e * plane_c, row pitch ldc, plane_c >= (K - 1) * ldc + N.  All
+ *   pitches and plane_c % 8 == 0.  A group without rows gets zeros.  For
+ *   weights stored N x K exchange A and G (and K and N).
+ *
+ * tg_gemm_grouped_w8a8 -- the product with 8-bit rows and weights, the sum, scales and
+ *   limits as tg_gemm_w8a8: row_scales M floats, col_scales N floats per
+ *   group, plane_s floats apart.  lda, ldb and plane_b % 16 == 0.
+ *
+ * All run on CTA pairs; a refused cluster launch returns TG_ERR_UNSUPPORTED.
+ * They use no workspace.  plane_b of 0 is TG_ERR_INVALID_ARG unless E is 1.
+ */
+TG_API tg_status tg_gemm_grouped_f16(int64_t M, int64_t N, int64_t K, int E,
+                                     const void *A, int64_t lda, const int32_t *offsets,
+                                     const void *B, int64_t ldb, int64_t plane_b, int trans_b,
+                                     void *C, int64_t ldc, int epilogue, void *stream);
+TG_API tg_status tg_gemm_grouped_bf16(int64_t M, int64_t N, int64_t K, int E,
+                                      const void *A, int64_t lda, const int32_t *offsets,
+                                      const void *B, int64_t ldb, int64_t plane_b, int trans_b,
+                                      void *C, int64_t ldc, int epilogue, void *stream);
+TG_API tg_status tg_gemm_grouped_wgrad_f16(int64_t M, int64_t N, int64_t K, int E,
+                                           const void *A, int64_t lda, const void *G, int64_t ldg,
+                                           const int32_t *offsets,
+                                           void *C, int64_t ldc, int64_t plane_c, void *stream);
+TG_API tg_status tg_gemm_grouped_wgrad_bf16(int64_t M, int64_t N, int64_t K, int E,
+                                            const void *A, int64_t lda, const void *G, int64_t ldg,
+                                            const int32_t *offsets,
+                                            void *C, int64_t ldc, int64_t plane_c, void *stream);
+TG_API tg_status tg_gemm_grouped_w8a8(int64_t M, int64_t N, int64_t K, int E,
+                                      const int8_t *A, int64_t lda, const float *row_scales,
+                                      const int32_t *offsets,
+                                      const int8_t *B, int64_t ldb, int64_t plane_b, int trans_b,
+                                      const float *col_scales, int64_t plane_s,
+                                      void *C, int64_t ldc, int type, int epilogue, void *stream);
+
+/*
+ * Tokens sorted by expert, and back.
+ *
+ * tg_expert_sort -- ids holds the experts of tokens x topk choices (int32 or
+ *   int64: id_bytes 4 or 8), choice i = token * topk + j.  Stable sort by expert:
+ *   pos[i] is the row of choice i, src[r] the choice of row r, the rows of
+ *   expert e are [offsets[e], offsets[e + 1]).  A number outside 0..E-1 is a
+ *   dropped choice; these follow, in order, from row offsets[E] on.  offsets
+ *   (E + 1), pos and src (tokens * topk each) are int32.  1 <= E <= 1024,
+ *   tokens * topk < 2^31.  scratch: tg_expert_sort_scratch(tokens * topk, E)
+ *   bytes of device memory, 4-byte aligned (NULL where that is 0), free again when the call's work
+ *   is done; -1 from it names a size that the sort refuses.
+ * tg_expert_gather -- out[pos[i]][:] = X[i / topk][:] for kept choices; the
+ *   rows of dropped choices are zero.  X: tokens x H elements of elem_bytes (1 or
+ *   2), row pitch ldx;  out: tokens * topk rows, row pitch ldo (pitches in
+ *   elements, a multiple of 16 bytes).  scales, if not NULL: one float per
+ *   token, gathered alike into out_scales.
+ * tg_expert_combine -- out[t][:] = sum over the kept choices j, in order, of
+ *   weights[t * topk + j] * Y[pos[t * topk + j]][:], in fp32, rounded once; weights NULL:
+ *   all 1, which is the gradient of gather.  Y: tokens * topk rows, out:
+ *   tokens rows of H values of `type`.
+ * tg_expert_combine_grad -- for the gradient dout (tokens x H) of combine's
+ *   out: dY[pos[i]][:] = weights[i] * dout[i / topk][:] (zero for dropped
+ *   choices) and dweights[i] = <Y[pos[i]], dout[i / topk]> in fp32 (0 for
+ *   dropped choices).
+ * kept is a pointer to one int32 in device memory, the number of kept
+ * choices: offsets + E of the sort.  Entries of pos outside 0..tokens * topk
+ * - 1 are skipped.  The outputs must not overlap the inputs.
+ */
+TG_API int64_t tg_expert_sort_scratch(int64_t choices, int E);
+TG_API tg_status tg_expert_sort(int64_t tokens, int topk, int E, const void *ids, int id_bytes,
+                                int32_t *offsets, int32_t *pos, int32_t *src,
+                                void *scratch, void *stream);
+TG_API tg_status tg_expert_gather(int64_t tokens, int topk, int64_t H, int elem_bytes,
+                                  const void *X, int64_t ldx, const float *scales,
+                                  const int32_t *pos, const int32_t *kept,
+                                  void *out, int64_t ldo, float *out_scales, void *stream);
+TG_API tg_status tg_expert_combine(int64_t tokens, int topk, int64_t H, int type,
+                                   const void *Y, int64_t ldy,
+                                   const int32_t *pos, const int32_t *kept, const float *weights,
+                                   void *out, int64_t ldo, void *stream);
+TG_API tg_status tg_expert_combine_grad(int64_t tokens, int topk, int64_t H, int type,
+                                        const void *Y, int64_t ldy, const void *dout, int64_t ldd,
+                                        const int32_t *pos, const int32_t *kept,
+                                        const float *weights, void *dY, int64_t lddy,
+                                        float *dweights, void *stream);
+
+/*
  * tg_gemm_bf16_small_m_static -- tg_gemm_bf16 for M <= 128 that never
  * allocates device memory.  The pages have no counterpart: this entry point
  * exists for callers that may not call cudaMalloc / cudaFree where they run

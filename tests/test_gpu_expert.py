@@ -1,0 +1,420 @@
+"""The experts' operators on a B200: sort, gather, products, combine and their
+gradients against their definitions in 64 bits."""
+import pytest
+import torch
+
+from expert_util import (DTYPES, H, TINY, close, ints8, normal, offsets_of, pitched, positive, product16,
+                         product8)
+from gpu_util import check_guard, guarded_out
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def tg():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    import tiled_dense_gemm_tma_b200 as tg
+    tg.load_library()
+    return tg
+
+
+def _status(tg):
+    torch.cuda.synchronize()
+    assert tg.last_device_status() == 0
+
+
+# ------------------------------------------------------------------- sort
+
+def sort_ref(ids, E):
+    flat = ids.reshape(-1).tolist()
+    buckets = [[] for _ in range(E + 1)]
+    for i, e in enumerate(flat):
+        buckets[e if 0 <= e < E else E].append(i)
+    offsets = [0]
+    for b in buckets[:E]:
+        offsets.append(offsets[-1] + len(b))
+    src = [i for b in buckets for i in b]
+    pos = [0] * len(flat)
+    for r, i in enumerate(src):
+        pos[i] = r
+    return offsets, pos, src
+
+
+def make_ids(T, k, E, seed, drop=0.0, dtype=torch.int64):
+    g = torch.Generator().manual_seed(seed)
+    ids = torch.randint(0, E, (T, k), generator=g)
+    if drop:
+        gone = torch.rand((T, k), generator=g) < drop
+        ids[gone] = torch.where(ids[gone] % 2 == 0, -1, E + ids[gone])
+    return ids.to(dtype).cuda()
+
+
+@pytest.mark.parametrize("dtype", [torch.int32, torch.int64])
+@pytest.mark.parametrize("T,k,E,drop", [(0, 2, 4, 0), (1, 1, 1, 0), (1, 8, 8, 0.5), (16, 2, 8, 0), (33, 3, 5, 0.3),
+                                        (700, 4, 64, 0.01), (1024, 8, 128, 0), (1025, 8, 129, 0.1), (2731, 3, 1024, 0),
+                                        (9000, 8, 256, 0.02), (40000, 8, 1024, 0.1), (100, 2, 8, 1.0),
+                                        (50000, 1, 1, 0.5), (148 * 2048 + 77, 1, 7, 0)])
+def test_sort(tg, T, k, E, drop, dtype):
+    ids = make_ids(T, k, E, T + E, drop, dtype)
+    plan = tg.expert_sort(ids, E)
+    _status(tg)
+    offsets, pos, src = sort_ref(ids, E)
+    assert plan.offsets.tolist() == offsets
+    assert plan.src.tolist() == src
+    assert plan.pos.reshape(-1).tolist() == pos and tuple(plan.pos.shape) == (T, k)
+
+
+def test_sort_far_numbers_are_dropped(tg):
+    """64-bit numbers whose low words name an expert."""
+    ids = torch.tensor([[1, 1 << 32], [-(1 << 32), (1 << 33) + 1], [0, -1]], device="cuda")
+    plan = tg.expert_sort(ids, 2)
+    assert plan.offsets.tolist() == [0, 1, 2]
+    assert plan.src.tolist() == [4, 0, 1, 2, 3, 5]
+
+
+# -------------------------------------------------------- gather, combine
+
+MOVES = [(1, 1, 1, 1, 0), (3, 2, 4, 7, 0), (16, 2, 8, 4096, 0), (50, 6, 16, 1030, 0.2), (257, 5, 9, 63, 0.5),
+         (100, 8, 128, 2048, 0.02), (20, 33, 40, 136, 0.1), (5, 3, 8, 20001, 0.3), (12, 2, 4, 64, 1.0)]
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("T,k,E,W,drop", MOVES)
+def test_gather_and_gradient(tg, T, k, E, W, drop, dtype):
+    dt = DTYPES[dtype]
+    ids = make_ids(T, k, E, T, drop)
+    plan = tg.expert_sort(ids, E)
+    X = normal((T, W), dt, 1, extra=1).requires_grad_(True)
+    Xs = tg.expert_gather(X, plan)
+    kept = ((ids >= 0) & (ids < E)).reshape(-1)
+    pos = plan.pos.reshape(-1).long()
+    ref = torch.zeros(T * k, W, dtype=dt, device="cuda")
+    ref[pos[kept]] = X.detach().repeat_interleave(k, 0)[kept]
+    assert torch.equal(Xs.detach(), ref)
+    g = normal((T * k, W), dt, 2)
+    dX, = torch.autograd.grad(Xs, X, g)
+    _status(tg)
+    rows = torch.where(kept[:, None], g[pos].double(), 0).view(T, k, W)
+    want = rows.sum(1)
+    close(dX, want, want.abs() * H[dt] * 1.01 + TINY[dt] + k * 2.0 ** -24 * rows.abs().sum(1))
+
+
+def test_gather_int8_with_scales(tg):
+    ids = make_ids(40, 3, 6, 1, 0.2)
+    plan = tg.expert_sort(ids, 6)
+    X, s = ints8((40, 515), 1), positive((40,), 2)
+    Xs, ss = tg.expert_gather(X, plan, scales=s)
+    _status(tg)
+    n = int(plan.offsets[-1])
+    tok = (plan.src // 3).long()
+    assert torch.equal(Xs[:n], X[tok[:n]]) and not Xs[n:].any()
+    assert torch.equal(ss[:n], s[tok[:n]]) and not ss[n:].any()
+    assert torch.equal(tg.expert_gather(X, plan), Xs)
+
+
+@pytest.mark.parametrize("weighted", [True, False])
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("T,k,E,W,drop", MOVES)
+def test_combine_and_gradients(tg, T, k, E, W, drop, dtype, weighted):
+    dt = DTYPES[dtype]
+    ids = make_ids(T, k, E, T + 5, drop)
+    plan = tg.expert_sort(ids, E)
+    Y = normal((T * k, W), dt, 1, extra=1).requires_grad_(True)
+    w = normal((T, k), torch.float32, 2)[:, :].contiguous().requires_grad_(True) if weighted else None
+    out = tg.expert_combine(Y, plan, w)
+    kept = (ids >= 0) & (ids < E)
+    wk = torch.where(kept, w.detach().double() if weighted else 1.0, 0.0)
+    pos = plan.pos.long()
+    rows = torch.where(kept[:, :, None], Y.detach().double()[pos], 0)
+    terms = rows * wk[:, :, None]
+    want = terms.sum(1)
+    close(out.detach(), want, want.abs() * H[dt] * 1.01 + TINY[dt] + (k + 1) * 2.0 ** -24 * terms.abs().sum(1))
+    g = normal((T, W), dt, 3)
+    grads = torch.autograd.grad(out, (Y, w) if weighted else (Y,), g)
+    _status(tg)
+    dY = torch.zeros(T * k, W, dtype=torch.float64, device="cuda")
+    dY[pos.reshape(-1)] = (wk[:, :, None] * g.double()[:, None, :]).reshape(T * k, W)
+    close(grads[0], dY, dY.abs() * (H[dt] * 1.01 + 2.0 ** -24) + TINY[dt], "dY")
+    if weighted:
+        prod = rows * g.double()[:, None, :]
+        close(grads[1], prod.sum(2), W * 2.0 ** -24 * prod.abs().sum(2) + 2.0 ** -149, "dw")
+
+
+def test_infinite_rows_of_dropped_choices_do_not_count(tg):
+    ids = torch.tensor([[0, -1], [1, 0]], device="cuda")
+    plan = tg.expert_sort(ids, 2)
+    Y = pitched((4, 16), torch.bfloat16)
+    Y.fill_(1)
+    Y[3] = float("nan")                                   # the dropped choice's row
+    Y.requires_grad_(True)
+    w = torch.full((2, 2), 2.0, device="cuda")
+    w[0, 1] = float("inf")
+    w.requires_grad_(True)
+    out = tg.expert_combine(Y, plan, w)
+    assert out.tolist() == [[2.0] * 16, [4.0] * 16]
+    g = pitched((2, 16), torch.bfloat16)
+    g.fill_(1)
+    dY, dw = torch.autograd.grad(out, (Y, w), g)
+    assert dY[:3].tolist() == [[2.0] * 16] * 3 and not dY[3].any()
+    assert dw.tolist() == [[16.0, 0.0], [16.0, 16.0]]
+    _status(tg)
+
+
+# --------------------------------------------------------------- products
+
+GROUPS = {
+    "one": [37], "ones": [1, 1, 1, 1], "empty": [0, 0, 0], "edges": [255, 0, 256, 257, 0, 1, 31, 32, 33],
+    "ends_empty": [0, 5, 0], "mixed": [300, 3, 0, 64, 129, 513], "many": [7] * 100 + [0] * 30 + [40],
+}
+
+
+@pytest.mark.parametrize("trans", [False, True])
+@pytest.mark.parametrize("groups,K,N,tail", [("one", 1, 1, 0), ("one", 64, 8, 3), ("ones", 65, 31, 0),
+                                             ("empty", 16, 24, 9), ("empty", 8, 8, 0), ("edges", 130, 257, 5),
+                                             ("edges", 63, 300, 0), ("ends_empty", 200, 129, 40),
+                                             ("mixed", 520, 264, 11), ("many", 96, 136, 2), ("mixed", 1024, 72, 300)])
+def test_product_and_gradients(tg, groups, K, N, tail, trans):
+    dtype = "bf16" if (K + N) % 2 else "f16"
+    dt = DTYPES[dtype]
+    counts = GROUPS[groups]
+    E, live = len(counts), sum(counts)
+    R = live + tail
+    offsets = offsets_of(counts)
+    X = normal((R, K), dt, 1, extra=1).requires_grad_(True)
+    S = normal((E, N, K) if trans else (E, K, N), dt, 2, K ** -0.5).requires_grad_(True)
+    W = S.transpose(1, 2) if trans else S
+    Y = tg.expert_matmul(X, W, offsets)
+    g = normal((R, N), dt, 3, extra=1)
+    if R:
+        dX, dS = torch.autograd.grad(Y, (X, S), g)
+    _status(tg)
+    if not R:
+        return
+    x, w, gd = X.detach(), W.detach(), g
+    at = 0
+    for e, n in enumerate(counts):
+        part = slice(at, at + n)
+        ref, bound = product16(x[part], w[e], dt)
+        close(Y.detach()[part], ref, bound, f"Y of group {e}")
+        ref, bound = product16(gd[part], w[e].t(), dt)
+        close(dX[part], ref, bound, f"dX of group {e}")
+        ref, bound = product16(x[part].t(), gd[part], dt)
+        got = dS[e].t() if trans else dS[e]
+        close(got, ref, bound, f"dW of group {e}")
+        at += n
+    assert not Y.detach()[live:].any() and not dX[live:].any()
+
+
+@pytest.mark.parametrize("trans", [False, True])
+@pytest.mark.parametrize("groups,K,N,tail", [("one", 1, 1, 0), ("ones", 129, 31, 2), ("edges", 256, 257, 5),
+                                             ("mixed", 1000, 264, 11), ("many", 136, 136, 2), ("empty", 16, 24, 9)])
+def test_product8(tg, groups, K, N, tail, trans):
+    dtype = "bf16" if (K + N) % 2 else "f16"
+    dt = DTYPES[dtype]
+    counts = GROUPS[groups]
+    E, live = len(counts), sum(counts)
+    R = live + tail
+    offsets = offsets_of(counts)
+    A, B = ints8((R, K), 1, extra=1), ints8((E, N, K) if trans else (E, K, N), 2)
+    rs, cs = positive((R,), 3, 1e-3, 2e-3), positive((E, N), 4, 1e-3, 2e-3)
+    big, C, pad = guarded_out(R, N, dtype)
+    tg.gemm_grouped_w8a8(A, rs, offsets, B, cs, C=C, trans_b=trans, relu=K % 2 == 0)
+    _status(tg)
+    at = 0
+    for e, n in enumerate(counts):
+        part = slice(at, at + n)
+        ref, bound = product8(A[part], rs[part], B[e].t() if trans else B[e], cs[e], dt)
+        close(C[part], ref.clamp(min=0) if K % 2 == 0 else ref, bound, f"group {e}")
+        at += n
+    assert not C[live:].any()
+    check_guard(big, dtype, R, N, pad)
+
+
+@pytest.mark.parametrize("N", [8, 40, 64, 200, 260])
+def test_product_writes_only_its_output(tg, N):
+    counts = [70, 0, 131, 3]
+    A = normal((210, 100), torch.bfloat16, 1)
+    B = normal((4, 100, N), torch.bfloat16, 2)
+    big, C, pad = guarded_out(210, N, "bf16")
+    tg.gemm_grouped(A, offsets_of(counts), B, C=C, relu=True)
+    _status(tg)
+    check_guard(big, "bf16", 210, N, pad)
+    at = 0
+    for e, n in enumerate(counts):
+        ref, bound = product16(A[at:at + n], B[e], torch.bfloat16)
+        close(C[at:at + n], ref.clamp(min=0), bound)
+        at += n
+
+
+@pytest.mark.parametrize("K,N", [(7, 9), (40, 72), (300, 65)])
+def test_wgrad_writes_only_its_output(tg, K, N):
+    """Into matrices with rows and columns to spare between them."""
+    counts = [70, 0, 13]
+    A, G = normal((90, K), torch.float16, 1), normal((90, N), torch.float16, 2)
+    ld = -(-N // 8) * 8 + 8
+    big = torch.full((3, K + 3, ld), 7.0, dtype=torch.float16, device="cuda")
+    C = big[:, :K, :N]
+    tg.gemm_grouped_wgrad(A, G, offsets_of(counts), C=C)
+    _status(tg)
+    assert bool((big[:, K:] == 7).all()) and bool((big[:, :, N:] == 7).all())
+    at = 0
+    for e, n in enumerate(counts):
+        ref, bound = product16(A[at:at + n].t(), G[at:at + n], torch.float16)
+        close(C[e], ref, bound)
+        at += n
+
+
+@pytest.mark.parametrize("n", [1, 15, 17, 63, 64, 65, 80, 100])
+def test_nothing_leaks_between_groups(tg, n):
+    """NaN and infinities in one group's rows and weights stay there: a group
+    that ends inside a 16-row step or a 64-row block reads its neighbour's."""
+    K, N = 72, 136
+    counts = [n, 40, n]
+    R = sum(counts) + 20
+    X, g = normal((R, K), torch.bfloat16, 1), normal((R, N), torch.bfloat16, 2)
+    W = normal((3, K, N), torch.bfloat16, 3)
+    bad = slice(n, n + 40)
+    X[bad], g[bad], W[1] = float("nan"), float("inf"), float("nan")
+    X[-20:], g[-20:] = float("nan"), float("nan")         # behind the last group
+    X.requires_grad_(True)
+    W.requires_grad_(True)
+    Y = tg.expert_matmul(X, W, offsets_of(counts))
+    dX, dW = torch.autograd.grad(Y, (X, W), g)
+    _status(tg)
+    for got in (Y.detach(), dX):
+        assert not torch.isnan(got[:n]).any() and not torch.isnan(got[n + 40:]).any()
+        assert torch.isnan(got[bad]).all() and not got[-20:].any()
+    assert torch.isfinite(dW[0]).all() and torch.isfinite(dW[2]).all() and torch.isnan(dW[1]).all()
+    ref, bound = product16(X.detach()[:n].t(), g[:n], torch.bfloat16)
+    close(dW[0], ref, bound)
+
+
+def test_offsets_outside_the_rows_are_clamped(tg):
+    """Bad offsets never lead outside the matrices: the calls return, report no
+    time-out and write nothing outside C."""
+    A, G = normal((50, 64), torch.bfloat16, 1), normal((50, 72), torch.bfloat16, 2)
+    W = normal((3, 64, 72), torch.bfloat16, 3)
+    for bad in ([-5, 20, 1000, 2000], [10, 5, 60, 3], [2 ** 31 - 1, -2 ** 31, 7, 2 ** 31 - 1]):
+        o = torch.tensor(bad, dtype=torch.int32, device="cuda")
+        big, C, pad = guarded_out(50, 72, "bf16")
+        tg.gemm_grouped(A, o, W, C=C)
+        wide = torch.full((4, 64, 72), 7.0, dtype=torch.bfloat16, device="cuda")
+        tg.gemm_grouped_wgrad(A, G, o, C=wide[:3])
+        _status(tg)
+        check_guard(big, "bf16", 50, 72, pad)
+        assert bool((wide[3] == 7).all())
+
+
+def test_strided_weights(tg):
+    """Matrices of a wider buffer, experts interleaved by row."""
+    E, K, N = 3, 72, 40
+    buf = normal((K, E, N + 24), torch.bfloat16, 1)
+    W = buf.transpose(0, 1)[:, :, :N]                     # plane N + 24, pitch E * (N + 24)
+    A = normal((60, K), torch.bfloat16, 2)
+    counts = [10, 30, 20]
+    C = tg.gemm_grouped(A, offsets_of(counts), W)
+    _status(tg)
+    at = 0
+    for e, n in enumerate(counts):
+        ref, bound = product16(A[at:at + n], W[e], torch.bfloat16)
+        close(C[at:at + n], ref, bound)
+        at += n
+
+
+# ------------------------------------------------------------ as one layer
+
+def layer(tg, x, scores, ids, W1, W2, E):
+    plan = tg.expert_sort(ids, E)
+    h = torch.relu(tg.expert_matmul(tg.expert_gather(x, plan), W1, plan))
+    return tg.expert_combine(tg.expert_matmul(h, W2.transpose(1, 2), plan), plan, scores)
+
+
+def make_layer(T=70, k=3, E=6, D=80, F=136, seed=0, drop=0.1):
+    ids = make_ids(T, k, E, seed, drop)
+    x = normal((T, D), torch.bfloat16, seed + 1)
+    scores = positive((T, k), seed + 2, 0.1, 0.6)
+    W1, W2 = normal((E, D, F), torch.bfloat16, seed + 3, D ** -0.5), normal((E, D, F), torch.bfloat16, seed + 4, F ** -0.5)
+    return [t.requires_grad_(True) for t in (x, scores, W1, W2)], ids
+
+
+def test_layer_against_64_bit_autograd(tg):
+    """Router weights, two products and the joins, forward and backward.
+    Every stage rounds once to bf16 (2^-8), forward four of them and backward
+    four more; sums of at most 136 terms of alike sizes: 5 % of the largest
+    value bounds them with room for the sums' growth."""
+    E = 6
+    leaves, ids = make_layer()
+    y = layer(tg, leaves[0], leaves[1], ids, leaves[2], leaves[3], E)
+    g = normal(tuple(y.shape), torch.bfloat16, 77)
+    got = torch.autograd.grad(y, leaves, g)
+    _status(tg)
+    d = [t.detach().double().requires_grad_(True) for t in leaves]
+    out = torch.zeros_like(d[0])
+    for t in range(ids.shape[0]):
+        for j in range(ids.shape[1]):
+            e = int(ids[t, j])
+            if 0 <= e < E:
+                out = out.index_add(0, torch.tensor([t], device="cuda"),
+                                    (d[1][t, j] * (torch.relu(d[0][t] @ d[2][e]) @ d[3][e].t()))[None])
+    want = torch.autograd.grad(out, d, g.double())
+    for a, b in zip([y.detach(), *got], [out.detach(), *want]):
+        assert (a.double() - b).abs().max() <= 0.05 * b.abs().max()
+
+
+def test_gradient_against_differences(tg):
+    """d<Y, G>/dW along a direction: a step large enough that bf16's rounding
+    of the weights is exact (integers), so only Y's own rounding counts."""
+    counts = [40, 0, 25]
+    X = ints8((65, 32), 1, -2, 3).to(torch.bfloat16)
+    W = ints8((3, 32, 24), 2, -2, 3).to(torch.bfloat16).requires_grad_(True)
+    G = ints8((65, 24), 3, -2, 3).to(torch.bfloat16)
+    D = ints8((3, 32, 24), 4, -1, 2).to(torch.bfloat16)
+    o = offsets_of(counts)
+
+    def value(w):
+        return (tg.gemm_grouped(X, o, w).double() * G.double()).sum()
+
+    dW, = torch.autograd.grad(tg.expert_matmul(X, W, o), W, G)
+    # |Y| <= 32 * 2 * 3 = 192 and |dW| <= 40 * 4 = 160 are integers below 256: exact in bf16
+    diff = (value(W.detach() + D) - value(W.detach() - D)) / 2
+    assert diff.item() == (dW.double() * D.double()).sum().item()
+    _status(tg)
+
+
+def test_two_graphs_side_by_side(tg):
+    """Two captured layers replayed on two streams at once, each with its own
+    inputs, against their eager runs."""
+    E = 6
+    runs = []
+    for seed in (0, 50):
+        leaves, ids = make_layer(T=400, seed=seed)
+        with torch.no_grad():
+            args = [t.detach() for t in leaves]
+            eager = layer(tg, args[0], args[1], ids, args[2], args[3], E)
+            s = torch.cuda.Stream()
+            s.wait_stream(torch.cuda.current_stream())
+            graph = torch.cuda.CUDAGraph()
+            with torch.cuda.graph(graph, stream=s):
+                out = layer(tg, args[0], args[1], ids, args[2], args[3], E)
+        runs.append((graph, s, out, eager, args, ids))        # a graph reads its inputs' memory: keep them
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for graph, s, out, eager, *_ in runs:
+            with torch.cuda.stream(s):
+                graph.replay()
+    _status(tg)
+    for graph, s, out, eager, *_ in runs:
+        assert torch.equal(out, eager)
+
+
+def test_repeated_calls_give_the_same_bits(tg):
+    leaves, ids = make_layer(T=300)
+    first = None
+    for _ in range(3):
+        y = layer(tg, leaves[0], leaves[1], ids, leaves[2], leaves[3], 6)
+        got = [y.detach(), *torch.autograd.grad(y, leaves, torch.ones_like(y))]
+        if first is None:
+            first = got
+        assert all(torch.equal(a, b) for a, b in zip(first, got))
+    _status(tg)

@@ -23,6 +23,10 @@ STATUS = {0: "TG_OK", 1: "TG_ERR_INVALID_ARG", 2: "TG_ERR_ALIGNMENT",
 EXPORTS = ("tg_gemm_f32", "tg_gemm_f16", "tg_gemm_bf16", "tg_gemm_w4a16", "tg_gemm_wfp4",
            "tg_gemm_f16_ex", "tg_gemm_bf16_ex", "tg_gemm_bf16_small_m_static",
            "tg_gemm_sp24_f16", "tg_gemm_sp24_bf16",
+           "tg_quant_i8", "tg_gemm_w8a8", "tg_gemm_grouped_f16", "tg_gemm_grouped_bf16",
+           "tg_gemm_grouped_wgrad_f16", "tg_gemm_grouped_wgrad_bf16", "tg_gemm_grouped_w8a8",
+           "tg_expert_sort_scratch", "tg_expert_sort", "tg_expert_gather", "tg_expert_combine",
+           "tg_expert_combine_grad",
            "tg_tune_set", "tg_tune_builtin", "tg_tune_query",
            "tg_status_string", "tg_last_device_status", "tg_num_sms")
 
@@ -81,6 +85,27 @@ def load_library():
         for name in ("tg_gemm_f32", "tg_gemm_f16", "tg_gemm_bf16", "tg_gemm_w4a16",
                      "tg_gemm_wfp4", "tg_gemm_f16_ex", "tg_gemm_bf16_ex",
                      "tg_gemm_bf16_small_m_static", "tg_last_device_status"):
+            getattr(lib, name).restype = ci
+        lib.tg_quant_i8.argtypes = [i64, i64, vp, i64, ci, vp, i64, vp, vp]
+        lib.tg_gemm_w8a8.argtypes = [i64, i64, i64, vp, i64, vp, vp, i64, ci, vp, vp, i64, ci, ci, vp]
+        for name in ("tg_gemm_grouped_f16", "tg_gemm_grouped_bf16"):
+            getattr(lib, name).argtypes = [i64, i64, i64, ci, vp, i64, vp, vp, i64, i64, ci,
+                                           vp, i64, ci, vp]
+        for name in ("tg_gemm_grouped_wgrad_f16", "tg_gemm_grouped_wgrad_bf16"):
+            getattr(lib, name).argtypes = [i64, i64, i64, ci, vp, i64, vp, i64, vp, vp, i64, i64, vp]
+        lib.tg_gemm_grouped_w8a8.argtypes = [i64, i64, i64, ci, vp, i64, vp, vp, vp, i64, i64, ci,
+                                             vp, i64, vp, i64, ci, ci, vp]
+        lib.tg_expert_sort_scratch.argtypes = [i64, ci]
+        lib.tg_expert_sort_scratch.restype = i64
+        lib.tg_expert_sort.argtypes = [i64, ci, ci, vp, ci, vp, vp, vp, vp, vp]
+        lib.tg_expert_gather.argtypes = [i64, ci, i64, ci, vp, i64, vp, vp, vp, vp, i64, vp, vp]
+        lib.tg_expert_combine.argtypes = [i64, ci, i64, ci, vp, i64, vp, vp, vp, vp, i64, vp]
+        lib.tg_expert_combine_grad.argtypes = [i64, ci, i64, ci, vp, i64, vp, i64, vp, vp, vp,
+                                               vp, i64, vp, vp]
+        for name in ("tg_quant_i8", "tg_gemm_w8a8", "tg_gemm_grouped_f16", "tg_gemm_grouped_bf16",
+                     "tg_gemm_grouped_wgrad_f16", "tg_gemm_grouped_wgrad_bf16",
+                     "tg_gemm_grouped_w8a8", "tg_expert_sort", "tg_expert_gather",
+                     "tg_expert_combine", "tg_expert_combine_grad"):
             getattr(lib, name).restype = ci
         lib.tg_status_string.argtypes = [ci]
         lib.tg_status_string.restype = ctypes.c_char_p
@@ -397,6 +422,508 @@ def gemm_bf16_small_m_static(A, B, C=None, relu=False, stream=None):
                                                _stream_handle(stream))
     _check(code, "tg_gemm_bf16_small_m_static")
     return C
+
+
+# ------------------------------------------------------ 8-bit linear layers
+
+TYPE_F16, TYPE_BF16 = 0, 1
+
+
+def _type16(dtype, name):
+    import torch
+    if dtype == torch.bfloat16:
+        return TYPE_BF16
+    if dtype == torch.float16:
+        return TYPE_F16
+    raise TypeError(f"{name} must be float16 or bfloat16")
+
+
+def _on_device(t):
+    """As _device_ctx, without the switch where t's device is current already."""
+    import torch
+    if not t.is_cuda or torch.cuda.current_device() == t.device.index:
+        return contextlib.nullcontext()
+    return torch.cuda.device(t.device)
+
+
+def _pitch(t, name):
+    """Row pitch (elements) of a row-major 2-D tensor or of the matrices of a
+    3-D one; for fewer than two rows, whose stride says nothing, the row
+    length rounded up to 16 bytes."""
+    if t.stride(-1) != 1 and t.shape[-1] > 1:
+        raise ValueError(f"{name} must be row-major (unit column stride)")
+    if t.shape[-2] <= 1:
+        per = 16 // t.element_size()
+        return max(per, -(-t.shape[-1] // per) * per)
+    return t.stride(-2)
+
+
+def _plane(t):
+    """Elements between the matrices of a 3-D tensor."""
+    return t.stride(0) if t.shape[0] > 1 else 0
+
+
+def _vector(t, n, dtype, name):
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}")
+    if t.dim() != 1 or t.shape[0] != n or (n > 1 and t.stride(0) != 1):
+        raise ValueError(f"{name} must be a contiguous vector of {n}")
+
+
+def _out(C, M, N, dtype, device):
+    if C is None:
+        return empty_out(M, N, dtype, device)
+    if C.shape != (M, N) or C.dtype != dtype:
+        raise ValueError("C has the wrong shape or dtype")
+    return C
+
+
+def quant_i8(X, Q=None, scales=None, stream=None):
+    """Rows of X (M x K, float16 / bfloat16) to signed 8-bit integers with one
+    float32 scale per row: scale = max|x| / 127, q = round(x * 127 / max|x|),
+    ties to even.  Returns (Q, scales).  A row of zeros gets scale 0; a row
+    with an infinity or a NaN gets scale NaN."""
+    import torch
+    lib = load_library()
+    if X.dim() != 2:
+        raise ValueError("X must be 2-D")
+    kind = _type16(X.dtype, "X")
+    M, K = X.shape
+    if Q is None:
+        Q = empty_out(M, K, torch.int8, X.device)
+    elif Q.shape != (M, K) or Q.dtype != torch.int8:
+        raise ValueError("Q has the wrong shape or dtype")
+    if scales is None:
+        scales = torch.empty(M, dtype=torch.float32, device=X.device)
+    _vector(scales, M, torch.float32, "scales")
+    _require_cuda(X.device, (X, "X"), (Q, "Q"), (scales, "scales"))
+    with _on_device(X):
+        code = lib.tg_quant_i8(M, K, X.data_ptr(), _pitch(X, "X"), kind, Q.data_ptr(),
+                               _pitch(Q, "Q"), scales.data_ptr(), _stream_handle(stream))
+    _check(code, "tg_quant_i8")
+    return Q, scales
+
+
+def gemm_w8a8(A, row_scales, B, col_scales, C=None, out_dtype=None, relu=False, stream=None,
+              trans_b=False):
+    """C = epi((A @ W) * row_scales[:, None] * col_scales) for int8 A (M x K)
+    and W: B is K x N, or N x K with trans_b.  The scales are float32 vectors
+    of M and N.  C is float16 or bfloat16 (out_dtype, by default C's or
+    bfloat16)."""
+    import torch
+    lib = load_library()
+    if A.dtype != torch.int8 or B.dtype != torch.int8:
+        raise TypeError("A and B must be int8")
+    if A.dim() != 2 or B.dim() != 2:
+        raise ValueError("A and B must be 2-D")
+    M, K = A.shape
+    K2, N = B.shape[::-1] if trans_b else B.shape
+    if K != K2:
+        raise ValueError(f"inner dimensions differ: {K} vs {K2}")
+    _vector(row_scales, M, torch.float32, "row_scales")
+    _vector(col_scales, N, torch.float32, "col_scales")
+    if out_dtype is None:
+        out_dtype = torch.bfloat16 if C is None else C.dtype
+    kind = _type16(out_dtype, "C")
+    C = _out(C, M, N, out_dtype, A.device)
+    _require_cuda(A.device, (A, "A"), (B, "B"), (row_scales, "row_scales"),
+                  (col_scales, "col_scales"), (C, "C"))
+    with _on_device(A):
+        code = lib.tg_gemm_w8a8(M, N, K, A.data_ptr(), _pitch(A, "A"), row_scales.data_ptr(),
+                                B.data_ptr(), _pitch(B, "B"), int(trans_b), col_scales.data_ptr(),
+                                C.data_ptr(), _pitch(C, "C"), kind,
+                                EPI_RELU if relu else EPI_NONE, _stream_handle(stream))
+    _check(code, "tg_gemm_w8a8")
+    return C
+
+
+# ------------------------------------------------------- experts' operators
+
+class ExpertPlan:
+    """Where expert_sort put each choice.
+
+    offsets: int32 [E + 1], the rows of expert e are offsets[e]:offsets[e + 1],
+    dropped choices follow from offsets[E] on; pos: int32, the shape of the
+    expert numbers, the row of each choice; src: int32 [tokens * topk], the
+    flat choice of each row."""
+    __slots__ = ("offsets", "pos", "src")
+
+    def __init__(self, offsets, pos, src):
+        self.offsets, self.pos, self.src = offsets, pos, src
+
+    @property
+    def num_experts(self):
+        return self.offsets.shape[0] - 1
+
+    @property
+    def tokens(self):
+        return self.pos.shape[0]
+
+    @property
+    def topk(self):
+        return self.pos.shape[1]
+
+
+def expert_sort(ids, num_experts, stream=None):
+    """Stable sort of the choices ids (tokens x topk, int32 or int64) by
+    expert, as an ExpertPlan.  Numbers outside 0..num_experts - 1 are dropped
+    choices."""
+    import torch
+    lib = load_library()
+    if ids.dim() != 2:
+        raise ValueError("ids must be 2-D (tokens x topk)")
+    if ids.dtype not in (torch.int32, torch.int64):
+        raise TypeError("ids must be int32 or int64")
+    _require_cuda(ids.device, (ids, "ids"))
+    T, k = ids.shape
+    if k < 1:
+        raise ValueError("ids must hold at least one choice per token")
+    need = lib.tg_expert_sort_scratch(T * k, num_experts)
+    if need < 0:
+        raise ValueError("expert_sort takes 1 to 1024 experts and fewer than 2^31 choices")
+    ids = ids.contiguous()
+    # one allocation: offsets, pos, src, scratch (each 16-byte aligned)
+    n, E1 = T * k, num_experts + 1
+    cuts = [-(-c // 4) * 4 for c in (E1, n, n, need // 4)]
+    buf = torch.empty(sum(cuts), dtype=torch.int32, device=ids.device)
+    offsets, pos, src = buf[:E1], buf[cuts[0]:cuts[0] + n], buf[cuts[0] + cuts[1]:cuts[0] + cuts[1] + n]
+    base = buf.data_ptr()
+    with _on_device(ids):
+        code = lib.tg_expert_sort(T, k, num_experts, ids.data_ptr(), ids.element_size(), base,
+                                  base + 4 * cuts[0], base + 4 * (cuts[0] + cuts[1]),
+                                  base + 4 * (cuts[0] + cuts[1] + cuts[2]) if need else None,
+                                  _stream_handle(stream))
+    _check(code, "tg_expert_sort")
+    return ExpertPlan(offsets, pos.view(T, k), src)
+
+
+def _kept_ptr(offsets):
+    return offsets.data_ptr() + 4 * (offsets.shape[0] - 1)
+
+
+def _check_plan(offsets, pos):
+    import torch
+    if offsets.dtype != torch.int32 or pos.dtype != torch.int32:
+        raise TypeError("the plan's tensors must be int32")
+    if offsets.dim() != 1 or pos.dim() != 2 or not offsets.is_contiguous() or not pos.is_contiguous():
+        raise ValueError("the plan's tensors must be contiguous")
+
+
+def _gather(X, offsets, pos, scales=None):
+    import torch
+    lib = load_library()
+    _check_plan(offsets, pos)
+    T, k = pos.shape
+    if X.dim() != 2 or X.shape[0] != T:
+        raise ValueError("X must have one row per token of the plan")
+    if X.dtype not in (torch.float16, torch.bfloat16, torch.int8):
+        raise TypeError("X must be float16, bfloat16 or int8")
+    H = X.shape[1]
+    out = empty_out(T * k, H, X.dtype, X.device)
+    ss = None
+    if scales is not None:
+        _vector(scales, T, torch.float32, "scales")
+        ss = torch.empty(T * k, dtype=torch.float32, device=X.device)
+        _require_cuda(X.device, (scales, "scales"))
+    _require_cuda(X.device, (X, "X"), (offsets, "offsets"), (pos, "pos"))
+    with _on_device(X):
+        code = lib.tg_expert_gather(T, k, H, X.element_size(), X.data_ptr(), _pitch(X, "X"),
+                                    scales.data_ptr() if scales is not None else None,
+                                    pos.data_ptr(), _kept_ptr(offsets), out.data_ptr(),
+                                    _pitch(out, "out"), ss.data_ptr() if ss is not None else None,
+                                    _stream_handle(None))
+    _check(code, "tg_expert_gather")
+    return out if scales is None else (out, ss)
+
+
+def _combine(Y, offsets, pos, weights):
+    import torch
+    lib = load_library()
+    _check_plan(offsets, pos)
+    T, k = pos.shape
+    if Y.dim() != 2 or Y.shape[0] != T * k:
+        raise ValueError("the sorted rows must be one per choice of the plan")
+    kind = _type16(Y.dtype, "the sorted rows")
+    H = Y.shape[1]
+    if weights is not None:
+        if weights.dtype != torch.float32:
+            raise TypeError("weights must be float32")
+        if weights.shape != (T, k):
+            raise ValueError("weights must be tokens x topk")
+        weights = weights.contiguous()
+        _require_cuda(Y.device, (weights, "weights"))
+    out = empty_out(T, H, Y.dtype, Y.device)
+    _require_cuda(Y.device, (Y, "the sorted rows"), (offsets, "offsets"), (pos, "pos"))
+    with _on_device(Y):
+        code = lib.tg_expert_combine(T, k, H, kind, Y.data_ptr(), _pitch(Y, "Y"), pos.data_ptr(),
+                                     _kept_ptr(offsets),
+                                     weights.data_ptr() if weights is not None else None,
+                                     out.data_ptr(), _pitch(out, "out"), _stream_handle(None))
+    _check(code, "tg_expert_combine")
+    return out
+
+
+def _combine_grad(Y, g, offsets, pos, weights):
+    import torch
+    lib = load_library()
+    T, k = pos.shape
+    H = Y.shape[1]
+    weights = weights.contiguous()
+    dY = empty_out(T * k, H, Y.dtype, Y.device)
+    dw = torch.empty((T, k), dtype=torch.float32, device=Y.device)
+    _require_cuda(Y.device, (g, "the gradient"))
+    with _on_device(Y):
+        code = lib.tg_expert_combine_grad(T, k, H, _type16(Y.dtype, "Y"), Y.data_ptr(),
+                                          _pitch(Y, "Y"), g.data_ptr(), _pitch(g, "gradient"),
+                                          pos.data_ptr(), _kept_ptr(offsets), weights.data_ptr(),
+                                          dY.data_ptr(), _pitch(dY, "dY"), dw.data_ptr(),
+                                          _stream_handle(None))
+    _check(code, "tg_expert_combine_grad")
+    return dY, dw
+
+
+def _aligned_rows(g):
+    """A gradient as the kernels take it: itself where it is row-major with a
+    16-byte pitch and base, else a copy (autograd hands out expanded and
+    oddly pitched gradients that the caller has no say in)."""
+    eb = g.element_size()
+    if (g.stride(1) == 1 or g.shape[1] <= 1) and g.data_ptr() % 16 == 0 and \
+            (g.shape[0] <= 1 or (g.stride(0) >= g.shape[1] and (g.stride(0) * eb) % 16 == 0)):
+        return g
+    out = empty_out(g.shape[0], g.shape[1], g.dtype, g.device)
+    out.copy_(g)
+    return out
+
+
+def _offsets_of(groups):
+    import torch
+    offsets = groups.offsets if isinstance(groups, ExpertPlan) else groups
+    if offsets.dtype != torch.int32:
+        raise TypeError("offsets must be int32")
+    if offsets.dim() != 1 or offsets.shape[0] < 2 or not offsets.is_contiguous():
+        raise ValueError("offsets must be a contiguous vector of E + 1")
+    return offsets
+
+
+def gemm_grouped(A, groups, B, C=None, relu=False, stream=None, trans_b=False):
+    """C[r] = epi(A[r] @ W[e]) for the rows r of group e: A is M x K (float16
+    or bfloat16), W is B (E x K x N), or with trans_b stored E x N x K; groups
+    is an ExpertPlan or its offsets.  Rows behind the last group are zero."""
+    lib = load_library()
+    offsets = _offsets_of(groups)
+    E = offsets.shape[0] - 1
+    kind = _type16(A.dtype, "A")
+    if B.dtype != A.dtype:
+        raise TypeError("A and B must have one dtype")
+    if A.dim() != 2 or B.dim() != 3 or B.shape[0] != E:
+        raise ValueError("A must be 2-D and B one matrix per group")
+    M, K = A.shape
+    K2, N = (B.shape[2], B.shape[1]) if trans_b else B.shape[1:]
+    if K != K2:
+        raise ValueError(f"inner dimensions differ: {K} vs {K2}")
+    C = _out(C, M, N, A.dtype, A.device)
+    _require_cuda(A.device, (A, "A"), (B, "B"), (offsets, "offsets"), (C, "C"))
+    name = "tg_gemm_grouped_bf16" if kind == TYPE_BF16 else "tg_gemm_grouped_f16"
+    with _on_device(A):
+        code = getattr(lib, name)(M, N, K, E, A.data_ptr(), _pitch(A, "A"), offsets.data_ptr(),
+                                  B.data_ptr(), _pitch(B, "B"), _plane(B), int(trans_b),
+                                  C.data_ptr(), _pitch(C, "C"), EPI_RELU if relu else EPI_NONE,
+                                  _stream_handle(stream))
+    _check(code, name)
+    return C
+
+
+def gemm_grouped_wgrad(A, G, groups, C=None, stream=None):
+    """C[e] = A_e^T @ G_e over the rows of each group (float16 or bfloat16, A
+    M x K, G M x N, C E x K x N): the gradient of gemm_grouped's W for the
+    gradient G of its rows.  A group without rows gets zeros."""
+    import torch
+    lib = load_library()
+    offsets = _offsets_of(groups)
+    E = offsets.shape[0] - 1
+    kind = _type16(A.dtype, "A")
+    if G.dtype != A.dtype:
+        raise TypeError("A and G must have one dtype")
+    if A.dim() != 2 or G.dim() != 2 or A.shape[0] != G.shape[0]:
+        raise ValueError("A and G must be 2-D with the same rows")
+    (M, K), N = A.shape, G.shape[1]
+    if C is None:
+        per = 16 // A.element_size()
+        ld = max(per, -(-N // per) * per)
+        C = torch.empty((E, K, ld), dtype=A.dtype, device=A.device)[:, :, :N]
+    elif C.shape != (E, K, N) or C.dtype != A.dtype:
+        raise ValueError("C has the wrong shape or dtype")
+    _require_cuda(A.device, (A, "A"), (G, "G"), (offsets, "offsets"), (C, "C"))
+    name = "tg_gemm_grouped_wgrad_bf16" if kind == TYPE_BF16 else "tg_gemm_grouped_wgrad_f16"
+    with _on_device(A):
+        code = getattr(lib, name)(M, N, K, E, A.data_ptr(), _pitch(A, "A"), G.data_ptr(),
+                                  _pitch(G, "G"), offsets.data_ptr(), C.data_ptr(),
+                                  _pitch(C, "C"), _plane(C), _stream_handle(stream))
+    _check(code, name)
+    return C
+
+
+def gemm_grouped_w8a8(A, row_scales, groups, B, col_scales, C=None, out_dtype=None, relu=False,
+                      stream=None, trans_b=False):
+    """gemm_grouped on 8-bit rows and weights: int8 A (M x K) with float32
+    row_scales (M), int8 B (E x K x N, or E x N x K with trans_b) with float32
+    col_scales (E x N); sum and scales as gemm_w8a8."""
+    import torch
+    lib = load_library()
+    offsets = _offsets_of(groups)
+    E = offsets.shape[0] - 1
+    if A.dtype != torch.int8 or B.dtype != torch.int8:
+        raise TypeError("A and B must be int8")
+    if A.dim() != 2 or B.dim() != 3 or B.shape[0] != E:
+        raise ValueError("A must be 2-D and B one matrix per group")
+    M, K = A.shape
+    K2, N = (B.shape[2], B.shape[1]) if trans_b else B.shape[1:]
+    if K != K2:
+        raise ValueError(f"inner dimensions differ: {K} vs {K2}")
+    _vector(row_scales, M, torch.float32, "row_scales")
+    if col_scales.dtype != torch.float32:
+        raise TypeError("col_scales must be float32")
+    if col_scales.shape != (E, N) or (N > 1 and col_scales.stride(1) != 1):
+        raise ValueError("col_scales must be one row-major row of N per group")
+    if out_dtype is None:
+        out_dtype = torch.bfloat16 if C is None else C.dtype
+    kind = _type16(out_dtype, "C")
+    C = _out(C, M, N, out_dtype, A.device)
+    _require_cuda(A.device, (A, "A"), (B, "B"), (row_scales, "row_scales"),
+                  (col_scales, "col_scales"), (offsets, "offsets"), (C, "C"))
+    with _on_device(A):
+        code = lib.tg_gemm_grouped_w8a8(M, N, K, E, A.data_ptr(), _pitch(A, "A"),
+                                        row_scales.data_ptr(), offsets.data_ptr(), B.data_ptr(),
+                                        _pitch(B, "B"), _plane(B), int(trans_b),
+                                        col_scales.data_ptr(), _plane(col_scales), C.data_ptr(),
+                                        _pitch(C, "C"), kind, EPI_RELU if relu else EPI_NONE,
+                                        _stream_handle(stream))
+    _check(code, "tg_gemm_grouped_w8a8")
+    return C
+
+
+def _stored3(W):
+    """How the logical E x K x N weights reach the kernels: (storage,
+    transposed) with W[e] == storage[e] or its transpose and the storage's
+    matrices row-major; a view that is neither is copied."""
+    def ok(v):
+        return (v.stride(2) == 1 or v.shape[2] <= 1) and \
+            (v.shape[1] <= 1 or v.stride(1) >= v.shape[2]) and (v.shape[0] <= 1 or v.stride(0) > 0)
+
+    cands = [(v, tr) for v, tr in ((W, False), (W.transpose(1, 2), True)) if ok(v)]
+    for v, tr in cands:
+        if v.shape[1] <= 1 or (v.stride(1) * v.element_size()) % 16 == 0:
+            return v, tr
+    if cands:
+        return cands[0]
+    return W.contiguous(), False
+
+
+def _expert_functions():
+    import torch
+    from torch.autograd.function import once_differentiable
+
+    class _Gather(torch.autograd.Function):
+        """Xs[pos[i]] = X[i // topk]; the gradient adds each token's rows."""
+
+        @staticmethod
+        def forward(ctx, X, offsets, pos):
+            ctx.save_for_backward(offsets, pos)
+            return _gather(X, offsets, pos)
+
+        @staticmethod
+        @once_differentiable
+        def backward(ctx, g):
+            offsets, pos = ctx.saved_tensors
+            return _combine(_aligned_rows(g), offsets, pos, None), None, None
+
+    class _Combine(torch.autograd.Function):
+        """Y[t] = sum_j w[t, j] Ys[pos[t, j]], with both gradients."""
+
+        @staticmethod
+        def forward(ctx, Ys, weights, offsets, pos):
+            ctx.save_for_backward(Ys, weights, offsets, pos)
+            return _combine(Ys, offsets, pos, weights)
+
+        @staticmethod
+        @once_differentiable
+        def backward(ctx, g):
+            Ys, weights, offsets, pos = ctx.saved_tensors
+            g = _aligned_rows(g)
+            if weights is None:
+                return _gather(g, offsets, pos), None, None, None
+            dY, dw = _combine_grad(Ys, g, offsets, pos, weights)
+            return (dY if ctx.needs_input_grad[0] else None,
+                    dw if ctx.needs_input_grad[1] else None, None, None)
+
+    class _Product(torch.autograd.Function):
+        """C[r] = A[r] @ W[e], with dA = dC W[e]^T and dW[e] = A_e^T dC_e;
+        the weights are read, and their gradient is written, as stored."""
+
+        @staticmethod
+        def forward(ctx, A, W, offsets):
+            ctx.save_for_backward(A, W, offsets)
+            w, tr = _stored3(W)
+            return gemm_grouped(A, offsets, w, trans_b=tr)
+
+        @staticmethod
+        @once_differentiable
+        def backward(ctx, g):
+            A, W, offsets = ctx.saved_tensors
+            g = _aligned_rows(g)
+            w, tr = _stored3(W)
+            dA = dW = None
+            if ctx.needs_input_grad[0]:
+                dA = gemm_grouped(g, offsets, w, trans_b=not tr)
+            if ctx.needs_input_grad[1]:
+                if tr:
+                    dW = gemm_grouped_wgrad(g, A, offsets).transpose(1, 2)
+                else:
+                    dW = gemm_grouped_wgrad(A, g, offsets)
+            return dA, dW, None
+
+    return _Gather, _Combine, _Product
+
+
+_EXPERT = None
+
+
+def _expert(i):
+    global _EXPERT
+    if _EXPERT is None:
+        _EXPERT = _expert_functions()
+    return _EXPERT[i]
+
+
+def expert_gather(X, plan, scales=None):
+    """The rows of X (tokens x H) sorted by expert: row plan.pos[t, j] is X[t];
+    the rows of dropped choices are zero.  X is float16, bfloat16
+    (differentiable) or int8; with scales (int8 rows only: float32, one per
+    token) returns (rows, their scales)."""
+    if scales is not None:
+        import torch
+        if X.dtype != torch.int8:
+            raise TypeError("scales go with int8 rows")
+        return _gather(X, plan.offsets, plan.pos, scales)
+    return _expert(0).apply(X, plan.offsets, plan.pos)
+
+
+def expert_combine(Ys, plan, weights=None):
+    """Sorted rows back to tokens: Y[t] = sum_j weights[t, j] *
+    Ys[plan.pos[t, j]] over the kept choices, summed in float32 in the order of
+    j.  Ys is float16 or bfloat16, weights float32 (tokens x topk; all 1 where
+    None).  Differentiable in Ys and weights."""
+    return _expert(1).apply(Ys, weights, plan.offsets, plan.pos)
+
+
+def expert_matmul(Xs, W, groups):
+    """Differentiable experts' product: row r of group e times W[e].
+
+    Xs: M x K sorted rows (float16 or bfloat16); W: E x K x N, or a transposed
+    view of E x N x K storage (W.transpose(1, 2)), which needs no copy; groups:
+    an ExpertPlan or its offsets.  Rows behind the last group are zero and get
+    zero gradient."""
+    return _expert(2).apply(Xs, W, _offsets_of(groups))
 
 
 def last_device_status(stream=None):

@@ -23,11 +23,12 @@ EncodeTiledFn g_encode = nullptr;
 std::once_flag g_encode_once;
 
 struct MapKey {
-    uint64_t base, cols, rows, ld;
+    uint64_t base, cols, rows, ld, depth, plane;   // depth, plane: 0 for a 2-D map
     uint32_t box_cols, box_rows;
     int dtype, swz;
     bool operator==(const MapKey& o) const {
         return base == o.base && cols == o.cols && rows == o.rows && ld == o.ld &&
+               depth == o.depth && plane == o.plane &&
                box_cols == o.box_cols && box_rows == o.box_rows && dtype == o.dtype &&
                swz == o.swz;
     }
@@ -38,6 +39,7 @@ struct MapKeyHash {
         h ^= (k.cols + 0x7F4A7C15ull) * 0xBF58476D1CE4E5B9ull;
         h ^= (k.rows + (h << 6) + (h >> 2)) * 0x94D049BB133111EBull;
         h ^= k.ld + (static_cast<uint64_t>(k.box_cols) << 32) + k.box_rows + (k.dtype << 3) + k.swz;
+        h ^= k.depth * 0xD6E8FEB86659FD93ull + k.plane * 0xA24BAED4963EE407ull;
         return static_cast<size_t>(h ^ (h >> 31));
     }
 };
@@ -75,9 +77,12 @@ const DeviceInfo* current_device(int* dev_out) {
     return g_dev[dev].ok ? &g_dev[dev] : nullptr;
 }
 
-bool tensor_map_2d(CUtensorMap* out, const void* base, CUtensorMapDataType dtype,
-                   int elem_bytes, uint64_t cols, uint64_t rows, uint64_t ld_bytes,
-                   uint32_t box_cols, uint32_t box_rows, CUtensorMapSwizzle swz) {
+namespace {
+
+// A 2-D map (depth 0), or a 3-D map of `depth` matrices `plane` bytes apart.
+bool tensor_map(CUtensorMap* out, const void* base, CUtensorMapDataType dtype, uint64_t cols,
+                uint64_t rows, uint64_t ld_bytes, uint64_t depth, uint64_t plane,
+                uint32_t box_cols, uint32_t box_rows, CUtensorMapSwizzle swz) {
     std::call_once(g_encode_once, [] {
         void* fn = nullptr;
         cudaDriverEntryPointQueryResult q;
@@ -89,25 +94,24 @@ bool tensor_map_2d(CUtensorMap* out, const void* base, CUtensorMapDataType dtype
     // A map over a 1-row / 1-column matrix still needs a legal stride.
     if (rows < 1) rows = 1;
     if (cols < 1) cols = 1;
-    MapKey key{reinterpret_cast<uint64_t>(base), cols, rows, ld_bytes, box_cols, box_rows,
+    MapKey key{reinterpret_cast<uint64_t>(base), cols, rows, ld_bytes, depth, plane, box_cols, box_rows,
                static_cast<int>(dtype), static_cast<int>(swz)};
     {
         std::lock_guard<std::mutex> lk(g_map_mu);
         auto it = g_maps.find(key);
         if (it != g_maps.end()) { *out = it->second; return true; }
     }
-    cuuint64_t dims[2] = {cols, rows};
-    cuuint64_t strides[1] = {ld_bytes};
-    cuuint32_t box[2] = {box_cols, box_rows};
-    cuuint32_t estr[2] = {1, 1};
+    cuuint64_t dims[3] = {cols, rows, depth};
+    cuuint64_t strides[2] = {ld_bytes, plane};
+    cuuint32_t box[3] = {box_cols, box_rows, 1};
+    cuuint32_t estr[3] = {1, 1, 1};
     CUtensorMap m;
     std::memset(&m, 0, sizeof m);
-    CUresult r = g_encode(&m, dtype, 2, const_cast<void*>(base), dims, strides, box, estr,
+    CUresult r = g_encode(&m, dtype, depth ? 3 : 2, const_cast<void*>(base), dims, strides, box, estr,
                           CU_TENSOR_MAP_INTERLEAVE_NONE,
                           swz,
                           CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     if (r != CUDA_SUCCESS) return false;
-    (void)elem_bytes;
     {
         std::lock_guard<std::mutex> lk(g_map_mu);
         if (g_maps.size() >= kMaxCachedMaps) g_maps.clear();
@@ -115,6 +119,22 @@ bool tensor_map_2d(CUtensorMap* out, const void* base, CUtensorMapDataType dtype
     }
     *out = m;
     return true;
+}
+
+}  // namespace
+
+bool tensor_map_2d(CUtensorMap* out, const void* base, CUtensorMapDataType dtype,
+                   int elem_bytes, uint64_t cols, uint64_t rows, uint64_t ld_bytes,
+                   uint32_t box_cols, uint32_t box_rows, CUtensorMapSwizzle swz) {
+    (void)elem_bytes;
+    return tensor_map(out, base, dtype, cols, rows, ld_bytes, 0, 0, box_cols, box_rows, swz);
+}
+
+bool tensor_map_3d(CUtensorMap* out, const void* base, CUtensorMapDataType dtype, uint64_t cols,
+                   uint64_t rows, uint64_t ld_bytes, uint64_t depth, uint64_t plane_bytes,
+                   uint32_t box_cols, uint32_t box_rows, CUtensorMapSwizzle swz) {
+    return tensor_map(out, base, dtype, cols, rows, ld_bytes, depth < 1 ? 1 : depth, plane_bytes,
+                      box_cols, box_rows, swz);
 }
 
 unsigned long long wait_limit_ns() {

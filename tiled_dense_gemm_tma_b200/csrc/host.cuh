@@ -23,6 +23,12 @@ bool tensor_map_2d(CUtensorMap* out, const void* base, CUtensorMapDataType dtype
                    int elem_bytes, uint64_t cols, uint64_t rows, uint64_t ld_bytes,
                    uint32_t box_cols, uint32_t box_rows, CUtensorMapSwizzle swz);
 
+// The same over `depth` matrices, `plane_bytes` apart (a multiple of 16); the
+// box covers one of them.
+bool tensor_map_3d(CUtensorMap* out, const void* base, CUtensorMapDataType dtype, uint64_t cols,
+                   uint64_t rows, uint64_t ld_bytes, uint64_t depth, uint64_t plane_bytes,
+                   uint32_t box_cols, uint32_t box_rows, CUtensorMapSwizzle swz);
+
 constexpr CUtensorMapSwizzle SWZ_NONE = CU_TENSOR_MAP_SWIZZLE_NONE;
 constexpr CUtensorMapSwizzle SWZ_64 = CU_TENSOR_MAP_SWIZZLE_64B;
 constexpr CUtensorMapSwizzle SWZ_128 = CU_TENSOR_MAP_SWIZZLE_128B;
@@ -62,6 +68,7 @@ int* device_status_ptr();
 //   56-57  gemm_sp24.cu (one CTA)   61-62  gemm_sp24.cu (CTA pairs)
 //   64-67  gemm_tc.cu        CTA-pair bf16/f16 with the operands swapped (M <= 128)
 //   68     gemm_tc.cu        CTA-pair TF32
+//   70-81  gemm_group.cu     experts' products and 8-bit products
 constexpr int kMaxSlots = 128;
 cudaError_t set_smem_attr(const void* func, int bytes, int slot);
 

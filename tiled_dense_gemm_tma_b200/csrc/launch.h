@@ -45,6 +45,41 @@ inline long long persistent_grid(long long units, int cap, int ctas) {
     return units < c ? units : c;
 }
 
+// Products over groups of rows (gemm_group.cuh): g.M rows of A, K columns,
+// weights (or, for the weight gradient, the rows' gradient) in g.B.
+struct GroupArgs {
+    GemmArgs g;
+    int E;                           // groups
+    const int* offsets;              // device, E + 1; null: one group of all rows (E = 1)
+    int trans_b;                     // weights stored N x K
+    int64_t plane_b;                 // elements between the weights of two groups
+    int64_t plane;                   // weight gradient: elements between two matrices of C
+    const float* row_scale;          // 8-bit only: g.M
+    const float* col_scale;          // 8-bit only: N per group, scale_plane apart
+    int64_t scale_plane;
+};
+int launch_group(const GroupArgs& a, int bf16);
+int launch_group_grad(const GroupArgs& a, int bf16);
+int launch_group_i8(const GroupArgs& a, int bf16);
+
+// Rows of 16-bit values to 8-bit integers with one scale per row.
+int launch_quant_i8(int64_t M, int64_t K, const void* X, int64_t ldx, int bf16, int8_t* Q,
+                    int64_t ldq, float* scales, void* stream);
+// Tokens sorted by expert, and back (expert.cu).
+int64_t expert_sort_scratch(int64_t n, int E);
+int launch_expert_sort(int64_t tokens, int topk, int E, const void* ids, int id_bytes, int* offsets,
+                       int* pos, int* src, void* scratch, void* stream);
+int launch_expert_gather(int64_t tokens, int topk, int64_t H, int eb, const void* X, int64_t ldx,
+                         const float* scales, const int* pos, const int* kept, void* out,
+                         int64_t ldo, float* out_scales, void* stream);
+int launch_expert_combine(int64_t tokens, int topk, int64_t H, int bf16, const void* Y, int64_t ldy,
+                          const int* pos, const int* kept, const float* weights, void* out,
+                          int64_t ldo, void* stream);
+int launch_expert_combine_grad(int64_t tokens, int topk, int64_t H, int bf16, const void* Y,
+                               int64_t ldy, const void* dout, int64_t ldd, const int* pos,
+                               const int* kept, const float* weights, void* dY, int64_t lddy,
+                               float* dweights, void* stream);
+
 int launch_tc_bf16(const GemmArgs& a);
 int launch_tc_f16(const GemmArgs& a);
 int launch_tc_tf32(const GemmArgs& a);

@@ -149,6 +149,34 @@ TG_HD void tile_coords(int t, int ntm, int ntn, int group_m, int& tm, int& tn) {
     tn = local / gsz;
 }
 
+// ------------------------------------------------------ groups of rows
+// The experts' products: a group of `rows` > 0 consecutive rows is cut into
+// grp_tiles(rows) tiles of grp_width(rows) rows (the last one may hold
+// fewer), as even as whole MMA widths (multiples of 32, at most 256) allow, so
+// that a group of 300 rows is 160 + 140 and not 256 + 44.  No tile is empty:
+// the width is at most 256, and 256 * (tiles - 1) < rows.
+
+TG_HD int grp_tiles(int rows) { return (rows - 1) / 256 + 1; }
+
+TG_HD int grp_width(int rows) {
+    const int nt = grp_tiles(rows);
+    const int per = (rows - 1) / nt + 1;
+    return (per + 31) / 32 * 32;
+}
+
+// Rows [r0, r1) of group e from the offsets (ng + 1 of them), clamped to
+// 0 <= r0 <= r1 <= M so that no offset leads outside the matrices; group ng
+// is the rows behind the last one.
+TG_HD void grp_rows(const int* offsets, int e, int ng, int M, int& r0, int& r1) {
+    if (!offsets) {                        // one group of all rows
+        r0 = e == 0 ? 0 : M;
+        r1 = M;
+        return;
+    }
+    r0 = sched_min(sched_max(offsets[e], 0), M);
+    r1 = e < ng ? sched_min(sched_max(offsets[e + 1], r0), M) : M;
+}
+
 // ------------------------------------------------------- fp32 split-K
 // Number of k ranges per output tile: 1 when the tiles already fill the SMs;
 // otherwise enough to fill them, with at most 8 ranges and no more ranges than
