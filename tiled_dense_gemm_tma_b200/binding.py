@@ -438,12 +438,34 @@ def _type16(dtype, name):
     raise TypeError(f"{name} must be float16 or bfloat16")
 
 
-def _on_device(t):
-    """As _device_ctx, without the switch where t's device is current already."""
+def _launch(name, t, stream, *args):
+    """Call the entry point on t's device (made current where it is not) and on
+    `stream`, by default that device's current stream; raise on an error.  The
+    calls of this section go through here: they are made once per layer and
+    token step, where the host's time per call is what a user waits for."""
     import torch
-    if not t.is_cuda or torch.cuda.current_device() == t.device.index:
-        return contextlib.nullcontext()
-    return torch.cuda.device(t.device)
+    index = t.device.index
+    if stream is None:
+        stream = torch._C._cuda_getCurrentRawStream(index) if t.is_cuda else 0
+    elif not isinstance(stream, int):
+        stream = stream.cuda_stream
+    fn = getattr(load_library(), name)
+    if not t.is_cuda or torch.cuda.current_device() == index:
+        code = fn(*args, stream)
+    else:
+        with torch.cuda.device(index):
+            code = fn(*args, stream)
+    if code:
+        raise TgError(code, name)
+
+
+def _rows_out(M, N, dtype, device):
+    """empty_out, without the view where the rows fill whole 16-byte units."""
+    import torch
+    per = 16 // dtype.itemsize
+    if N % per == 0 and N:
+        return torch.empty((M, N), dtype=dtype, device=device)
+    return torch.empty((M, max(per, -(-N // per) * per)), dtype=dtype, device=device)[:, :N]
 
 
 def _pitch(t, name):
@@ -472,7 +494,7 @@ def _vector(t, n, dtype, name):
 
 def _out(C, M, N, dtype, device):
     if C is None:
-        return empty_out(M, N, dtype, device)
+        return _rows_out(M, N, dtype, device)
     if C.shape != (M, N) or C.dtype != dtype:
         raise ValueError("C has the wrong shape or dtype")
     return C
@@ -484,23 +506,20 @@ def quant_i8(X, Q=None, scales=None, stream=None):
     ties to even.  Returns (Q, scales).  A row of zeros gets scale 0; a row
     with an infinity or a NaN gets scale NaN."""
     import torch
-    lib = load_library()
     if X.dim() != 2:
         raise ValueError("X must be 2-D")
     kind = _type16(X.dtype, "X")
     M, K = X.shape
     if Q is None:
-        Q = empty_out(M, K, torch.int8, X.device)
+        Q = _rows_out(M, K, torch.int8, X.device)
     elif Q.shape != (M, K) or Q.dtype != torch.int8:
         raise ValueError("Q has the wrong shape or dtype")
     if scales is None:
         scales = torch.empty(M, dtype=torch.float32, device=X.device)
     _vector(scales, M, torch.float32, "scales")
     _require_cuda(X.device, (X, "X"), (Q, "Q"), (scales, "scales"))
-    with _on_device(X):
-        code = lib.tg_quant_i8(M, K, X.data_ptr(), _pitch(X, "X"), kind, Q.data_ptr(),
-                               _pitch(Q, "Q"), scales.data_ptr(), _stream_handle(stream))
-    _check(code, "tg_quant_i8")
+    _launch("tg_quant_i8", X, stream, M, K, X.data_ptr(), _pitch(X, "X"), kind,
+            Q.data_ptr(), _pitch(Q, "Q"), scales.data_ptr())
     return Q, scales
 
 
@@ -511,7 +530,6 @@ def gemm_w8a8(A, row_scales, B, col_scales, C=None, out_dtype=None, relu=False, 
     of M and N.  C is float16 or bfloat16 (out_dtype, by default C's or
     bfloat16)."""
     import torch
-    lib = load_library()
     if A.dtype != torch.int8 or B.dtype != torch.int8:
         raise TypeError("A and B must be int8")
     if A.dim() != 2 or B.dim() != 2:
@@ -528,12 +546,10 @@ def gemm_w8a8(A, row_scales, B, col_scales, C=None, out_dtype=None, relu=False, 
     C = _out(C, M, N, out_dtype, A.device)
     _require_cuda(A.device, (A, "A"), (B, "B"), (row_scales, "row_scales"),
                   (col_scales, "col_scales"), (C, "C"))
-    with _on_device(A):
-        code = lib.tg_gemm_w8a8(M, N, K, A.data_ptr(), _pitch(A, "A"), row_scales.data_ptr(),
-                                B.data_ptr(), _pitch(B, "B"), int(trans_b), col_scales.data_ptr(),
-                                C.data_ptr(), _pitch(C, "C"), kind,
-                                EPI_RELU if relu else EPI_NONE, _stream_handle(stream))
-    _check(code, "tg_gemm_w8a8")
+    _launch("tg_gemm_w8a8", A, stream, M, N, K, A.data_ptr(), _pitch(A, "A"),
+            row_scales.data_ptr(), B.data_ptr(), _pitch(B, "B"), int(trans_b),
+            col_scales.data_ptr(), C.data_ptr(), _pitch(C, "C"), kind, EPI_RELU if relu else
+            EPI_NONE)
     return C
 
 
@@ -569,7 +585,6 @@ def expert_sort(ids, num_experts, stream=None):
     expert, as an ExpertPlan.  Numbers outside 0..num_experts - 1 are dropped
     choices."""
     import torch
-    lib = load_library()
     if ids.dim() != 2:
         raise ValueError("ids must be 2-D (tokens x topk)")
     if ids.dtype not in (torch.int32, torch.int64):
@@ -578,7 +593,7 @@ def expert_sort(ids, num_experts, stream=None):
     T, k = ids.shape
     if k < 1:
         raise ValueError("ids must hold at least one choice per token")
-    need = lib.tg_expert_sort_scratch(T * k, num_experts)
+    need = load_library().tg_expert_sort_scratch(T * k, num_experts)
     if need < 0:
         raise ValueError("expert_sort takes 1 to 1024 experts and fewer than 2^31 choices")
     ids = ids.contiguous()
@@ -588,12 +603,9 @@ def expert_sort(ids, num_experts, stream=None):
     buf = torch.empty(sum(cuts), dtype=torch.int32, device=ids.device)
     offsets, pos, src = buf[:E1], buf[cuts[0]:cuts[0] + n], buf[cuts[0] + cuts[1]:cuts[0] + cuts[1] + n]
     base = buf.data_ptr()
-    with _on_device(ids):
-        code = lib.tg_expert_sort(T, k, num_experts, ids.data_ptr(), ids.element_size(), base,
-                                  base + 4 * cuts[0], base + 4 * (cuts[0] + cuts[1]),
-                                  base + 4 * (cuts[0] + cuts[1] + cuts[2]) if need else None,
-                                  _stream_handle(stream))
-    _check(code, "tg_expert_sort")
+    _launch("tg_expert_sort", ids, stream, T, k, num_experts, ids.data_ptr(),
+            ids.element_size(), base, base + 4 * cuts[0], base + 4 * (cuts[0] + cuts[1]),
+            base + 4 * (cuts[0] + cuts[1] + cuts[2]) if need else None)
     return ExpertPlan(offsets, pos.view(T, k), src)
 
 
@@ -611,7 +623,6 @@ def _check_plan(offsets, pos):
 
 def _gather(X, offsets, pos, scales=None):
     import torch
-    lib = load_library()
     _check_plan(offsets, pos)
     T, k = pos.shape
     if X.dim() != 2 or X.shape[0] != T:
@@ -619,26 +630,22 @@ def _gather(X, offsets, pos, scales=None):
     if X.dtype not in (torch.float16, torch.bfloat16, torch.int8):
         raise TypeError("X must be float16, bfloat16 or int8")
     H = X.shape[1]
-    out = empty_out(T * k, H, X.dtype, X.device)
+    out = _rows_out(T * k, H, X.dtype, X.device)
     ss = None
     if scales is not None:
         _vector(scales, T, torch.float32, "scales")
         ss = torch.empty(T * k, dtype=torch.float32, device=X.device)
         _require_cuda(X.device, (scales, "scales"))
     _require_cuda(X.device, (X, "X"), (offsets, "offsets"), (pos, "pos"))
-    with _on_device(X):
-        code = lib.tg_expert_gather(T, k, H, X.element_size(), X.data_ptr(), _pitch(X, "X"),
-                                    scales.data_ptr() if scales is not None else None,
-                                    pos.data_ptr(), _kept_ptr(offsets), out.data_ptr(),
-                                    _pitch(out, "out"), ss.data_ptr() if ss is not None else None,
-                                    _stream_handle(None))
-    _check(code, "tg_expert_gather")
+    _launch("tg_expert_gather", X, None, T, k, H, X.element_size(), X.data_ptr(), _pitch(X,
+            "X"), scales.data_ptr() if scales is not None else None, pos.data_ptr(),
+            _kept_ptr(offsets), out.data_ptr(), _pitch(out, "out"), ss.data_ptr() if ss is
+            not None else None)
     return out if scales is None else (out, ss)
 
 
 def _combine(Y, offsets, pos, weights):
     import torch
-    lib = load_library()
     _check_plan(offsets, pos)
     T, k = pos.shape
     if Y.dim() != 2 or Y.shape[0] != T * k:
@@ -652,33 +659,26 @@ def _combine(Y, offsets, pos, weights):
             raise ValueError("weights must be tokens x topk")
         weights = weights.contiguous()
         _require_cuda(Y.device, (weights, "weights"))
-    out = empty_out(T, H, Y.dtype, Y.device)
+    out = _rows_out(T, H, Y.dtype, Y.device)
     _require_cuda(Y.device, (Y, "the sorted rows"), (offsets, "offsets"), (pos, "pos"))
-    with _on_device(Y):
-        code = lib.tg_expert_combine(T, k, H, kind, Y.data_ptr(), _pitch(Y, "Y"), pos.data_ptr(),
-                                     _kept_ptr(offsets),
-                                     weights.data_ptr() if weights is not None else None,
-                                     out.data_ptr(), _pitch(out, "out"), _stream_handle(None))
-    _check(code, "tg_expert_combine")
+    _launch("tg_expert_combine", Y, None, T, k, H, kind, Y.data_ptr(), _pitch(Y, "Y"),
+            pos.data_ptr(), _kept_ptr(offsets), weights.data_ptr() if weights is not None
+            else None, out.data_ptr(), _pitch(out, "out"))
     return out
 
 
-def _combine_grad(Y, g, offsets, pos, weights):
+def _combine_grad(Y, weights, g, offsets, pos):
     import torch
-    lib = load_library()
     T, k = pos.shape
     H = Y.shape[1]
     weights = weights.contiguous()
-    dY = empty_out(T * k, H, Y.dtype, Y.device)
+    dY = _rows_out(T * k, H, Y.dtype, Y.device)
     dw = torch.empty((T, k), dtype=torch.float32, device=Y.device)
     _require_cuda(Y.device, (g, "the gradient"))
-    with _on_device(Y):
-        code = lib.tg_expert_combine_grad(T, k, H, _type16(Y.dtype, "Y"), Y.data_ptr(),
-                                          _pitch(Y, "Y"), g.data_ptr(), _pitch(g, "gradient"),
-                                          pos.data_ptr(), _kept_ptr(offsets), weights.data_ptr(),
-                                          dY.data_ptr(), _pitch(dY, "dY"), dw.data_ptr(),
-                                          _stream_handle(None))
-    _check(code, "tg_expert_combine_grad")
+    _launch("tg_expert_combine_grad", Y, None, T, k, H, _type16(Y.dtype, "Y"), Y.data_ptr(),
+            _pitch(Y, "Y"), g.data_ptr(), _pitch(g, "gradient"), pos.data_ptr(),
+            _kept_ptr(offsets), weights.data_ptr(), dY.data_ptr(), _pitch(dY, "dY"),
+            dw.data_ptr())
     return dY, dw
 
 
@@ -690,7 +690,7 @@ def _aligned_rows(g):
     if (g.stride(1) == 1 or g.shape[1] <= 1) and g.data_ptr() % 16 == 0 and \
             (g.shape[0] <= 1 or (g.stride(0) >= g.shape[1] and (g.stride(0) * eb) % 16 == 0)):
         return g
-    out = empty_out(g.shape[0], g.shape[1], g.dtype, g.device)
+    out = _rows_out(g.shape[0], g.shape[1], g.dtype, g.device)
     out.copy_(g)
     return out
 
@@ -709,7 +709,6 @@ def gemm_grouped(A, groups, B, C=None, relu=False, stream=None, trans_b=False):
     """C[r] = epi(A[r] @ W[e]) for the rows r of group e: A is M x K (float16
     or bfloat16), W is B (E x K x N), or with trans_b stored E x N x K; groups
     is an ExpertPlan or its offsets.  Rows behind the last group are zero."""
-    lib = load_library()
     offsets = _offsets_of(groups)
     E = offsets.shape[0] - 1
     kind = _type16(A.dtype, "A")
@@ -724,12 +723,9 @@ def gemm_grouped(A, groups, B, C=None, relu=False, stream=None, trans_b=False):
     C = _out(C, M, N, A.dtype, A.device)
     _require_cuda(A.device, (A, "A"), (B, "B"), (offsets, "offsets"), (C, "C"))
     name = "tg_gemm_grouped_bf16" if kind == TYPE_BF16 else "tg_gemm_grouped_f16"
-    with _on_device(A):
-        code = getattr(lib, name)(M, N, K, E, A.data_ptr(), _pitch(A, "A"), offsets.data_ptr(),
-                                  B.data_ptr(), _pitch(B, "B"), _plane(B), int(trans_b),
-                                  C.data_ptr(), _pitch(C, "C"), EPI_RELU if relu else EPI_NONE,
-                                  _stream_handle(stream))
-    _check(code, name)
+    _launch(name, A, stream, M, N, K, E, A.data_ptr(), _pitch(A, "A"), offsets.data_ptr(),
+            B.data_ptr(), _pitch(B, "B"), _plane(B), int(trans_b), C.data_ptr(), _pitch(C,
+            "C"), EPI_RELU if relu else EPI_NONE)
     return C
 
 
@@ -738,7 +734,6 @@ def gemm_grouped_wgrad(A, G, groups, C=None, stream=None):
     M x K, G M x N, C E x K x N): the gradient of gemm_grouped's W for the
     gradient G of its rows.  A group without rows gets zeros."""
     import torch
-    lib = load_library()
     offsets = _offsets_of(groups)
     E = offsets.shape[0] - 1
     kind = _type16(A.dtype, "A")
@@ -755,11 +750,8 @@ def gemm_grouped_wgrad(A, G, groups, C=None, stream=None):
         raise ValueError("C has the wrong shape or dtype")
     _require_cuda(A.device, (A, "A"), (G, "G"), (offsets, "offsets"), (C, "C"))
     name = "tg_gemm_grouped_wgrad_bf16" if kind == TYPE_BF16 else "tg_gemm_grouped_wgrad_f16"
-    with _on_device(A):
-        code = getattr(lib, name)(M, N, K, E, A.data_ptr(), _pitch(A, "A"), G.data_ptr(),
-                                  _pitch(G, "G"), offsets.data_ptr(), C.data_ptr(),
-                                  _pitch(C, "C"), _plane(C), _stream_handle(stream))
-    _check(code, name)
+    _launch(name, A, stream, M, N, K, E, A.data_ptr(), _pitch(A, "A"), G.data_ptr(),
+            _pitch(G, "G"), offsets.data_ptr(), C.data_ptr(), _pitch(C, "C"), _plane(C))
     return C
 
 
@@ -769,7 +761,6 @@ def gemm_grouped_w8a8(A, row_scales, groups, B, col_scales, C=None, out_dtype=No
     row_scales (M), int8 B (E x K x N, or E x N x K with trans_b) with float32
     col_scales (E x N); sum and scales as gemm_w8a8."""
     import torch
-    lib = load_library()
     offsets = _offsets_of(groups)
     E = offsets.shape[0] - 1
     if A.dtype != torch.int8 or B.dtype != torch.int8:
@@ -791,14 +782,10 @@ def gemm_grouped_w8a8(A, row_scales, groups, B, col_scales, C=None, out_dtype=No
     C = _out(C, M, N, out_dtype, A.device)
     _require_cuda(A.device, (A, "A"), (B, "B"), (row_scales, "row_scales"),
                   (col_scales, "col_scales"), (offsets, "offsets"), (C, "C"))
-    with _on_device(A):
-        code = lib.tg_gemm_grouped_w8a8(M, N, K, E, A.data_ptr(), _pitch(A, "A"),
-                                        row_scales.data_ptr(), offsets.data_ptr(), B.data_ptr(),
-                                        _pitch(B, "B"), _plane(B), int(trans_b),
-                                        col_scales.data_ptr(), _plane(col_scales), C.data_ptr(),
-                                        _pitch(C, "C"), kind, EPI_RELU if relu else EPI_NONE,
-                                        _stream_handle(stream))
-    _check(code, "tg_gemm_grouped_w8a8")
+    _launch("tg_gemm_grouped_w8a8", A, stream, M, N, K, E, A.data_ptr(), _pitch(A, "A"),
+            row_scales.data_ptr(), offsets.data_ptr(), B.data_ptr(), _pitch(B, "B"),
+            _plane(B), int(trans_b), col_scales.data_ptr(), _plane(col_scales),
+            C.data_ptr(), _pitch(C, "C"), kind, EPI_RELU if relu else EPI_NONE)
     return C
 
 
@@ -821,40 +808,45 @@ def _stored3(W):
 
 def _expert_functions():
     import torch
-    from torch.autograd.function import once_differentiable
+
+    def once():
+        # a backward that itself records a graph would lose the kernels' part
+        if torch.is_grad_enabled():
+            raise RuntimeError("the experts' operators are differentiable once")
 
     class _Gather(torch.autograd.Function):
         """Xs[pos[i]] = X[i // topk]; the gradient adds each token's rows."""
 
         @staticmethod
-        def forward(ctx, X, offsets, pos):
-            ctx.save_for_backward(offsets, pos)
-            return _gather(X, offsets, pos)
+        def forward(ctx, X, plan):
+            ctx.plan = plan
+            return _gather(X, plan.offsets, plan.pos)
 
         @staticmethod
-        @once_differentiable
         def backward(ctx, g):
-            offsets, pos = ctx.saved_tensors
-            return _combine(_aligned_rows(g), offsets, pos, None), None, None
+            once()
+            return _combine(_aligned_rows(g), ctx.plan.offsets, ctx.plan.pos, None), None
 
     class _Combine(torch.autograd.Function):
         """Y[t] = sum_j w[t, j] Ys[pos[t, j]], with both gradients."""
 
         @staticmethod
-        def forward(ctx, Ys, weights, offsets, pos):
-            ctx.save_for_backward(Ys, weights, offsets, pos)
-            return _combine(Ys, offsets, pos, weights)
+        def forward(ctx, Ys, weights, plan):
+            ctx.plan = plan
+            if weights is not None:
+                ctx.save_for_backward(Ys, weights)
+            return _combine(Ys, plan.offsets, plan.pos, weights)
 
         @staticmethod
-        @once_differentiable
         def backward(ctx, g):
-            Ys, weights, offsets, pos = ctx.saved_tensors
+            once()
             g = _aligned_rows(g)
-            if weights is None:
-                return _gather(g, offsets, pos), None, None, None
-            dY, dw = _combine_grad(Ys, g, offsets, pos, weights)
+            offsets, pos = ctx.plan.offsets, ctx.plan.pos
+            if not ctx.saved_tensors:
+                return _gather(g, offsets, pos), None, None
+            dY, dw = _combine_grad(*ctx.saved_tensors, g, offsets, pos)
             return (dY if ctx.needs_input_grad[0] else None,
-                    dw if ctx.needs_input_grad[1] else None, None, None)
+                    dw if ctx.needs_input_grad[1] else None, None)
 
     class _Product(torch.autograd.Function):
         """C[r] = A[r] @ W[e], with dA = dC W[e]^T and dW[e] = A_e^T dC_e;
@@ -867,8 +859,8 @@ def _expert_functions():
             return gemm_grouped(A, offsets, w, trans_b=tr)
 
         @staticmethod
-        @once_differentiable
         def backward(ctx, g):
+            once()
             A, W, offsets = ctx.saved_tensors
             g = _aligned_rows(g)
             w, tr = _stored3(W)
@@ -905,7 +897,7 @@ def expert_gather(X, plan, scales=None):
         if X.dtype != torch.int8:
             raise TypeError("scales go with int8 rows")
         return _gather(X, plan.offsets, plan.pos, scales)
-    return _expert(0).apply(X, plan.offsets, plan.pos)
+    return _expert(0).apply(X, plan)
 
 
 def expert_combine(Ys, plan, weights=None):
@@ -913,7 +905,7 @@ def expert_combine(Ys, plan, weights=None):
     Ys[plan.pos[t, j]] over the kept choices, summed in float32 in the order of
     j.  Ys is float16 or bfloat16, weights float32 (tokens x topk; all 1 where
     None).  Differentiable in Ys and weights."""
-    return _expert(1).apply(Ys, weights, plan.offsets, plan.pos)
+    return _expert(1).apply(Ys, weights, plan)
 
 
 def expert_matmul(Xs, W, groups):
