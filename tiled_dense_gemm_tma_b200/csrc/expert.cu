@@ -32,25 +32,29 @@ namespace {
 // expert, so no counter is shared and the order is the input's.  Counters:
 // [warp][E + 1] in shared memory (the last for dropped choices), turned into
 // each warp's first row by a sum over the warps before it, the blocks before
-// it (several blocks only), and all smaller experts.
+// it (several blocks only), and all smaller experts.  A warp keeps the first
+// kKeep x 32 of its choices in registers between counting and placing.
 //
-// Up to kOneBlock choices one block does it all in one launch.  More of them
-// are cut among up to kMaxBlocks blocks: a first launch writes each block's
-// counts, the second starts from them.
+// Bound by latency, not by its 12 bytes a choice.  Up to kOneBlock choices one
+// block does it all in one launch.  More of them are cut among up to
+// kMaxBlocks blocks: a first launch writes each block's counts; the second,
+// which starts and counts its own choices while the first still runs, waits
+// for those counts and places.
 
-constexpr int kSortThreads = 1024;
-constexpr int kSortWarps = kSortThreads / 32;
+constexpr int kKeep = 8;
 constexpr int kOneBlock = 8192;
-constexpr int kPerBlock = 2048;
+constexpr int kPerBlock = 1024;
 constexpr int kMaxBlocks = 148;
 
 struct SortPlan {
+    int warps;                // per block
     int blocks;
     int64_t chunk;            // choices per block
 };
 
 SortPlan sort_plan(int64_t n) {
     SortPlan p;
+    p.warps = n <= 8 * 32 * 4 ? 8 : 32;
     p.blocks = 1;
     if (n > kOneBlock) {
         const int64_t b = (n + kPerBlock - 1) / kPerBlock;
@@ -60,26 +64,51 @@ SortPlan sort_plan(int64_t n) {
     return p;
 }
 
+// The choices [w0, w1) of one warp.
 template <typename Id>
-__device__ __forceinline__ int choice(const Id* ids, int64_t i, int64_t end, int E) {
-    if (i >= end) return -1;                          // no choice: counted nowhere
-    const Id v = ids[i];
-    return v >= 0 && v < static_cast<Id>(E) ? static_cast<int>(v) : E;
-}
+struct WarpChoices {
+    const Id* ids;
+    int64_t w0, w1;
+    int E, lane;
+    int e[kKeep];
 
-// This warp's counts of its choices [w0, w1) into cnt (E + 1, zeroed).
-template <typename Id>
-__device__ __forceinline__ void count_choices(const Id* ids, int64_t w0, int64_t w1, int E, int* cnt, int lane) {
-    for (int64_t i = w0; i < w1; i += 32) {
-        const int e = choice(ids, i + lane, w1, E);
-        const uint32_t same = __match_any_sync(0xffffffffu, e);
-        if (e >= 0 && lane == __ffs(same) - 1) cnt[e] += __popc(same);
-        __syncwarp();
+    // expert of this lane's choice from i on: E if dropped, -1 past the end
+    __device__ __forceinline__ int fetch(int64_t i) const {
+        if (i + lane >= w1) return -1;
+        const Id v = ids[i + lane];
+        return v >= 0 && v < static_cast<Id>(E) ? static_cast<int>(v) : E;
     }
-}
+    __device__ __forceinline__ void start(const Id* p, int64_t n, int64_t chunk, int warps, int experts) {
+        ids = p;
+        E = experts;
+        lane = threadIdx.x & 31;
+        const int64_t b0 = blockIdx.x * chunk, b1 = min(n, b0 + chunk);
+        const int64_t per = (chunk / 32 + warps - 1) / warps * 32;
+        w0 = min(b1, b0 + static_cast<int64_t>(threadIdx.x >> 5) * per);
+        w1 = min(b1, w0 + per);
+#pragma unroll
+        for (int k = 0; k < kKeep; ++k) e[k] = fetch(w0 + 32 * k);
+    }
+    // f(expert or -1, index of lane 0's choice) for every 32 choices, in order
+    template <typename F>
+    __device__ __forceinline__ void each(F f) const {
+#pragma unroll
+        for (int k = 0; k < kKeep; ++k)
+            if (w0 + 32 * k < w1) f(e[k], w0 + 32 * k);
+        for (int64_t i = w0 + 32 * kKeep; i < w1; i += 32) f(fetch(i), i);
+    }
+    __device__ __forceinline__ void count(int* cnt) const {
+        each([&](int x, int64_t) {
+            const uint32_t same = __match_any_sync(0xffffffffu, x);
+            if (x >= 0 && lane == __ffs(same) - 1) cnt[x] += __popc(same);
+            __syncwarp();
+        });
+    }
+};
 
 // Exclusive prefix sums of v over the block's threads, in thread order; total
-// gets their sum.  `part` is kSortWarps + 1 ints of shared memory.
+// gets their sum.  `part`: WARPS ints of shared memory.
+template <int WARPS>
 __device__ __forceinline__ int block_exclusive(int v, int* part, int& total) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     int s = v;
@@ -91,121 +120,143 @@ __device__ __forceinline__ int block_exclusive(int v, int* part, int& total) {
     __syncthreads();                                  // part may still be read from an earlier call
     if (lane == 31) part[warp] = s;
     __syncthreads();
-    if (warp == 0) {
-        int t = part[lane];
+    int before = 0;
+    total = 0;
 #pragma unroll
-        for (int d = 1; d < 32; d <<= 1) {
-            const int y = __shfl_up_sync(0xffffffffu, t, d);
-            if (lane >= d) t += y;
-        }
-        part[lane] = t;
+    for (int w = 0; w < WARPS; ++w) {
+        const int x = part[w];
+        before += w < warp ? x : 0;
+        total += x;
     }
-    __syncthreads();
-    total = part[kSortWarps - 1];
-    return (warp ? part[warp - 1] : 0) + s - v;
+    return before + s - v;
 }
 
-template <typename Id>
-__global__ void __launch_bounds__(kSortThreads)
+template <typename Id, int WARPS>
+__global__ void __launch_bounds__(32 * WARPS)
 sort_count_kernel(const Id* __restrict__ ids, int64_t n, int64_t chunk, int E, int* __restrict__ counts) {
     extern __shared__ int cnt[];                      // [warp][E + 1]
-    const int W = E + 1, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    for (int i = threadIdx.x; i < kSortWarps * W; i += kSortThreads) cnt[i] = 0;
+    asm volatile("griddepcontrol.launch_dependents;");   // the second launch may start now
+    const int W = E + 1, warp = threadIdx.x >> 5;
+    WarpChoices<Id> mine;
+    mine.start(ids, n, chunk, WARPS, E);
+    for (int i = threadIdx.x; i < WARPS * W; i += 32 * WARPS) cnt[i] = 0;
     __syncthreads();
-    const int64_t b0 = blockIdx.x * chunk, b1 = min(n, b0 + chunk);
-    const int64_t per = (chunk / 32 + kSortWarps - 1) / kSortWarps * 32;
-    const int64_t w0 = min(b1, b0 + warp * per), w1 = min(b1, w0 + per);
-    count_choices(ids, w0, w1, E, cnt + warp * W, lane);
+    mine.count(cnt + warp * W);
     __syncthreads();
-    for (int e = threadIdx.x; e < W; e += kSortThreads) {
+    for (int e = threadIdx.x; e < W; e += 32 * WARPS) {
         int s = 0;
-        for (int w = 0; w < kSortWarps; ++w) s += cnt[w * W + e];
+#pragma unroll
+        for (int w = 0; w < WARPS; ++w) s += cnt[w * W + e];
         counts[static_cast<int64_t>(blockIdx.x) * W + e] = s;
     }
 }
 
 // counts: [gridDim.x][E + 1] of sort_count_kernel, or null for a lone block.
-template <typename Id>
-__global__ void __launch_bounds__(kSortThreads)
-sort_place_kernel(const Id* __restrict__ ids, int64_t n, int64_t chunk, int E, const int* __restrict__ counts,
+template <typename Id, int WARPS>
+__global__ void __launch_bounds__(32 * WARPS)
+sort_place_kernel(const Id* __restrict__ ids, int64_t n, int64_t chunk, int E, const int* counts,
                   int* __restrict__ offsets, int* __restrict__ pos, int* __restrict__ src) {
+    constexpr int THREADS = 32 * WARPS;
     extern __shared__ int cnt[];                      // [warp][E + 1], then all [E + 1], before [E + 1]
-    __shared__ int part[kSortWarps + 1];
-    const int W = E + 1, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    int* all = cnt + kSortWarps * W;
+    __shared__ int part[WARPS];
+    const int W = E + 1, warp = threadIdx.x >> 5;
+    int* all = cnt + WARPS * W;
     int* before = all + W;
-    for (int i = threadIdx.x; i < (kSortWarps + 2) * W; i += kSortThreads) cnt[i] = 0;
+    WarpChoices<Id> mine;
+    mine.start(ids, n, chunk, WARPS, E);
+    for (int i = threadIdx.x; i < (WARPS + 2) * W; i += THREADS) cnt[i] = 0;
     __syncthreads();
-    const int64_t b0 = blockIdx.x * chunk, b1 = min(n, b0 + chunk);
-    const int64_t per = (chunk / 32 + kSortWarps - 1) / kSortWarps * 32;
-    const int64_t w0 = min(b1, b0 + warp * per), w1 = min(b1, w0 + per);
-    count_choices(ids, w0, w1, E, cnt + warp * W, lane);
+    mine.count(cnt + warp * W);
     if (counts) {
+        asm volatile("griddepcontrol.wait;" ::: "memory");   // the first launch's counts
         // each expert's count in all blocks and in the blocks before this one:
         // the threads take (block, expert) pairs in memory order
-        const int total = gridDim.x * W, mine = blockIdx.x * W;
-        for (int i = threadIdx.x; i < total; i += kSortThreads) {
-            const int c = counts[i];
+        const int total = gridDim.x * W, own = blockIdx.x * W;
+#pragma unroll 4
+        for (int i = threadIdx.x; i < total; i += THREADS) {
+            const int c = __ldcg(counts + i);
             if (c) {
                 const int e = i % W;
                 atomicAdd(all + e, c);                // integers: any order gives the same sum
-                if (i < mine) atomicAdd(before + e, c);
+                if (i < own) atomicAdd(before + e, c);
             }
         }
     }
     __syncthreads();
     // first row of each warp's choices of each expert
     int run = 0;
-    for (int e0 = 0; e0 < W; e0 += kSortThreads) {
+    for (int e0 = 0; e0 < W; e0 += THREADS) {
         const int e = e0 + threadIdx.x;
-        int mine = 0;
-        if (e < W && !counts)
-            for (int w = 0; w < kSortWarps; ++w) mine += cnt[w * W + e];
-        const int sum = e < W ? (counts ? all[e] : mine) : 0;
+        int c[WARPS], sum = 0;
+#pragma unroll
+        for (int w = 0; w < WARPS; ++w) {
+            c[w] = e < W ? cnt[w * W + e] : 0;
+            sum += c[w];
+        }
+        if (counts) sum = e < W ? all[e] : 0;
         int total;
-        int at = run + block_exclusive(sum, part, total);
+        int at = run + block_exclusive<WARPS>(sum, part, total);
         run += total;
         if (e < W) {
             if (blockIdx.x == 0) offsets[e] = at;     // W entries: offsets[E] starts the dropped
             at += before[e];
-            for (int w = 0; w < kSortWarps; ++w) {
-                const int c = cnt[w * W + e];
+#pragma unroll
+            for (int w = 0; w < WARPS; ++w) {
                 cnt[w * W + e] = at;
-                at += c;
+                at += c[w];
             }
         }
     }
     __syncthreads();
     int* first = cnt + warp * W;
-    for (int64_t i = w0; i < w1; i += 32) {
-        const int e = choice(ids, i + lane, w1, E);
-        const uint32_t same = __match_any_sync(0xffffffffu, e);
-        const int rank = __popc(same & ((1u << lane) - 1));
-        const int r = e >= 0 ? first[e] + rank : 0;
+    mine.each([&](int x, int64_t i) {
+        const uint32_t same = __match_any_sync(0xffffffffu, x);
+        const int rank = __popc(same & ((1u << mine.lane) - 1));
+        const int r = x >= 0 ? first[x] + rank : 0;
         __syncwarp();
-        if (e >= 0 && rank == 0) first[e] += __popc(same);
+        if (x >= 0 && rank == 0) first[x] += __popc(same);
         __syncwarp();
-        if (e >= 0) {
-            pos[i + lane] = r;
-            src[r] = static_cast<int>(i + lane);
+        if (x >= 0) {
+            pos[i + mine.lane] = r;
+            src[r] = static_cast<int>(i + mine.lane);
         }
-    }
+    });
+}
+
+template <typename Id, int WARPS>
+int run_sort(const SortPlan& pl, int slot, int64_t n, int E, const Id* ids, int* offsets, int* pos, int* src,
+             int* scratch, cudaStream_t s) {
+    constexpr int most = (WARPS + 2) * 1025 * 4;
+    const int W = E + 1;
+    auto count = sort_count_kernel<Id, WARPS>;
+    auto place = sort_place_kernel<Id, WARPS>;
+    if (set_smem_attr(reinterpret_cast<const void*>(count), most, slot) != cudaSuccess ||
+        set_smem_attr(reinterpret_cast<const void*>(place), most, slot + 1) != cudaSuccess)
+        return kCudaError;
+    const bool many = pl.blocks > 1;
+    if (many) count<<<pl.blocks, 32 * WARPS, WARPS * W * 4, s>>>(ids, n, pl.chunk, E, scratch);
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(pl.blocks), 1, 1);
+    cfg.blockDim = dim3(32 * WARPS, 1, 1);
+    cfg.dynamicSmemBytes = static_cast<size_t>((WARPS + 2) * W * 4);
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = many ? 1 : 0;                      // only behind the counting launch
+    if (cudaLaunchKernelEx(&cfg, place, ids, n, pl.chunk, E, static_cast<const int*>(many ? scratch : nullptr), offsets,
+                           pos, src) != cudaSuccess)
+        return kCudaError;
+    return cudaGetLastError() == cudaSuccess ? kOk : kCudaError;
 }
 
 template <typename Id>
-int run_sort(int64_t n, int E, const Id* ids, int* offsets, int* pos, int* src, int* scratch, cudaStream_t s) {
+int pick_sort(int64_t n, int E, const Id* ids, int* offsets, int* pos, int* src, int* scratch, cudaStream_t s) {
     const SortPlan pl = sort_plan(n);
-    const int W = E + 1;
-    const int smem1 = kSortWarps * W * 4, smem2 = (kSortWarps + 2) * W * 4;
-    const int slot = sizeof(Id) == 4 ? 82 : 84;
-    if (set_smem_attr(reinterpret_cast<const void*>(sort_count_kernel<Id>), (kSortWarps) * 1025 * 4, slot) != cudaSuccess ||
-        set_smem_attr(reinterpret_cast<const void*>(sort_place_kernel<Id>), (kSortWarps + 2) * 1025 * 4, slot + 1) != cudaSuccess)
-        return kCudaError;
-    const bool many = pl.blocks > 1;
-    if (many) sort_count_kernel<Id><<<pl.blocks, kSortThreads, smem1, s>>>(ids, n, pl.chunk, E, scratch);
-    sort_place_kernel<Id><<<pl.blocks, kSortThreads, smem2, s>>>(ids, n, pl.chunk, E, many ? scratch : nullptr,
-                                                                offsets, pos, src);
-    return cudaGetLastError() == cudaSuccess ? kOk : kCudaError;
+    const int slot = sizeof(Id) == 4 ? 82 : 86;
+    if (pl.warps == 8) return run_sort<Id, 8>(pl, slot, n, E, ids, offsets, pos, src, scratch, s);
+    return run_sort<Id, 32>(pl, slot + 2, n, E, ids, offsets, pos, src, scratch, s);
 }
 
 // ----------------------------------------------------------------- gather
@@ -309,9 +360,34 @@ __device__ __forceinline__ void store_vec(uint16_t* row, int64_t v, int64_t nv, 
         if (j < tail) row[8 * nv + j] = static_cast<uint16_t>(w[j >> 1] >> (16 * (j & 1)));
 }
 
-// A warp takes one token's row, or a piece of it, and sums its choices' rows
-// in order.
-template <bool BF16>
+// The rows of up to J of a token's choices from j0 on: row numbers (-1: none
+// there) and weights, 0 for what does not count so that 0 * 0 is added.
+template <int J>
+struct Choices {
+    int r[J];
+    float w[J];
+    __device__ __forceinline__ void load(const int* pos, const float* weights, int64_t at, int j0, int topk,
+                                         int64_t n, int live) {
+#pragma unroll
+        for (int j = 0; j < J; ++j) r[j] = j0 + j < topk ? __ldg(pos + at + j0 + j) : -1;
+#pragma unroll
+        for (int j = 0; j < J; ++j) w[j] = weights && j0 + j < topk ? __ldg(weights + at + j0 + j) : 1.f;
+#pragma unroll
+        for (int j = 0; j < J; ++j) {
+            if (r[j] < 0 || r[j] >= n) r[j] = -1;
+            if (r[j] < 0 || r[j] >= live) w[j] = 0.f;
+        }
+    }
+    __device__ __forceinline__ bool kept(int j, int live) const { return r[j] >= 0 && r[j] < live; }
+};
+
+// A warp takes one token's row, or a 1 KB piece of it, and sums its choices'
+// rows in order, J of them requested before the first is used.  Measured with
+// the caches flushed, event times of which about 5 us are the launch: one row
+// at a time 80 us for 8 rows of 2048 values each of 8192 tokens, J = 4 61 us
+// (floor 46), J = 2 63; 6 rows of 2040 values 55 and 51 (floor 36), 2 rows of
+// 4096 53 and 45 (floor 31): what J rounds topk up to counts.
+template <bool BF16, int J>
 __global__ void __launch_bounds__(256)
 combine_kernel(int64_t tokens, int topk, int64_t H, const uint16_t* __restrict__ Y, int64_t ldy,
                const int* __restrict__ pos, const int* __restrict__ kept, const float* __restrict__ weights,
@@ -321,7 +397,8 @@ combine_kernel(int64_t tokens, int topk, int64_t H, const uint16_t* __restrict__
     const int64_t t = id / pieces;
     if (t >= tokens) return;
     const int piece = static_cast<int>(id - t * pieces), lane = threadIdx.x & 31;
-    const int live = kept_rows(kept, tokens * topk);
+    const int64_t n = tokens * topk;
+    const int live = kept_rows(kept, n);
     const int64_t nv = H >> 3;
     const int tail = static_cast<int>(H & 7);
     const int64_t vecs = nv + (tail ? 1 : 0);
@@ -331,19 +408,24 @@ combine_kernel(int64_t tokens, int topk, int64_t H, const uint16_t* __restrict__
     for (int i = 0; i < V; ++i)
 #pragma unroll
         for (int e = 0; e < 8; ++e) acc[i][e] = 0.f;
-#pragma unroll 4
-    for (int j = 0; j < topk; ++j) {
-        const int r = __ldg(pos + t * topk + j);
-        if (r < 0 || r >= live) continue;             // dropped
-        const float w = weights ? __ldg(weights + t * topk + j) : 1.f;
-        const uint16_t* y = Y + r * ldy;
+    for (int j0 = 0; j0 < topk; j0 += J) {
+        Choices<J> c;
+        c.load(pos, weights, t * topk, j0, topk, n, live);
+        uint4 y[J][V];
 #pragma unroll
-        for (int i = 0; i < V; ++i)
-            if (v0 + 32 * i < vecs) {
+        for (int j = 0; j < J; ++j)
+#pragma unroll
+            for (int i = 0; i < V; ++i)
+                y[j][i] = c.kept(j, live) && v0 + 32 * i < vecs ? load_vec(Y + c.r[j] * ldy, v0 + 32 * i, nv, tail)
+                                                                : make_uint4(0, 0, 0, 0);
+#pragma unroll
+        for (int j = 0; j < J; ++j)
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
                 float f[8];
-                widen8<BF16>(load_vec(y, v0 + 32 * i, nv, tail), f);
+                widen8<BF16>(y[j][i], f);
 #pragma unroll
-                for (int e = 0; e < 8; ++e) acc[i][e] = fmaf(w, f[e], acc[i][e]);
+                for (int e = 0; e < 8; ++e) acc[i][e] = fmaf(c.w[j], f[e], acc[i][e]);
             }
     }
     uint16_t* o = out + t * ldo;
@@ -352,71 +434,108 @@ combine_kernel(int64_t tokens, int topk, int64_t H, const uint16_t* __restrict__
         if (v0 + 32 * i < vecs) store_vec(o, v0 + 32 * i, nv, tail, narrow8<BF16>(acc[i]));
 }
 
-// A block takes one token: four choices at a time it reads their rows, writes
-// the rows' gradient and sums the four dot products, over the threads in a
+// A block takes one token: J choices at a time it reads their rows, writes
+// the rows' gradient and sums the J dot products, over the threads in a
 // fixed order.
-constexpr int kGradThreads = 128;
-
-template <bool BF16>
-__global__ void __launch_bounds__(kGradThreads)
+template <bool BF16, int J, int V, int THREADS>
+__global__ void __launch_bounds__(THREADS)
 combine_grad_kernel(int topk, int64_t n, int64_t H, const uint16_t* __restrict__ Y, int64_t ldy,
                     const uint16_t* __restrict__ dout, int64_t ldd, const int* __restrict__ pos,
                     const int* __restrict__ kept, const float* __restrict__ weights,
                     uint16_t* __restrict__ dY, int64_t lddy, float* __restrict__ dweights) {
-    constexpr int J = 4;
-    __shared__ float part[kGradThreads / 32][J];
+    __shared__ float part[THREADS / 32][J];
     const int64_t t = blockIdx.x;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int live = kept_rows(kept, n);
     const int64_t nv = H >> 3;
     const int tail = static_cast<int>(H & 7);
     const int64_t vecs = nv + (tail ? 1 : 0);
     const uint16_t* g = dout + t * ldd;
     for (int j0 = 0; j0 < topk; j0 += J) {
-        int r[J];
-        float w[J], dot[J];
+        Choices<J> c;
+        c.load(pos, weights, t * topk, j0, topk, n, live);
+        float dot[J];
 #pragma unroll
-        for (int j = 0; j < J; ++j) {
-            r[j] = j0 + j < topk ? __ldg(pos + t * topk + j0 + j) : -1;
-            if (r[j] >= n) r[j] = -1;                 // not a row
-            w[j] = j0 + j < topk ? __ldg(weights + t * topk + j0 + j) : 0.f;
-            dot[j] = 0.f;
-        }
-        for (int64_t v = threadIdx.x; v < vecs; v += kGradThreads) {
-            float d[8];
-            widen8<BF16>(load_vec(g, v, nv, tail), d);
-            uint4 y[J];
+        for (int j = 0; j < J; ++j) dot[j] = 0.f;
+        for (int64_t v0 = threadIdx.x; v0 < vecs; v0 += V * THREADS) {
+            uint4 y[V][J], gv[V];
 #pragma unroll
-            for (int j = 0; j < J; ++j)
-                y[j] = r[j] >= 0 && r[j] < live ? load_vec(Y + r[j] * ldy, v, nv, tail) : make_uint4(0, 0, 0, 0);
+            for (int i = 0; i < V; ++i) {
+                const int64_t v = v0 + i * THREADS;
+                gv[i] = v < vecs ? load_vec(g, v, nv, tail) : make_uint4(0, 0, 0, 0);
 #pragma unroll
-            for (int j = 0; j < J; ++j) {
-                if (r[j] < 0) continue;
-                float f[8], o[8];
-                const bool keep = r[j] < live;
-                widen8<BF16>(y[j], f);
+                for (int j = 0; j < J; ++j)
+                    y[i][j] = v < vecs && c.kept(j, live) ? load_vec(Y + c.r[j] * ldy, v, nv, tail)
+                                                          : make_uint4(0, 0, 0, 0);
+            }
 #pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    if (keep) dot[j] = fmaf(f[e], d[e], dot[j]);
-                    o[e] = keep ? w[j] * d[e] : 0.f;
+            for (int i = 0; i < V; ++i) {
+                const int64_t v = v0 + i * THREADS;
+                if (v >= vecs) break;
+                float d[8];
+                widen8<BF16>(gv[i], d);
+#pragma unroll
+                for (int j = 0; j < J; ++j) {
+                    if (c.r[j] < 0) continue;
+                    float f[8], o[8];
+                    const bool keep = c.r[j] < live;
+                    widen8<BF16>(y[i][j], f);
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+                        if (keep) dot[j] = fmaf(f[e], d[e], dot[j]);
+                        o[e] = keep ? c.w[j] * d[e] : 0.f;
+                    }
+                    store_vec(dY + c.r[j] * lddy, v, nv, tail, narrow8<BF16>(o));
                 }
-                store_vec(dY + r[j] * lddy, v, nv, tail, narrow8<BF16>(o));
             }
         }
+        // J sums over 32 lanes: halve the lanes' share of the J sums as long
+        // as there are several, so that J + log2(32 / J) exchanges do
+        int at = 0;                                   // which sum this lane ends up with
 #pragma unroll
-        for (int j = 0; j < J; ++j) {
+        for (int m = J / 2, d = 16; m >= 1; m >>= 1, d >>= 1) {
+            const bool up = lane & d;
 #pragma unroll
-            for (int d = 16; d; d >>= 1) dot[j] += __shfl_xor_sync(0xffffffffu, dot[j], d);
-            if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5][j] = dot[j];
+            for (int j = 0; j < m; ++j) {
+                const float give = up ? dot[j] : dot[j + m], keep = up ? dot[j + m] : dot[j];
+                dot[j] = keep + __shfl_xor_sync(0xffffffffu, give, d);
+            }
+            at += up ? m : 0;
         }
+#pragma unroll
+        for (int d = 16 / J; d >= 1; d >>= 1) dot[0] += __shfl_xor_sync(0xffffffffu, dot[0], d);
+        if (lane % (32 / J) == 0) part[warp][at] = dot[0];
         __syncthreads();
         if (threadIdx.x < J && j0 + threadIdx.x < topk) {
             float s = 0.f;
 #pragma unroll
-            for (int i = 0; i < kGradThreads / 32; ++i) s += part[i][threadIdx.x];
+            for (int i = 0; i < THREADS / 32; ++i) s += part[i][threadIdx.x];
             dweights[t * topk + j0 + threadIdx.x] = s;
         }
-        __syncthreads();
+        if (j0 + J < topk) __syncthreads();
     }
+}
+
+template <bool BF16>
+void start_combine_grad(unsigned tokens, cudaStream_t s, int topk, int64_t n, int64_t H, const uint16_t* Y,
+                        int64_t ldy, const uint16_t* dout, int64_t ldd, const int* pos, const int* kept,
+                        const float* weights, uint16_t* dY, int64_t lddy, float* dweights) {
+    // Threads a token and what they hold, measured (us; the floors of 2 n H + T H
+    // 2-byte values are 66, 87, 51 and 23): with 6 x 2040, 8 x 2048, 2 x 4096 (8192
+    // tokens) and 4 x 512 (16384 tokens) values a token, two choices and two
+    // vectors at a time take 80, 98, 59, 41 on two warps and 88, 111, 64, 33 on
+    // one; eight choices at a time on eight warps 121, 137, 70, 55: small blocks
+    // wait for each other less at the dot products' end.  Few tokens leave SMs
+    // idle, and then eight warps a token shorten each one's chain of loads.
+    if (H <= 512)
+        combine_grad_kernel<BF16, 2, 2, 32><<<tokens, 32, 0, s>>>(topk, n, H, Y, ldy, dout, ldd, pos, kept, weights,
+                                                                  dY, lddy, dweights);
+    else if (tokens > 512)
+        combine_grad_kernel<BF16, 2, 2, 64><<<tokens, 64, 0, s>>>(topk, n, H, Y, ldy, dout, ldd, pos, kept, weights,
+                                                                  dY, lddy, dweights);
+    else
+        combine_grad_kernel<BF16, 2, 2, 256><<<tokens, 256, 0, s>>>(topk, n, H, Y, ldy, dout, ldd, pos, kept, weights,
+                                                                    dY, lddy, dweights);
 }
 
 bool grid_ok(int64_t blocks) { return blocks <= 0x7fffffffll; }
@@ -434,8 +553,8 @@ int launch_expert_sort(int64_t tokens, int topk, int E, const void* ids, int id_
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
     const int64_t n = tokens * topk;
     if (id_bytes == 4)
-        return run_sort(n, E, static_cast<const int32_t*>(ids), offsets, pos, src, static_cast<int*>(scratch), s);
-    return run_sort(n, E, static_cast<const long long*>(ids), offsets, pos, src, static_cast<int*>(scratch), s);
+        return pick_sort(n, E, static_cast<const int32_t*>(ids), offsets, pos, src, static_cast<int*>(scratch), s);
+    return pick_sort(n, E, static_cast<const long long*>(ids), offsets, pos, src, static_cast<int*>(scratch), s);
 }
 
 int launch_expert_gather(int64_t tokens, int topk, int64_t H, int eb, const void* X, int64_t ldx,
@@ -460,7 +579,9 @@ int launch_expert_combine(int64_t tokens, int topk, int64_t H, int bf16, const v
     const int64_t pieces = ((H + 7) / 8 + 63) / 64;
     const int64_t blocks = (tokens * pieces + 7) / 8;
     if (!grid_ok(blocks)) return kUnsupported;
-    auto k = bf16 ? combine_kernel<true> : combine_kernel<false>;
+    const bool four = (topk + 1) / 2 % 2 == 0;        // whole fours, or all but one of them
+    auto k = bf16 ? (four ? combine_kernel<true, 4> : combine_kernel<true, 2>)
+                  : (four ? combine_kernel<false, 4> : combine_kernel<false, 2>);
     k<<<static_cast<unsigned>(blocks), 256, 0, static_cast<cudaStream_t>(stream)>>>(
         tokens, topk, H, static_cast<const uint16_t*>(Y), ldy, pos, kept, weights, static_cast<uint16_t*>(out),
         ldo, static_cast<int>(pieces));
@@ -473,10 +594,10 @@ int launch_expert_combine_grad(int64_t tokens, int topk, int64_t H, int bf16, co
                                float* dweights, void* stream) {
     if (!current_device(nullptr)) return kNoDevice;
     if (!grid_ok(tokens)) return kUnsupported;
-    auto k = bf16 ? combine_grad_kernel<true> : combine_grad_kernel<false>;
-    k<<<static_cast<unsigned>(tokens), kGradThreads, 0, static_cast<cudaStream_t>(stream)>>>(
-        topk, tokens * topk, H, static_cast<const uint16_t*>(Y), ldy, static_cast<const uint16_t*>(dout), ldd, pos,
-        kept, weights, static_cast<uint16_t*>(dY), lddy, dweights);
+    auto start = bf16 ? start_combine_grad<true> : start_combine_grad<false>;
+    start(static_cast<unsigned>(tokens), static_cast<cudaStream_t>(stream), topk, tokens * topk, H,
+          static_cast<const uint16_t*>(Y), ldy, static_cast<const uint16_t*>(dout), ldd, pos, kept, weights,
+          static_cast<uint16_t*>(dY), lddy, dweights);
     return cudaGetLastError() == cudaSuccess ? kOk : kCudaError;
 }
 
