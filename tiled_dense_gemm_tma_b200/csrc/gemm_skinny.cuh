@@ -38,6 +38,10 @@
 //   weights + scales that converter warps expand (dequant.cuh): signed
 //   integers with fp16 group scales into fp16 tiles, or FP4 (E2M1) codes
 //   with E8M0 block scales into bf16 tiles.
+// * Signed 8-bit weights and activations (kind::i8): a 128-byte row holds 128
+//   columns or 128 k, a unit is 256 k, every sum and partial is a 32-bit
+//   integer (exact in any order), and each output is scaled once by its row's
+//   and its column's scale.  They never take stream-K: no workspace.
 #pragma once
 #include "ptx.cuh"
 #include "dequant.cuh"
@@ -50,8 +54,9 @@ namespace tg {
 
 // Weight kinds: 16-bit weights, signed 4-bit integers with fp16 group scales
 // (fp16 activations and output), FP4 E2M1 codes with E8M0 block scales
-// (bf16 activations and output).
-enum class WKind { F16 = 0, BF16 = 1, INT4 = 2, FP4 = 3 };
+// (bf16 activations and output), signed 8-bit weights and activations with a
+// scale per row and column (f16 or bf16 output, SkParams::out_bf16).
+enum class WKind { F16 = 0, BF16 = 1, INT4 = 2, FP4 = 3, I8 = 4 };
 
 // WK_ = 1: 16-bit weights stored transposed (B is N x K row-major, the
 // op(B) = B^T of a transposed-operand call): each weight tile arrives as
@@ -65,18 +70,21 @@ struct SkCfg {
     static constexpr int TN = 128;                      // weight columns per MMA (MMA M)
     static constexpr bool Q4 = W_ == WKind::INT4 || W_ == WKind::FP4;   // packed 4-bit weights
     static constexpr bool FP4 = W_ == WKind::FP4;
+    static constexpr bool I8 = W_ == WKind::I8;
     // activation, MMA operand and output type
     static constexpr WKind OUTW = (W_ == WKind::BF16 || W_ == WKind::FP4) ? WKind::BF16 : WKind::F16;
     // k rows per unit: 16-bit weights come in 128-row boxes (taller TMA
-    // copies stream faster), 4-bit weights in 64-row slices
-    static constexpr int BK = Q4 ? 64 : 128;
-    static constexpr int KSL = BK / 64;                 // 64-wide activation k-slices per unit
+    // copies stream faster; 8-bit: 256 rows), 4-bit weights in 64-row slices
+    static constexpr int BK = Q4 ? 64 : I8 ? 256 : 128;
+    static constexpr int KW = I8 ? 128 : 64;            // k in a 128-byte activation row
+    static constexpr int KSL = BK / KW;                 // activation k-slices per unit
+    static constexpr int MMA_K = I8 ? 32 : 16;          // k per MMA
     // 4-bit units span two 128-column sub-tiles so packed rows arrive as
     // 128-byte runs (narrower rows stream markedly slower from HBM)
     static constexpr int NSUB = Q4 ? 2 : 1;
     static constexpr int GN = NSUB * TN;                // weight columns per unit
-    static constexpr int W_CHUNK = BK * 128;            // 64 columns x BK rows, bytes
-    static constexpr int W_BYTES = NSUB * 2 * W_CHUNK;  // fp16 weight tile of one unit
+    static constexpr int W_CHUNK = BK * 128;            // 64 (8-bit: 128) columns x BK rows, bytes
+    static constexpr int W_BYTES = (I8 ? 1 : NSUB * 2) * W_CHUNK;   // weight tile of one unit
     static constexpr int X_SLICE = MPAD * 128;          // MPAD rows x 64 fp16
     static constexpr int X_BYTES = KSL * X_SLICE;
     static constexpr int Q_BYTES = Q4 ? BK * GN / 2 : 0;   // 8 KB packed
@@ -128,8 +136,8 @@ struct SkCfg {
     static_assert(RAW_STAGES >= 3, "ring");
     static_assert(SMEM_BYTES <= 227 * 1024, "shared memory per CTA");
     static_assert(!Q4 || GN / 2 == 128, "packed row");
-    static_assert(!WK || (!Q4 && W_CHUNK == 64 * 2 * BK && TN * 128 == 16384),
-                  "K-major weights: 16-bit only; BK/64 boxes of 128 rows x 128 B fill W_BYTES");
+    static_assert(!WK || (!Q4 && KSL * TN * 128 == W_BYTES),
+                  "K-major weights: not packed; BK/KW boxes of 128 rows x 128 B fill W_BYTES");
 };
 
 struct SkParams {
@@ -146,6 +154,9 @@ struct SkParams {
     long long ldc;
     float* ws;                // [T][J] slots of MPAD*GN fp32: row-major partials (row m: GN values)
     int* tickets;             // [T], zero between calls
+    const float* row_scale;   // 8-bit: M
+    const float* col_scale;   // 8-bit: N
+    int out_bf16;             // 8-bit: C's type
 };
 
 template <WKind W>
@@ -178,6 +189,27 @@ __device__ __forceinline__ void store_out4(void* C, long long ldc, int m, int n,
         for (int e = 0; e < 4; ++e)
             if (n + e < N) store_out<W>(C, ldc, m, n + e, o[e]);
     }
+}
+
+// 8-bit: one output, or four neighbouring ones (n a multiple of 4), from the
+// exact sums: rounded to fp32, times the row's scale, times the column's.
+__device__ __forceinline__ float sk_scaled(const SkParams& p, int m, int n, int v) {
+    const float x = (__int2float_rn(v) * __ldg(p.row_scale + m)) * __ldg(p.col_scale + n);
+    return p.relu ? fmaxf(x, 0.f) : x;
+}
+
+__device__ __forceinline__ void store_scaled(const SkParams& p, int m, int n, int v) {
+    const float x = sk_scaled(p, m, n, v);
+    if (p.out_bf16) store_out<WKind::BF16>(p.C, p.ldc, m, n, x);
+    else store_out<WKind::F16>(p.C, p.ldc, m, n, x);
+}
+
+__device__ __forceinline__ void store_scaled4(const SkParams& p, int m, int n, const int (&v)[4]) {
+    float o[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) o[e] = n + e < p.N ? sk_scaled(p, m, n + e, v[e]) : 0.f;
+    if (p.out_bf16) store_out4<WKind::BF16>(p.C, p.ldc, m, n, p.N, o);
+    else store_out4<WKind::F16>(p.C, p.ldc, m, n, p.N, o);
 }
 
 // tmW: fp16/bf16 weights (N x K view: 64-column boxes of BK rows), or the
@@ -312,9 +344,17 @@ skinny_kernel(const __grid_constant__ CUtensorMap tmW,
 #pragma unroll
                     for (int ks = 0; ks < Cfg::KSL; ++ks) {
                         tma_load_2d(slot_w(s) + ks * (Cfg::TN * 128), &tmW, &full[s],
-                                    kb * Cfg::BK + 64 * ks, t * Cfg::TN);
-                        tma_load_2d(slot_x(s) + ks * Cfg::X_SLICE, &tmX, &full[s], kb * Cfg::BK + 64 * ks, 0);
+                                    kb * Cfg::BK + Cfg::KW * ks, t * Cfg::TN);
+                        tma_load_2d(slot_x(s) + ks * Cfg::X_SLICE, &tmX, &full[s], kb * Cfg::BK + Cfg::KW * ks, 0);
                     }
+                } else if constexpr (Cfg::I8) {
+                    if (p.inject == 1 && it == 0 && c == 0) continue;   // debug: never arm slot 0
+                    // one box holds the tile's 128 columns
+                    mbar_arrive_expect_tx(&full[s], Cfg::X_BYTES + Cfg::W_BYTES);
+                    tma_load_2d(slot_w(s), &tmW, &full[s], t * Cfg::TN, kb * Cfg::BK);
+#pragma unroll
+                    for (int ks = 0; ks < Cfg::KSL; ++ks)
+                        tma_load_2d(slot_x(s) + ks * Cfg::X_SLICE, &tmX, &full[s], kb * Cfg::BK + Cfg::KW * ks, 0);
                 } else {
                     if (p.inject == 1 && it == 0 && c == 0) continue;   // debug: never arm slot 0
                     // the second 64-column box is skipped when it starts past N
@@ -349,7 +389,8 @@ skinny_kernel(const __grid_constant__ CUtensorMap tmW,
         // ------------------------------------------------------- MMA issuer
         if (elect_one()) {
             constexpr uint32_t fmt = Cfg::OUTW == WKind::BF16 ? 1u : 0u;
-            constexpr uint32_t idesc = make_idesc(fmt, Cfg::TN, Cfg::MPAD, Cfg::WK ? 0 : 1, 0);
+            constexpr uint32_t idesc = Cfg::I8 ? make_idesc_i8(Cfg::TN, Cfg::MPAD, Cfg::WK ? 0 : 1, 0)
+                                               : make_idesc(fmt, Cfg::TN, Cfg::MPAD, Cfg::WK ? 0 : 1, 0);
             bool ok = true;
             int it = 0, seg = 0;
             uint32_t d_tmem = tmem_base;
@@ -389,18 +430,21 @@ skinny_kernel(const __grid_constant__ CUtensorMap tmW,
 #pragma unroll
                 for (int j = 0; j < Cfg::NSUB; ++j) {
 #pragma unroll
-                    for (int k = 0; k < Cfg::BK / 16; ++k) {
-                        // weights: N-major, 16 k rows of 128 B per MMA (or, stored
+                    for (int k = 0; k < Cfg::BK / Cfg::MMA_K; ++k) {
+                        // weights: N-major, 16 (8-bit: 32) k rows of 128 B per MMA (or, stored
                         // transposed, K-major: 32 B of k inside the 128-byte rows of
                         // the k/4-th box); activations: K-major
                         const uint64_t ad = Cfg::WK
                             ? sw128_desc(w_addr + (k >> 2) * (Cfg::TN * 128) + (k & 3) * 32, 16, 1024)
-                            : sw128_desc(w_addr + j * 2 * Cfg::W_CHUNK + k * 16 * 128, Cfg::W_CHUNK, 1024);
+                            : sw128_desc(w_addr + j * 2 * Cfg::W_CHUNK + k * Cfg::MMA_K * 128, Cfg::W_CHUNK, 1024);
                         const uint64_t bd = sw128_desc(x_addr + (k >> 2) * Cfg::X_SLICE + (k & 3) * 32,
                                                        16, 1024);
                         const int set = k % Cfg::R;
-                        mma_f16(d_tmem + (set * Cfg::NSUB + j) * Cfg::MPAD, ad, bd, idesc,
-                                (first && k < Cfg::R) ? 0u : 1u);
+                        if constexpr (Cfg::I8)
+                            mma_i8(d_tmem + set * Cfg::MPAD, ad, bd, idesc, (first && k < Cfg::R) ? 0u : 1u);
+                        else
+                            mma_f16(d_tmem + (set * Cfg::NSUB + j) * Cfg::MPAD, ad, bd, idesc,
+                                    (first && k < Cfg::R) ? 0u : 1u);
                     }
                 }
                 if constexpr (Cfg::Q4) {
@@ -485,12 +529,17 @@ skinny_kernel(const __grid_constant__ CUtensorMap tmW,
                     for (int r = 1; r < Cfg::R; ++r)
 #pragma unroll
                         for (int i = 0; i < 16; ++i)
-                            v[i] = __float_as_uint(__uint_as_float(v[i]) + __uint_as_float(vr[r - 1][i]));
+                            v[i] = Cfg::I8 ? v[i] + vr[r - 1][i]
+                                           : __float_as_uint(__uint_as_float(v[i]) + __uint_as_float(vr[r - 1][i]));
                     if (whole) {
 #pragma unroll
                         for (int i = 0; i < 16; ++i) {
                             const int m = mc + i;
                             if (m >= p.M) break;
+                            if constexpr (Cfg::I8) {
+                                if (n < p.N) store_scaled(p, m, n, static_cast<int>(v[i]));
+                                continue;
+                            }
                             const float x = __uint_as_float(v[i]);
                             if (n < p.N) store_out<Cfg::OUTW>(p.C, p.ldc, m, n, p.relu ? fmaxf(x, 0.f) : x);
                         }
@@ -535,6 +584,18 @@ skinny_kernel(const __grid_constant__ CUtensorMap tmW,
                 const int c4 = etid & ((CW >> 2) - 1);
                 const int n = t * Cfg::GN + crank * CW + 4 * c4;
                 for (int m = etid >> lg; m < p.M; m += (32 * Cfg::EPI_WARPS) >> lg) {
+                    if constexpr (Cfg::I8) {
+                        const int4* ibuf = reinterpret_cast<const int4*>(ring);
+                        int o[4] = {0, 0, 0, 0};
+#pragma unroll
+                        for (int r = 0; r < 8; ++r)
+                            if (r < p.S) {
+                                const int4 v4 = ibuf[((r * Cfg::MPAD + m) << lg) + c4];
+                                o[0] += v4.x; o[1] += v4.y; o[2] += v4.z; o[3] += v4.w;
+                            }
+                        store_scaled4(p, m, n, o);
+                        continue;
+                    }
                     float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
                     for (int r = 0; r < 8; ++r)
@@ -550,6 +611,7 @@ skinny_kernel(const __grid_constant__ CUtensorMap tmW,
                 }
                 continue;
             }
+            if constexpr (Cfg::I8) break;                     // whole groups or cluster splits only
             // Publish the partial, take a ticket; the tile's last contributor
             // reduces.  The epilogue warps meet on mbarriers with bounded waits
             // (never an unbounded bar.sync, which a warp that gave up would hang).

@@ -70,6 +70,7 @@ int* device_status_ptr();
 //   68     gemm_tc.cu        CTA-pair TF32
 //   70-79  gemm_group.cu     experts' products and 8-bit products
 //   82-89  expert.cu         sort by expert
+//   90-97  gemm_skinny_i8.cu
 constexpr int kMaxSlots = 128;
 cudaError_t set_smem_attr(const void* func, int bytes, int slot);
 

@@ -10,9 +10,10 @@
 // The integer is exactly the one that the formula names in real arithmetic.
 // With x of at most 11 significant bits, x * 127 has at most 18, and
 // x * 127 / top is either exactly halfway between two integers or at least
-// 2^-19 of itself away from it; r = x * (127 / top) in fp32 is off by less
-// than 2^-22 of itself (two roundings), so rint(r) is right unless r lies
-// within 2^-11 of halfway (127 * 2^-22 is less).  Those few values, and rows whose
+// 2^-19 of itself away from it; r = x * inv with inv = 127 / top in fp32 is
+// off by 2^-24 of itself (r is never rounded: one fused multiply-add rounds
+// it to the integer, another gives its distance from it), so rint(r) is right
+// unless r lies within 2^-11 of halfway (127 * 2^-24 is less).  Those few values, and rows whose
 // 127 / top could overflow, take the division, which is off by 2^-24 of the
 // quotient and keeps exact halves exact.
 //
@@ -39,31 +40,53 @@ __device__ __forceinline__ float2 widen(uint32_t w) {
         return __half22float2(*reinterpret_cast<const __half2*>(&w));
 }
 
+__device__ __forceinline__ uint64_t pair(float a, float b) {
+    uint64_t d;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "f"(a), "f"(b));
+    return d;
+}
+__device__ __forceinline__ float2 unpair(uint64_t d) {
+    float2 f;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(f.x), "=f"(f.y) : "l"(d));
+    return f;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+    return d;
+}
+__device__ __forceinline__ uint64_t sub2(uint64_t a, uint64_t b) {
+    uint64_t d;
+    asm("sub.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+
 // Eight values -> eight integers.
 template <bool BF16>
 __device__ __forceinline__ uint2 round8(const uint4& v, float inv, float top, bool divide) {
     constexpr float kMagic = 12582912.f;             // 1.5 * 2^23: adding it leaves rint(r) in the low bits
-    float x[8];
+    const uint64_t magic = pair(kMagic, kMagic), inv2 = pair(inv, inv);
     const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-        const float2 f = widen<BF16>(w[j]);
-        x[2 * j] = f.x;
-        x[2 * j + 1] = f.y;
-    }
     uint32_t t[8];
     float off = 0.f;                                 // largest distance from an integer
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-        const float r = x[j] * inv;
-        const float s = r + kMagic;
-        t[j] = __float_as_uint(s);
-        off = fmaxf(off, fabsf(r - (s - kMagic)));
+    for (int j = 0; j < 4; ++j) {
+        const float2 x = widen<BF16>(w[j]);
+        const uint64_t x2 = pair(x.x, x.y);
+        const uint64_t s2 = fma2(x2, inv2, magic);
+        const float2 s = unpair(s2);
+        t[2 * j] = __float_as_uint(s.x);
+        t[2 * j + 1] = __float_as_uint(s.y);
+        const float2 d = unpair(fma2(x2, inv2, sub2(magic, s2)));       // r - rint(r)
+        off = fmaxf(off, fmaxf(fabsf(d.x), fabsf(d.y)));
     }
     if (divide || off > 0.5f - 0x1p-11f) {
 #pragma unroll
-        for (int j = 0; j < 8; ++j)
-            t[j] = __float_as_uint(__fdiv_rn(x[j] * 127.f, top) + kMagic);
+        for (int j = 0; j < 4; ++j) {
+            const float2 x = widen<BF16>(w[j]);
+            t[2 * j] = __float_as_uint(__fdiv_rn(x.x * 127.f, top) + kMagic);
+            t[2 * j + 1] = __float_as_uint(__fdiv_rn(x.y * 127.f, top) + kMagic);
+        }
     }
     uint2 o;
     o.x = __byte_perm(__byte_perm(t[0], t[1], 0x0040), __byte_perm(t[2], t[3], 0x0040), 0x5410);
@@ -72,9 +95,12 @@ __device__ __forceinline__ uint2 round8(const uint4& v, float inv, float top, bo
 }
 
 // TPR threads per row, a block of max(TPR, 128).  FITS: the row's vectors fit
-// the threads' registers.
+// the threads' registers.  From 128 threads on three quarters of the SM's
+// threads are asked for (40 registers a thread and not 47): 4096 rows of 16384
+// values 47 us against 54, of 8192 27 both ways; one-warp rows of 1024 lose by
+// it (18.2 against 16.7).  Event times; an empty call reads 7 to 8 us there.
 template <bool BF16, int TPR, bool FITS>
-__global__ void __launch_bounds__(TPR < 128 ? 128 : TPR)
+__global__ void __launch_bounds__(TPR < 128 ? 128 : TPR, TPR < 128 ? 1 : 1536 / TPR)
 quant_i8_kernel(int M, int K, const uint16_t* __restrict__ X, long long ldx, int8_t* __restrict__ Q,
                 long long ldq, float* __restrict__ scales) {
     constexpr int RPB = TPR < 128 ? 128 / TPR : 1;   // rows per block
