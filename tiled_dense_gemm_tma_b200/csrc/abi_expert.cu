@@ -150,8 +150,7 @@ tg_status tg_gemm_w8a8(int64_t M, int64_t N, int64_t K, const int8_t* A, int64_t
     tg::GroupArgs a = group_args(M, N, K, 1, A, lda, nullptr, B, ldb, 0, trans_b, C, ldc, epilogue, stream);
     a.row_scale = row_scales;
     a.col_scale = col_scales;
-    return static_cast<tg_status>(M <= tg::kSkinnyMaxM ? tg::launch_skinny_i8(a, type == TG_TYPE_BF16)
-                                                       : tg::launch_group_i8(a, type == TG_TYPE_BF16));
+    return static_cast<tg_status>(tg::launch_w8a8(a, type == TG_TYPE_BF16));
 }
 
 tg_status tg_gemm_grouped_f16(int64_t M, int64_t N, int64_t K, int E, const void* A, int64_t lda,

@@ -12,8 +12,9 @@
 // C[r][n] = epi( (sum * row_scale[r]) * col_scale_e[n] ), in fp32, rounded once.
 //
 // Two CTAs on neighbouring SMs (cluster of 2, tcgen05 cta_group::2) share a
-// 256-lane tile, as in gemm_tc2.cuh; the roles (one TMA warp, one MMA warp,
-// four epilogue warps), the barriers and the bounded waits are the same.
+// 256-lane tile, as in gemm_tc2.cuh; the roles (TMA, MMA and four epilogue
+// warps), the barriers and the bounded waits are the same, but two TMA warps
+// take the k blocks in turn.
 //
 // Product: the operands are swapped, D = C^T.  The 256 lanes are weight
 // columns n (each CTA stages its 128), and the rows r are the MMA's N side,
@@ -85,7 +86,9 @@ struct GrpCfg {
     static constexpr int B_STAGE = 128 * 128;           // up to 128 of the N side
     static constexpr int EPI_WARPS = 4;
     static constexpr int FIX_WARPS = WG_ ? 1 : 0;
-    static constexpr int THREADS = 32 * (2 + EPI_WARPS + FIX_WARPS);
+    static constexpr int PRODUCERS = 2;                 // warp 0, and the first behind the epilogue
+    static_assert(STAGES % PRODUCERS == 0, "a producer keeps its own ring slots");
+    static constexpr int THREADS = 32 * (1 + PRODUCERS + EPI_WARPS + FIX_WARPS);
     static constexpr int STG_BUF = 4096;                // [64 rows][32 columns] or [32 rows][128 bytes]
     static constexpr int NBUF = WG_ ? 2 : 1;
     static constexpr int TMEM_COLS = 512;               // two accumulators of 256 columns
@@ -389,8 +392,15 @@ grp_gemm_kernel(const __grid_constant__ CUtensorMap tmA,
     auto last_rows = [&](const GrpItem& it) { return it.rows - (it.kb - 1) * Cfg::BK; };
     auto is_cut = [&](const GrpItem& it) { return it.kb > 0 && last_rows(it) % Cfg::MMA_K != 0; };
 
-    if (warp == 0) {
-        // ------------------------------------------------ TMA producer (both)
+    if (warp == 0 || warp == 2 + Cfg::EPI_WARPS) {
+        // ----------------------------------------------- TMA producers (both)
+        // Two warps take the blocks in turn.  A thread issues a copy about
+        // every 95 clocks and needs some 240 more for a block's wait and
+        // arrival: with 3 to 5 copies a block that is more than the 512 (for
+        // a 256-row tile) or 448 clocks of its MMAs, and one warp alone paced
+        // the kernel (148 groups of 224 rows, K = 4096, weights K x N: 790
+        // clocks a block).
+        const uint32_t turn = warp == 0 ? 0 : 1;
         if (elect_one()) {
             uint32_t armed = 0, armed_par = 0, ld = 0;
             bool ok = true;
@@ -411,6 +421,7 @@ grp_gemm_kernel(const __grid_constant__ CUtensorMap tmA,
                 const uint32_t b_bytes = Cfg::WG ? b_live * (Cfg::BK * 128) : hn * 128;
                 const bool cut_last = Cfg::WG && is_cut(it);
                 for (int kb = 0; kb < it.kb; ++kb, ++ld) {
+                    if (ld % Cfg::PRODUCERS != turn) continue;
                     const uint32_t s = ld % Cfg::STAGES;
                     const uint32_t ph = (ld / Cfg::STAGES) & 1;
                     if (!bounded_wait(&empty[s], ph ^ 1, abort_flag, limit, p.status)) { ok = false; break; }
@@ -522,7 +533,7 @@ grp_gemm_kernel(const __grid_constant__ CUtensorMap tmA,
             bounded_wait(drain, 0, &never, limit, p.status);
         }
         __syncwarp();
-    } else if (warp < 2 + Cfg::EPI_WARPS) {
+    } else if (warp >= 2 && warp < 2 + Cfg::EPI_WARPS) {
         // --------------------------------------------------- epilogue (both)
         const int q = warp & 3;
         uint8_t* stg = smStg + (warp - 2) * Cfg::NBUF * Cfg::STG_BUF;

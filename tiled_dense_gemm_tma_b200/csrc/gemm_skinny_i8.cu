@@ -75,8 +75,20 @@ int dispatch(const GroupArgs& a, int bf16, int slot) {
 
 }  // namespace
 
-int launch_skinny_i8(const GroupArgs& a, int bf16) {
-    return a.trans_b ? dispatch<1>(a, bf16, 90) : dispatch<0>(a, bf16, 94);
+// The dense 8-bit product.  With at most 128 rows it streams the weights, where
+// their 128-column groups can be split over the SMs (at least two CTAs a
+// group) or the rows are so few that the row side does not matter.  Measured
+// (us by events, L2 flushed, an empty kernel reads 6; weight-streaming / CTA
+// pairs): 8192 x 8192 weights 20.6 / 26.8 with 16 rows, 28.3 / 28.7 with 128;
+// 1024 x 8192 12.6 / 26.8 and 18.7 / 28.3; unsplit 14336 x 4096 18.5 / 20.5
+// with 16 rows but 22.7 / 20.5 with 64 and 30.6 / 20.8 with 128.
+int launch_w8a8(const GroupArgs& a, int bf16) {
+    const DeviceInfo* di = current_device(nullptr);
+    if (!di) return kNoDevice;
+    const bool splits = (a.g.N + 127) / 128 * 2 <= di->num_sms;
+    if (a.g.M <= 16 || (a.g.M <= kSkinnyMaxM && splits))
+        return a.trans_b ? dispatch<1>(a, bf16, 90) : dispatch<0>(a, bf16, 94);
+    return launch_group_i8(a, bf16);
 }
 
 }  // namespace tg

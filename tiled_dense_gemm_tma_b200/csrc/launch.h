@@ -61,8 +61,8 @@ struct GroupArgs {
 int launch_group(const GroupArgs& a, int bf16);
 int launch_group_grad(const GroupArgs& a, int bf16);
 int launch_group_i8(const GroupArgs& a, int bf16);
-// One group of at most kSkinnyMaxM rows.
-int launch_skinny_i8(const GroupArgs& a, int bf16);
+// One group of all rows: the weight-streaming or the CTA-pair kernel.
+int launch_w8a8(const GroupArgs& a, int bf16);
 
 // Rows of 16-bit values to 8-bit integers with one scale per row.
 int launch_quant_i8(int64_t M, int64_t K, const void* X, int64_t ldx, int bf16, int8_t* Q,
