@@ -438,19 +438,24 @@ def _type16(dtype, name):
     raise TypeError(f"{name} must be float16 or bfloat16")
 
 
-def _launch(name, t, stream, *args):
-    """Call the entry point on t's device (made current where it is not) and on
+_fns = {}
+
+
+def _launch(name, device, stream, *args):
+    """Call the entry point on `device` (made current where it is not) and on
     `stream`, by default that device's current stream; raise on an error.  The
     calls of this section go through here: they are made once per layer and
     token step, where the host's time per call is what a user waits for."""
     import torch
-    index = t.device.index
+    fn = _fns.get(name)
+    if fn is None:
+        fn = _fns[name] = getattr(load_library(), name)
+    index = device.index
     if stream is None:
-        stream = torch._C._cuda_getCurrentRawStream(index) if t.is_cuda else 0
+        stream = torch._C._cuda_getCurrentRawStream(index)
     elif not isinstance(stream, int):
         stream = stream.cuda_stream
-    fn = getattr(load_library(), name)
-    if not t.is_cuda or torch.cuda.current_device() == index:
+    if torch._C._cuda_getDevice() == index:
         code = fn(*args, stream)
     else:
         with torch.cuda.device(index):
@@ -460,29 +465,44 @@ def _launch(name, t, stream, *args):
 
 
 def _rows_out(M, N, dtype, device):
-    """empty_out, without the view where the rows fill whole 16-byte units."""
+    """(a new M x N tensor, its row pitch): as empty_out, without the view
+    where the rows fill whole 16-byte units."""
     import torch
     per = 16 // dtype.itemsize
     if N % per == 0 and N:
-        return torch.empty((M, N), dtype=dtype, device=device)
-    return torch.empty((M, max(per, -(-N // per) * per)), dtype=dtype, device=device)[:, :N]
+        return torch.empty((M, N), dtype=dtype, device=device), N
+    ld = max(per, -(-N // per) * per)
+    return torch.empty((M, ld), dtype=dtype, device=device)[:, :N], ld
 
 
 def _pitch(t, name):
     """Row pitch (elements) of a row-major 2-D tensor or of the matrices of a
     3-D one; for fewer than two rows, whose stride says nothing, the row
     length rounded up to 16 bytes."""
-    if t.stride(-1) != 1 and t.shape[-1] > 1:
+    *_, rows, cols = t.shape
+    *_, ld, one = t.stride()
+    if one != 1 and cols > 1:
         raise ValueError(f"{name} must be row-major (unit column stride)")
-    if t.shape[-2] <= 1:
+    if rows <= 1:
         per = 16 // t.element_size()
-        return max(per, -(-t.shape[-1] // per) * per)
-    return t.stride(-2)
+        return max(per, -(-cols // per) * per)
+    return ld
 
 
 def _plane(t):
     """Elements between the matrices of a 3-D tensor."""
     return t.stride(0) if t.shape[0] > 1 else 0
+
+
+def _one_device(device, *named):
+    """As _require_cuda, without its list where all is well."""
+    if device.type == "cuda":
+        for t, _ in named:
+            if t.device != device:
+                break
+        else:
+            return
+    _require_cuda(device, *named)
 
 
 def _vector(t, n, dtype, name):
@@ -493,11 +513,12 @@ def _vector(t, n, dtype, name):
 
 
 def _out(C, M, N, dtype, device):
+    """(C, its row pitch), C made where it is None."""
     if C is None:
         return _rows_out(M, N, dtype, device)
     if C.shape != (M, N) or C.dtype != dtype:
         raise ValueError("C has the wrong shape or dtype")
-    return C
+    return C, _pitch(C, "C")
 
 
 def quant_i8(X, Q=None, scales=None, stream=None):
@@ -510,16 +531,20 @@ def quant_i8(X, Q=None, scales=None, stream=None):
         raise ValueError("X must be 2-D")
     kind = _type16(X.dtype, "X")
     M, K = X.shape
+    device = X.device
     if Q is None:
-        Q = _rows_out(M, K, torch.int8, X.device)
+        Q, ldq = _rows_out(M, K, torch.int8, device)
     elif Q.shape != (M, K) or Q.dtype != torch.int8:
         raise ValueError("Q has the wrong shape or dtype")
+    else:
+        ldq = _pitch(Q, "Q")
     if scales is None:
-        scales = torch.empty(M, dtype=torch.float32, device=X.device)
-    _vector(scales, M, torch.float32, "scales")
-    _require_cuda(X.device, (X, "X"), (Q, "Q"), (scales, "scales"))
-    _launch("tg_quant_i8", X, stream, M, K, X.data_ptr(), _pitch(X, "X"), kind,
-            Q.data_ptr(), _pitch(Q, "Q"), scales.data_ptr())
+        scales = torch.empty(M, dtype=torch.float32, device=device)
+    else:
+        _vector(scales, M, torch.float32, "scales")
+    _one_device(device, (Q, "Q"), (scales, "scales"))
+    _launch("tg_quant_i8", device, stream, M, K, X.data_ptr(), _pitch(X, "X"), kind,
+            Q.data_ptr(), ldq, scales.data_ptr())
     return Q, scales
 
 
@@ -543,13 +568,13 @@ def gemm_w8a8(A, row_scales, B, col_scales, C=None, out_dtype=None, relu=False, 
     if out_dtype is None:
         out_dtype = torch.bfloat16 if C is None else C.dtype
     kind = _type16(out_dtype, "C")
-    C = _out(C, M, N, out_dtype, A.device)
-    _require_cuda(A.device, (A, "A"), (B, "B"), (row_scales, "row_scales"),
+    device = A.device
+    C, ldc = _out(C, M, N, out_dtype, device)
+    _one_device(device, (B, "B"), (row_scales, "row_scales"),
                   (col_scales, "col_scales"), (C, "C"))
-    _launch("tg_gemm_w8a8", A, stream, M, N, K, A.data_ptr(), _pitch(A, "A"),
+    _launch("tg_gemm_w8a8", device, stream, M, N, K, A.data_ptr(), _pitch(A, "A"),
             row_scales.data_ptr(), B.data_ptr(), _pitch(B, "B"), int(trans_b),
-            col_scales.data_ptr(), C.data_ptr(), _pitch(C, "C"), kind, EPI_RELU if relu else
-            EPI_NONE)
+            col_scales.data_ptr(), C.data_ptr(), ldc, kind, EPI_RELU if relu else EPI_NONE)
     return C
 
 
@@ -559,28 +584,53 @@ class ExpertPlan:
     """Where expert_sort put each choice.
 
     offsets: int32 [E + 1], the rows of expert e are offsets[e]:offsets[e + 1],
-    dropped choices follow from offsets[E] on; pos: int32, the shape of the
-    expert numbers, the row of each choice; src: int32 [tokens * topk], the
-    flat choice of each row."""
-    __slots__ = ("offsets", "pos", "src")
+    dropped choices follow from offsets[E] on; pos: int32 [tokens, topk], the
+    row of each choice; src: int32 [tokens * topk], the flat choice of each
+    row (None where a plan is made by hand: nothing here reads it)."""
+    __slots__ = ("_offsets", "_pos", "_src")
 
-    def __init__(self, offsets, pos, src):
-        self.offsets, self.pos, self.src = offsets, pos, src
+    def __init__(self, offsets, pos, src=None):
+        import torch
+        if offsets.dtype != torch.int32 or pos.dtype != torch.int32:
+            raise TypeError("a plan's tensors must be int32")
+        if offsets.dim() != 1 or offsets.shape[0] < 2 or pos.dim() != 2 or pos.shape[1] < 1 or \
+                not offsets.is_contiguous() or not pos.is_contiguous():
+            raise ValueError("a plan has a vector of offsets and a tokens x topk matrix pos, "
+                             "both contiguous")
+        _one_device(offsets.device, (pos, "pos"))
+        self._offsets, self._pos, self._src = offsets, pos, src
+
+    @property
+    def offsets(self):
+        return self._offsets
+
+    @property
+    def pos(self):
+        return self._pos
+
+    @property
+    def src(self):
+        return self._src
 
     @property
     def num_experts(self):
-        return self.offsets.shape[0] - 1
+        return self._offsets.shape[0] - 1
 
     @property
     def tokens(self):
-        return self.pos.shape[0]
+        return self._pos.shape[0]
 
     @property
     def topk(self):
-        return self.pos.shape[1]
+        return self._pos.shape[1]
+
+    def _kept(self):
+        """Address of the number of kept choices."""
+        o = self._offsets
+        return o.data_ptr() + 4 * (o.shape[0] - 1)
 
 
-def expert_sort(ids, num_experts, stream=None):
+def expert_sort(ids, num_experts):
     """Stable sort of the choices ids (tokens x topk, int32 or int64) by
     expert, as an ExpertPlan.  Numbers outside 0..num_experts - 1 are dropped
     choices."""
@@ -589,96 +639,93 @@ def expert_sort(ids, num_experts, stream=None):
         raise ValueError("ids must be 2-D (tokens x topk)")
     if ids.dtype not in (torch.int32, torch.int64):
         raise TypeError("ids must be int32 or int64")
-    _require_cuda(ids.device, (ids, "ids"))
+    device = ids.device
+    _one_device(device)
     T, k = ids.shape
     if k < 1:
         raise ValueError("ids must hold at least one choice per token")
-    need = load_library().tg_expert_sort_scratch(T * k, num_experts)
+    n = T * k
+    need = load_library().tg_expert_sort_scratch(n, num_experts)
     if need < 0:
         raise ValueError("expert_sort takes 1 to 1024 experts and fewer than 2^31 choices")
     ids = ids.contiguous()
-    # one allocation: offsets, pos, src, scratch (each 16-byte aligned)
-    n, E1 = T * k, num_experts + 1
-    cuts = [-(-c // 4) * 4 for c in (E1, n, n, need // 4)]
-    buf = torch.empty(sum(cuts), dtype=torch.int32, device=ids.device)
-    offsets, pos, src = buf[:E1], buf[cuts[0]:cuts[0] + n], buf[cuts[0] + cuts[1]:cuts[0] + cuts[1] + n]
+    # one allocation, each part on a 16-byte boundary: offsets, pos, src, scratch
+    E1 = num_experts + 1
+    at_pos = -(-E1 // 4) * 4
+    at_src = at_pos + -(-n // 4) * 4
+    at_scratch = at_src + -(-n // 4) * 4
+    buf = torch.empty(at_scratch + need // 4, dtype=torch.int32, device=device)
     base = buf.data_ptr()
-    _launch("tg_expert_sort", ids, stream, T, k, num_experts, ids.data_ptr(),
-            ids.element_size(), base, base + 4 * cuts[0], base + 4 * (cuts[0] + cuts[1]),
-            base + 4 * (cuts[0] + cuts[1] + cuts[2]) if need else None)
-    return ExpertPlan(offsets, pos.view(T, k), src)
+    _launch("tg_expert_sort", device, None, T, k, num_experts, ids.data_ptr(), ids.element_size(),
+            base, base + 4 * at_pos, base + 4 * at_src, base + 4 * at_scratch if need else None)
+    plan = ExpertPlan.__new__(ExpertPlan)
+    plan._offsets = buf[:E1]
+    plan._pos = buf.as_strided((T, k), (k, 1), at_pos)
+    plan._src = buf[at_src:at_src + n]
+    return plan
 
 
-def _kept_ptr(offsets):
-    return offsets.data_ptr() + 4 * (offsets.shape[0] - 1)
-
-
-def _check_plan(offsets, pos):
+def _gather(X, plan, scales=None):
     import torch
-    if offsets.dtype != torch.int32 or pos.dtype != torch.int32:
-        raise TypeError("the plan's tensors must be int32")
-    if offsets.dim() != 1 or pos.dim() != 2 or not offsets.is_contiguous() or not pos.is_contiguous():
-        raise ValueError("the plan's tensors must be contiguous")
-
-
-def _gather(X, offsets, pos, scales=None):
-    import torch
-    _check_plan(offsets, pos)
+    pos = plan._pos
     T, k = pos.shape
     if X.dim() != 2 or X.shape[0] != T:
         raise ValueError("X must have one row per token of the plan")
     if X.dtype not in (torch.float16, torch.bfloat16, torch.int8):
         raise TypeError("X must be float16, bfloat16 or int8")
-    H = X.shape[1]
-    out = _rows_out(T * k, H, X.dtype, X.device)
+    H, device = X.shape[1], X.device
+    out, ldo = _rows_out(T * k, H, X.dtype, device)
     ss = None
     if scales is not None:
         _vector(scales, T, torch.float32, "scales")
-        ss = torch.empty(T * k, dtype=torch.float32, device=X.device)
-        _require_cuda(X.device, (scales, "scales"))
-    _require_cuda(X.device, (X, "X"), (offsets, "offsets"), (pos, "pos"))
-    _launch("tg_expert_gather", X, None, T, k, H, X.element_size(), X.data_ptr(), _pitch(X,
-            "X"), scales.data_ptr() if scales is not None else None, pos.data_ptr(),
-            _kept_ptr(offsets), out.data_ptr(), _pitch(out, "out"), ss.data_ptr() if ss is
-            not None else None)
-    return out if scales is None else (out, ss)
+        ss = torch.empty(T * k, dtype=torch.float32, device=device)
+        _one_device(device, (scales, "scales"))
+    _one_device(device, (pos, "the plan"))
+    _launch("tg_expert_gather", device, None, T, k, H, X.element_size(), X.data_ptr(),
+            _pitch(X, "X"), None if ss is None else scales.data_ptr(), pos.data_ptr(),
+            plan._kept(), out.data_ptr(), ldo, None if ss is None else ss.data_ptr())
+    return out if ss is None else (out, ss)
 
 
-def _combine(Y, offsets, pos, weights):
+def _check_weights(weights, T, k, device):
     import torch
-    _check_plan(offsets, pos)
+    if weights.dtype != torch.float32:
+        raise TypeError("weights must be float32")
+    if weights.shape != (T, k):
+        raise ValueError("weights must be tokens x topk")
+    _one_device(device, (weights, "weights"))
+    return weights.contiguous()
+
+
+def _combine(Y, plan, weights):
+    pos = plan._pos
     T, k = pos.shape
     if Y.dim() != 2 or Y.shape[0] != T * k:
         raise ValueError("the sorted rows must be one per choice of the plan")
     kind = _type16(Y.dtype, "the sorted rows")
-    H = Y.shape[1]
+    H, device = Y.shape[1], Y.device
     if weights is not None:
-        if weights.dtype != torch.float32:
-            raise TypeError("weights must be float32")
-        if weights.shape != (T, k):
-            raise ValueError("weights must be tokens x topk")
-        weights = weights.contiguous()
-        _require_cuda(Y.device, (weights, "weights"))
-    out = _rows_out(T, H, Y.dtype, Y.device)
-    _require_cuda(Y.device, (Y, "the sorted rows"), (offsets, "offsets"), (pos, "pos"))
-    _launch("tg_expert_combine", Y, None, T, k, H, kind, Y.data_ptr(), _pitch(Y, "Y"),
-            pos.data_ptr(), _kept_ptr(offsets), weights.data_ptr() if weights is not None
-            else None, out.data_ptr(), _pitch(out, "out"))
+        weights = _check_weights(weights, T, k, device)
+    out, ldo = _rows_out(T, H, Y.dtype, device)
+    _one_device(device, (pos, "the plan"))
+    _launch("tg_expert_combine", device, None, T, k, H, kind, Y.data_ptr(), _pitch(Y, "Y"),
+            pos.data_ptr(), plan._kept(), None if weights is None else weights.data_ptr(),
+            out.data_ptr(), ldo)
     return out
 
 
-def _combine_grad(Y, weights, g, offsets, pos):
+def _combine_grad(Y, weights, g, plan):
     import torch
+    pos = plan._pos
     T, k = pos.shape
-    H = Y.shape[1]
+    H, device = Y.shape[1], Y.device
     weights = weights.contiguous()
-    dY = _rows_out(T * k, H, Y.dtype, Y.device)
-    dw = torch.empty((T, k), dtype=torch.float32, device=Y.device)
-    _require_cuda(Y.device, (g, "the gradient"))
-    _launch("tg_expert_combine_grad", Y, None, T, k, H, _type16(Y.dtype, "Y"), Y.data_ptr(),
-            _pitch(Y, "Y"), g.data_ptr(), _pitch(g, "gradient"), pos.data_ptr(),
-            _kept_ptr(offsets), weights.data_ptr(), dY.data_ptr(), _pitch(dY, "dY"),
-            dw.data_ptr())
+    dY, ldd = _rows_out(T * k, H, Y.dtype, device)
+    dw = torch.empty((T, k), dtype=torch.float32, device=device)
+    _one_device(device, (g, "the gradient"))
+    _launch("tg_expert_combine_grad", device, None, T, k, H, _type16(Y.dtype, "Y"), Y.data_ptr(),
+            _pitch(Y, "Y"), g.data_ptr(), _pitch(g, "the gradient"), pos.data_ptr(), plan._kept(),
+            weights.data_ptr(), dY.data_ptr(), ldd, dw.data_ptr())
     return dY, dw
 
 
@@ -690,14 +737,16 @@ def _aligned_rows(g):
     if (g.stride(1) == 1 or g.shape[1] <= 1) and g.data_ptr() % 16 == 0 and \
             (g.shape[0] <= 1 or (g.stride(0) >= g.shape[1] and (g.stride(0) * eb) % 16 == 0)):
         return g
-    out = _rows_out(g.shape[0], g.shape[1], g.dtype, g.device)
+    out, _ = _rows_out(g.shape[0], g.shape[1], g.dtype, g.device)
     out.copy_(g)
     return out
 
 
 def _offsets_of(groups):
     import torch
-    offsets = groups.offsets if isinstance(groups, ExpertPlan) else groups
+    if isinstance(groups, ExpertPlan):
+        return groups._offsets
+    offsets = groups
     if offsets.dtype != torch.int32:
         raise TypeError("offsets must be int32")
     if offsets.dim() != 1 or offsets.shape[0] < 2 or not offsets.is_contiguous():
@@ -720,12 +769,13 @@ def gemm_grouped(A, groups, B, C=None, relu=False, stream=None, trans_b=False):
     K2, N = (B.shape[2], B.shape[1]) if trans_b else B.shape[1:]
     if K != K2:
         raise ValueError(f"inner dimensions differ: {K} vs {K2}")
-    C = _out(C, M, N, A.dtype, A.device)
-    _require_cuda(A.device, (A, "A"), (B, "B"), (offsets, "offsets"), (C, "C"))
+    device = A.device
+    C, ldc = _out(C, M, N, A.dtype, device)
+    _one_device(device, (B, "B"), (offsets, "offsets"), (C, "C"))
     name = "tg_gemm_grouped_bf16" if kind == TYPE_BF16 else "tg_gemm_grouped_f16"
-    _launch(name, A, stream, M, N, K, E, A.data_ptr(), _pitch(A, "A"), offsets.data_ptr(),
-            B.data_ptr(), _pitch(B, "B"), _plane(B), int(trans_b), C.data_ptr(), _pitch(C,
-            "C"), EPI_RELU if relu else EPI_NONE)
+    _launch(name, device, stream, M, N, K, E, A.data_ptr(), _pitch(A, "A"), offsets.data_ptr(),
+            B.data_ptr(), _pitch(B, "B"), _plane(B), int(trans_b), C.data_ptr(), ldc,
+            EPI_RELU if relu else EPI_NONE)
     return C
 
 
@@ -748,9 +798,9 @@ def gemm_grouped_wgrad(A, G, groups, C=None, stream=None):
         C = torch.empty((E, K, ld), dtype=A.dtype, device=A.device)[:, :, :N]
     elif C.shape != (E, K, N) or C.dtype != A.dtype:
         raise ValueError("C has the wrong shape or dtype")
-    _require_cuda(A.device, (A, "A"), (G, "G"), (offsets, "offsets"), (C, "C"))
+    _one_device(A.device, (G, "G"), (offsets, "offsets"), (C, "C"))
     name = "tg_gemm_grouped_wgrad_bf16" if kind == TYPE_BF16 else "tg_gemm_grouped_wgrad_f16"
-    _launch(name, A, stream, M, N, K, E, A.data_ptr(), _pitch(A, "A"), G.data_ptr(),
+    _launch(name, A.device, stream, M, N, K, E, A.data_ptr(), _pitch(A, "A"), G.data_ptr(),
             _pitch(G, "G"), offsets.data_ptr(), C.data_ptr(), _pitch(C, "C"), _plane(C))
     return C
 
@@ -779,13 +829,14 @@ def gemm_grouped_w8a8(A, row_scales, groups, B, col_scales, C=None, out_dtype=No
     if out_dtype is None:
         out_dtype = torch.bfloat16 if C is None else C.dtype
     kind = _type16(out_dtype, "C")
-    C = _out(C, M, N, out_dtype, A.device)
-    _require_cuda(A.device, (A, "A"), (B, "B"), (row_scales, "row_scales"),
+    device = A.device
+    C, ldc = _out(C, M, N, out_dtype, device)
+    _one_device(device, (B, "B"), (row_scales, "row_scales"),
                   (col_scales, "col_scales"), (offsets, "offsets"), (C, "C"))
-    _launch("tg_gemm_grouped_w8a8", A, stream, M, N, K, E, A.data_ptr(), _pitch(A, "A"),
-            row_scales.data_ptr(), offsets.data_ptr(), B.data_ptr(), _pitch(B, "B"),
-            _plane(B), int(trans_b), col_scales.data_ptr(), _plane(col_scales),
-            C.data_ptr(), _pitch(C, "C"), kind, EPI_RELU if relu else EPI_NONE)
+    _launch("tg_gemm_grouped_w8a8", device, stream, M, N, K, E, A.data_ptr(), _pitch(A, "A"),
+            row_scales.data_ptr(), offsets.data_ptr(), B.data_ptr(), _pitch(B, "B"), _plane(B),
+            int(trans_b), col_scales.data_ptr(), _plane(col_scales), C.data_ptr(), ldc, kind,
+            EPI_RELU if relu else EPI_NONE)
     return C
 
 
@@ -820,12 +871,12 @@ def _expert_functions():
         @staticmethod
         def forward(ctx, X, plan):
             ctx.plan = plan
-            return _gather(X, plan.offsets, plan.pos)
+            return _gather(X, plan)
 
         @staticmethod
         def backward(ctx, g):
             once()
-            return _combine(_aligned_rows(g), ctx.plan.offsets, ctx.plan.pos, None), None
+            return _combine(_aligned_rows(g), ctx.plan, None), None
 
     class _Combine(torch.autograd.Function):
         """Y[t] = sum_j w[t, j] Ys[pos[t, j]], with both gradients."""
@@ -835,16 +886,16 @@ def _expert_functions():
             ctx.plan = plan
             if weights is not None:
                 ctx.save_for_backward(Ys, weights)
-            return _combine(Ys, plan.offsets, plan.pos, weights)
+            return _combine(Ys, plan, weights)
 
         @staticmethod
         def backward(ctx, g):
             once()
             g = _aligned_rows(g)
-            offsets, pos = ctx.plan.offsets, ctx.plan.pos
-            if not ctx.saved_tensors:
-                return _gather(g, offsets, pos), None, None
-            dY, dw = _combine_grad(*ctx.saved_tensors, g, offsets, pos)
+            saved = ctx.saved_tensors
+            if not saved:
+                return _gather(g, ctx.plan), None, None
+            dY, dw = _combine_grad(*saved, g, ctx.plan)
             return (dY if ctx.needs_input_grad[0] else None,
                     dw if ctx.needs_input_grad[1] else None, None)
 
@@ -896,7 +947,7 @@ def expert_gather(X, plan, scales=None):
         import torch
         if X.dtype != torch.int8:
             raise TypeError("scales go with int8 rows")
-        return _gather(X, plan.offsets, plan.pos, scales)
+        return _gather(X, plan, scales)
     return _expert(0).apply(X, plan)
 
 
