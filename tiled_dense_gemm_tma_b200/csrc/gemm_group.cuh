@@ -99,10 +99,6 @@ struct GrpCfg {
     static_assert(!(I8 && WG_), "the 8-bit product has no gradient");
 };
 
-__device__ __forceinline__ void mbar_arrive_release_cluster(uint32_t cl_addr) {
-    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cl_addr) : "memory");
-}
-
 // One work item: a 256-lane tile of the weight columns (WG: of A's columns)
 // starting at n0, against the rows [m0, m1) (WG: the columns of G from m0).
 struct GrpItem {
@@ -587,9 +583,14 @@ grp_gemm_kernel(const __grid_constant__ CUtensorMap tmA,
                     *reinterpret_cast<uint4*>(b + i * 16) = z;
                     *reinterpret_cast<uint4*>(b + Cfg::BK * 128 + i * 16) = z;
                 }
-                fence_proxy_async_smem();               // for the tensor cores' reads
+                // Each lane's zeros reach the async proxy, whose reads of this CTA's
+                // shared memory (by its own SM's tensor core) the arrival lets
+                // start, as the converters' do in gemm_w4a16_pair.cu.  An arrival
+                // with release at cluster scope waits some 1500 clocks here, three
+                // blocks of MMAs: groups of 1000 and 1048 rows lost 13 % to it.
+                fence_proxy_async_smem();
                 __syncwarp();
-                if (lane == 0) mbar_arrive_release_cluster(mapa_shared(smem_u32(&full[s]), 0));
+                if (lane == 0) mbar_arrive_cluster(mapa_shared(smem_u32(&full[s]), 0));
             }
         }
     }
