@@ -42,7 +42,8 @@ int launch(const GroupArgs& a, long long items, const CUtensorMap& tA, const CUt
            const CUtensorMap& tC, int num_sms) {
     const GrpParams p = params(a);
     if (!p.status) return kCudaError;
-    const long long npairs = persistent_grid(items, num_sms / 2, 0);
+    // a tile of a thin wave runs as up to four pieces (WG: two)
+    const long long npairs = persistent_grid(items * (Cfg::WG ? 2 : 4), num_sms / 2, 0);
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(2 * npairs), 1, 1);
     cfg.blockDim = dim3(Cfg::THREADS, 1, 1);

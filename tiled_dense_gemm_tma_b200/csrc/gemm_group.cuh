@@ -103,7 +103,7 @@ struct GrpCfg {
 // starting at n0, against the rows [m0, m1) (WG: the columns of G from m0).
 struct GrpItem {
     int e;                    // group
-    int n0, m0, m1;
+    int n0, m0, m1;           // m0 >= m1: nothing to do
     int width;                // MMA N
     int kb;                   // k blocks; 0: the tile is zero
     int r0, rows;             // WG: the group's rows
@@ -203,9 +203,8 @@ __device__ __forceinline__ void grp_store_grad(const CUtensorMap* tmC, const Grp
                                                uint32_t& nstore) {
     if (kr >= p.K) return;                                  // warp-uniform
 #pragma unroll 1
-    for (int c = 0; c < 256; c += 64) {
+    for (int c = 0; it.m0 + c < it.m1; c += 64) {
         const int col0 = it.m0 + c;
-        if (col0 >= p.N) break;
         uint32_t v[64];
         if (it.kb) {
             tmem_ld_32x32b_x32(taddr + c, *reinterpret_cast<uint32_t(*)[32]>(&v[0]));
@@ -349,11 +348,17 @@ grp_gemm_kernel(const __grid_constant__ CUtensorMap tmA,
     cluster_sync_all();          // peer barriers initialised before any remote use
     tc_fence_after();
     const uint32_t tmem_base = *tmem_slot;
-    const int num_items = Cfg::WG ? p.E * ntl * ntg : gstart[*gcount];
+    // the tiles of a thin last wave in narrower pieces
+    const int num_tiles = Cfg::WG ? p.E * ntl * ntg : gstart[*gcount];
+    const int pieces = grp_pieces(num_tiles, npairs, Cfg::WG ? 2 : 4);
+    const int dp = tail_dp(num_tiles, npairs, pieces);
+    const int num_items = tail_items(num_tiles, dp, pieces);
 
     // item w; g walks forward through the product's groups
-    auto item = [&](int w, int& g) -> GrpItem {
+    auto item = [&](int i, int& g) -> GrpItem {
         GrpItem it;
+        const int w = i < dp ? i : dp + (i - dp) / pieces;
+        const int piece = i < dp ? -1 : (i - dp) % pieces;
         if constexpr (Cfg::WG) {
             const int per = ntl * ntg;
             it.e = w / per;
@@ -361,7 +366,7 @@ grp_gemm_kernel(const __grid_constant__ CUtensorMap tmA,
             tile_coords(w - it.e * per, ntl, ntg, p.group_m, tl, tt);
             it.n0 = tl * 256;
             it.m0 = tt * 256;
-            it.m1 = p.N;
+            it.m1 = min(p.N, it.m0 + 256);
             it.width = 256;
             int r1;
             grp_rows(p.offsets, it.e, p.E, p.M, it.r0, r1);
@@ -380,6 +385,12 @@ grp_gemm_kernel(const __grid_constant__ CUtensorMap tmA,
             it.m0 = it.r0 + tt * it.width;
             it.m1 = min(r1, it.m0 + it.width);
             it.kb = it.e < p.E ? (p.K - 1) / Cfg::BK + 1 : 0;
+        }
+        if (piece >= 0) {
+            it.width = grp_piece_width(it.width, pieces);
+            it.m0 += piece * it.width;
+            it.m1 = min(it.m1, it.m0 + it.width);
+            if (it.m0 >= it.m1) it.kb = 0;              // no rows left for this piece
         }
         return it;
     };
@@ -411,7 +422,7 @@ grp_gemm_kernel(const __grid_constant__ CUtensorMap tmA,
                 // feed lanes and columns that are never stored
                 const int a_live = left <= 0 ? 0 : (Cfg::CHUNK >= 128 || left > 64) ? 128 / Cfg::CHUNK : 1;
                 const int b_left = p.N - b0;
-                const int b_live = b_left <= 0 ? 0 : b_left > 64 ? 2 : 1;          // WG
+                const int b_live = b_left <= 0 ? 0 : min(hn / 64, b_left > 64 ? 2 : 1);   // WG
                 constexpr bool A_MN = Cfg::WG || Cfg::W_MN;
                 const uint32_t a_bytes = A_MN ? a_live * (Cfg::BK * 128) : (a_live ? Cfg::A_STAGE : 0);
                 const uint32_t b_bytes = Cfg::WG ? b_live * (Cfg::BK * 128) : hn * 128;

@@ -164,6 +164,21 @@ TG_HD int grp_width(int rows) {
     return (per + 31) / 32 * 32;
 }
 
+// The last wave of T tiles on npairs pairs: where its R = T mod npairs tiles
+// leave at least half (three quarters) of the pairs idle, each is cut into 2
+// (at most `most`: 4) narrower ones, pieces of at least 64 rows.  The pieces
+// of a tile add the same terms in the same order as the whole one.
+TG_HD int grp_pieces(int T, int npairs, int most) {
+    const int R = T % npairs;
+    return R == 0 ? 1 : (most >= 4 && 4 * R <= npairs) ? 4 : 2 * R <= npairs ? 2 : 1;
+}
+
+// Width of the pieces of a tile of `width` rows (a multiple of 32).
+TG_HD int grp_piece_width(int width, int pieces) {
+    const int w = ((width - 1) / pieces + 32) / 32 * 32;
+    return w < 64 ? sched_min(64, width) : w;
+}
+
 // Rows [r0, r1) of group e from the offsets (ng + 1 of them), clamped to
 // 0 <= r0 <= r1 <= M so that no offset leads outside the matrices; group ng
 // is the rows behind the last one.
