@@ -418,3 +418,114 @@ def test_repeated_calls_give_the_same_bits(tg):
             first = got
         assert all(torch.equal(a, b) for a, b in zip(first, got))
     _status(tg)
+
+
+def test_captured_training_step(tg):
+    """Forward and backward in one graph, many enough choices for the sort's two
+    launches, replayed on new contents of the same buffers."""
+    E = 7
+    leaves, ids = make_layer(T=3000, k=3, E=E, seed=5)
+    g = normal((3000, 80), torch.bfloat16, 9)
+
+    def step():
+        y = layer(tg, leaves[0], leaves[1], ids, leaves[2], leaves[3], E)
+        return [y.detach(), *torch.autograd.grad(y, leaves, g)]
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        step()
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = step()
+    with torch.no_grad():
+        ids.copy_(make_ids(3000, 3, E, 77, 0.2))
+        leaves[0].copy_(normal((3000, 80), torch.bfloat16, 78))
+    graph.replay()
+    graph.replay()
+    torch.cuda.synchronize()
+    eager = step()
+    _status(tg)
+    assert all(torch.equal(a, b) for a, b in zip(out, eager))
+
+
+def test_layer_on_its_own_stream(tg):
+    """Every operator on a stream that is not the default one, behind work that
+    delays its inputs."""
+    leaves, ids = make_layer(T=500)
+    want = layer(tg, leaves[0], leaves[1], ids, leaves[2], leaves[3], 6).detach().clone()
+    g = torch.ones_like(want)
+    want_g = torch.autograd.grad(layer(tg, leaves[0], leaves[1], ids, leaves[2], leaves[3], 6), leaves, g)
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream()
+    with torch.cuda.stream(s):
+        torch.cuda._sleep(20_000_000)
+        late = torch.full_like(ids, -1)
+        late.copy_(ids)
+        x = leaves[0].detach().clone().requires_grad_(True)
+        y = layer(tg, x, leaves[1], late, leaves[2], leaves[3], 6)
+        got_g = torch.autograd.grad(y, [x, *leaves[1:]], g)
+    s.synchronize()
+    _status(tg)
+    assert torch.equal(y.detach(), want) and all(torch.equal(a, b) for a, b in zip(got_g, want_g))
+
+
+@pytest.mark.parametrize("R,E", [(0, 3), (1, 1), (1, 1024), (5, 1000)])
+def test_smallest_and_most_groups(tg, R, E):
+    counts = [0] * E
+    for i in range(R):
+        counts[(i * 313) % E] += 1
+    X = normal((R, 24), torch.bfloat16, 1).requires_grad_(True)
+    W = normal((E, 24, 16), torch.bfloat16, 2).requires_grad_(True)
+    Y = tg.expert_matmul(X, W, offsets_of(counts))
+    dX, dW = torch.autograd.grad(Y, (X, W), normal((R, 16), torch.bfloat16, 3))
+    _status(tg)
+    assert tuple(Y.shape) == (R, 16) and tuple(dX.shape) == (R, 24)
+    row = 0
+    for e, n in enumerate(counts):
+        if n:
+            ref, bound = product16(X.detach()[row:row + n], W.detach()[e], torch.bfloat16)
+            close(Y.detach()[row:row + n], ref, bound)
+        else:
+            assert not dW[e].any()
+        row += n
+
+
+def test_shared_gradient_of_expanded_weights(tg):
+    """One matrix for all experts, expanded: its gradient adds all groups'."""
+    counts = [20, 0, 33]
+    X = ints8((53, 32), 1, -2, 3).to(torch.bfloat16)
+    W1 = ints8((32, 24), 2, -1, 2).to(torch.bfloat16).requires_grad_(True)
+    G = ints8((53, 24), 3, -1, 2).to(torch.bfloat16)
+    Y = tg.expert_matmul(X, W1[None].expand(3, 32, 24), offsets_of(counts))
+    dW, = torch.autograd.grad(Y, W1, G)
+    _status(tg)
+    # integers: |Y| <= 32 * 2, the groups' gradients at most 66, their sum at most 106: all exact
+    assert torch.equal(Y.detach().double(), X.double() @ W1.detach().double())
+    assert torch.equal(dW.double(), X.double().t() @ G.double())
+
+
+def test_gather_the_same_token_to_one_expert_twice(tg):
+    ids = torch.tensor([[1, 1], [0, 1]], device="cuda")
+    plan = tg.expert_sort(ids, 2)
+    assert plan.offsets.tolist() == [0, 1, 4] and plan.src.tolist() == [2, 0, 1, 3]
+    X = normal((2, 24), torch.float16, 1).requires_grad_(True)
+    Xs = tg.expert_gather(X, plan)
+    assert torch.equal(Xs.detach(), X.detach()[[1, 0, 0, 1]])
+    dX, = torch.autograd.grad(Xs, X, torch.ones(4, 24, dtype=torch.float16, device="cuda"))
+    assert bool((dX == 2).all())
+    _status(tg)
+
+
+@pytest.mark.parametrize("pos", [[[7, 100]], [[-1, -2147483648]], [[2147483647, 1]]])
+def test_positions_outside_the_rows_are_skipped(tg, pos):
+    p = torch.tensor(pos, dtype=torch.int32, device="cuda")
+    for offsets in ([0, 2], [0, -7], [0, 2147483647]):
+        plan = tg.ExpertPlan(torch.tensor(offsets, dtype=torch.int32, device="cuda"), p)
+        X = normal((1, 40), torch.bfloat16, 1).requires_grad_(True)
+        Y = normal((2, 40), torch.bfloat16, 2).requires_grad_(True)
+        w = torch.ones((1, 2), device="cuda").requires_grad_(True)
+        tg.expert_gather(X, plan).sum().backward()
+        tg.expert_combine(Y, plan, w).sum().backward()
+    _status(tg)

@@ -640,7 +640,7 @@ def expert_sort(ids, num_experts):
     if ids.dtype not in (torch.int32, torch.int64):
         raise TypeError("ids must be int32 or int64")
     device = ids.device
-    _one_device(device)
+    _one_device(device, (ids, "ids"))
     T, k = ids.shape
     if k < 1:
         raise ValueError("ids must hold at least one choice per token")
@@ -843,17 +843,24 @@ def gemm_grouped_w8a8(A, row_scales, groups, B, col_scales, C=None, out_dtype=No
 def _stored3(W):
     """How the logical E x K x N weights reach the kernels: (storage,
     transposed) with W[e] == storage[e] or its transpose and the storage's
-    matrices row-major; a view that is neither is copied."""
-    def ok(v):
-        return (v.stride(2) == 1 or v.shape[2] <= 1) and \
-            (v.shape[1] <= 1 or v.stride(1) >= v.shape[2]) and (v.shape[0] <= 1 or v.stride(0) > 0)
-
-    cands = [(v, tr) for v, tr in ((W, False), (W.transpose(1, 2), True)) if ok(v)]
-    for v, tr in cands:
-        if v.shape[1] <= 1 or (v.stride(1) * v.element_size()) % 16 == 0:
-            return v, tr
-    if cands:
-        return cands[0]
+    matrices row-major; a view that is neither is copied.  Where both readings
+    hold, the one with a 16-byte row pitch wins, the plain one first."""
+    if W.dim() != 3:
+        raise ValueError("W must be 3-D (experts x K x N)")
+    E, K, N = W.shape
+    se, sk, sn = W.stride()
+    apart = E <= 1 or se > 0
+    plain = apart and (sn == 1 or N <= 1) and (K <= 1 or sk >= N)
+    trans = apart and (sk == 1 or K <= 1) and (N <= 1 or sn >= K)
+    per = 16 // W.element_size()
+    if plain and (K <= 1 or sk % per == 0):
+        return W, False
+    if trans and (N <= 1 or sn % per == 0):
+        return W.transpose(1, 2), True
+    if plain:
+        return W, False
+    if trans:
+        return W.transpose(1, 2), True
     return W.contiguous(), False
 
 
@@ -871,11 +878,13 @@ def _expert_functions():
         @staticmethod
         def forward(ctx, X, plan):
             ctx.plan = plan
+            ctx.save_for_backward(plan._offsets, plan._pos)      # for the check on changes in place
             return _gather(X, plan)
 
         @staticmethod
         def backward(ctx, g):
             once()
+            ctx.saved_tensors
             return _combine(_aligned_rows(g), ctx.plan, None), None
 
     class _Combine(torch.autograd.Function):
@@ -884,18 +893,18 @@ def _expert_functions():
         @staticmethod
         def forward(ctx, Ys, weights, plan):
             ctx.plan = plan
-            if weights is not None:
-                ctx.save_for_backward(Ys, weights)
+            ctx.save_for_backward(Ys if weights is not None else None, weights, plan._offsets,
+                                  plan._pos)
             return _combine(Ys, plan, weights)
 
         @staticmethod
         def backward(ctx, g):
             once()
             g = _aligned_rows(g)
-            saved = ctx.saved_tensors
-            if not saved:
+            Ys, weights, _, _ = ctx.saved_tensors
+            if weights is None:
                 return _gather(g, ctx.plan), None, None
-            dY, dw = _combine_grad(*saved, g, ctx.plan)
+            dY, dw = _combine_grad(Ys, weights, g, ctx.plan)
             return (dY if ctx.needs_input_grad[0] else None,
                     dw if ctx.needs_input_grad[1] else None, None)
 
