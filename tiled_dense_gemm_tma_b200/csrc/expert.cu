@@ -37,9 +37,8 @@ namespace {
 //
 // Bound by latency, not by its 12 bytes a choice.  Up to kOneBlock choices one
 // block does it all in one launch.  More of them are cut among up to
-// kMaxBlocks blocks: a first launch writes each block's counts; the second,
-// which starts and counts its own choices while the first still runs, waits
-// for those counts and places.
+// kMaxBlocks blocks: a first launch writes each block's counts, the second
+// places.
 
 constexpr int kKeep = 8;
 constexpr int kOneBlock = 8192;
@@ -135,7 +134,6 @@ template <typename Id, int WARPS>
 __global__ void __launch_bounds__(32 * WARPS)
 sort_count_kernel(const Id* __restrict__ ids, int64_t n, int64_t chunk, int E, int* __restrict__ counts) {
     extern __shared__ int cnt[];                      // [warp][E + 1]
-    asm volatile("griddepcontrol.launch_dependents;");   // the second launch may start now
     const int W = E + 1, warp = threadIdx.x >> 5;
     WarpChoices<Id> mine;
     mine.start(ids, n, chunk, WARPS, E);
@@ -154,7 +152,7 @@ sort_count_kernel(const Id* __restrict__ ids, int64_t n, int64_t chunk, int E, i
 // counts: [gridDim.x][E + 1] of sort_count_kernel, or null for a lone block.
 template <typename Id, int WARPS>
 __global__ void __launch_bounds__(32 * WARPS)
-sort_place_kernel(const Id* __restrict__ ids, int64_t n, int64_t chunk, int E, const int* counts,
+sort_place_kernel(const Id* __restrict__ ids, int64_t n, int64_t chunk, int E, const int* __restrict__ counts,
                   int* __restrict__ offsets, int* __restrict__ pos, int* __restrict__ src) {
     constexpr int THREADS = 32 * WARPS;
     extern __shared__ int cnt[];                      // [warp][E + 1], then all [E + 1], before [E + 1]
@@ -168,7 +166,6 @@ sort_place_kernel(const Id* __restrict__ ids, int64_t n, int64_t chunk, int E, c
     __syncthreads();
     mine.count(cnt + warp * W);
     if (counts) {
-        asm volatile("griddepcontrol.wait;" ::: "memory");   // the first launch's counts
         // each expert's count in all blocks and in the blocks before this one:
         // the threads take (block, expert) pairs in memory order
         const int total = gridDim.x * W, own = blockIdx.x * W;
@@ -235,19 +232,8 @@ int run_sort(const SortPlan& pl, int slot, int64_t n, int E, const Id* ids, int*
         return kCudaError;
     const bool many = pl.blocks > 1;
     if (many) count<<<pl.blocks, 32 * WARPS, WARPS * W * 4, s>>>(ids, n, pl.chunk, E, scratch);
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>(pl.blocks), 1, 1);
-    cfg.blockDim = dim3(32 * WARPS, 1, 1);
-    cfg.dynamicSmemBytes = static_cast<size_t>((WARPS + 2) * W * 4);
-    cfg.stream = s;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = many ? 1 : 0;                      // only behind the counting launch
-    if (cudaLaunchKernelEx(&cfg, place, ids, n, pl.chunk, E, static_cast<const int*>(many ? scratch : nullptr), offsets,
-                           pos, src) != cudaSuccess)
-        return kCudaError;
+    place<<<pl.blocks, 32 * WARPS, (WARPS + 2) * W * 4, s>>>(ids, n, pl.chunk, E, many ? scratch : nullptr, offsets, pos,
+                                                              src);
     return cudaGetLastError() == cudaSuccess ? kOk : kCudaError;
 }
 
