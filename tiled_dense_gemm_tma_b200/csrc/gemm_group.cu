@@ -117,9 +117,15 @@ int launch_group(const GroupArgs& a, int bf16) {
     return a.trans_b ? run_product<GrpCfg<0, OutT::F16, 0>>(a, th, 72) : run_product<GrpCfg<0, OutT::F16, 1>>(a, th, 73);
 }
 
+// Eight epilogue warps where groups have few rows and writing their gradients
+// takes longer than their MMAs, else four with two staging tiles each.  Measured
+// (us, four / eight) on 32 groups of 4096 x 2048 with 64 rows 117 / 105, 128 rows
+// 122 / 103, 256 rows 137 / 138, 384 rows 165 / 170, 1024 rows 366 / 375.
 int launch_group_grad(const GroupArgs& a, int bf16) {
-    return bf16 ? run_grad<GrpCfg<1, OutT::BF16, 1, 1>>(a, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 74)
-                : run_grad<GrpCfg<0, OutT::F16, 1, 1>>(a, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 75);
+    constexpr CUtensorMapDataType tb = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, th = CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
+    if (a.g.M < 256ll * a.E)
+        return bf16 ? run_grad<GrpCfg<1, OutT::BF16, 1, 1, 8>>(a, tb, 74) : run_grad<GrpCfg<0, OutT::F16, 1, 1, 8>>(a, th, 75);
+    return bf16 ? run_grad<GrpCfg<1, OutT::BF16, 1, 1, 4>>(a, tb, 80) : run_grad<GrpCfg<0, OutT::F16, 1, 1, 4>>(a, th, 81);
 }
 
 int launch_group_i8(const GroupArgs& a, int bf16) {

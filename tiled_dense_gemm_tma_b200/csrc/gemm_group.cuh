@@ -12,9 +12,11 @@
 // C[r][n] = epi( (sum * row_scale[r]) * col_scale_e[n] ), in fp32, rounded once.
 //
 // Two CTAs on neighbouring SMs (cluster of 2, tcgen05 cta_group::2) share a
-// 256-lane tile, as in gemm_tc2.cuh; the roles (TMA, MMA and four epilogue
-// warps), the barriers and the bounded waits are the same, but two TMA warps
-// take the k blocks in turn.
+// 256-lane tile, as in gemm_tc2.cuh; the roles (TMA, MMA, epilogue), the
+// barriers and the bounded waits are the same, but two TMA warps take the k
+// blocks in turn and up to eight epilogue warps share a tile (four took 26.5 us
+// for 2048 x 8192 x 1024 in 8 bits, eight 23.9: its 8 blocks of MMAs a tile are
+// shorter than the epilogue).
 //
 // Product: the operands are swapped, D = C^T.  The 256 lanes are weight
 // columns n (each CTA stages its 128), and the rows r are the MMA's N side,
@@ -23,7 +25,7 @@
 // rows on the 256-lane side would always pay for 256, and the loads of a
 // small group are almost only its weights.  A tile is read from tensor
 // memory as MMA fragments (16x256b), rounded, transposed by stmatrix into a
-// [64 rows][32 columns] staging tile and written with 16-byte stores, which
+// [32 rows][32 columns] staging tile and written with 16-byte stores, which
 // stop at the group's last row; the rows past it belong to the next group
 // and were only read.  Row tiles of a group are as even as whole widths
 // allow (grp_width of tile_sched.h).  Rows behind the last group are written
@@ -68,8 +70,9 @@ struct GrpParams {
 
 // TYPE: 0 f16, 1 bf16 (idesc formats), 3 signed 8-bit.  W_MN = 1: the weights
 // are stored K x N, their tiles MN-major; 0: N x K, K-major.  WG: the weight
-// gradient (16-bit; both operands MN-major).
-template <int TYPE_, OutT OUT_, int W_MN_, int WG_ = 0>
+// gradient (16-bit; both operands MN-major).  EPI: epilogue warps, one or two
+// to each quarter of the lanes.
+template <int TYPE_, OutT OUT_, int W_MN_, int WG_ = 0, int EPI_ = 8>
 struct GrpCfg {
     static constexpr int TYPE = TYPE_;
     static constexpr OutT OUT = OUT_;
@@ -84,13 +87,15 @@ struct GrpCfg {
     static constexpr int STAGES = 6;
     static constexpr int A_STAGE = 128 * 128;           // 128 lanes' operand, either major-ness
     static constexpr int B_STAGE = 128 * 128;           // up to 128 of the N side
-    static constexpr int EPI_WARPS = 4;
+    static constexpr int EPI_WARPS = EPI_;
+    static constexpr int HALVES = EPI_ / 4;             // warps to a quarter of the lanes
+    static_assert(EPI_ == 4 || EPI_ == 8, "epilogue warps");
     static constexpr int FIX_WARPS = WG_ ? 1 : 0;
     static constexpr int PRODUCERS = 2;                 // warp 0, and the first behind the epilogue
     static_assert(STAGES % PRODUCERS == 0, "a producer keeps its own ring slots");
     static constexpr int THREADS = 32 * (1 + PRODUCERS + EPI_WARPS + FIX_WARPS);
-    static constexpr int STG_BUF = 4096;                // [64 rows][32 columns] or [32 rows][128 bytes]
-    static constexpr int NBUF = WG_ ? 2 : 1;
+    static constexpr int STG_BUF = WG_ ? 4096 : 2048;   // a warp's [32 rows][128 bytes] or [32 rows][32 columns]
+    static constexpr int NBUF = WG_ ? 8 / EPI_ : 1;     // staging tiles a warp
     static constexpr int TMEM_COLS = 512;               // two accumulators of 256 columns
     static constexpr int TABLE = WG_ ? 0 : (2 * (kMaxGroups + 2)) * 4;
     static constexpr int SMEM_DATA = STAGES * (A_STAGE + B_STAGE) + EPI_WARPS * NBUF * STG_BUF;
@@ -109,10 +114,11 @@ struct GrpItem {
     int r0, rows;             // WG: the group's rows
 };
 
-// Epilogue of a product tile (this warp's 32 weight columns from nw).
+// Epilogue of a product tile: this warp's 32 weight columns from nw, its share
+// of the tile's rows, 32 at a time (half: which of HALVES warps).
 template <class Cfg>
 __device__ __forceinline__ void grp_store_rows(const GrpParams& p, const GrpItem& it, uint32_t taddr,
-                                               int nw, int lane, uint8_t* stg) {
+                                               int nw, int half, int lane, uint8_t* stg) {
     if (nw >= p.N) return;                                  // warp-uniform
     float cs[4] = {0.f, 0.f, 0.f, 0.f};
     if constexpr (Cfg::I8) {
@@ -143,19 +149,19 @@ __device__ __forceinline__ void grp_store_rows(const GrpParams& p, const GrpItem
     const int mj = lane >> 3, mc = lane & 7;                // stmatrix: this lane's matrix and column
     const int rr = lane >> 2, ch = lane & 3;                // row store: row and 16-byte chunk
 #pragma unroll 1
-    for (int m = it.m0; m < it.m1; m += 64) {
-        uint32_t v0[32], v1[32];
+    for (int m = it.m0 + 32 * half; m < it.m1; m += 32 * Cfg::HALVES) {
+        uint32_t v0[16], v1[16];
         if (it.kb) {
-            tmem_ld_16x256b_x8(taddr + (m - it.m0), v0);
-            tmem_ld_16x256b_x8(taddr + (16u << 16) + (m - it.m0), v1);
+            tmem_ld_16x256b_x4(taddr + (m - it.m0), v0);
+            tmem_ld_16x256b_x4(taddr + (16u << 16) + (m - it.m0), v1);
         } else {
 #pragma unroll
-            for (int i = 0; i < 32; ++i) v0[i] = v1[i] = 0;
+            for (int i = 0; i < 16; ++i) v0[i] = v1[i] = 0;
         }
-        float rs[16];
+        float rs[8];
         if constexpr (Cfg::I8) {
 #pragma unroll
-            for (int i = 0; i < 16; ++i) {
+            for (int i = 0; i < 8; ++i) {
                 const int r = m + 8 * (i >> 1) + 2 * (lane & 3) + (i & 1);
                 rs[i] = (it.kb && r < it.m1) ? __ldg(p.row_scale + r) : 0.f;
             }
@@ -163,7 +169,7 @@ __device__ __forceinline__ void grp_store_rows(const GrpParams& p, const GrpItem
         if (it.kb) tmem_ld_wait();
         __syncwarp();                                       // the last chunk's rows are read
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
+        for (int i = 0; i < 4; ++i) {
             const float ra = Cfg::I8 ? rs[2 * i] : 0.f, rb = Cfg::I8 ? rs[2 * i + 1] : 0.f;
             const uint32_t w0 = pack(finish(v0[4 * i], ra, cs[0]), finish(v0[4 * i + 1], rb, cs[0]));
             const uint32_t w1 = pack(finish(v0[4 * i + 2], ra, cs[1]), finish(v0[4 * i + 3], rb, cs[1]));
@@ -177,7 +183,7 @@ __device__ __forceinline__ void grp_store_rows(const GrpParams& p, const GrpItem
         uint16_t* dst0 = static_cast<uint16_t*>(p.C) + nw + ch * 8;
         const int left = p.N - (nw + ch * 8);               // columns from this chunk on
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
+        for (int i = 0; i < 4; ++i) {
             const int r = 8 * i + rr;
             const uint4 x = *reinterpret_cast<const uint4*>(stg + r * 64 + ((ch ^ ((r >> 1) & 3)) << 4));
             if (m + r < it.m1) {
@@ -196,14 +202,14 @@ __device__ __forceinline__ void grp_store_rows(const GrpParams& p, const GrpItem
 }
 
 // Epilogue of a weight-gradient tile: this warp's 32 rows k from kr of C_e,
-// columns from it.m0.
+// its share of the columns from it.m0 on, 64 at a time.
 template <class Cfg>
 __device__ __forceinline__ void grp_store_grad(const CUtensorMap* tmC, const GrpParams& p, const GrpItem& it,
-                                               uint32_t taddr, int kr, int lane, uint8_t* stg0,
+                                               uint32_t taddr, int kr, int half, int lane, uint8_t* stg0,
                                                uint32_t& nstore) {
     if (kr >= p.K) return;                                  // warp-uniform
 #pragma unroll 1
-    for (int c = 0; it.m0 + c < it.m1; c += 64) {
+    for (int c = 64 * half; it.m0 + c < it.m1; c += 64 * Cfg::HALVES) {
         const int col0 = it.m0 + c;
         uint32_t v[64];
         if (it.kb) {
@@ -225,7 +231,7 @@ __device__ __forceinline__ void grp_store_grad(const CUtensorMap* tmC, const Grp
             continue;
         }
         uint8_t* stg = stg0 + (nstore % Cfg::NBUF) * Cfg::STG_BUF;
-        if (lane == 0) bulk_wait_read<Cfg::NBUF - 1>();     // this buffer's last store has read it
+        if (lane == 0) bulk_wait_read<Cfg::NBUF - 1>();     // this tile's last store has read it
         __syncwarp();
         uint8_t* row = stg + lane * 128;
 #pragma unroll
@@ -543,6 +549,7 @@ grp_gemm_kernel(const __grid_constant__ CUtensorMap tmA,
     } else if (warp >= 2 && warp < 2 + Cfg::EPI_WARPS) {
         // --------------------------------------------------- epilogue (both)
         const int q = warp & 3;
+        const int half = (warp - 2) >> 2;
         uint8_t* stg = smStg + (warp - 2) * Cfg::NBUF * Cfg::STG_BUF;
         uint32_t tl = 0, nstore = 0;
         int g = 0;
@@ -557,8 +564,8 @@ grp_gemm_kernel(const __grid_constant__ CUtensorMap tmA,
             }
             const uint32_t taddr = tmem_base + acc * 256 + (static_cast<uint32_t>(q * 32) << 16);
             const int l0 = it.n0 + static_cast<int>(rank) * 128 + q * 32;
-            if constexpr (Cfg::WG) grp_store_grad<Cfg>(&tmC, p, it, taddr, l0, lane, stg, nstore);
-            else grp_store_rows<Cfg>(p, it, taddr, l0, lane, stg);
+            if constexpr (Cfg::WG) grp_store_grad<Cfg>(&tmC, p, it, taddr, l0, half, lane, stg, nstore);
+            else grp_store_rows<Cfg>(p, it, taddr, l0, half, lane, stg);
             if (it.kb) {
                 tc_fence_before();
                 __syncwarp();

@@ -68,7 +68,7 @@ int* device_status_ptr();
 //   56-57  gemm_sp24.cu (one CTA)   61-62  gemm_sp24.cu (CTA pairs)
 //   64-67  gemm_tc.cu        CTA-pair bf16/f16 with the operands swapped (M <= 128)
 //   68     gemm_tc.cu        CTA-pair TF32
-//   70-79  gemm_group.cu     experts' products and 8-bit products
+//   70-81  gemm_group.cu     experts' products and 8-bit products
 //   82-89  expert.cu         sort by expert
 //   90-97  gemm_skinny_i8.cu
 constexpr int kMaxSlots = 128;
