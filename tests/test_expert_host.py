@@ -330,9 +330,9 @@ def test_how_weights_reach_the_kernels():
     assert tr and st.data_ptr() == S.data_ptr() and tuple(st.shape) == (4, 24, 40)
     st, tr = binding._stored3(S[:, :, 8:24])              # a column slice keeps its pitch
     assert not tr and st.stride(1) == 40
-    x = torch.empty(4, 24, 40, dtype=torch.bfloat16)[:, ::2, ::2]
+    x = bf((4, 24, 40), 1)[:, ::2, ::2]
     st, tr = binding._stored3(x)
-    assert not tr and st.is_contiguous()
+    assert not tr and torch.equal(st, x) and st.stride() == (12 * 24, 24, 1)      # 20 columns, 16-byte pitch
     one = torch.empty(1, 24, 40, dtype=torch.bfloat16).expand(4, 24, 40)
     st, tr = binding._stored3(one)                        # shared weights are copied
     assert not tr and st.stride(0) == 24 * 40
@@ -385,3 +385,36 @@ def test_cpu_tensors_are_refused():
               lambda: binding.gemm_grouped(bf((4, 16), 1), torch.tensor([0, 4], dtype=torch.int32), bf((1, 16, 8), 2))):
         with pytest.raises(ValueError, match="CUDA"):
             f()
+
+
+@pytest.mark.parametrize("trans", [False, True])
+@pytest.mark.parametrize("N", [8, 11])
+def test_saved_tensors_in_another_layout(fake, trans, N):
+    """A saved-tensor hook (offloading) may give back contiguous copies of what
+    were strided views; shared weights were copied in forward."""
+    K, E = 13, 3
+    plan = plan_of(IDS, E)
+    X = bf((10, K), 1, 24).requires_grad_(True)
+    S = (bf((E, N, K), 2, 24) if trans else bf((E, K, N), 2, 24)).requires_grad_(True)
+    g = bf((10, N), 3, 16)
+
+    def grads(x, s):
+        y = binding.expert_matmul(x, s.transpose(1, 2) if trans else s, plan)
+        return torch.autograd.grad(y, (X, S), g)
+
+    want = grads(X, S)
+    with torch.autograd.graph.saved_tensors_hooks(lambda t: t.clone(memory_format=torch.contiguous_format), lambda t: t):
+        got = grads(X, S)
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+    one = bf((K, N), 4, 24).requires_grad_(True)
+    y = binding.expert_matmul(X.detach(), one.expand(E, K, N), plan)
+    d, = torch.autograd.grad(y, one, g)
+    n = int(plan.offsets[-1])
+    # the groups' gradients are rounded before autograd adds them, in bfloat16
+    near(d, X.detach().double()[:n].t() @ g.double()[:n], 2 * E)
+    Y = bf((10, N), 5, 16).requires_grad_(True)
+    w = torch.rand(5, 2).requires_grad_(True)
+    want = torch.autograd.grad(binding.expert_combine(Y, plan, w), (Y, w), bf((5, N), 6, 16))
+    with torch.autograd.graph.saved_tensors_hooks(lambda t: t.clone(memory_format=torch.contiguous_format), lambda t: t):
+        got = torch.autograd.grad(binding.expert_combine(Y, plan, w), (Y, w), bf((5, N), 6, 16))
+    assert all(torch.equal(a, b) for a, b in zip(got, want))

@@ -529,3 +529,42 @@ def test_positions_outside_the_rows_are_skipped(tg, pos):
         tg.expert_gather(X, plan).sum().backward()
         tg.expert_combine(Y, plan, w).sum().backward()
     _status(tg)
+
+
+def test_rows_past_32_bit_offsets(tg):
+    """More than 2^31 elements: the last rows are where they belong."""
+    T, k, H = 300_001, 2, 4096                            # 2.46e9 sorted values
+    ids = (torch.arange(T * k, device="cuda") % 3).view(T, k)
+    plan = tg.expert_sort(ids, 3)
+    X = torch.arange(T, device="cuda", dtype=torch.float32)[:, None].remainder(251).to(torch.bfloat16).expand(T, H)
+    X = X.contiguous()
+    Xs = tg.expert_gather(X, plan)
+    tail = plan.src[-5:].long() // k
+    assert torch.equal(Xs[-5:], X[tail])
+    Y = tg.expert_combine(Xs, plan)
+    assert torch.equal(Y[-5:], X[-5:] * 2)                # small integers: exact
+    W = torch.zeros(3, 4096, 16, dtype=torch.bfloat16, device="cuda")
+    W[:, 7, :] = 1
+    P = tg.gemm_grouped(Xs, plan, W)
+    assert torch.equal(P[-5:], X[tail][:, :16])
+    del Y, P
+    q, s = tg.quant_i8(Xs)
+    _status(tg)
+    top = Xs[-5:, :1].float().abs()
+    assert torch.equal(q[-5:, :1].float() * s[-5:, None], torch.where(top > 0, 127 * (top / 127), 0))
+
+
+def test_activations_kept_on_the_host(tg):
+    """torch.autograd.graph.save_on_cpu gives back contiguous copies of the
+    strided operands."""
+    E, counts = 3, [20, 0, 33]
+    o = offsets_of(counts)
+    X = normal((53, 20), torch.bfloat16, 1, extra=1).requires_grad_(True)
+    S = normal((E, 20, 13), torch.bfloat16, 2).requires_grad_(True)
+    g = normal((53, 13), torch.bfloat16, 3)
+    want = torch.autograd.grad(tg.expert_matmul(X, S, o), (X, S), g)
+    with torch.autograd.graph.save_on_cpu():
+        Y = tg.expert_matmul(X, S, o)
+    got = torch.autograd.grad(Y, (X, S), g)
+    _status(tg)
+    assert all(torch.equal(a, b) for a, b in zip(got, want))

@@ -861,7 +861,32 @@ def _stored3(W):
         return W, False
     if trans:
         return W.transpose(1, 2), True
-    return W.contiguous(), False
+    return _pitched_copy3(W), False
+
+
+def _pitched_copy3(W):
+    """A row-major copy whose row pitch is a multiple of 16 bytes."""
+    import torch
+    per = 16 // W.element_size()
+    E, K, N = W.shape
+    copy = torch.empty((E, K, -(-N // per) * per), dtype=W.dtype, device=W.device)[:, :, :N]
+    return copy.copy_(W)
+
+
+def _product_grads(A, W, offsets, g, needed):
+    """The gradients of expert_matmul from operands of any layout."""
+    A = _aligned_rows(A)
+    w, tr = _stored3(W)
+    per = 16 // w.element_size()
+    if w.data_ptr() % 16 or (w.shape[1] > 1 and w.stride(1) % per) or \
+            (w.shape[0] > 1 and w.stride(0) % per):
+        w = _pitched_copy3(w)
+    dA = gemm_grouped(g, offsets, w, trans_b=not tr) if needed[0] else None
+    dW = None
+    if needed[1]:
+        dW = (gemm_grouped_wgrad(g, A, offsets).transpose(1, 2) if tr
+              else gemm_grouped_wgrad(A, g, offsets))
+    return dA, dW, None
 
 
 def _expert_functions():
@@ -904,7 +929,7 @@ def _expert_functions():
             Ys, weights, _, _ = ctx.saved_tensors
             if weights is None:
                 return _gather(g, ctx.plan), None, None
-            dY, dw = _combine_grad(Ys, weights, g, ctx.plan)
+            dY, dw = _combine_grad(_aligned_rows(Ys), weights, g, ctx.plan)
             return (dY if ctx.needs_input_grad[0] else None,
                     dw if ctx.needs_input_grad[1] else None, None)
 
@@ -916,22 +941,44 @@ def _expert_functions():
         def forward(ctx, A, W, offsets):
             ctx.save_for_backward(A, W, offsets)
             w, tr = _stored3(W)
-            return gemm_grouped(A, offsets, w, trans_b=tr)
+            C = gemm_grouped(A, offsets, w, trans_b=tr)
+            # what backward reads again, as checked for the call above
+            own = w.data_ptr() == W.data_ptr()
+            ctx.strides = (A.stride(), W.stride()) if own else None
+            ctx.layout = (C.shape[0], C.shape[1], A.shape[1], w.shape[0], _pitch(A, "A"),
+                          _pitch(w, "W"), _plane(w), tr)
+            return C
 
         @staticmethod
         def backward(ctx, g):
             once()
             A, W, offsets = ctx.saved_tensors
             g = _aligned_rows(g)
-            w, tr = _stored3(W)
+            if (A.stride(), W.stride()) != ctx.strides:
+                # weights that were copied, or tensors that a saved-tensor hook gave back
+                # in another layout than it took
+                return _product_grads(A, W, offsets, g, ctx.needs_input_grad)
+            M, N, K, E, lda, ldb, plane, tr = ctx.layout
+            device, dtype = A.device, A.dtype
+            ldg = _pitch(g, "the gradient")
+            kind = "bf16" if dtype == torch.bfloat16 else "f16"
             dA = dW = None
             if ctx.needs_input_grad[0]:
-                dA = gemm_grouped(g, offsets, w, trans_b=not tr)
+                dA, ldd = _rows_out(M, K, dtype, device)
+                _launch("tg_gemm_grouped_" + kind, device, None, M, K, N, E, g.data_ptr(), ldg,
+                        offsets.data_ptr(), W.data_ptr(), ldb, plane,
+                        int(not tr), dA.data_ptr(), ldd, EPI_NONE)
             if ctx.needs_input_grad[1]:
+                # (A, K) and (g, N) change places for weights stored N x K
+                x, ldx, k, y, ldy, n = (g, ldg, N, A, lda, K) if tr else (A, lda, K, g, ldg, N)
+                ld = -(-n // 8) * 8
+                dW = torch.empty((E, k, ld), dtype=dtype, device=device)
+                _launch("tg_gemm_grouped_wgrad_" + kind, device, None, M, n, k, E, x.data_ptr(),
+                        ldx, y.data_ptr(), ldy, offsets.data_ptr(), dW.data_ptr(), ld, k * ld)
+                if ld != n:
+                    dW = dW[:, :, :n]
                 if tr:
-                    dW = gemm_grouped_wgrad(g, A, offsets).transpose(1, 2)
-                else:
-                    dW = gemm_grouped_wgrad(A, g, offsets)
+                    dW = dW.transpose(1, 2)
             return dA, dW, None
 
     return _Gather, _Combine, _Product
