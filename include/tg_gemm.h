@@ -1,7 +1,8 @@
 /*
  * tg_gemm.h -- C ABI of the tiled dense GEMM library for one NVIDIA B200.
  *
- * Operation (every entry point):
+ * Operation (the dense products; the experts' operators and the row
+ * quantiser state theirs below):
  *
  *     C[i][j] = epi( sum_{k<K} A[i][k] * B[k][j] ),   0 <= i < M, 0 <= j < N
  *
