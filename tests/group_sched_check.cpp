@@ -11,29 +11,33 @@ using namespace tg;
 extern "C" {
 
 // The row tiles of a group, whole or in pieces: they tile [0, rows) in order,
-// whole ones are not empty, widths are multiples of 32 in [32, 256], an MMA
-// takes them (and pieces are no wider than their tile).
+// whole ones are not empty, widths are multiples of 32 in [32, 256] as an MMA
+// takes them, their sum pads less than 32 rows, and pieces are no wider than
+// their tile.
 long long check_group_tiles(int max_rows, long long* checked) {
     long long bad = 0, n = 0;
     for (int rows = 1; rows <= max_rows; ++rows) {
-        const int nt = grp_tiles(rows), w = grp_width(rows);
-        ++n; bad += w % 32 != 0 || w < 32 || w > 256;
-        ++n; bad += static_cast<long long>(nt) * w < rows || (nt - 1) * w >= rows;
+        const int nt = grp_tiles(rows);
+        ++n; bad += nt != (rows + 255) / 256;
         for (int pieces : {1, 2, 4}) {
-            const int pw = grp_piece_width(w, pieces);
-            ++n; bad += pw % 32 != 0 || pw < 32 || pw > w || pw * pieces < w;
-            // as the kernel walks them
-            int at = 0;
+            int end = 0, sum = 0;
             for (int t = 0; t < nt; ++t) {
-                const int m0 = t * w, m1 = std::min(rows, m0 + w);
+                int at, w;
+                grp_tile(rows, t, at, w);
+                ++n; bad += w % 32 != 0 || w < 32 || w > 256 || at >= rows || at != sum;
+                sum += w;
+                const int pw = grp_piece_width(w, pieces);
+                ++n; bad += pw % 32 != 0 || pw < 32 || pw > w || pw * pieces < w;
+                // as the kernel walks them
+                const int m1 = std::min(rows, at + w);
                 for (int i = 0; i < pieces; ++i) {
-                    const int a = m0 + i * pw, b = std::min(m1, a + pw);
+                    const int a = at + i * pw, b = std::min(m1, a + pw);
                     if (a >= b) continue;
-                    ++n; bad += a != at;
-                    at = b;
+                    ++n; bad += a != end;
+                    end = b;
                 }
             }
-            ++n; bad += at != rows;
+            ++n; bad += end != rows || sum - rows >= 32;
         }
     }
     *checked = n;
@@ -44,9 +48,13 @@ long long check_group_tiles(int max_rows, long long* checked) {
 long long check_group_large(long long* checked) {
     long long bad = 0, n = 0;
     for (int rows : {2147483647, 2147483393, 1 << 30}) {
-        const int nt = grp_tiles(rows), w = grp_width(rows);
+        const int nt = grp_tiles(rows);
         ++n; bad += nt != static_cast<int>((static_cast<long long>(rows) + 255) / 256);
-        ++n; bad += w != 256;
+        for (int t : {0, 1, nt / 2, nt - 1}) {
+            int at, w;
+            grp_tile(rows, t, at, w);
+            ++n; bad += at < 0 || at >= rows || (w != 256 && w != 224);
+        }
     }
     *checked = n;
     return bad;

@@ -28,7 +28,7 @@
 // [32 rows][32 columns] staging tile and written with 16-byte stores, which
 // stop at the group's last row; the rows past it belong to the next group
 // and were only read.  Row tiles of a group are as even as whole widths
-// allow (grp_width of tile_sched.h).  Rows behind the last group are written
+// allow (grp_tile of tile_sched.h).  Rows behind the last group are written
 // as zero.
 //
 // Weight gradient: the 256 lanes are the columns k of A, the MMA's N side
@@ -384,11 +384,11 @@ grp_gemm_kernel(const __grid_constant__ CUtensorMap tmA,
             int r1;
             grp_rows(p.offsets, it.e, p.E, p.M, it.r0, r1);
             it.rows = r1 - it.r0;
-            it.width = grp_width(it.rows);
-            int tl, tt;
+            int tl, tt, at;
             tile_coords(w - gstart[g], ntl, grp_tiles(it.rows), p.group_m, tl, tt);
+            grp_tile(it.rows, tt, at, it.width);
             it.n0 = tl * 256;
-            it.m0 = it.r0 + tt * it.width;
+            it.m0 = it.r0 + at;
             it.m1 = min(r1, it.m0 + it.width);
             it.kb = it.e < p.E ? (p.K - 1) / Cfg::BK + 1 : 0;
         }

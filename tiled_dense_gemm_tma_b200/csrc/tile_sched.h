@@ -151,17 +151,20 @@ TG_HD void tile_coords(int t, int ntm, int ntn, int group_m, int& tm, int& tn) {
 
 // ------------------------------------------------------ groups of rows
 // The experts' products: a group of `rows` > 0 consecutive rows is cut into
-// grp_tiles(rows) tiles of grp_width(rows) rows (the last one may hold
-// fewer), as even as whole MMA widths (multiples of 32, at most 256) allow, so
-// that a group of 300 rows is 160 + 140 and not 256 + 44.  No tile is empty:
-// the width is at most 256, and 256 * (tiles - 1) < rows.
+// grp_tiles(rows) tiles, as few as 256 rows a tile allow.  An MMA takes
+// widths in units of 32 rows: the group's units are dealt out evenly, so that
+// no more than the last unit is padding (1348 rows are 256 + 5 x 224, not
+// 6 x 256, nor 5 x 256 + 96).
 
 TG_HD int grp_tiles(int rows) { return (rows - 1) / 256 + 1; }
 
-TG_HD int grp_width(int rows) {
-    const int nt = grp_tiles(rows);
-    const int per = (rows - 1) / nt + 1;
-    return (per + 31) / 32 * 32;
+// Tile i of the group: its first row in the group and its MMA width (a
+// multiple of 32, at most 256; the last tile may hold fewer rows).
+TG_HD void grp_tile(int rows, int i, int& at, int& width) {
+    const int nt = grp_tiles(rows), units = (rows - 1) / 32 + 1;
+    const int each = units / nt, more = units - each * nt;     // the first `more` tiles take one more
+    at = 32 * (i * each + sched_min(i, more));
+    width = 32 * (each + (i < more ? 1 : 0));
 }
 
 // The last wave of T tiles on npairs pairs: where its R = T mod npairs tiles
