@@ -446,18 +446,20 @@ def _launch(name, device, stream, *args):
     `stream`, by default that device's current stream; raise on an error.  The
     calls of this section go through here: they are made once per layer and
     token step, where the host's time per call is what a user waits for."""
-    import torch
     fn = _fns.get(name)
     if fn is None:
+        import torch
+        _fns["stream"], _fns["device"] = torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice
         fn = _fns[name] = getattr(load_library(), name)
     index = device.index
     if stream is None:
-        stream = torch._C._cuda_getCurrentRawStream(index)
+        stream = _fns["stream"](index)
     elif not isinstance(stream, int):
         stream = stream.cuda_stream
-    if torch._C._cuda_getDevice() == index:
+    if _fns["device"]() == index:
         code = fn(*args, stream)
     else:
+        import torch
         with torch.cuda.device(index):
             code = fn(*args, stream)
     if code:
@@ -479,14 +481,13 @@ def _pitch(t, name):
     """Row pitch (elements) of a row-major 2-D tensor or of the matrices of a
     3-D one; for fewer than two rows, whose stride says nothing, the row
     length rounded up to 16 bytes."""
-    *_, rows, cols = t.shape
-    *_, ld, one = t.stride()
-    if one != 1 and cols > 1:
+    shape, strides = t.shape, t.stride()
+    if strides[-1] != 1 and shape[-1] > 1:
         raise ValueError(f"{name} must be row-major (unit column stride)")
-    if rows <= 1:
-        per = 16 // t.element_size()
-        return max(per, -(-cols // per) * per)
-    return ld
+    if shape[-2] > 1:
+        return strides[-2]
+    per = 16 // t.element_size()
+    return max(per, -(-shape[-1] // per) * per)
 
 
 def _plane(t):
@@ -494,15 +495,11 @@ def _plane(t):
     return t.stride(0) if t.shape[0] > 1 else 0
 
 
-def _one_device(device, *named):
-    """As _require_cuda, without its list where all is well."""
-    if device.type == "cuda":
-        for t, _ in named:
-            if t.device != device:
-                break
-        else:
-            return
-    _require_cuda(device, *named)
+def _one_device(device, tensors, names):
+    """As _require_cuda, naming the tensors only where something is wrong."""
+    for t in tensors:
+        if t.device != device or not t.is_cuda:
+            _require_cuda(device, *zip(tensors, names.split(", ")))
 
 
 def _vector(t, n, dtype, name):
@@ -542,7 +539,7 @@ def quant_i8(X, Q=None, scales=None, stream=None):
         scales = torch.empty(M, dtype=torch.float32, device=device)
     else:
         _vector(scales, M, torch.float32, "scales")
-    _one_device(device, (Q, "Q"), (scales, "scales"))
+    _one_device(device, (Q, scales), "Q, scales")
     _launch("tg_quant_i8", device, stream, M, K, X.data_ptr(), _pitch(X, "X"), kind,
             Q.data_ptr(), ldq, scales.data_ptr())
     return Q, scales
@@ -560,7 +557,10 @@ def gemm_w8a8(A, row_scales, B, col_scales, C=None, out_dtype=None, relu=False, 
     if A.dim() != 2 or B.dim() != 2:
         raise ValueError("A and B must be 2-D")
     M, K = A.shape
-    K2, N = B.shape[::-1] if trans_b else B.shape
+    if trans_b:
+        N, K2 = B.shape
+    else:
+        K2, N = B.shape
     if K != K2:
         raise ValueError(f"inner dimensions differ: {K} vs {K2}")
     _vector(row_scales, M, torch.float32, "row_scales")
@@ -570,8 +570,7 @@ def gemm_w8a8(A, row_scales, B, col_scales, C=None, out_dtype=None, relu=False, 
     kind = _type16(out_dtype, "C")
     device = A.device
     C, ldc = _out(C, M, N, out_dtype, device)
-    _one_device(device, (B, "B"), (row_scales, "row_scales"),
-                  (col_scales, "col_scales"), (C, "C"))
+    _one_device(device, (B, row_scales, col_scales, C), "B, row_scales, col_scales, C")
     _launch("tg_gemm_w8a8", device, stream, M, N, K, A.data_ptr(), _pitch(A, "A"),
             row_scales.data_ptr(), B.data_ptr(), _pitch(B, "B"), int(trans_b),
             col_scales.data_ptr(), C.data_ptr(), ldc, kind, EPI_RELU if relu else EPI_NONE)
@@ -597,7 +596,7 @@ class ExpertPlan:
                 not offsets.is_contiguous() or not pos.is_contiguous():
             raise ValueError("a plan has a vector of offsets and a tokens x topk matrix pos, "
                              "both contiguous")
-        _one_device(offsets.device, (pos, "pos"))
+        _one_device(offsets.device, (pos,), "pos")
         self._offsets, self._pos, self._src = offsets, pos, src
 
     @property
@@ -630,6 +629,9 @@ class ExpertPlan:
         return o.data_ptr() + 4 * (o.shape[0] - 1)
 
 
+_scratch = {}            # bytes of scratch the sort asks for, by size
+
+
 def expert_sort(ids, num_experts):
     """Stable sort of the choices ids (tokens x topk, int32 or int64) by
     expert, as an ExpertPlan.  Numbers outside 0..num_experts - 1 are dropped
@@ -640,12 +642,17 @@ def expert_sort(ids, num_experts):
     if ids.dtype not in (torch.int32, torch.int64):
         raise TypeError("ids must be int32 or int64")
     device = ids.device
-    _one_device(device, (ids, "ids"))
+    _one_device(device, (ids,), "ids")
     T, k = ids.shape
     if k < 1:
         raise ValueError("ids must hold at least one choice per token")
     n = T * k
-    need = load_library().tg_expert_sort_scratch(n, num_experts)
+    need = _scratch.get((n, num_experts))
+    if need is None:
+        if len(_scratch) > 1000:
+            _scratch.clear()
+        need = load_library().tg_expert_sort_scratch(n, num_experts)
+        _scratch[n, num_experts] = need
     if need < 0:
         raise ValueError("expert_sort takes 1 to 1024 experts and fewer than 2^31 choices")
     ids = ids.contiguous()
@@ -679,8 +686,8 @@ def _gather(X, plan, scales=None):
     if scales is not None:
         _vector(scales, T, torch.float32, "scales")
         ss = torch.empty(T * k, dtype=torch.float32, device=device)
-        _one_device(device, (scales, "scales"))
-    _one_device(device, (pos, "the plan"))
+        _one_device(device, (scales,), "scales")
+    _one_device(device, (pos,), "the plan")
     _launch("tg_expert_gather", device, None, T, k, H, X.element_size(), X.data_ptr(),
             _pitch(X, "X"), None if ss is None else scales.data_ptr(), pos.data_ptr(),
             plan._kept(), out.data_ptr(), ldo, None if ss is None else ss.data_ptr())
@@ -693,7 +700,7 @@ def _check_weights(weights, T, k, device):
         raise TypeError("weights must be float32")
     if weights.shape != (T, k):
         raise ValueError("weights must be tokens x topk")
-    _one_device(device, (weights, "weights"))
+    _one_device(device, (weights,), "weights")
     return weights.contiguous()
 
 
@@ -707,7 +714,7 @@ def _combine(Y, plan, weights):
     if weights is not None:
         weights = _check_weights(weights, T, k, device)
     out, ldo = _rows_out(T, H, Y.dtype, device)
-    _one_device(device, (pos, "the plan"))
+    _one_device(device, (pos,), "the plan")
     _launch("tg_expert_combine", device, None, T, k, H, kind, Y.data_ptr(), _pitch(Y, "Y"),
             pos.data_ptr(), plan._kept(), None if weights is None else weights.data_ptr(),
             out.data_ptr(), ldo)
@@ -722,7 +729,7 @@ def _combine_grad(Y, weights, g, plan):
     weights = weights.contiguous()
     dY, ldd = _rows_out(T * k, H, Y.dtype, device)
     dw = torch.empty((T, k), dtype=torch.float32, device=device)
-    _one_device(device, (g, "the gradient"))
+    _one_device(device, (g,), "the gradient")
     _launch("tg_expert_combine_grad", device, None, T, k, H, _type16(Y.dtype, "Y"), Y.data_ptr(),
             _pitch(Y, "Y"), g.data_ptr(), _pitch(g, "the gradient"), pos.data_ptr(), plan._kept(),
             weights.data_ptr(), dY.data_ptr(), ldd, dw.data_ptr())
@@ -771,7 +778,7 @@ def gemm_grouped(A, groups, B, C=None, relu=False, stream=None, trans_b=False):
         raise ValueError(f"inner dimensions differ: {K} vs {K2}")
     device = A.device
     C, ldc = _out(C, M, N, A.dtype, device)
-    _one_device(device, (B, "B"), (offsets, "offsets"), (C, "C"))
+    _one_device(device, (B, offsets, C), "B, offsets, C")
     name = "tg_gemm_grouped_bf16" if kind == TYPE_BF16 else "tg_gemm_grouped_f16"
     _launch(name, device, stream, M, N, K, E, A.data_ptr(), _pitch(A, "A"), offsets.data_ptr(),
             B.data_ptr(), _pitch(B, "B"), _plane(B), int(trans_b), C.data_ptr(), ldc,
@@ -798,7 +805,7 @@ def gemm_grouped_wgrad(A, G, groups, C=None, stream=None):
         C = torch.empty((E, K, ld), dtype=A.dtype, device=A.device)[:, :, :N]
     elif C.shape != (E, K, N) or C.dtype != A.dtype:
         raise ValueError("C has the wrong shape or dtype")
-    _one_device(A.device, (G, "G"), (offsets, "offsets"), (C, "C"))
+    _one_device(A.device, (G, offsets, C), "G, offsets, C")
     name = "tg_gemm_grouped_wgrad_bf16" if kind == TYPE_BF16 else "tg_gemm_grouped_wgrad_f16"
     _launch(name, A.device, stream, M, N, K, E, A.data_ptr(), _pitch(A, "A"), G.data_ptr(),
             _pitch(G, "G"), offsets.data_ptr(), C.data_ptr(), _pitch(C, "C"), _plane(C))
@@ -831,8 +838,7 @@ def gemm_grouped_w8a8(A, row_scales, groups, B, col_scales, C=None, out_dtype=No
     kind = _type16(out_dtype, "C")
     device = A.device
     C, ldc = _out(C, M, N, out_dtype, device)
-    _one_device(device, (B, "B"), (row_scales, "row_scales"),
-                  (col_scales, "col_scales"), (offsets, "offsets"), (C, "C"))
+    _one_device(device, (B, row_scales, col_scales, offsets, C), "B, row_scales, col_scales, offsets, C")
     _launch("tg_gemm_grouped_w8a8", device, stream, M, N, K, E, A.data_ptr(), _pitch(A, "A"),
             row_scales.data_ptr(), offsets.data_ptr(), B.data_ptr(), _pitch(B, "B"), _plane(B),
             int(trans_b), col_scales.data_ptr(), _plane(col_scales), C.data_ptr(), ldc, kind,
