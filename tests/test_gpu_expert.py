@@ -568,3 +568,49 @@ def test_activations_kept_on_the_host(tg):
     got = torch.autograd.grad(Y, (X, S), g)
     _status(tg)
     assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+def test_moves_against_differences(tg):
+    """Gather and combine are linear in each argument: central differences of
+    <output, G> along a direction equal <gradient, direction> exactly on small
+    integers (every sum below 256, exact in bf16)."""
+    ids = make_ids(30, 4, 5, 3, 0.2)
+    plan = tg.expert_sort(ids, 5)
+    X, D = (ints8((30, 40), i, -3, 4).to(torch.bfloat16) for i in (1, 2))
+    Y, F = (ints8((120, 40), i, -3, 4).to(torch.bfloat16) for i in (3, 4))
+    w, v = (ints8((30, 4), i, -2, 3).float().contiguous() for i in (5, 6))
+    Gx, Gy = ints8((120, 40), 7, -3, 4).to(torch.bfloat16), ints8((30, 40), 8, -3, 4).to(torch.bfloat16)
+
+    def check(f, at, along, grad):
+        diff = (f(at + along).double() - f(at - along).double()) / 2
+        assert diff.item() == (grad.double() * along.double()).sum().item()
+
+    x = X.clone().requires_grad_(True)
+    dX, = torch.autograd.grad(tg.expert_gather(x, plan), x, Gx)
+    check(lambda t: (tg.expert_gather(t, plan).double() * Gx.double()).sum(), X, D, dX)
+    y, u = Y.clone().requires_grad_(True), w.clone().requires_grad_(True)
+    dY, dw = torch.autograd.grad(tg.expert_combine(y, plan, u), (y, u), Gy)
+    check(lambda t: (tg.expert_combine(t, plan, w).double() * Gy.double()).sum(), Y, F, dY)
+    check(lambda t: (tg.expert_combine(Y, plan, t).double() * Gy.double()).sum(), w, v, dw)
+    _status(tg)
+
+
+def test_empty_products(tg):
+    """No columns, no k: what is left of the outputs is zero."""
+    o = offsets_of([3, 0, 2])
+    for K, N in ((0, 16), (16, 0), (0, 0)):
+        X = pitched((5, K), torch.bfloat16).requires_grad_(True)
+        W = pitched((3, K, N), torch.bfloat16).requires_grad_(True)
+        Y = tg.expert_matmul(X, W, o)
+        dX, dW = torch.autograd.grad(Y, (X, W), torch.ones(5, N, dtype=torch.bfloat16, device="cuda"))
+        assert tuple(Y.shape) == (5, N) and not Y.any()
+        assert tuple(dX.shape) == (5, K) and tuple(dW.shape) == (3, K, N) and not dX.any() and not dW.any()
+    A, B = ints8((5, 0), 1), ints8((0, 24), 2)
+    C = tg.gemm_w8a8(A, positive((5,), 1), B, positive((24,), 2))
+    assert tuple(C.shape) == (5, 24) and not C.any()
+    q, s = tg.quant_i8(pitched((4, 0), torch.float16))
+    assert tuple(q.shape) == (4, 0) and not s.any()
+    for M in (0, 3):
+        C = tg.gemm_w8a8(ints8((M, 16), 1), positive((M,), 1), ints8((16, 0 if M else 8), 2), positive((0 if M else 8,), 2))
+        assert tuple(C.shape) == (M, 0 if M else 8)
+    _status(tg)

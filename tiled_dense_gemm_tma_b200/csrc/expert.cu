@@ -41,6 +41,7 @@ namespace {
 // places.
 
 constexpr int kKeep = 8;
+constexpr int kSortWarps = 32;          // 8 for up to 1024 choices
 constexpr int kOneBlock = 8192;
 constexpr int kPerBlock = 1024;
 constexpr int kMaxBlocks = 148;
@@ -53,7 +54,7 @@ struct SortPlan {
 
 SortPlan sort_plan(int64_t n) {
     SortPlan p;
-    p.warps = n <= 8 * 32 * 4 ? 8 : 32;
+    p.warps = n <= 1024 ? 8 : kSortWarps;
     p.blocks = 1;
     if (n > kOneBlock) {
         const int64_t b = (n + kPerBlock - 1) / kPerBlock;
@@ -130,9 +131,10 @@ __device__ __forceinline__ int block_exclusive(int v, int* part, int& total) {
     return before + s - v;
 }
 
-template <typename Id, int WARPS>
-__global__ void __launch_bounds__(32 * WARPS)
+template <typename Id>
+__global__ void __launch_bounds__(32 * kSortWarps)
 sort_count_kernel(const Id* __restrict__ ids, int64_t n, int64_t chunk, int E, int* __restrict__ counts) {
+    constexpr int WARPS = kSortWarps;
     extern __shared__ int cnt[];                      // [warp][E + 1]
     const int W = E + 1, warp = threadIdx.x >> 5;
     WarpChoices<Id> mine;
@@ -221,28 +223,27 @@ sort_place_kernel(const Id* __restrict__ ids, int64_t n, int64_t chunk, int E, c
 }
 
 template <typename Id, int WARPS>
-int run_sort(const SortPlan& pl, int slot, int64_t n, int E, const Id* ids, int* offsets, int* pos, int* src,
-             int* scratch, cudaStream_t s) {
-    constexpr int most = (WARPS + 2) * 1025 * 4;
-    const int W = E + 1;
-    auto count = sort_count_kernel<Id, WARPS>;
+int run_place(const SortPlan& pl, int slot, int64_t n, int E, const Id* ids, const int* counts, int* offsets, int* pos,
+              int* src, cudaStream_t s) {
     auto place = sort_place_kernel<Id, WARPS>;
-    if (set_smem_attr(reinterpret_cast<const void*>(count), most, slot) != cudaSuccess ||
-        set_smem_attr(reinterpret_cast<const void*>(place), most, slot + 1) != cudaSuccess)
-        return kCudaError;
-    const bool many = pl.blocks > 1;
-    if (many) count<<<pl.blocks, 32 * WARPS, WARPS * W * 4, s>>>(ids, n, pl.chunk, E, scratch);
-    place<<<pl.blocks, 32 * WARPS, (WARPS + 2) * W * 4, s>>>(ids, n, pl.chunk, E, many ? scratch : nullptr, offsets, pos,
-                                                              src);
+    if (set_smem_attr(reinterpret_cast<const void*>(place), (WARPS + 2) * 1025 * 4, slot) != cudaSuccess) return kCudaError;
+    place<<<pl.blocks, 32 * WARPS, (WARPS + 2) * (E + 1) * 4, s>>>(ids, n, pl.chunk, E, counts, offsets, pos, src);
     return cudaGetLastError() == cudaSuccess ? kOk : kCudaError;
 }
 
 template <typename Id>
-int pick_sort(int64_t n, int E, const Id* ids, int* offsets, int* pos, int* src, int* scratch, cudaStream_t s) {
+int run_sort(int64_t n, int E, const Id* ids, int* offsets, int* pos, int* src, int* scratch, cudaStream_t s) {
     const SortPlan pl = sort_plan(n);
-    const int slot = sizeof(Id) == 4 ? 82 : 86;
-    if (pl.warps == 8) return run_sort<Id, 8>(pl, slot, n, E, ids, offsets, pos, src, scratch, s);
-    return run_sort<Id, 32>(pl, slot + 2, n, E, ids, offsets, pos, src, scratch, s);
+    const int slot = sizeof(Id) == 4 ? 82 : 85;
+    if (pl.warps == 8) return run_place<Id, 8>(pl, slot, n, E, ids, nullptr, offsets, pos, src, s);
+    if (pl.blocks > 1) {
+        auto count = sort_count_kernel<Id>;
+        if (set_smem_attr(reinterpret_cast<const void*>(count), kSortWarps * 1025 * 4, slot + 1) != cudaSuccess)
+            return kCudaError;
+        count<<<pl.blocks, 32 * kSortWarps, kSortWarps * (E + 1) * 4, s>>>(ids, n, pl.chunk, E, scratch);
+        if (cudaGetLastError() != cudaSuccess) return kCudaError;
+    }
+    return run_place<Id, kSortWarps>(pl, slot + 2, n, E, ids, pl.blocks > 1 ? scratch : nullptr, offsets, pos, src, s);
 }
 
 // ----------------------------------------------------------------- gather
@@ -539,8 +540,8 @@ int launch_expert_sort(int64_t tokens, int topk, int E, const void* ids, int id_
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
     const int64_t n = tokens * topk;
     if (id_bytes == 4)
-        return pick_sort(n, E, static_cast<const int32_t*>(ids), offsets, pos, src, static_cast<int*>(scratch), s);
-    return pick_sort(n, E, static_cast<const long long*>(ids), offsets, pos, src, static_cast<int*>(scratch), s);
+        return run_sort(n, E, static_cast<const int32_t*>(ids), offsets, pos, src, static_cast<int*>(scratch), s);
+    return run_sort(n, E, static_cast<const long long*>(ids), offsets, pos, src, static_cast<int*>(scratch), s);
 }
 
 int launch_expert_gather(int64_t tokens, int topk, int64_t H, int eb, const void* X, int64_t ldx,
