@@ -28,7 +28,7 @@ namespace {
 //
 // Counting sort with ranks from warp votes.  A warp takes 32 consecutive
 // choices at a time; the lanes that hold the same expert find each other with
-// a match vote, the lowest adds their number to the warp's own counter of that
+// votes, the lowest adds their number to the warp's own counter of that
 // expert, so no counter is shared and the order is the input's.  Counters:
 // [warp][E + 1] in shared memory (the last for dropped choices), turned into
 // each warp's first row by a sum over the warps before it, the blocks before
@@ -36,31 +36,35 @@ namespace {
 // kKeep x 32 of its choices in registers between counting and placing.
 //
 // Bound by latency, not by its 12 bytes a choice.  Up to kOneBlock choices one
-// block does it all in one launch.  More of them are cut among up to
-// kMaxBlocks blocks: a first launch writes each block's counts, the second
-// places.
+// block does it all in one launch.  More of them are cut among several blocks: a
+// first launch writes each block's counts, the second places.  Every block of it
+// reads all counts, so that many experts ask for fewer blocks (kMaxCounts).
+// Blocks of 8 warps, or of 32 where that leaves a warp more than kKeep x 32
+// choices.  Measured, us (8 warps / 32): 1024 choices 4.1 / 5.1, 4096 of 128
+// experts 10.3 / 12.3, 65536 14.6 / 16.4; 524288 of 256 38.9 / 22.6.
 
 constexpr int kKeep = 8;
-constexpr int kSortWarps = 32;          // 8 for up to 1024 choices
-constexpr int kOneBlock = 8192;
+constexpr int kOneBlock = 2048;
 constexpr int kPerBlock = 1024;
 constexpr int kMaxBlocks = 148;
+constexpr int kMaxCounts = 40960;
 
 struct SortPlan {
-    int warps;                // per block
-    int blocks;
+    int blocks, warps;
     int64_t chunk;            // choices per block
 };
 
-SortPlan sort_plan(int64_t n) {
+SortPlan sort_plan(int64_t n, int E) {
     SortPlan p;
-    p.warps = n <= 1024 ? 8 : kSortWarps;
     p.blocks = 1;
     if (n > kOneBlock) {
-        const int64_t b = (n + kPerBlock - 1) / kPerBlock;
+        int64_t b = (n + kPerBlock - 1) / kPerBlock;
+        const int most = kMaxCounts / (E + 1);
+        if (b > most) b = most;
         p.blocks = static_cast<int>(b < kMaxBlocks ? b : kMaxBlocks);
     }
     p.chunk = ((n + p.blocks - 1) / p.blocks + 31) / 32 * 32;
+    p.warps = p.chunk <= 8 * 32 * kKeep ? 8 : 32;
     return p;
 }
 
@@ -69,9 +73,23 @@ template <typename Id>
 struct WarpChoices {
     const Id* ids;
     int64_t w0, w1;
-    int E, lane;
+    int E, lane, bits;
     int e[kKeep];
+    uint32_t same[kKeep];     // the lanes that hold the same expert, from count on
 
+    // Lanes whose x (0..E, or -1: none) equals this lane's: one vote a bit.  The
+    // match instruction does it at once, but an SM takes one about every 64
+    // clocks: with it 8192 choices in one block took 22 us.
+    __device__ __forceinline__ uint32_t alike(int x) const {
+        uint32_t m = __ballot_sync(0xffffffffu, x >= 0);
+#pragma unroll 4
+        for (int b = 0; b < bits; ++b) {
+            const bool on = (x >> b) & 1;
+            const uint32_t v = __ballot_sync(0xffffffffu, on);
+            m &= on ? v : ~v;
+        }
+        return m;
+    }
     // expert of this lane's choice from i on: E if dropped, -1 past the end
     __device__ __forceinline__ int fetch(int64_t i) const {
         if (i + lane >= w1) return -1;
@@ -82,6 +100,7 @@ struct WarpChoices {
         ids = p;
         E = experts;
         lane = threadIdx.x & 31;
+        bits = 32 - __clz(experts);                   // of the numbers 0..E
         const int64_t b0 = blockIdx.x * chunk, b1 = min(n, b0 + chunk);
         const int64_t per = (chunk / 32 + warps - 1) / warps * 32;
         w0 = min(b1, b0 + static_cast<int64_t>(threadIdx.x >> 5) * per);
@@ -89,20 +108,34 @@ struct WarpChoices {
 #pragma unroll
         for (int k = 0; k < kKeep; ++k) e[k] = fetch(w0 + 32 * k);
     }
-    // f(expert or -1, index of lane 0's choice) for every 32 choices, in order
+    // the number of each expert's choices, added to cnt
+    __device__ __forceinline__ void count(int* cnt) {
+        auto add = [&](int x, uint32_t m) {
+            if (x >= 0 && lane == __ffs(m) - 1) cnt[x] += __popc(m);
+            __syncwarp();
+        };
+#pragma unroll
+        for (int k = 0; k < kKeep; ++k)
+            if (w0 + 32 * k < w1) {
+                same[k] = alike(e[k]);
+                add(e[k], same[k]);
+            }
+        for (int64_t i = w0 + 32 * kKeep; i < w1; i += 32) {
+            const int x = fetch(i);
+            add(x, alike(x));
+        }
+    }
+    // after count: f(expert or -1, lanes that hold it, index of lane 0's choice)
+    // for every 32 choices, in order
     template <typename F>
     __device__ __forceinline__ void each(F f) const {
 #pragma unroll
         for (int k = 0; k < kKeep; ++k)
-            if (w0 + 32 * k < w1) f(e[k], w0 + 32 * k);
-        for (int64_t i = w0 + 32 * kKeep; i < w1; i += 32) f(fetch(i), i);
-    }
-    __device__ __forceinline__ void count(int* cnt) const {
-        each([&](int x, int64_t) {
-            const uint32_t same = __match_any_sync(0xffffffffu, x);
-            if (x >= 0 && lane == __ffs(same) - 1) cnt[x] += __popc(same);
-            __syncwarp();
-        });
+            if (w0 + 32 * k < w1) f(e[k], same[k], w0 + 32 * k);
+        for (int64_t i = w0 + 32 * kKeep; i < w1; i += 32) {
+            const int x = fetch(i);
+            f(x, alike(x), i);
+        }
     }
 };
 
@@ -131,17 +164,16 @@ __device__ __forceinline__ int block_exclusive(int v, int* part, int& total) {
     return before + s - v;
 }
 
-template <typename Id>
-__global__ void __launch_bounds__(32 * kSortWarps)
+template <typename Id, int WARPS>
+__global__ void __launch_bounds__(32 * WARPS)
 sort_count_kernel(const Id* __restrict__ ids, int64_t n, int64_t chunk, int E, int* __restrict__ counts) {
-    constexpr int WARPS = kSortWarps;
     extern __shared__ int cnt[];                      // [warp][E + 1]
-    const int W = E + 1, warp = threadIdx.x >> 5;
+    const int W = E + 1;
     WarpChoices<Id> mine;
     mine.start(ids, n, chunk, WARPS, E);
     for (int i = threadIdx.x; i < WARPS * W; i += 32 * WARPS) cnt[i] = 0;
     __syncthreads();
-    mine.count(cnt + warp * W);
+    mine.count(cnt + (threadIdx.x >> 5) * W);
     __syncthreads();
     for (int e = threadIdx.x; e < W; e += 32 * WARPS) {
         int s = 0;
@@ -159,25 +191,37 @@ sort_place_kernel(const Id* __restrict__ ids, int64_t n, int64_t chunk, int E, c
     constexpr int THREADS = 32 * WARPS;
     extern __shared__ int cnt[];                      // [warp][E + 1], then all [E + 1], before [E + 1]
     __shared__ int part[WARPS];
-    const int W = E + 1, warp = threadIdx.x >> 5;
+    const int W = E + 1;
     int* all = cnt + WARPS * W;
     int* before = all + W;
+    int* first = cnt + (threadIdx.x >> 5) * W;
     WarpChoices<Id> mine;
     mine.start(ids, n, chunk, WARPS, E);
     for (int i = threadIdx.x; i < (WARPS + 2) * W; i += THREADS) cnt[i] = 0;
     __syncthreads();
-    mine.count(cnt + warp * W);
+    mine.count(first);
     if (counts) {
         // each expert's count in all blocks and in the blocks before this one:
-        // the threads take (block, expert) pairs in memory order
+        // the threads take (block, expert) pairs in memory order, eight loads
+        // under way at a time
         const int total = gridDim.x * W, own = blockIdx.x * W;
-#pragma unroll 4
-        for (int i = threadIdx.x; i < total; i += THREADS) {
-            const int c = __ldcg(counts + i);
-            if (c) {
-                const int e = i % W;
-                atomicAdd(all + e, c);                // integers: any order gives the same sum
-                if (i < own) atomicAdd(before + e, c);
+        int e = threadIdx.x % W;
+        const int step = THREADS % W;
+        for (int i0 = threadIdx.x; i0 < total; i0 += 8 * THREADS) {
+            int c[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const int i = i0 + j * THREADS;
+                c[j] = i < total ? __ldg(counts + i) : 0;
+            }
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                if (c[j]) {
+                    atomicAdd(all + e, c[j]);         // integers: any order gives the same sum
+                    if (i0 + j * THREADS < own) atomicAdd(before + e, c[j]);
+                }
+                e += step;
+                if (e >= W) e -= W;
             }
         }
     }
@@ -186,13 +230,15 @@ sort_place_kernel(const Id* __restrict__ ids, int64_t n, int64_t chunk, int E, c
     int run = 0;
     for (int e0 = 0; e0 < W; e0 += THREADS) {
         const int e = e0 + threadIdx.x;
-        int c[WARPS], sum = 0;
+        int sum = 0;
+        if (e < W) {
+            if (counts) {
+                sum = all[e];
+            } else {
 #pragma unroll
-        for (int w = 0; w < WARPS; ++w) {
-            c[w] = e < W ? cnt[w * W + e] : 0;
-            sum += c[w];
+                for (int w = 0; w < WARPS; ++w) sum += cnt[w * W + e];
+            }
         }
-        if (counts) sum = e < W ? all[e] : 0;
         int total;
         int at = run + block_exclusive<WARPS>(sum, part, total);
         run += total;
@@ -200,20 +246,24 @@ sort_place_kernel(const Id* __restrict__ ids, int64_t n, int64_t chunk, int E, c
             if (blockIdx.x == 0) offsets[e] = at;     // W entries: offsets[E] starts the dropped
             at += before[e];
 #pragma unroll
-            for (int w = 0; w < WARPS; ++w) {
-                cnt[w * W + e] = at;
-                at += c[w];
+            for (int w0 = 0; w0 < WARPS; w0 += 8) {
+                int c[8];
+#pragma unroll
+                for (int w = 0; w < 8; ++w) c[w] = cnt[(w0 + w) * W + e];
+#pragma unroll
+                for (int w = 0; w < 8; ++w) {
+                    cnt[(w0 + w) * W + e] = at;
+                    at += c[w];
+                }
             }
         }
     }
     __syncthreads();
-    int* first = cnt + warp * W;
-    mine.each([&](int x, int64_t i) {
-        const uint32_t same = __match_any_sync(0xffffffffu, x);
-        const int rank = __popc(same & ((1u << mine.lane) - 1));
+    mine.each([&](int x, uint32_t m, int64_t i) {
+        const int rank = __popc(m & ((1u << mine.lane) - 1));
         const int r = x >= 0 ? first[x] + rank : 0;
         __syncwarp();
-        if (x >= 0 && rank == 0) first[x] += __popc(same);
+        if (x >= 0 && rank == 0) first[x] += __popc(m);
         __syncwarp();
         if (x >= 0) {
             pos[i + mine.lane] = r;
@@ -223,27 +273,29 @@ sort_place_kernel(const Id* __restrict__ ids, int64_t n, int64_t chunk, int E, c
 }
 
 template <typename Id, int WARPS>
-int run_place(const SortPlan& pl, int slot, int64_t n, int E, const Id* ids, const int* counts, int* offsets, int* pos,
-              int* src, cudaStream_t s) {
+int run_sort(const SortPlan& pl, int slot, int64_t n, int E, const Id* ids, int* offsets, int* pos, int* src,
+             int* scratch, cudaStream_t s) {
+    const int W = E + 1;
+    auto count = sort_count_kernel<Id, WARPS>;
     auto place = sort_place_kernel<Id, WARPS>;
-    if (set_smem_attr(reinterpret_cast<const void*>(place), (WARPS + 2) * 1025 * 4, slot) != cudaSuccess) return kCudaError;
-    place<<<pl.blocks, 32 * WARPS, (WARPS + 2) * (E + 1) * 4, s>>>(ids, n, pl.chunk, E, counts, offsets, pos, src);
+    if (set_smem_attr(reinterpret_cast<const void*>(count), WARPS * 1025 * 4, slot) != cudaSuccess ||
+        set_smem_attr(reinterpret_cast<const void*>(place), (WARPS + 2) * 1025 * 4, slot + 1) != cudaSuccess)
+        return kCudaError;
+    if (pl.blocks > 1) {
+        count<<<pl.blocks, 32 * WARPS, WARPS * W * 4, s>>>(ids, n, pl.chunk, E, scratch);
+        if (cudaGetLastError() != cudaSuccess) return kCudaError;
+    }
+    place<<<pl.blocks, 32 * WARPS, (WARPS + 2) * W * 4, s>>>(ids, n, pl.chunk, E, pl.blocks > 1 ? scratch : nullptr,
+                                                              offsets, pos, src);
     return cudaGetLastError() == cudaSuccess ? kOk : kCudaError;
 }
 
 template <typename Id>
-int run_sort(int64_t n, int E, const Id* ids, int* offsets, int* pos, int* src, int* scratch, cudaStream_t s) {
-    const SortPlan pl = sort_plan(n);
-    const int slot = sizeof(Id) == 4 ? 82 : 85;
-    if (pl.warps == 8) return run_place<Id, 8>(pl, slot, n, E, ids, nullptr, offsets, pos, src, s);
-    if (pl.blocks > 1) {
-        auto count = sort_count_kernel<Id>;
-        if (set_smem_attr(reinterpret_cast<const void*>(count), kSortWarps * 1025 * 4, slot + 1) != cudaSuccess)
-            return kCudaError;
-        count<<<pl.blocks, 32 * kSortWarps, kSortWarps * (E + 1) * 4, s>>>(ids, n, pl.chunk, E, scratch);
-        if (cudaGetLastError() != cudaSuccess) return kCudaError;
-    }
-    return run_place<Id, kSortWarps>(pl, slot + 2, n, E, ids, pl.blocks > 1 ? scratch : nullptr, offsets, pos, src, s);
+int pick_sort(int64_t n, int E, const Id* ids, int* offsets, int* pos, int* src, int* scratch, cudaStream_t s) {
+    const SortPlan pl = sort_plan(n, E);
+    const int slot = sizeof(Id) == 4 ? 82 : 86;
+    return pl.warps == 8 ? run_sort<Id, 8>(pl, slot, n, E, ids, offsets, pos, src, scratch, s)
+                         : run_sort<Id, 32>(pl, slot + 2, n, E, ids, offsets, pos, src, scratch, s);
 }
 
 // ----------------------------------------------------------------- gather
@@ -530,7 +582,7 @@ bool grid_ok(int64_t blocks) { return blocks <= 0x7fffffffll; }
 }  // namespace
 
 int64_t expert_sort_scratch(int64_t n, int E) {
-    const SortPlan p = sort_plan(n);
+    const SortPlan p = sort_plan(n, E);
     return p.blocks > 1 ? static_cast<int64_t>(p.blocks) * (E + 1) * 4 : 0;
 }
 
@@ -540,8 +592,8 @@ int launch_expert_sort(int64_t tokens, int topk, int E, const void* ids, int id_
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
     const int64_t n = tokens * topk;
     if (id_bytes == 4)
-        return run_sort(n, E, static_cast<const int32_t*>(ids), offsets, pos, src, static_cast<int*>(scratch), s);
-    return run_sort(n, E, static_cast<const long long*>(ids), offsets, pos, src, static_cast<int*>(scratch), s);
+        return pick_sort(n, E, static_cast<const int32_t*>(ids), offsets, pos, src, static_cast<int*>(scratch), s);
+    return pick_sort(n, E, static_cast<const long long*>(ids), offsets, pos, src, static_cast<int*>(scratch), s);
 }
 
 int launch_expert_gather(int64_t tokens, int topk, int64_t H, int eb, const void* X, int64_t ldx,

@@ -69,7 +69,7 @@ int* device_status_ptr();
 //   64-67  gemm_tc.cu        CTA-pair bf16/f16 with the operands swapped (M <= 128)
 //   68     gemm_tc.cu        CTA-pair TF32
 //   70-81  gemm_group.cu     experts' products and 8-bit products
-//   82-87  expert.cu         sort by expert
+//   82-89  expert.cu         sort by expert
 //   90-97  gemm_skinny_i8.cu
 constexpr int kMaxSlots = 128;
 cudaError_t set_smem_attr(const void* func, int bytes, int slot);
