@@ -614,3 +614,28 @@ def test_empty_products(tg):
         C = tg.gemm_w8a8(ints8((M, 16), 1), positive((M,), 1), ints8((16, 0 if M else 8), 2), positive((0 if M else 8,), 2))
         assert tuple(C.shape) == (M, 0 if M else 8)
     _status(tg)
+
+
+@pytest.mark.parametrize("handle", [False, True])
+def test_outputs_for_another_stream_use_its_memory(tg, handle):
+    """A call on another stream does not write into memory that the current
+    stream has freed but is still to use."""
+    s = torch.cuda.Stream()
+    A, B, o = normal((256, 64), torch.bfloat16, 1), normal((1, 64, 512), torch.bfloat16, 2), offsets_of([256])
+    q, w = ints8((256, 64), 3), ints8((64, 512), 4)
+    rs, cs = positive((256,), 5), positive((512,), 6)
+    calls = [lambda st: tg.gemm_grouped(A, o, B, stream=st), lambda st: tg.gemm_w8a8(q, rs, w, cs, stream=st),
+             lambda st: tg.gemm_grouped_w8a8(q, rs, o, w[None], cs[None], stream=st),
+             lambda st: tg.gemm_grouped_wgrad(A, A, o, stream=st), lambda st: tg.quant_i8(A, stream=st)[0]]
+    for call in calls:
+        want = call(None).clone()
+        torch.cuda.synchronize()
+        late = torch.empty_like(want)
+        torch.cuda._sleep(20_000_000)
+        late.fill_(7)                                     # pending on the current stream
+        del late                                          # its block is free for the current stream
+        got = call(s.cuda_stream if handle else s)
+        torch.cuda.synchronize()
+        assert torch.equal(got, want)
+        del got, want
+    _status(tg)

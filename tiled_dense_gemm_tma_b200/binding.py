@@ -509,10 +509,23 @@ def _vector(t, n, dtype, name):
         raise ValueError(f"{name} must be a contiguous vector of {n}")
 
 
-def _out(C, M, N, dtype, device):
-    """(C, its row pitch), C made where it is None."""
+def _memory_of(stream, device):
+    """Allocate for `stream`, not the current one: a block that is free on the
+    current stream may still be in use there when another one writes it."""
+    import torch
+    if isinstance(stream, int):
+        stream = (torch.cuda.ExternalStream(stream, device) if stream
+                  else torch.cuda.default_stream(device))
+    return torch.cuda.stream(stream)
+
+
+def _out(C, M, N, dtype, device, stream):
+    """(C, its row pitch), C made for `stream` where it is None."""
     if C is None:
-        return _rows_out(M, N, dtype, device)
+        if stream is None:
+            return _rows_out(M, N, dtype, device)
+        with _memory_of(stream, device):
+            return _rows_out(M, N, dtype, device)
     if C.shape != (M, N) or C.dtype != dtype:
         raise ValueError("C has the wrong shape or dtype")
     return C, _pitch(C, "C")
@@ -530,13 +543,17 @@ def quant_i8(X, Q=None, scales=None, stream=None):
     M, K = X.shape
     device = X.device
     if Q is None:
-        Q, ldq = _rows_out(M, K, torch.int8, device)
+        Q, ldq = _out(None, M, K, torch.int8, device, stream)
     elif Q.shape != (M, K) or Q.dtype != torch.int8:
         raise ValueError("Q has the wrong shape or dtype")
     else:
         ldq = _pitch(Q, "Q")
     if scales is None:
-        scales = torch.empty(M, dtype=torch.float32, device=device)
+        if stream is None:
+            scales = torch.empty(M, dtype=torch.float32, device=device)
+        else:
+            with _memory_of(stream, device):
+                scales = torch.empty(M, dtype=torch.float32, device=device)
     else:
         _vector(scales, M, torch.float32, "scales")
     _one_device(device, (Q, scales), "Q, scales")
@@ -569,7 +586,7 @@ def gemm_w8a8(A, row_scales, B, col_scales, C=None, out_dtype=None, relu=False, 
         out_dtype = torch.bfloat16 if C is None else C.dtype
     kind = _type16(out_dtype, "C")
     device = A.device
-    C, ldc = _out(C, M, N, out_dtype, device)
+    C, ldc = _out(C, M, N, out_dtype, device, stream)
     _one_device(device, (B, row_scales, col_scales, C), "B, row_scales, col_scales, C")
     _launch("tg_gemm_w8a8", device, stream, M, N, K, A.data_ptr(), _pitch(A, "A"),
             row_scales.data_ptr(), B.data_ptr(), _pitch(B, "B"), int(trans_b),
@@ -777,7 +794,7 @@ def gemm_grouped(A, groups, B, C=None, relu=False, stream=None, trans_b=False):
     if K != K2:
         raise ValueError(f"inner dimensions differ: {K} vs {K2}")
     device = A.device
-    C, ldc = _out(C, M, N, A.dtype, device)
+    C, ldc = _out(C, M, N, A.dtype, device, stream)
     _one_device(device, (B, offsets, C), "B, offsets, C")
     name = "tg_gemm_grouped_bf16" if kind == TYPE_BF16 else "tg_gemm_grouped_f16"
     _launch(name, device, stream, M, N, K, E, A.data_ptr(), _pitch(A, "A"), offsets.data_ptr(),
@@ -802,7 +819,8 @@ def gemm_grouped_wgrad(A, G, groups, C=None, stream=None):
     if C is None:
         per = 16 // A.element_size()
         ld = max(per, -(-N // per) * per)
-        C = torch.empty((E, K, ld), dtype=A.dtype, device=A.device)[:, :, :N]
+        with contextlib.nullcontext() if stream is None else _memory_of(stream, A.device):
+            C = torch.empty((E, K, ld), dtype=A.dtype, device=A.device)[:, :, :N]
     elif C.shape != (E, K, N) or C.dtype != A.dtype:
         raise ValueError("C has the wrong shape or dtype")
     _one_device(A.device, (G, offsets, C), "G, offsets, C")
@@ -837,7 +855,7 @@ def gemm_grouped_w8a8(A, row_scales, groups, B, col_scales, C=None, out_dtype=No
         out_dtype = torch.bfloat16 if C is None else C.dtype
     kind = _type16(out_dtype, "C")
     device = A.device
-    C, ldc = _out(C, M, N, out_dtype, device)
+    C, ldc = _out(C, M, N, out_dtype, device, stream)
     _one_device(device, (B, row_scales, col_scales, offsets, C), "B, row_scales, col_scales, offsets, C")
     _launch("tg_gemm_grouped_w8a8", device, stream, M, N, K, E, A.data_ptr(), _pitch(A, "A"),
             row_scales.data_ptr(), offsets.data_ptr(), B.data_ptr(), _pitch(B, "B"), _plane(B),
