@@ -467,14 +467,17 @@ def _launch(name, device, stream, *args):
 
 
 def _rows_out(M, N, dtype, device):
-    """(a new M x N tensor, its row pitch): as empty_out, without the view
-    where the rows fill whole 16-byte units."""
+    """(a new M x N tensor, its row pitch), the pitch a multiple of 16 bytes.
+    empty_strided is the cheapest of torch's allocations on the host."""
     import torch
     per = 16 // dtype.itemsize
-    if N % per == 0 and N:
-        return torch.empty((M, N), dtype=dtype, device=device), N
     ld = max(per, -(-N // per) * per)
-    return torch.empty((M, ld), dtype=dtype, device=device)[:, :N], ld
+    return torch.empty_strided((M, N), (ld, 1), dtype=dtype, device=device), ld
+
+
+def _vector_out(n, dtype, device):
+    import torch
+    return torch.empty_strided((n,), (1,), dtype=dtype, device=device)
 
 
 def _pitch(t, name):
@@ -550,10 +553,10 @@ def quant_i8(X, Q=None, scales=None, stream=None):
         ldq = _pitch(Q, "Q")
     if scales is None:
         if stream is None:
-            scales = torch.empty(M, dtype=torch.float32, device=device)
+            scales = _vector_out(M, torch.float32, device)
         else:
             with _memory_of(stream, device):
-                scales = torch.empty(M, dtype=torch.float32, device=device)
+                scales = _vector_out(M, torch.float32, device)
     else:
         _vector(scales, M, torch.float32, "scales")
     _one_device(device, (Q, scales), "Q, scales")
@@ -678,7 +681,7 @@ def expert_sort(ids, num_experts):
     at_pos = -(-E1 // 4) * 4
     at_src = at_pos + -(-n // 4) * 4
     at_scratch = at_src + -(-n // 4) * 4
-    buf = torch.empty(at_scratch + need // 4, dtype=torch.int32, device=device)
+    buf = _vector_out(at_scratch + need // 4, torch.int32, device)
     base = buf.data_ptr()
     _launch("tg_expert_sort", device, None, T, k, num_experts, ids.data_ptr(), ids.element_size(),
             base, base + 4 * at_pos, base + 4 * at_src, base + 4 * at_scratch if need else None)
@@ -702,7 +705,7 @@ def _gather(X, plan, scales=None):
     ss = None
     if scales is not None:
         _vector(scales, T, torch.float32, "scales")
-        ss = torch.empty(T * k, dtype=torch.float32, device=device)
+        ss = _vector_out(T * k, torch.float32, device)
         _one_device(device, (scales,), "scales")
     _one_device(device, (pos,), "the plan")
     _launch("tg_expert_gather", device, None, T, k, H, X.element_size(), X.data_ptr(),
@@ -745,7 +748,7 @@ def _combine_grad(Y, weights, g, plan):
     H, device = Y.shape[1], Y.device
     weights = weights.contiguous()
     dY, ldd = _rows_out(T * k, H, Y.dtype, device)
-    dw = torch.empty((T, k), dtype=torch.float32, device=device)
+    dw = torch.empty_strided((T, k), (k, 1), dtype=torch.float32, device=device)
     _one_device(device, (g,), "the gradient")
     _launch("tg_expert_combine_grad", device, None, T, k, H, _type16(Y.dtype, "Y"), Y.data_ptr(),
             _pitch(Y, "Y"), g.data_ptr(), _pitch(g, "the gradient"), pos.data_ptr(), plan._kept(),
@@ -820,7 +823,7 @@ def gemm_grouped_wgrad(A, G, groups, C=None, stream=None):
         per = 16 // A.element_size()
         ld = max(per, -(-N // per) * per)
         with contextlib.nullcontext() if stream is None else _memory_of(stream, A.device):
-            C = torch.empty((E, K, ld), dtype=A.dtype, device=A.device)[:, :, :N]
+            C = torch.empty_strided((E, K, N), (K * ld, ld, 1), dtype=A.dtype, device=A.device)
     elif C.shape != (E, K, N) or C.dtype != A.dtype:
         raise ValueError("C has the wrong shape or dtype")
     _one_device(A.device, (G, offsets, C), "G, offsets, C")
@@ -893,7 +896,8 @@ def _pitched_copy3(W):
     import torch
     per = 16 // W.element_size()
     E, K, N = W.shape
-    copy = torch.empty((E, K, -(-N // per) * per), dtype=W.dtype, device=W.device)[:, :, :N]
+    ld = -(-N // per) * per
+    copy = torch.empty_strided((E, K, N), (K * ld, ld, 1), dtype=W.dtype, device=W.device)
     return copy.copy_(W)
 
 
@@ -996,11 +1000,9 @@ def _expert_functions():
                 # (A, K) and (g, N) change places for weights stored N x K
                 x, ldx, k, y, ldy, n = (g, ldg, N, A, lda, K) if tr else (A, lda, K, g, ldg, N)
                 ld = -(-n // 8) * 8
-                dW = torch.empty((E, k, ld), dtype=dtype, device=device)
+                dW = torch.empty_strided((E, k, n), (k * ld, ld, 1), dtype=dtype, device=device)
                 _launch("tg_gemm_grouped_wgrad_" + kind, device, None, M, n, k, E, x.data_ptr(),
                         ldx, y.data_ptr(), ldy, offsets.data_ptr(), dW.data_ptr(), ld, k * ld)
-                if ld != n:
-                    dW = dW[:, :, :n]
                 if tr:
                     dW = dW.transpose(1, 2)
             return dA, dW, None
