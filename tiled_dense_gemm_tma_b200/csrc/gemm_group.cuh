@@ -97,7 +97,7 @@ struct GrpCfg {
     static constexpr int STG_BUF = WG_ ? 4096 : 2048;   // a warp's [32 rows][128 bytes] or [32 rows][32 columns]
     static constexpr int NBUF = WG_ ? 8 / EPI_ : 1;     // staging tiles a warp
     static constexpr int TMEM_COLS = 512;               // two accumulators of 256 columns
-    static constexpr int TABLE = WG_ ? 0 : (2 * (kMaxGroups + 2)) * 4;
+    static constexpr int TABLE = WG_ ? 0 : (4 * (kMaxGroups + 2)) * 4;
     static constexpr int SMEM_DATA = STAGES * (A_STAGE + B_STAGE) + EPI_WARPS * NBUF * STG_BUF;
     static constexpr int SMEM_BYTES = SMEM_DATA + 512 + TABLE + 1024;
     static_assert(SMEM_BYTES <= 227 * 1024, "shared memory per CTA");
@@ -276,6 +276,8 @@ grp_gemm_kernel(const __grid_constant__ CUtensorMap tmA,
     int* gcount = const_cast<int*>(abort_flag) + 1;
     int* gstart = gcount + 1;                   // product: first item of each group that has rows
     int* gexp = gstart + kMaxGroups + 2;        // product: which group that is
+    int* grow = gexp + kMaxGroups + 2;          // product: its first row
+    int* gend = grow + kMaxGroups + 2;          // product: the row after its last
 
     const int warp = threadIdx.x >> 5;
     const int lane = threadIdx.x & 31;
@@ -317,17 +319,26 @@ grp_gemm_kernel(const __grid_constant__ CUtensorMap tmA,
     }
     if constexpr (!Cfg::WG) {
         if (warp == 2) {
-            // the groups that have rows and their first items, the rows behind
-            // the last group as one more
-            int base = 0, n = 0;
+            // the groups that have rows, their rows and first items, the rows behind
+            // the last group as one more.  A group starts at the largest offset so
+            // far (its own, where they do not decrease): whatever the offsets hold,
+            // no row belongs to two groups, and the items are no more than the host
+            // counted.
+            int base = 0, n = 0, reached = 0;
             for (int e0 = 0; e0 <= p.E; e0 += 32) {
                 const int e = e0 + lane;
-                int cnt = 0;
-                if (e <= p.E) {
-                    int r0, r1;
-                    grp_rows(p.offsets, e, p.E, p.M, r0, r1);
-                    if (r1 > r0) cnt = grp_tiles(r1 - r0) * ntl;
+                int r0 = p.M, r1 = p.M, cnt = 0;
+                if (e <= p.E) grp_rows(p.offsets, e, p.E, p.M, r0, r1);
+                int low = max(r0, reached);
+#pragma unroll
+                for (int d = 1; d < 32; d <<= 1) {
+                    const int y = __shfl_up_sync(0xffffffffu, low, d);
+                    if (lane >= d) low = max(low, y);
                 }
+                reached = __shfl_sync(0xffffffffu, low, 31);
+                r0 = low;
+                r1 = max(r1, r0);
+                if (r1 > r0) cnt = grp_tiles(r1 - r0) * ntl;
                 int sum = cnt;
 #pragma unroll
                 for (int d = 1; d < 32; d <<= 1) {
@@ -339,6 +350,8 @@ grp_gemm_kernel(const __grid_constant__ CUtensorMap tmA,
                     const int i = n + __popc(live & ((1u << lane) - 1));
                     gstart[i] = base + sum - cnt;
                     gexp[i] = e;
+                    grow[i] = r0;
+                    gend[i] = r1;
                 }
                 n += __popc(live);
                 base += __shfl_sync(0xffffffffu, sum, 31);
@@ -381,8 +394,8 @@ grp_gemm_kernel(const __grid_constant__ CUtensorMap tmA,
         } else {
             while (w >= gstart[g + 1]) ++g;
             it.e = gexp[g];
-            int r1;
-            grp_rows(p.offsets, it.e, p.E, p.M, it.r0, r1);
+            const int r1 = gend[g];
+            it.r0 = grow[g];
             it.rows = r1 - it.r0;
             int tl, tt, at;
             tile_coords(w - gstart[g], ntl, grp_tiles(it.rows), p.group_m, tl, tt);
