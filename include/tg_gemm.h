@@ -316,7 +316,8 @@ TG_API tg_status tg_gemm_w8a8(int64_t M, int64_t N, int64_t K,
  *   limits as tg_gemm_w8a8: row_scales M floats, col_scales N floats per
  *   group, plane_s floats apart.  lda, ldb and plane_b % 16 == 0.
  *
- * All run on CTA pairs; a refused cluster launch returns TG_ERR_UNSUPPORTED.
+ * All run on CTA pairs; a refused cluster launch returns TG_ERR_UNSUPPORTED, as
+ * does a size above 2^31 - 1025 (here and for tg_gemm_w8a8).
  * They use no workspace.  plane_b of 0 is TG_ERR_INVALID_ARG unless E is 1.
  */
 TG_API tg_status tg_gemm_grouped_f16(int64_t M, int64_t N, int64_t K, int E,

@@ -60,7 +60,8 @@ REFUSED = [
         (dict(C=None), INVALID), (dict(rs=None), INVALID), (dict(cs=None), INVALID), (dict(lda=16), INVALID),
         (dict(ldb=0), INVALID), (dict(trans=1, ldb=16), INVALID), (dict(ldc=8), INVALID), (dict(A=P + 8), ALIGN),
         (dict(lda=40), ALIGN), (dict(ldc=20), ALIGN), (dict(rs=P + 1), ALIGN), (dict(K=131072, lda=131072), UNSUP),
-        (dict(M=BIG), UNSUP), (dict(ldb=1 << 40), UNSUP), (dict(M=0), OK), (dict(N=0), OK)]),
+        (dict(M=BIG), UNSUP), (dict(M=BIG - 1024), UNSUP), (dict(ldb=1 << 40), UNSUP), (dict(M=0), OK),
+        (dict(N=0), OK)]),
     ("tg_gemm_grouped_bf16", GRP, GRP_OK, [
         (dict(M=-1), INVALID), (dict(E=0), INVALID), (dict(E=1025), UNSUP), (dict(off=None), INVALID),
         (dict(off=P + 2), ALIGN), (dict(plane=0), INVALID), (dict(plane=-8), INVALID), (dict(plane=516), ALIGN),

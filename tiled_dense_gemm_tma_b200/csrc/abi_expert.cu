@@ -12,6 +12,7 @@
 namespace {
 
 constexpr int64_t kMaxDim = (1ll << 31) - 1;      // kernel indices and TMA coords are int32
+constexpr int64_t kMaxTiled = kMaxDim - 1024;     // a tile past the last row stays inside 32 bits
 constexpr int64_t kMaxK8 = 131071;                // 128 * 128 * K stays inside 32 bits
 constexpr int kMaxExperts = 1024;                 // the kernels' tables in shared memory
 
@@ -82,7 +83,7 @@ tg_status check_product(int64_t M, int64_t N, int64_t K, int E, const void* A, i
     tg_status s = worst({check_matrix(C, ldc, N, 2), K > 0 ? check_matrix(A, lda, K, eb) : TG_OK,
                          K > 0 ? check_matrix(B, ldb, trans_b ? K : N, eb) : TG_OK,
                          K > 0 ? check_plane(plane_b, E, eb) : TG_OK,
-                         (M > kMaxDim || N > kMaxDim || K > kMaxDim || E > kMaxExperts) ? TG_ERR_UNSUPPORTED : TG_OK,
+                         (M > kMaxTiled || N > kMaxTiled || K > kMaxTiled || E > kMaxExperts) ? TG_ERR_UNSUPPORTED : TG_OK,
                          (eb == 1 && K > kMaxK8) ? TG_ERR_UNSUPPORTED : TG_OK});
     if (s != TG_OK) return s;
     if (K == 0) return zero_rows(C, ldc, M, N, stream);
@@ -108,9 +109,8 @@ tg_status wgrad16(int64_t M, int64_t N, int64_t K, int E, const void* A, int64_t
     const bool overlap = E > 1 && plane_c < static_cast<__int128>(K - 1) * ldc + N;
     tg_status s = worst({check_matrix(C, ldc, N, 2), M > 0 ? check_matrix(A, lda, K, 2) : TG_OK,
                          M > 0 ? check_matrix(G, ldg, N, 2) : TG_OK, check_plane(plane_c, E, 2),
-                         M > 0 ? float_ptr(offsets) : TG_OK,
-                         (M > kMaxDim || N > kMaxDim || K > kMaxDim || E > kMaxExperts) ? TG_ERR_UNSUPPORTED : TG_OK});
-    if (s == TG_OK && overlap) s = TG_ERR_INVALID_ARG;
+                         M > 0 ? float_ptr(offsets) : TG_OK, overlap ? TG_ERR_INVALID_ARG : TG_OK,
+                         (M > kMaxTiled || N > kMaxTiled || K > kMaxTiled || E > kMaxExperts) ? TG_ERR_UNSUPPORTED : TG_OK});
     if (s != TG_OK) return s;
     if (M == 0) {
         for (int e = 0; e < E && s == TG_OK; ++e)

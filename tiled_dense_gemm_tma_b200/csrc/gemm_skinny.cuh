@@ -41,7 +41,9 @@
 // * Signed 8-bit weights and activations (kind::i8): a 128-byte row holds 128
 //   columns or 128 k, a unit is 256 k, every sum and partial is a 32-bit
 //   integer (exact in any order), and each output is scaled once by its row's
-//   and its column's scale.  They never take stream-K: no workspace.
+//   and its column's scale.  They never take stream-K: no workspace.  Bound by
+//   the weight stream: 1 x 8192 x 8192 16.4 us cold, 4.1 TB/s on 128 CTAs (the
+//   CTA-pair kernel of gemm_group.cuh, 32 pairs there: 23.4).
 #pragma once
 #include "ptx.cuh"
 #include "dequant.cuh"
