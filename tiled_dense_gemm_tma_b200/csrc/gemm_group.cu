@@ -97,8 +97,10 @@ int run_grad(const GroupArgs& a, CUtensorMapDataType dt, int slot) {
     const long long per = ((g.K - 1) / 256 + 1) * ((g.N - 1) / 256 + 1);
     if (per > 0x7fffffffll / a.E) return kUnsupported;
     CUtensorMap tA, tB[4], tC;
-    if (!tensor_map_2d(&tA, g.A, dt, 2, g.K, g.M, g.lda * 2, 64, 64, SWZ_128) ||
-        !tensor_map_2d(&tB[0], g.B, dt, 2, g.N, g.M, g.ldb * 2, 64, 64, SWZ_128) ||
+    // rows of A and G as M overlapping windows of 64 rows (the same pitch twice):
+    // no copy takes more of a window than its group has rows, so none reads past M
+    if (!tensor_map_3d(&tA, g.A, dt, g.K, 64, g.lda * 2, g.M, g.lda * 2, 64, 64, SWZ_128) ||
+        !tensor_map_3d(&tB[0], g.B, dt, g.N, 64, g.ldb * 2, g.M, g.ldb * 2, 64, 64, SWZ_128) ||
         !tensor_map_3d(&tC, g.C, dt, g.N, g.K, g.ldc * 2, a.E,
                        static_cast<uint64_t>(a.E > 1 ? a.plane : g.ldc) * 2, 64, 32, SWZ_128))
         return kCudaError;

@@ -33,14 +33,17 @@
 //
 // Weight gradient: the 256 lanes are the columns k of A, the MMA's N side
 // the columns n of G, the reduction runs over the group's rows.  Both
-// operands are read MN-major (a shared-memory row is one row r).  The rows
-// of the last 64-row block that lie past the group belong to the next group:
-// MMA steps (16 rows) that hold none of the group's are skipped, and where
-// the group ends inside a step, a fix-up warp clears the step's other rows
-// in shared memory, in both operands (0 * NaN is NaN), before the MMA reads
-// them.  Such a block's loads complete on a barrier of their own, and the
-// fix-up warps' arrivals replace the producers' on the full barrier.  A group
-// of no rows gets zeros.
+// operands are read MN-major (a shared-memory row is one row r).  What lies
+// past the group belongs to the next one and must not enter the sums, nor
+// meet a zero there (0 * NaN is NaN).  The tensor maps cut it off: their
+// third coordinate is a row of the matrix, their second counts the 64 rows
+// from that one on (both strides are the row pitch), and a box that starts
+// 64 - q rows before such a window holds 64 - q rows of the zeros that TMA
+// fills in outside it and the window's first q rows.  A group's last block is
+// that box, zeros first, in both operands; the MMA steps (16 rows) of zeros
+// alone are skipped.  So every byte that an MMA reads came by a copy that
+// completed on the barrier which the MMA's issuer waits on, in either CTA of
+// the pair.  A group of no rows gets zeros.
 //
 // Every CTA derives the tile list from the offsets itself: no host knows the
 // group sizes, and no launch precedes this one.
@@ -96,10 +99,9 @@ struct GrpCfg {
     static constexpr int EPI_WARPS = EPI_;
     static constexpr int HALVES = EPI_ / 4;             // warps to a quarter of the lanes
     static_assert(EPI_ == 4 || EPI_ == 8, "epilogue warps");
-    static constexpr int FIX_WARPS = WG_ ? 1 : 0;
     static constexpr int PRODUCERS = 2;                 // warp 0, and the first behind the epilogue
     static_assert(STAGES % PRODUCERS == 0, "a producer keeps its own ring slots");
-    static constexpr int THREADS = 32 * (1 + PRODUCERS + EPI_WARPS + FIX_WARPS);
+    static constexpr int THREADS = 32 * (1 + PRODUCERS + EPI_WARPS);
     static constexpr int STG_BUF = WG_ ? 4096 : 2048;   // a warp's [32 rows][128 bytes] or [32 rows][32 columns]
     static constexpr int NBUF = WG_ ? 8 / EPI_ : 1;     // staging tiles a warp
     static constexpr int TMEM_COLS = 512;               // two accumulators of 256 columns
@@ -253,9 +255,9 @@ __device__ __forceinline__ void grp_store_grad(const CUtensorMap* tmC, const Grp
     }
 }
 
-// tmA: the 256-lane operand (product: weights, 3-D; WG: A).  tmB .. tmB16:
-// the N-side operand (product: rows of A in boxes of 128, 64, 32 and 16 rows;
-// WG: G in tmB).  tmC: C (WG only).
+// tmA: the 256-lane operand (product: weights, 3-D; WG: A's windows of 64
+// rows).  tmB .. tmB16: the N-side operand (product: rows of A in boxes of
+// 128, 64, 32 and 16 rows; WG: G's windows in tmB).  tmC: C (WG only).
 template <class Cfg>
 __global__ void __launch_bounds__(Cfg::THREADS, 1)
 grp_gemm_kernel(const __grid_constant__ CUtensorMap tmA,
@@ -273,8 +275,7 @@ grp_gemm_kernel(const __grid_constant__ CUtensorMap tmA,
     uint8_t* smStg = smB + Cfg::STAGES * Cfg::B_STAGE;
     uint64_t* full = reinterpret_cast<uint64_t*>(smStg + Cfg::EPI_WARPS * Cfg::NBUF * Cfg::STG_BUF);
     uint64_t* empty = full + Cfg::STAGES;
-    uint64_t* cut = empty + Cfg::STAGES;        // WG: a block that ends inside an MMA step has landed
-    uint64_t* tfull = cut + Cfg::STAGES;
+    uint64_t* tfull = empty + Cfg::STAGES;
     uint64_t* tempty = tfull + 2;
     uint64_t* drain = tempty + 2;
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
@@ -300,7 +301,6 @@ grp_gemm_kernel(const __grid_constant__ CUtensorMap tmA,
         for (int s = 0; s < Cfg::STAGES; ++s) {
             mbar_init(&full[s], 2);
             mbar_init(&empty[s], 1);
-            mbar_init(&cut[s], 1);
         }
         for (int a = 0; a < 2; ++a) { mbar_init(&tfull[a], 1); mbar_init(&tempty[a], 2 * Cfg::EPI_WARPS); }
         mbar_init(drain, 1);
@@ -419,10 +419,6 @@ grp_gemm_kernel(const __grid_constant__ CUtensorMap tmA,
         }
         return it;
     };
-    // WG: rows of the group in its last block, and whether they end inside an
-    // MMA step
-    auto last_rows = [&](const GrpItem& it) { return it.rows - (it.kb - 1) * Cfg::BK; };
-    auto is_cut = [&](const GrpItem& it) { return it.kb > 0 && last_rows(it) % Cfg::MMA_K != 0; };
 
     if (warp == 0 || warp == 2 + Cfg::EPI_WARPS) {
         // ----------------------------------------------- TMA producers (both)
@@ -451,30 +447,24 @@ grp_gemm_kernel(const __grid_constant__ CUtensorMap tmA,
                 constexpr bool A_MN = Cfg::WG || Cfg::W_MN;
                 const uint32_t a_bytes = A_MN ? a_live * (Cfg::BK * 128) : (a_live ? Cfg::A_STAGE : 0);
                 const uint32_t b_bytes = Cfg::WG ? b_live * (Cfg::BK * 128) : hn * 128;
-                const bool cut_last = Cfg::WG && is_cut(it);
                 for (int kb = 0; kb < it.kb; ++kb, ++ld) {
                     if (ld % Cfg::PRODUCERS != turn) continue;
                     const uint32_t s = ld % Cfg::STAGES;
                     const uint32_t ph = (ld / Cfg::STAGES) & 1;
                     if (!bounded_wait(&empty[s], ph ^ 1, abort_flag, limit, p.status)) { ok = false; break; }
                     if (p.inject == 1 && ld == 0 && pair == 0 && rank == 0) continue;   // debug
-                    // a block that needs the fix-up completes on this CTA's own barrier
-                    const bool fix = cut_last && kb == it.kb - 1;
-                    const uint32_t fbar = fix ? mapa_shared(smem_u32(&cut[s]), rank)
-                                              : mapa_shared(smem_u32(&full[s]), 0);
+                    const uint32_t fbar = mapa_shared(smem_u32(&full[s]), 0);
                     mbar_arrive_expect_tx_cluster(fbar, a_bytes + b_bytes);
-                    if (!fix) {
-                        armed |= 1u << s;
-                        armed_par = (armed_par & ~(1u << s)) | (ph << s);
-                    }
+                    armed |= 1u << s;
+                    armed_par = (armed_par & ~(1u << s)) | (ph << s);
                     uint8_t* a_dst = smA + s * Cfg::A_STAGE;
                     uint8_t* b_dst = smB + s * Cfg::B_STAGE;
                     if constexpr (Cfg::WG) {
-                        const int r = it.r0 + kb * Cfg::BK;
+                        const int r = it.r0 + kb * Cfg::BK, from = -grp_zero_rows(it.rows, kb, Cfg::BK);
                         for (int j = 0; j < a_live; ++j)
-                            tma_load_2d_pair(a_dst + j * (Cfg::BK * 128), &tmA, fbar, n0 + Cfg::CHUNK * j, r);
+                            tma_load_3d_pair(a_dst + j * (Cfg::BK * 128), &tmA, fbar, n0 + Cfg::CHUNK * j, from, r);
                         for (int j = 0; j < b_live; ++j)
-                            tma_load_2d_pair(b_dst + j * (Cfg::BK * 128), &tmB, fbar, b0 + Cfg::CHUNK * j, r);
+                            tma_load_3d_pair(b_dst + j * (Cfg::BK * 128), &tmB, fbar, b0 + Cfg::CHUNK * j, from, r);
                     } else {
                         if constexpr (Cfg::W_MN) {
                             for (int j = 0; j < a_live; ++j)
@@ -499,8 +489,8 @@ grp_gemm_kernel(const __grid_constant__ CUtensorMap tmA,
                             volatile int never = 0;
                             bounded_wait(&full[s], (armed_par >> s) & 1, &never, limit, p.status);
                         }
-                // copies that complete on barriers this thread cannot wait on (the
-                // leader's; a block under fix-up): a fixed 1 ms to land
+                // the peer's copies complete on the leader's barriers, which it
+                // cannot wait on: a fixed 1 ms to land
                 const uint64_t t0 = globaltimer_ns();
                 while (globaltimer_ns() - t0 < 1000000ull) __nanosleep(10000);
             }
@@ -525,21 +515,17 @@ grp_gemm_kernel(const __grid_constant__ CUtensorMap tmA,
                 tc_fence_after();
                 const uint32_t d_tmem = tmem_base + acc * 256;
                 const uint32_t idesc = idesc0 | (static_cast<uint32_t>(it.width >> 3) << 17);
-                const bool cut_last = Cfg::WG && is_cut(it);
                 for (int kb = 0; kb < it.kb; ++kb, ++ld) {
                     const uint32_t s = ld % Cfg::STAGES;
                     const uint32_t ph = (ld / Cfg::STAGES) & 1;
-                    const bool fix = cut_last && kb == it.kb - 1;
-                    if (fix ? !bounded_wait_cluster(&full[s], ph, abort_flag, limit, p.status)
-                            : !bounded_wait(&full[s], ph, abort_flag, limit, p.status)) { ok = false; break; }
+                    if (!bounded_wait(&full[s], ph, abort_flag, limit, p.status)) { ok = false; break; }
                     tc_fence_after();
                     const uint32_t a_addr = smem_u32(smA + s * Cfg::A_STAGE);
                     const uint32_t b_addr = smem_u32(smB + s * Cfg::B_STAGE);
-                    const int steps = Cfg::WG && kb == it.kb - 1
-                        ? (last_rows(it) + Cfg::MMA_K - 1) / Cfg::MMA_K : Cfg::STEPS;
+                    const int step0 = Cfg::WG ? grp_zero_rows(it.rows, kb, Cfg::BK) / Cfg::MMA_K : 0;
 #pragma unroll
                     for (int k = 0; k < Cfg::STEPS; ++k) {
-                        if (Cfg::WG && k >= steps) break;
+                        if (Cfg::WG && k < step0) continue;
                         // K-major: 32 bytes of k along the 128-byte rows; MN-major:
                         // MMA_K rows of 128 bytes, 128-byte wide chunks LBO apart
                         const uint64_t ad = A_MN
@@ -548,8 +534,8 @@ grp_gemm_kernel(const __grid_constant__ CUtensorMap tmA,
                         const uint64_t bd = Cfg::WG
                             ? sw128_desc(b_addr + k * Cfg::MMA_K * 128, Cfg::BK * 128, 1024)
                             : sw128_desc(b_addr + k * 32, 16, 1024);
-                        if constexpr (Cfg::I8) mma_i8_pair(d_tmem, ad, bd, idesc, kb != 0 || k != 0);
-                        else mma_f16_pair(d_tmem, ad, bd, idesc, kb != 0 || k != 0);
+                        if constexpr (Cfg::I8) mma_i8_pair(d_tmem, ad, bd, idesc, kb != 0 || k != step0);
+                        else mma_f16_pair(d_tmem, ad, bd, idesc, kb != 0 || k != step0);
                     }
                     const uint32_t e_loc = smem_u32(&empty[s]);
                     mma_commit_pair(mapa_shared(e_loc, 0));      // both CTAs' slots
@@ -565,7 +551,7 @@ grp_gemm_kernel(const __grid_constant__ CUtensorMap tmA,
             bounded_wait(drain, 0, &never, limit, p.status);
         }
         __syncwarp();
-    } else if (warp >= 2 && warp < 2 + Cfg::EPI_WARPS) {
+    } else {
         // --------------------------------------------------- epilogue (both)
         const int q = warp & 3;
         const int half = (warp - 2) >> 2;
@@ -594,41 +580,6 @@ grp_gemm_kernel(const __grid_constant__ CUtensorMap tmA,
         if constexpr (Cfg::WG) {
             if (lane == 0) bulk_wait<0>();
             __syncwarp();
-        }
-    } else {
-        // ------------------------------------------------- fix-up (WG, both)
-        if constexpr (Cfg::WG) {
-            uint32_t ld = 0, seen = 0;                  // seen: parity of each slot's cut barrier
-            int g = 0;
-            for (int w = pair; w < num_items; w += npairs) {
-                const GrpItem it = item(w, g);
-                ld += it.kb;
-                if (!is_cut(it)) continue;
-                const uint32_t s = (ld - 1) % Cfg::STAGES;
-                if (!bounded_wait(&cut[s], (seen >> s) & 1, abort_flag, limit, p.status)) break;
-                seen ^= 1u << s;
-                // rows [first, end of its MMA step) of both operands, both
-                // 64-column chunks: a row is 128 bytes of each chunk
-                const int first = last_rows(it);
-                const int count = (first + Cfg::MMA_K - 1) / Cfg::MMA_K * Cfg::MMA_K - first;
-                uint8_t* a = smA + s * Cfg::A_STAGE + first * 128;
-                uint8_t* b = smB + s * Cfg::B_STAGE + first * 128;
-                for (int i = lane; i < count * 8; i += 32) {
-                    const uint4 z = make_uint4(0, 0, 0, 0);
-                    *reinterpret_cast<uint4*>(a + i * 16) = z;
-                    *reinterpret_cast<uint4*>(a + Cfg::BK * 128 + i * 16) = z;
-                    *reinterpret_cast<uint4*>(b + i * 16) = z;
-                    *reinterpret_cast<uint4*>(b + Cfg::BK * 128 + i * 16) = z;
-                }
-                // Each lane's zeros reach the async proxy, whose reads of this CTA's
-                // shared memory (by its own SM's tensor core) the arrival lets
-                // start, as the converters' do in gemm_w4a16_pair.cu.  An arrival
-                // with release at cluster scope waits some 1500 clocks here, three
-                // blocks of MMAs: groups of 1000 and 1048 rows lost 13 % to it.
-                fence_proxy_async_smem();
-                __syncwarp();
-                if (lane == 0) mbar_arrive_cluster(mapa_shared(smem_u32(&full[s]), 0));
-            }
         }
     }
 
