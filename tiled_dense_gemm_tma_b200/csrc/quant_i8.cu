@@ -16,6 +16,9 @@
 // unless r lies within 2^-16 of halfway (127 * 2^-24 is less than 2^-17).
 // Those few values, and rows whose 127 / top could overflow, take the
 // division, which is off by 2^-24 of the quotient and keeps exact halves exact.
+// For bfloat16 it divides x * 127 * 2^-8 by top * 2^-8, since x * 127 alone
+// would leave fp32 where x is above 2^128 / 127; both are exact down to the
+// smallest subnormal (multiples of 2^-141, of at most 18 bits).
 //
 // Bound by HBM, 2 bytes in and 1 out per value, and close behind by the issue
 // of its instructions (72 % of the slots): 16384 rows of 8192 bf16 values take
@@ -34,6 +37,8 @@ namespace tg {
 namespace {
 
 constexpr int kVec = 4;                 // 16-byte vectors a thread keeps
+template <bool BF16>
+constexpr float kDown = BF16 ? 0x1p-8f : 1.f;       // keeps x * 127 finite in the division
 
 template <bool BF16>
 __device__ __forceinline__ float2 widen(uint32_t w) {
@@ -64,7 +69,7 @@ __device__ __forceinline__ uint64_t sub2(uint64_t a, uint64_t b) {
     return d;
 }
 
-// Eight values -> eight integers.  The division is asked for pair by pair: in
+// Eight values -> eight integers; top is the row's times kDown.  The division is asked for pair by pair: in
 // a row of bfloat16 about one value in 600 is the half of its largest (63.5),
 // so that 35 % of a warp's 256 values held one, and dividing all eight of each
 // lane was a third of the kernel's instructions.
@@ -82,8 +87,8 @@ __device__ __forceinline__ uint2 round8(const uint4& v, float inv, float top, bo
         float2 s = unpair(s2);
         const float2 d = unpair(fma2(x2, inv2, sub2(magic, s2)));       // r - rint(r)
         if (divide || fmaxf(fabsf(d.x), fabsf(d.y)) > 0.5f - 0x1p-16f) {
-            s.x = __fdiv_rn(x.x * 127.f, top) + kMagic;
-            s.y = __fdiv_rn(x.y * 127.f, top) + kMagic;
+            s.x = __fdiv_rn(x.x * (127.f * kDown<BF16>), top) + kMagic;
+            s.y = __fdiv_rn(x.y * (127.f * kDown<BF16>), top) + kMagic;
         }
         t[j] = __byte_perm(__float_as_uint(s.x), __float_as_uint(s.y), 0x0040);
     }
@@ -154,9 +159,9 @@ quant_i8_kernel(int M, int K, const uint16_t* __restrict__ X, long long ldx, int
     uint2* q = reinterpret_cast<uint2*>(q8) + t;
     const bool zero = bad || top == 0;
     const bool divide = ftop < 0x1p-100f;
-    const float inv = divide ? 0.f : __fdiv_rn(127.f, ftop);
+    const float inv = divide ? 0.f : __fdiv_rn(127.f, ftop), low = ftop * kDown<BF16>;
     auto store = [&](int i, const uint4& v) {
-        q[static_cast<int64_t>(i) * TPR] = zero ? make_uint2(0, 0) : round8<BF16>(v, inv, ftop, divide);
+        q[static_cast<int64_t>(i) * TPR] = zero ? make_uint2(0, 0) : round8<BF16>(v, inv, low, divide);
     };
     if constexpr (FITS) {
 #pragma unroll
@@ -166,7 +171,7 @@ quant_i8_kernel(int M, int K, const uint16_t* __restrict__ X, long long ldx, int
         for (int i = 0; i < mine; ++i) store(i, __ldg(x + static_cast<int64_t>(i) * TPR));
     }
     if (tail) {
-        const uint2 o = zero ? make_uint2(0, 0) : round8<BF16>(rest, inv, ftop, divide);
+        const uint2 o = zero ? make_uint2(0, 0) : round8<BF16>(rest, inv, low, divide);
 #pragma unroll
         for (int j = 0; j < 7; ++j)
             if (j < tail) q8[8ll * nv + j] = static_cast<int8_t>((j < 4 ? o.x >> (8 * j) : o.y >> (8 * (j - 4))) & 0xff);
