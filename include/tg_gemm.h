@@ -15,7 +15,8 @@
  * output post-processing of the blog.hotdry.top TileLang guide (landing
  * checklist, item 2).  C is overwritten (no alpha/beta, no accumulation).
  * Products are accumulated in fp32; the result is rounded once to C's type
- * with round-to-nearest-even after epi is applied.
+ * with round-to-nearest-even after epi is applied.  The ReLU of a NaN is 0
+ * (the larger of the two numbers), but for the 8-bit products, which keep it.
  *
  * Conventions shared by all entry points
  * --------------------------------------
@@ -263,7 +264,7 @@ TG_API tg_status tg_gemm_sp24_bf16(int64_t M, int64_t N, int64_t K,
  *
  * Q is exactly what the formula gives in real arithmetic.  A row of zeros gets scale 0 and
  * Q = 0; a row that holds an infinity or a NaN gets scale NaN and Q = 0, so
- * that its products are NaN.
+ * that its products are NaN, with TG_EPI_RELU too.
  *   X: M x K values of `type` (TG_TYPE_F16 or TG_TYPE_BF16), row pitch ldx
  *      (elements, % 8 == 0);  Q: M x K, row pitch ldq (% 16 == 0);  scales: M
  *      floats, 4-byte aligned.  K == 0 writes scales of 0.
@@ -276,7 +277,7 @@ TG_API tg_status tg_gemm_sp24_bf16(int64_t M, int64_t N, int64_t K,
  * The sum is an exact 32-bit integer (K above 131071, where 128 * 128 * K
  * could leave its range -> TG_ERR_UNSUPPORTED); it is rounded to fp32 and
  * multiplied by row_scales[m], then by col_scales[n], in fp32, and rounded once to C's
- * type after epi.
+ * type after epi.  A NaN stays a NaN, also under TG_EPI_RELU.
  */
 enum { TG_TYPE_F16 = 0, TG_TYPE_BF16 = 1 };
 

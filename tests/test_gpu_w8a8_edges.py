@@ -1,8 +1,9 @@
-"""Edges of the 8-bit linear layers on a B200: rows of very large values."""
+"""Edges of the 8-bit linear layers on a B200: rows of very large values, rows
+that hold a NaN or an infinity under ReLU."""
 import pytest
 import torch
 
-from expert_util import close, pitched
+from expert_util import DTYPES, close, ints8, normal, offsets_of, pitched, positive, product8
 
 pytestmark = pytest.mark.gpu
 
@@ -62,3 +63,49 @@ def test_quant_of_the_largest_halves(tg):
     q, s = tg.quant_i8(X)
     _status(tg)
     assert q[0].tolist() == [127, 64, -64, -127, 0, 32, 0, 0]     # 31.75 -> 32
+
+
+# ------------------------------------------------------------ NaN under ReLU
+
+@pytest.mark.parametrize("relu", [False, True])
+@pytest.mark.parametrize("trans", [False, True])
+@pytest.mark.parametrize("M,N", [(3, 40), (16, 9000), (100, 264), (200, 264), (100, 20000)])
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+def test_rows_with_a_nan_stay_nan(tg, M, N, trans, relu, dtype):
+    """A row that holds an infinity or a NaN makes its products NaN, also under
+    ReLU, on both kernels; its neighbours are as without it."""
+    dt = DTYPES[dtype]
+    K = 96
+    X = normal((M, K), dt, 1)
+    X[1, 5], X[M - 1, 95] = float("inf"), float("nan")
+    W = ints8((N, K) if trans else (K, N), 2)
+    ws = positive((N,), 3, 1e-3, 2e-3)
+    q, s = tg.quant_i8(X)
+    C = tg.gemm_w8a8(q, s, W, ws, out_dtype=dt, relu=relu, trans_b=trans)
+    _status(tg)
+    bad = torch.zeros(M, dtype=torch.bool, device="cuda")
+    bad[1] = bad[M - 1] = True
+    assert bool(torch.isnan(C[bad]).all())
+    ref, bound = product8(q[~bad], s[~bad], W.t() if trans else W, ws, dt)
+    close(C[~bad], ref.clamp(min=0) if relu else ref, bound)
+
+
+@pytest.mark.parametrize("trans", [False, True])
+def test_rows_with_a_nan_stay_nan_in_groups(tg, trans):
+    counts, K, N = [40, 0, 300, 7], 80, 136
+    R = sum(counts) + 5
+    A, B = ints8((R, K), 1), ints8((4, N, K) if trans else (4, K, N), 2)
+    rs, cs = positive((R,), 3, 1e-3, 2e-3), positive((4, N), 4, 1e-3, 2e-3)
+    rs[[0, 39, 41, 346, 350]] = float("nan")                  # row 350 lies behind the last group
+    C = tg.gemm_grouped_w8a8(A, rs, offsets_of(counts), B, cs, relu=True, trans_b=trans)
+    _status(tg)
+    nan = torch.isnan(C)
+    assert bool(nan[[0, 39, 41, 346]].all()) and int(nan.any(1).sum()) == 4
+    assert not C[347:].any()
+    at = 0
+    for e, n in enumerate(counts):
+        part = torch.arange(at, at + n, device="cuda")
+        part = part[~torch.isnan(rs[part])]
+        ref, bound = product8(A[part], rs[part], B[e].t() if trans else B[e], cs[e], torch.bfloat16)
+        close(C[part], ref.clamp(min=0), bound)
+        at += n

@@ -570,7 +570,7 @@ def gemm_w8a8(A, row_scales, B, col_scales, C=None, out_dtype=None, relu=False, 
     """C = epi((A @ W) * row_scales[:, None] * col_scales) for int8 A (M x K)
     and W: B is K x N, or N x K with trans_b.  The scales are float32 vectors
     of M and N.  C is float16 or bfloat16 (out_dtype, by default C's or
-    bfloat16)."""
+    bfloat16).  A NaN (of a row's scale) stays one, also with relu."""
     import torch
     if A.dtype != torch.int8 or B.dtype != torch.int8:
         raise TypeError("A and B must be int8")

@@ -139,10 +139,15 @@ __device__ __forceinline__ void grp_store_rows(const GrpParams& p, const GrpItem
         }
     }
     auto finish = [&](uint32_t v, float rs, float c) -> float {
-        float x;
-        if constexpr (Cfg::I8) x = (__int2float_rn(static_cast<int>(v)) * rs) * c;
-        else x = __uint_as_float(v);
-        return p.relu ? fmaxf(x, 0.f) : x;
+        if constexpr (Cfg::I8) {
+            // a NaN (of the row's scale) stays one under ReLU; fmaxf would hide it,
+            // and a comparison takes 2048 x 8192 x 1024 from 22.6 to 23.8 us
+            const float x = (__int2float_rn(static_cast<int>(v)) * rs) * c;
+            return p.relu ? max_nan(x, 0.f) : x;
+        } else {
+            const float x = __uint_as_float(v);
+            return p.relu ? fmaxf(x, 0.f) : x;
+        }
     };
     auto pack = [&](float a, float b) -> uint32_t {
         if constexpr (Cfg::OUT == OutT::BF16) {
