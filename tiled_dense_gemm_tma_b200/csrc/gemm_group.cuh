@@ -569,7 +569,9 @@ grp_gemm_kernel(const __grid_constant__ CUtensorMap tmA,
             const uint32_t aph = (tl >> 1) & 1;
             if (it.kb) {
                 ++tl;
-                if (!bounded_wait(&tfull[acc], aph, abort_flag, limit, p.status)) break;
+                // the only wait that lasts a whole tile, however long its sum: 4 us
+                // more for each block, of which 8 columns of 2^24 k take 0.3 us each
+                if (!bounded_wait(&tfull[acc], aph, abort_flag, limit + it.kb * 4096ull, p.status)) break;
                 tc_fence_after();
             }
             const uint32_t taddr = tmem_base + acc * 256 + (static_cast<uint32_t>(q * 32) << 16);
