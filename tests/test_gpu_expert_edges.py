@@ -8,7 +8,7 @@ import textwrap
 import pytest
 import torch
 
-from expert_util import DTYPES, close, normal, offsets_of, product16
+from expert_util import DTYPES, close, normal, offsets_of, pitched, positive, product16
 
 pytestmark = pytest.mark.gpu
 ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
@@ -121,3 +121,71 @@ def test_a_tile_may_take_longer_than_the_wait_limit(tg, what):
     status, right, ms = [l for l in r.stdout.splitlines() if l.startswith("RESULT")][0].split()[1:]
     assert (status, right) == ("0", "True"), (status, right, ms)
     assert float(ms) > 20                                     # or the case shows nothing
+
+
+# ------------------------------------------------------ widths of any alignment
+
+@pytest.mark.parametrize("D,F,shift", [(11, 11, 0), (8, 11, 0), (11, 8, 0), (7, 16, 0), (8, 16, 3)])
+@pytest.mark.parametrize("stored", ["plain", "transposed"])
+def test_layer_of_any_width(tg, D, F, shift, stored):
+    """Ordinary contiguous tensors whose rows do not start on 16-byte
+    boundaries, or (shift) views that start off one, through a whole layer and
+    its gradients.  All values are -1, 0 or 1, the router's weights 1, D F <= 128
+    and at most 22 rows: no stage's result exceeds 256, to which bfloat16 holds
+    every integer, so each equals the 64-bit one."""
+    E, T, k = 3, 11, 2
+    g = torch.Generator().manual_seed(1)
+
+    def small(*shape):
+        flat = torch.zeros(torch.Size(shape).numel() + shift, dtype=torch.bfloat16, device="cuda")
+        flat[shift:] = torch.randint(-1, 2, (flat.numel() - shift,), generator=g).to(torch.bfloat16).cuda()
+        return flat[shift:].view(shape)
+
+    x, W1, W2, gy = small(T, D), small(E, D, F), small(E, F, D), small(T, D)
+    if stored == "transposed":
+        W1, W2 = small(E, F, D), small(E, D, F)
+    ids = torch.randint(0, E + 1, (T, k), generator=g).cuda()                 # E: dropped
+    leaves = [t.requires_grad_(True) for t in (x, W1, W2, torch.ones((T, k), device="cuda"))]
+
+    def view(w):
+        return w.transpose(1, 2) if stored == "transposed" else w
+
+    plan = tg.expert_sort(ids, E)
+    h = torch.relu(tg.expert_matmul(tg.expert_gather(x, plan), view(W1), plan))
+    y = tg.expert_combine(tg.expert_matmul(h.contiguous(), view(W2), plan), plan, leaves[3])
+    got = torch.autograd.grad(y, leaves, gy)
+    _status(tg)
+    d = [t.detach().double().requires_grad_(True) for t in leaves]
+    hot = torch.nn.functional.one_hot(ids, E + 1)[..., :E].double()           # T x k x E
+    per = torch.einsum("td,edf->tef", d[0], view(d[1]))
+    per = torch.einsum("tef,efd->ted", torch.relu(per), view(d[2]))
+    out = torch.einsum("tke,tk,ted->td", hot, d[3], per)
+    want = torch.autograd.grad(out, d, gy.double())
+    for a, b in zip([y.detach(), *got], [out.detach(), *want]):
+        assert torch.equal(a.double(), b)
+
+
+def test_moves_of_any_width(tg):
+    """Gather and combine on dense rows of odd widths and on views that start
+    off a 16-byte boundary, 16-bit and int8, against the aligned call."""
+    ids = torch.tensor([[0, 2], [1, -1], [2, 0], [7, 2], [0, 1]], device="cuda")
+    plan = tg.expert_sort(ids, 3)
+    for W in (1, 9, 16, 515):
+        X = normal((5, W), torch.bfloat16, 1)
+        Y = normal((10, W), torch.float16, 2)
+        q, s = torch.randint(-128, 128, (5, W), dtype=torch.int8, device="cuda"), positive((5,), 3)
+        qp = pitched((5, W), torch.int8)
+        qp.copy_(q)
+        w = positive((5, 2), 4)
+
+        def off(t):                                           # the same rows one element off
+            return torch.cat([t[:, :1], t], 1)[:, 1:]
+
+        for f in (lambda t: t.contiguous(), off, lambda t: t.t().contiguous().t()):
+            assert torch.equal(tg.expert_gather(f(X), plan), tg.expert_gather(X, plan))
+            assert torch.equal(tg.expert_combine(f(Y), plan, w), tg.expert_combine(Y, plan, w))
+            a, b = tg.expert_gather(f(q), plan, scales=s), tg.expert_gather(qp, plan, scales=s)
+            assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+        one = X[:1].expand(5, W)
+        assert torch.equal(tg.expert_gather(one, plan), tg.expert_gather(one.contiguous(), plan))
+    _status(tg)

@@ -700,6 +700,7 @@ def _gather(X, plan, scales=None):
         raise ValueError("X must have one row per token of the plan")
     if X.dtype not in (torch.float16, torch.bfloat16, torch.int8):
         raise TypeError("X must be float16, bfloat16 or int8")
+    X = _aligned_rows(X)
     H, device = X.shape[1], X.device
     out, ldo = _rows_out(T * k, H, X.dtype, device)
     ss = None
@@ -730,6 +731,7 @@ def _combine(Y, plan, weights):
     if Y.dim() != 2 or Y.shape[0] != T * k:
         raise ValueError("the sorted rows must be one per choice of the plan")
     kind = _type16(Y.dtype, "the sorted rows")
+    Y = _aligned_rows(Y)
     H, device = Y.shape[1], Y.device
     if weights is not None:
         weights = _check_weights(weights, T, k, device)
@@ -756,17 +758,18 @@ def _combine_grad(Y, weights, g, plan):
     return dY, dw
 
 
-def _aligned_rows(g):
-    """A gradient as the kernels take it: itself where it is row-major with a
-    16-byte pitch and base, else a copy (autograd hands out expanded and
-    oddly pitched gradients that the caller has no say in)."""
-    eb = g.element_size()
-    if (g.stride(1) == 1 or g.shape[1] <= 1) and g.data_ptr() % 16 == 0 and \
-            (g.shape[0] <= 1 or (g.stride(0) >= g.shape[1] and (g.stride(0) * eb) % 16 == 0)):
-        return g
-    out, _ = _rows_out(g.shape[0], g.shape[1], g.dtype, g.device)
-    out.copy_(g)
-    return out
+def _aligned_rows(t):
+    """Rows as the kernels take them: t itself where it is row-major with a
+    16-byte pitch and base, else a copy.  Autograd hands out expanded and
+    oddly pitched gradients that the caller has no say in, and an elementwise
+    operation between two of the differentiable operators gives a dense result
+    for a pitched one."""
+    (rows, cols), (down, across) = t.shape, t.stride()
+    if (across == 1 or cols <= 1) and t.data_ptr() % 16 == 0 and \
+            (rows <= 1 or (down >= cols and down * t.element_size() % 16 == 0)):
+        return t
+    out, _ = _rows_out(rows, cols, t.dtype, t.device)
+    return out.copy_(t)
 
 
 def _offsets_of(groups):
@@ -891,6 +894,17 @@ def _stored3(W):
     return _pitched_copy3(W), False
 
 
+def _aligned3(w):
+    """Row-major matrices as the kernels take them: w itself, or a copy where
+    its base, row pitch or plane is no multiple of 16 bytes."""
+    per = 16 // w.element_size()
+    E, rows, _ = w.shape
+    plane, down, _ = w.stride()
+    if w.data_ptr() % 16 or (rows > 1 and down % per) or (E > 1 and plane % per):
+        return _pitched_copy3(w)
+    return w
+
+
 def _pitched_copy3(W):
     """A row-major copy whose row pitch is a multiple of 16 bytes."""
     import torch
@@ -905,10 +919,7 @@ def _product_grads(A, W, offsets, g, needed):
     """The gradients of expert_matmul from operands of any layout."""
     A = _aligned_rows(A)
     w, tr = _stored3(W)
-    per = 16 // w.element_size()
-    if w.data_ptr() % 16 or (w.shape[1] > 1 and w.stride(1) % per) or \
-            (w.shape[0] > 1 and w.stride(0) % per):
-        w = _pitched_copy3(w)
+    w = _aligned3(w)
     dA = gemm_grouped(g, offsets, w, trans_b=not tr) if needed[0] else None
     dW = None
     if needed[1]:
@@ -938,7 +949,7 @@ def _expert_functions():
         def backward(ctx, g):
             once()
             ctx.saved_tensors
-            return _combine(_aligned_rows(g), ctx.plan, None), None
+            return _combine(g, ctx.plan, None), None
 
     class _Combine(torch.autograd.Function):
         """Y[t] = sum_j w[t, j] Ys[pos[t, j]], with both gradients."""
@@ -953,11 +964,10 @@ def _expert_functions():
         @staticmethod
         def backward(ctx, g):
             once()
-            g = _aligned_rows(g)
             Ys, weights, _, _ = ctx.saved_tensors
             if weights is None:
                 return _gather(g, ctx.plan), None, None
-            dY, dw = _combine_grad(_aligned_rows(Ys), weights, g, ctx.plan)
+            dY, dw = _combine_grad(_aligned_rows(Ys), weights, _aligned_rows(g), ctx.plan)
             return (dY if ctx.needs_input_grad[0] else None,
                     dw if ctx.needs_input_grad[1] else None, None)
 
@@ -969,11 +979,13 @@ def _expert_functions():
         def forward(ctx, A, W, offsets):
             ctx.save_for_backward(A, W, offsets)
             w, tr = _stored3(W)
-            C = gemm_grouped(A, offsets, w, trans_b=tr)
+            w = _aligned3(w)
+            a = _aligned_rows(A) if A.dim() == 2 else A
+            C = gemm_grouped(a, offsets, w, trans_b=tr)
             # what backward reads again, as checked for the call above
-            own = w.data_ptr() == W.data_ptr()
+            own = a is A and w.data_ptr() == W.data_ptr()
             ctx.strides = (A.stride(), W.stride()) if own else None
-            ctx.layout = (C.shape[0], C.shape[1], A.shape[1], w.shape[0], _pitch(A, "A"),
+            ctx.layout = (C.shape[0], C.shape[1], A.shape[1], w.shape[0], _pitch(a, "A"),
                           _pitch(w, "W"), _plane(w), tr)
             return C
 
@@ -983,7 +995,7 @@ def _expert_functions():
             A, W, offsets = ctx.saved_tensors
             g = _aligned_rows(g)
             if (A.stride(), W.stride()) != ctx.strides:
-                # weights that were copied, or tensors that a saved-tensor hook gave back
+                # operands that were copied, or tensors that a saved-tensor hook gave back
                 # in another layout than it took
                 return _product_grads(A, W, offsets, g, ctx.needs_input_grad)
             M, N, K, E, lda, ldb, plane, tr = ctx.layout
@@ -1024,7 +1036,9 @@ def expert_gather(X, plan, scales=None):
     """The rows of X (tokens x H) sorted by expert: row plan.pos[t, j] is X[t];
     the rows of dropped choices are zero.  X is float16, bfloat16
     (differentiable) or int8; with scales (int8 rows only: float32, one per
-    token) returns (rows, their scales)."""
+    token) returns (rows, their scales).  Rows that are not row-major or do not
+    start on 16-byte boundaries (a dense X of a width that is no multiple of 8, or
+    16 for int8) are copied to such ones first."""
     if scales is not None:
         import torch
         if X.dtype != torch.int8:
@@ -1037,7 +1051,8 @@ def expert_combine(Ys, plan, weights=None):
     """Sorted rows back to tokens: Y[t] = sum_j weights[t, j] *
     Ys[plan.pos[t, j]] over the kept choices, summed in float32 in the order of
     j.  Ys is float16 or bfloat16, weights float32 (tokens x topk; all 1 where
-    None).  Differentiable in Ys and weights."""
+    None).  Differentiable in Ys and weights.  Rows that do not start on 16-byte
+    boundaries are copied as in expert_gather."""
     return _expert(1).apply(Ys, weights, plan)
 
 
@@ -1047,7 +1062,9 @@ def expert_matmul(Xs, W, groups):
     Xs: M x K sorted rows (float16 or bfloat16); W: E x K x N, or a transposed
     view of E x N x K storage (W.transpose(1, 2)), which needs no copy; groups:
     an ExpertPlan or its offsets.  Rows behind the last group are zero and get
-    zero gradient."""
+    zero gradient.  Operands whose rows do not start on 16-byte boundaries (dense
+    ones of widths that are no multiple of 8; the results here have padded rows)
+    are copied first, in backward again; gemm_grouped refuses them."""
     return _expert(2).apply(Xs, W, _offsets_of(groups))
 
 
