@@ -9,6 +9,7 @@ import pytest
 import torch
 
 from expert_util import DTYPES, close, normal, offsets_of, pitched, positive, product16
+from gpu_util import SENTINEL16, check_guard, guarded_out
 
 pytestmark = pytest.mark.gpu
 ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
@@ -188,4 +189,68 @@ def test_moves_of_any_width(tg):
             assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
         one = X[:1].expand(5, W)
         assert torch.equal(tg.expert_gather(one, plan), tg.expert_gather(one.contiguous(), plan))
+    _status(tg)
+
+
+# ------------------------------------------------- positions outside the rows
+
+@pytest.mark.parametrize("kept", [4, 2, 0, -7, 2147483647])
+@pytest.mark.parametrize("pos", [[[0, 4], [5, -1]], [[-1, 1], [2, 4]], [[3, -3], [0, 6]], [[-2147483648, 2], [2147483647, 3]],
+                                 [[0, 1], [2, 3]]])
+def test_positions_outside_the_rows_write_nothing(tg, pos, kept):
+    """4 rows inside a buffer of sentinels, positions just outside them: nothing
+    but the rows that a position names is written, and these as they should be."""
+    from tiled_dense_gemm_tma_b200 import binding
+    T, k, H, n = 2, 2, 40, 4
+    live = min(max(kept, 0), n)
+    p = torch.tensor(pos, dtype=torch.int32, device="cuda")
+    o = torch.tensor([0, kept], dtype=torch.int32, device="cuda")
+    X, Y, g = normal((T, H), torch.bfloat16, 1), normal((n, H), torch.bfloat16, 2), normal((T, H), torch.bfloat16, 3)
+    w, s = positive((T, k), 4), positive((T,), 5)
+    named = {r: (t, j) for t, row in enumerate(pos) for j, r in enumerate(row) if 0 <= r < n}
+
+    def rows_are(big, C, want):
+        """C's rows as in `want` (row -> values), all else the sentinel."""
+        ref = torch.full_like(big, SENTINEL16, dtype=torch.int16).view(torch.bfloat16)
+        pr, pc = 3, 8
+        for r, v in want.items():
+            ref[pr + r, pc:pc + H] = v
+        assert torch.equal(big.view(torch.int16), ref.view(torch.int16))
+
+    # gather, with scales
+    big, C, _ = guarded_out(n, H, "bf16")
+    ss = torch.full((n + 6,), -5.0, device="cuda")
+    binding._launch("tg_expert_gather", X.device, None, T, k, H, 2, X.data_ptr(), X.stride(0), s.data_ptr(), p.data_ptr(),
+                    o[1:].data_ptr(), C.data_ptr(), C.stride(0), ss[3:].data_ptr())
+    rows_are(big, C, {r: X[t] if r < live else 0 for r, (t, _) in named.items()})
+    want = torch.full_like(ss, -5.0)
+    for r, (t, _) in named.items():
+        want[3 + r] = s[t] if r < live else 0
+    assert torch.equal(ss, want)
+    # combine
+    big, C, _ = guarded_out(T, H, "bf16")
+    binding._launch("tg_expert_combine", X.device, None, T, k, H, 1, Y.data_ptr(), Y.stride(0), p.data_ptr(),
+                    o[1:].data_ptr(), w.data_ptr(), C.data_ptr(), C.stride(0))
+    check_guard(big, "bf16", T, H, (3, 8))
+    counts = [[0 <= r < live for r in row] for row in pos]
+    for t in range(T):
+        terms = [w[t, j].double() * Y[pos[t][j]].double() for j in range(k) if counts[t][j]]
+        ref = sum(terms, torch.zeros(H, dtype=torch.float64, device="cuda"))
+        mags = sum((v.abs() for v in terms), torch.zeros_like(ref))
+        close(C[t], ref, ref.abs() * 2.0 ** -8 * 1.01 + 3 * 2.0 ** -24 * mags + 2.0 ** -134, f"token {t}")
+    # its gradient
+    big, C, _ = guarded_out(n, H, "bf16")
+    dw = torch.full((T * k + 6,), -5.0, device="cuda")
+    binding._launch("tg_expert_combine_grad", X.device, None, T, k, H, 1, Y.data_ptr(), Y.stride(0), g.data_ptr(),
+                    g.stride(0), p.data_ptr(), o[1:].data_ptr(), w.data_ptr(), C.data_ptr(), C.stride(0), dw[3:].data_ptr())
+    rows_are(big, C, {r: (w[t, j] * g[t].float()).to(torch.bfloat16) if r < live else 0 for r, (t, j) in named.items()})
+    assert bool((dw[:3] == -5).all()) and bool((dw[3 + T * k:] == -5).all())
+    for t in range(T):
+        for j in range(k):
+            got = dw[3 + t * k + j].item()
+            if not counts[t][j]:
+                assert got == 0
+                continue
+            prod = Y[pos[t][j]].double() * g[t].double()
+            assert abs(got - prod.sum().item()) <= H * 2.0 ** -24 * prod.abs().sum().item()
     _status(tg)
