@@ -254,3 +254,35 @@ def test_positions_outside_the_rows_write_nothing(tg, pos, kept):
             prod = Y[pos[t][j]].double() * g[t].double()
             assert abs(got - prod.sum().item()) <= H * 2.0 ** -24 * prod.abs().sum().item()
     _status(tg)
+
+
+# ------------------------------------------------------------ the most groups
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("R,E", [(1, 1024), (5, 1000), (700, 1024), (3000, 1024), (2500, 1023)])
+def test_gradients_of_the_most_groups(tg, R, E, dtype):
+    """Every group's own weights and rows enter its results, near the limit of
+    1024 groups; weights of distinct sizes, so that another group's would show."""
+    dt = DTYPES[dtype]
+    counts = [0] * E
+    for i in range(R):
+        counts[(i * 313) % E] += 1
+    X = normal((R, 24), dt, 1).requires_grad_(True)
+    W = normal((E, 24, 16), dt, 2)
+    W *= (torch.arange(E, device="cuda") % 7 + 1)[:, None, None]
+    W.requires_grad_(True)
+    g = normal((R, 16), dt, 3)
+    Y = tg.expert_matmul(X, W, offsets_of(counts))
+    dX, dW = torch.autograd.grad(Y, (X, W), g)
+    _status(tg)
+    row = 0
+    for e, n in enumerate(counts):
+        if not n:
+            assert not dW[e].any()
+            continue
+        part = slice(row, row + n)
+        for got, a, b in ((Y.detach()[part], X.detach()[part], W.detach()[e]), (dX[part], g[part], W.detach()[e].t()),
+                          (dW[e], X.detach()[part].t(), g[part])):
+            close(got, *product16(a, b, dt), f"group {e}")
+        row += n
+    assert row == R
