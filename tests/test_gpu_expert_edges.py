@@ -8,7 +8,7 @@ import textwrap
 import pytest
 import torch
 
-from expert_util import DTYPES, close, normal, offsets_of, pitched, positive, product16
+from expert_util import DTYPES, H, TINY, close, normal, offsets_of, pitched, positive, product16
 from gpu_util import SENTINEL16, check_guard, guarded_out
 
 pytestmark = pytest.mark.gpu
@@ -286,3 +286,30 @@ def test_gradients_of_the_most_groups(tg, R, E, dtype):
             close(got, *product16(a, b, dt), f"group {e}")
         row += n
     assert row == R
+
+
+# -------------------------------------- combine's gradient at its variants' limits
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("T,k,W", [(256, 3, 520), (257, 3, 520), (300, 5, 512), (300, 2, 513), (512, 2, 2056),
+                                   (513, 2, 2056), (600, 4, 2048), (513, 3, 4099), (1500, 7, 1000)])
+def test_combine_gradients_of_many_tokens(tg, T, k, W, dtype):
+    """Either side of where the number of threads a token changes."""
+    dt = DTYPES[dtype]
+    E = 11
+    g0 = torch.Generator().manual_seed(T)
+    ids = torch.randint(0, E + 1, (T, k), generator=g0).cuda()               # E: dropped
+    plan = tg.expert_sort(ids, E)
+    Y = normal((T * k, W), dt, 1).requires_grad_(True)
+    w = normal((T, k), torch.float32, 2).contiguous().requires_grad_(True)
+    g = normal((T, W), dt, 3)
+    dY, dw = torch.autograd.grad(tg.expert_combine(Y, plan, w), (Y, w), g)
+    _status(tg)
+    kept = ids < E
+    pos = plan.pos.long()
+    wk = torch.where(kept, w.detach().double(), 0.0)
+    want = torch.zeros(T * k, W, dtype=torch.float64, device="cuda")
+    want[pos.reshape(-1)] = (wk[:, :, None] * g.double()[:, None, :]).reshape(T * k, W)
+    close(dY, want, want.abs() * (H[dt] * 1.01 + 2.0 ** -24) + TINY[dt], "dY")
+    prod = torch.where(kept[:, :, None], Y.detach().double()[pos], 0) * g.double()[:, None, :]
+    close(dw, prod.sum(2), W * 2.0 ** -24 * prod.abs().sum(2) + 2.0 ** -149, "dw")

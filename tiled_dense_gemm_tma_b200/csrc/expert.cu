@@ -567,11 +567,17 @@ void start_combine_grad(unsigned tokens, cudaStream_t s, int topk, int64_t n, in
     // vectors at a time take 80, 98, 59, 41 on two warps and 88, 111, 64, 33 on
     // one; eight choices at a time on eight warps 121, 137, 70, 55: small blocks
     // wait for each other less at the dot products' end.  Few tokens leave SMs
-    // idle, and then eight warps a token shorten each one's chain of loads.
+    // idle, and then eight warps a token shorten each one's chain of loads.  At the
+    // limits (us, rows of launches on inputs beyond L2, one / two / eight warps):
+    //   6 choices of   512 values   520 values          1024            2048            4096
+    //   256 tokens  7.7  6.5  7.1   9.1  7.8  7.7   12.4 8.3 8.3   18.0 12.0  8.8   32.3 19.0 10.8
+    //   512 tokens  8.3  8.3 12.4  10.3  8.3 12.4   12.0 8.6 12.2  19.5 13.1 14.4   32.9 20.8 18.5
+    //   1024        8.7  8.2 16.7  10.5 10.0 18.2   13.7 10.3 18.5 21.1 16.4 20.6   36.9 26.7 27.5
+    //   8192       22.8 30.0 94.3  28.7 34.9 98.3   39.0 41.0 102  83.4 71.8 121    166  151  164
     if (H <= 512)
         combine_grad_kernel<BF16, 2, 2, 32><<<tokens, 32, 0, s>>>(topk, n, H, Y, ldy, dout, ldd, pos, kept, weights,
                                                                   dY, lddy, dweights);
-    else if (tokens > 512)
+    else if (tokens > (H > 2048 ? 512 : 256))
         combine_grad_kernel<BF16, 2, 2, 64><<<tokens, 64, 0, s>>>(topk, n, H, Y, ldy, dout, ldd, pos, kept, weights,
                                                                   dY, lddy, dweights);
     else
