@@ -313,3 +313,47 @@ def test_combine_gradients_of_many_tokens(tg, T, k, W, dtype):
     close(dY, want, want.abs() * (H[dt] * 1.01 + 2.0 ** -24) + TINY[dt], "dY")
     prod = torch.where(kept[:, :, None], Y.detach().double()[pos], 0) * g.double()[:, None, :]
     close(dw, prod.sum(2), W * 2.0 ** -24 * prod.abs().sum(2) + 2.0 ** -149, "dw")
+
+
+# ------------------------------------------------------- a captured backward pass
+
+def test_captured_backward_into_grads(tg):
+    """A whole step with backward() into the leaves' grads, captured as torch
+    asks (a warm-up on the capture's stream, its graph gone before the capture),
+    replayed on new contents: the grads of an eager step, bit for bit.  Groups end
+    inside 16-row steps."""
+    T, k, E, D, F = 700, 3, 6, 80, 136
+    g0 = torch.Generator().manual_seed(3)
+    ids = torch.randint(0, E + 1, (T, k), generator=g0).cuda()
+    x, W1, W2 = (normal(s, torch.bfloat16, i, 0.1).requires_grad_(True)
+                 for i, s in enumerate([(T, D), (E, D, F), (E, F, D)]))
+    w = positive((T, k), 4).requires_grad_(True)
+    gy = normal((T, D), torch.bfloat16, 5)
+    leaves = (x, W1, W2, w)
+
+    def step():
+        for t in leaves:
+            t.grad = None
+        plan = tg.expert_sort(ids, E)
+        h = torch.relu(tg.expert_matmul(tg.expert_gather(x, plan), W1, plan))
+        tg.expert_combine(tg.expert_matmul(h, W2, plan), plan, w).backward(gy)
+
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        step()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=s):
+        step()
+    kept = [t.grad for t in leaves]
+    with torch.no_grad():
+        ids.copy_(torch.randint(0, E + 1, (T, k), generator=g0))
+        x.copy_(normal((T, D), torch.bfloat16, 9))
+    for _ in range(2):
+        graph.replay()
+    torch.cuda.synchronize()
+    step()
+    _status(tg)
+    for t, got in zip(leaves, kept):
+        assert torch.equal(t.grad, got)
