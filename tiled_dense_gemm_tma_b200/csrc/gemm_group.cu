@@ -121,8 +121,9 @@ int launch_group(const GroupArgs& a, int bf16) {
 
 // Eight epilogue warps where groups have few rows and writing their gradients
 // takes longer than their MMAs, else four with two staging tiles each.  Measured
-// (us, four / eight) on 32 groups of 4096 x 2048 with 64 rows 117 / 105, 128 rows
-// 122 / 103, 256 rows 137 / 138, 384 rows 165 / 170, 1024 rows 366 / 375.
+// (us, four / eight) on 32 groups of 4096 x 2048 with 64 rows 115 / 113, 100 rows
+// 123 / 102, 128 rows 121 / 107, 200 rows 128 / 133, 256 rows 133 / 137, 384 rows
+// 162 / 168, 1024 rows 353 / 364.
 int launch_group_grad(const GroupArgs& a, int bf16) {
     constexpr CUtensorMapDataType tb = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, th = CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
     if (a.g.M < 256ll * a.E)

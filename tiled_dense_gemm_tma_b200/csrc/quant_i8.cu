@@ -21,8 +21,8 @@
 // smallest subnormal (multiples of 2^-141, of at most 18 bits).
 //
 // Bound by HBM, 2 bytes in and 1 out per value, and close behind by the issue
-// of its instructions (72 % of the slots): 16384 rows of 8192 bf16 values take
-// 71 us (5.65 TB/s), 79 with the division asked for eight values at a time.
+// of its instructions (69 % of the slots): 16384 rows of 8192 bf16 values take
+// 70 us (5.75 TB/s), 79 with the division asked for eight values at a time.
 // One group of threads per row keeps the row in registers between the maximum
 // and the rounding; rows longer than that (16384 values) are read twice, the
 // second time from L2.
