@@ -97,10 +97,8 @@ int run_grad(const GroupArgs& a, CUtensorMapDataType dt, int slot) {
     const long long per = ((g.K - 1) / 256 + 1) * ((g.N - 1) / 256 + 1);
     if (per > 0x7fffffffll / a.E) return kUnsupported;
     CUtensorMap tA, tB[4], tC;
-    // rows of A and G as M overlapping windows of 64 rows (the same pitch twice):
-    // no copy takes more of a window than its group has rows, so none reads past M
-    if (!tensor_map_3d(&tA, g.A, dt, g.K, 64, g.lda * 2, g.M, g.lda * 2, 64, 64, SWZ_128) ||
-        !tensor_map_3d(&tB[0], g.B, dt, g.N, 64, g.ldb * 2, g.M, g.ldb * 2, 64, 64, SWZ_128) ||
+    if (!tensor_map_2d(&tA, g.A, dt, 2, g.K, g.M, g.lda * 2, 64, 64, SWZ_128) ||
+        !tensor_map_2d(&tB[0], g.B, dt, 2, g.N, g.M, g.ldb * 2, 64, 64, SWZ_128) ||
         !tensor_map_3d(&tC, g.C, dt, g.N, g.K, g.ldc * 2, a.E,
                        static_cast<uint64_t>(a.E > 1 ? a.plane : g.ldc) * 2, 64, 32, SWZ_128))
         return kCudaError;
@@ -121,9 +119,9 @@ int launch_group(const GroupArgs& a, int bf16) {
 
 // Eight epilogue warps where groups have few rows and writing their gradients
 // takes longer than their MMAs, else four with two staging tiles each.  Measured
-// (us, four / eight) on 32 groups of 4096 x 2048 with 64 rows 115 / 113, 100 rows
-// 123 / 102, 128 rows 121 / 107, 200 rows 128 / 133, 256 rows 133 / 137, 384 rows
-// 162 / 168, 1024 rows 353 / 364.
+// (us, four / eight) on 32 groups of 4096 x 2048 with 64 rows 116 / 114, 100 rows
+// 122 / 109, 128 rows 121 / 111, 200 rows 143 / 147, 256 rows 133 / 135, 384 rows
+// 163 / 168, 1000 rows 374 / 379.
 int launch_group_grad(const GroupArgs& a, int bf16) {
     constexpr CUtensorMapDataType tb = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, th = CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
     if (a.g.M < 256ll * a.E)

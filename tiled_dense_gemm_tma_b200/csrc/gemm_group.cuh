@@ -33,24 +33,21 @@
 //
 // Weight gradient: the 256 lanes are the columns k of A, the MMA's N side
 // the columns n of G, the reduction runs over the group's rows.  Both
-// operands are read MN-major (a shared-memory row is one row r).  What lies
-// past the group belongs to the next one and must not enter the sums, nor
-// meet a zero there (0 * NaN is NaN).  The tensor maps cut it off: their
-// third coordinate is a row of the matrix, their second counts the 64 rows
-// from that one on (both strides are the row pitch), and a box that starts
-// 64 - q rows before such a window holds 64 - q rows of the zeros that TMA
-// fills in outside it and the window's first q rows.  A group's last block is
-// that box, zeros first, in both operands; the MMA steps (16 rows) of zeros
-// alone are skipped.  So every byte that an MMA reads came by a copy that
-// completed on the barrier which the MMA's issuer waits on, in either CTA of
-// the pair.  A group of no rows gets zeros.
+// operands are read MN-major (a shared-memory row is one row r).  The rows
+// of the last 64-row block that lie past the group belong to the next group:
+// MMA steps (16 rows) that hold none of the group's are skipped, and where
+// the group ends inside a step, a fix-up warp of the leader CTA clears the
+// step's other rows in both CTAs' shared memory, in both operands (0 * NaN is
+// NaN), before the MMA reads them.  Such a block's loads complete on a barrier
+// of their own in the leader, and the fix-up warp arrives on the full barrier
+// in the producers' place.  A group of no rows gets zeros.
 //
 // Every CTA derives the tile list from the offsets itself: no host knows the
 // group sizes, and no launch precedes this one.
 //
 // What bounds it: the MMAs where groups are large (32 groups of 1024 rows,
 // 4096 x 2048 bf16: 352 us forward, 1560 TFLOP/s, 521 clocks a block of 512 MMA
-// clocks; its weight gradient 354; 8-bit 4096 x 8192 x 8192 141 to 159 us, 3450 to
+// clocks; its weight gradient 354, 374 with groups of 1000 rows; 8-bit 4096 x 8192 x 8192 141 to 159 us, 3450 to
 // 3900 TOP/s), the weight stream where they are small (64 groups of one row, 1024
 // x 2048: 47 us, 5.7 TB/s), and in long runs the power limit, at 1.1 to 1.7 GHz.
 #pragma once
@@ -99,9 +96,10 @@ struct GrpCfg {
     static constexpr int EPI_WARPS = EPI_;
     static constexpr int HALVES = EPI_ / 4;             // warps to a quarter of the lanes
     static_assert(EPI_ == 4 || EPI_ == 8, "epilogue warps");
+    static constexpr int FIX_WARPS = WG_ ? 1 : 0;
     static constexpr int PRODUCERS = 2;                 // warp 0, and the first behind the epilogue
     static_assert(STAGES % PRODUCERS == 0, "a producer keeps its own ring slots");
-    static constexpr int THREADS = 32 * (1 + PRODUCERS + EPI_WARPS);
+    static constexpr int THREADS = 32 * (1 + PRODUCERS + EPI_WARPS + FIX_WARPS);
     static constexpr int STG_BUF = WG_ ? 4096 : 2048;   // a warp's [32 rows][128 bytes] or [32 rows][32 columns]
     static constexpr int NBUF = WG_ ? 8 / EPI_ : 1;     // staging tiles a warp
     static constexpr int TMEM_COLS = 512;               // two accumulators of 256 columns
@@ -111,6 +109,22 @@ struct GrpCfg {
     static_assert(SMEM_BYTES <= 227 * 1024, "shared memory per CTA");
     static_assert(!(I8 && WG_), "the 8-bit product has no gradient");
 };
+
+// 16 bytes of zeros at a shared::cluster address, possibly in the peer CTA.
+__device__ __forceinline__ void clear_cluster(uint32_t cl_addr) {
+    asm volatile("st.shared::cluster.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(cl_addr), "r"(0) : "memory");
+}
+
+// The calling thread's earlier writes to either CTA's shared memory reach the
+// tensor cores and the copy engine.
+__device__ __forceinline__ void fence_proxy_async_cluster() {
+    asm volatile("fence.proxy.async.shared::cluster;" ::: "memory");
+}
+
+// Both arrivals of a phase at once.
+__device__ __forceinline__ void mbar_arrive_two(uint64_t* bar) {
+    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0], 2;" ::"r"(smem_u32(bar)) : "memory");
+}
 
 // One work item: a 256-lane tile of the weight columns (WG: of A's columns)
 // starting at n0, against the rows [m0, m1) (WG: the columns of G from m0).
@@ -260,9 +274,9 @@ __device__ __forceinline__ void grp_store_grad(const CUtensorMap* tmC, const Grp
     }
 }
 
-// tmA: the 256-lane operand (product: weights, 3-D; WG: A's windows of 64
-// rows).  tmB .. tmB16: the N-side operand (product: rows of A in boxes of
-// 128, 64, 32 and 16 rows; WG: G's windows in tmB).  tmC: C (WG only).
+// tmA: the 256-lane operand (product: weights, 3-D; WG: A).  tmB .. tmB16:
+// the N-side operand (product: rows of A in boxes of 128, 64, 32 and 16 rows;
+// WG: G in tmB).  tmC: C (WG only).
 template <class Cfg>
 __global__ void __launch_bounds__(Cfg::THREADS, 1)
 grp_gemm_kernel(const __grid_constant__ CUtensorMap tmA,
@@ -280,7 +294,8 @@ grp_gemm_kernel(const __grid_constant__ CUtensorMap tmA,
     uint8_t* smStg = smB + Cfg::STAGES * Cfg::B_STAGE;
     uint64_t* full = reinterpret_cast<uint64_t*>(smStg + Cfg::EPI_WARPS * Cfg::NBUF * Cfg::STG_BUF);
     uint64_t* empty = full + Cfg::STAGES;
-    uint64_t* tfull = empty + Cfg::STAGES;
+    uint64_t* cut = empty + Cfg::STAGES;        // WG: a block that ends inside an MMA step has landed
+    uint64_t* tfull = cut + Cfg::STAGES;
     uint64_t* tempty = tfull + 2;
     uint64_t* drain = tempty + 2;
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
@@ -306,6 +321,7 @@ grp_gemm_kernel(const __grid_constant__ CUtensorMap tmA,
         for (int s = 0; s < Cfg::STAGES; ++s) {
             mbar_init(&full[s], 2);
             mbar_init(&empty[s], 1);
+            mbar_init(&cut[s], 2);
         }
         for (int a = 0; a < 2; ++a) { mbar_init(&tfull[a], 1); mbar_init(&tempty[a], 2 * Cfg::EPI_WARPS); }
         mbar_init(drain, 1);
@@ -424,6 +440,10 @@ grp_gemm_kernel(const __grid_constant__ CUtensorMap tmA,
         }
         return it;
     };
+    // WG: rows of the group in its last block, and whether they end inside an
+    // MMA step
+    auto last_rows = [&](const GrpItem& it) { return it.rows - (it.kb - 1) * Cfg::BK; };
+    auto is_cut = [&](const GrpItem& it) { return it.kb > 0 && last_rows(it) % Cfg::MMA_K != 0; };
 
     if (warp == 0 || warp == 2 + Cfg::EPI_WARPS) {
         // ----------------------------------------------- TMA producers (both)
@@ -451,25 +471,36 @@ grp_gemm_kernel(const __grid_constant__ CUtensorMap tmA,
                 const int b_live = b_left <= 0 ? 0 : min(hn / 64, b_left > 64 ? 2 : 1);   // WG
                 constexpr bool A_MN = Cfg::WG || Cfg::W_MN;
                 const uint32_t a_bytes = A_MN ? a_live * (Cfg::BK * 128) : (a_live ? Cfg::A_STAGE : 0);
-                const uint32_t b_bytes = Cfg::WG ? b_live * (Cfg::BK * 128) : hn * 128;
+                // product: hn rows are whole boxes of 128, 64, 32 and 16; those that
+                // start past the last row are not loaded either
+                uint32_t b_boxes = 0;
+                if constexpr (!Cfg::WG)
+                    for (int box = 128; box >= 16; box >>= 1)
+                        if ((hn & box) && b0 + (hn & -2 * box) < p.M) b_boxes |= box;
+                const uint32_t b_bytes = Cfg::WG ? b_live * (Cfg::BK * 128) : b_boxes * 128;
+                const bool cut_last = Cfg::WG && is_cut(it);
                 for (int kb = 0; kb < it.kb; ++kb, ++ld) {
                     if (ld % Cfg::PRODUCERS != turn) continue;
                     const uint32_t s = ld % Cfg::STAGES;
                     const uint32_t ph = (ld / Cfg::STAGES) & 1;
                     if (!bounded_wait(&empty[s], ph ^ 1, abort_flag, limit, p.status)) { ok = false; break; }
                     if (p.inject == 1 && ld == 0 && pair == 0 && rank == 0) continue;   // debug
-                    const uint32_t fbar = mapa_shared(smem_u32(&full[s]), 0);
+                    // a block that needs the fix-up completes on a barrier of its own
+                    const bool fix = cut_last && kb == it.kb - 1;
+                    const uint32_t fbar = mapa_shared(smem_u32(fix ? &cut[s] : &full[s]), 0);
                     mbar_arrive_expect_tx_cluster(fbar, a_bytes + b_bytes);
-                    armed |= 1u << s;
-                    armed_par = (armed_par & ~(1u << s)) | (ph << s);
+                    if (!fix) {
+                        armed |= 1u << s;
+                        armed_par = (armed_par & ~(1u << s)) | (ph << s);
+                    }
                     uint8_t* a_dst = smA + s * Cfg::A_STAGE;
                     uint8_t* b_dst = smB + s * Cfg::B_STAGE;
                     if constexpr (Cfg::WG) {
-                        const int r = it.r0 + kb * Cfg::BK, from = -grp_zero_rows(it.rows, kb, Cfg::BK);
+                        const int r = it.r0 + kb * Cfg::BK;
                         for (int j = 0; j < a_live; ++j)
-                            tma_load_3d_pair(a_dst + j * (Cfg::BK * 128), &tmA, fbar, n0 + Cfg::CHUNK * j, from, r);
+                            tma_load_2d_pair(a_dst + j * (Cfg::BK * 128), &tmA, fbar, n0 + Cfg::CHUNK * j, r);
                         for (int j = 0; j < b_live; ++j)
-                            tma_load_3d_pair(b_dst + j * (Cfg::BK * 128), &tmB, fbar, b0 + Cfg::CHUNK * j, from, r);
+                            tma_load_2d_pair(b_dst + j * (Cfg::BK * 128), &tmB, fbar, b0 + Cfg::CHUNK * j, r);
                     } else {
                         if constexpr (Cfg::W_MN) {
                             for (int j = 0; j < a_live; ++j)
@@ -478,12 +509,14 @@ grp_gemm_kernel(const __grid_constant__ CUtensorMap tmA,
                         } else if (a_live) {
                             tma_load_3d_pair(a_dst, &tmA, fbar, kb * Cfg::BK, n0, it.e);
                         }
-                        // hn rows: whole boxes of 128, 64, 32 and 16
-                        int at = 0;
-                        if (hn & 128) { tma_load_2d_pair(b_dst, &tmB, fbar, kb * Cfg::BK, b0); at = 128; }
-                        if (hn & 64) { tma_load_2d_pair(b_dst + at * 128, &tmB64, fbar, kb * Cfg::BK, b0 + at); at += 64; }
-                        if (hn & 32) { tma_load_2d_pair(b_dst + at * 128, &tmB32, fbar, kb * Cfg::BK, b0 + at); at += 32; }
-                        if (hn & 16) tma_load_2d_pair(b_dst + at * 128, &tmB16, fbar, kb * Cfg::BK, b0 + at);
+                        auto rows = [&](const CUtensorMap* map, int box) {
+                            const int at = hn & -2 * box;
+                            if (b_boxes & box) tma_load_2d_pair(b_dst + at * 128, map, fbar, kb * Cfg::BK, b0 + at);
+                        };
+                        rows(&tmB, 128);
+                        rows(&tmB64, 64);
+                        rows(&tmB32, 32);
+                        rows(&tmB16, 16);
                     }
                 }
             }
@@ -494,8 +527,8 @@ grp_gemm_kernel(const __grid_constant__ CUtensorMap tmA,
                             volatile int never = 0;
                             bounded_wait(&full[s], (armed_par >> s) & 1, &never, limit, p.status);
                         }
-                // the peer's copies complete on the leader's barriers, which it
-                // cannot wait on: a fixed 1 ms to land
+                // copies that complete on barriers this thread cannot wait on (the
+                // leader's; a block under fix-up): a fixed 1 ms to land
                 const uint64_t t0 = globaltimer_ns();
                 while (globaltimer_ns() - t0 < 1000000ull) __nanosleep(10000);
             }
@@ -527,10 +560,11 @@ grp_gemm_kernel(const __grid_constant__ CUtensorMap tmA,
                     tc_fence_after();
                     const uint32_t a_addr = smem_u32(smA + s * Cfg::A_STAGE);
                     const uint32_t b_addr = smem_u32(smB + s * Cfg::B_STAGE);
-                    const int step0 = Cfg::WG ? grp_zero_rows(it.rows, kb, Cfg::BK) / Cfg::MMA_K : 0;
+                    const int steps = Cfg::WG && kb == it.kb - 1
+                        ? (last_rows(it) + Cfg::MMA_K - 1) / Cfg::MMA_K : Cfg::STEPS;
 #pragma unroll
                     for (int k = 0; k < Cfg::STEPS; ++k) {
-                        if (Cfg::WG && k < step0) continue;
+                        if (Cfg::WG && k >= steps) break;
                         // K-major: 32 bytes of k along the 128-byte rows; MN-major:
                         // MMA_K rows of 128 bytes, 128-byte wide chunks LBO apart
                         const uint64_t ad = A_MN
@@ -539,8 +573,8 @@ grp_gemm_kernel(const __grid_constant__ CUtensorMap tmA,
                         const uint64_t bd = Cfg::WG
                             ? sw128_desc(b_addr + k * Cfg::MMA_K * 128, Cfg::BK * 128, 1024)
                             : sw128_desc(b_addr + k * 32, 16, 1024);
-                        if constexpr (Cfg::I8) mma_i8_pair(d_tmem, ad, bd, idesc, kb != 0 || k != step0);
-                        else mma_f16_pair(d_tmem, ad, bd, idesc, kb != 0 || k != step0);
+                        if constexpr (Cfg::I8) mma_i8_pair(d_tmem, ad, bd, idesc, kb != 0 || k != 0);
+                        else mma_f16_pair(d_tmem, ad, bd, idesc, kb != 0 || k != 0);
                     }
                     const uint32_t e_loc = smem_u32(&empty[s]);
                     mma_commit_pair(mapa_shared(e_loc, 0));      // both CTAs' slots
@@ -556,7 +590,7 @@ grp_gemm_kernel(const __grid_constant__ CUtensorMap tmA,
             bounded_wait(drain, 0, &never, limit, p.status);
         }
         __syncwarp();
-    } else {
+    } else if (warp >= 2 && warp < 2 + Cfg::EPI_WARPS) {
         // --------------------------------------------------- epilogue (both)
         const int q = warp & 3;
         const int half = (warp - 2) >> 2;
@@ -587,6 +621,44 @@ grp_gemm_kernel(const __grid_constant__ CUtensorMap tmA,
         if constexpr (Cfg::WG) {
             if (lane == 0) bulk_wait<0>();
             __syncwarp();
+        }
+    } else {
+        // ------------------------------------------ fix-up (WG, leader only)
+        if constexpr (Cfg::WG) {
+            uint32_t ld = 0, seen = 0;                  // seen: parity of each slot's cut barrier
+            int g = 0;
+            for (int w = pair; w < num_items && rank == 0; w += npairs) {
+                const GrpItem it = item(w, g);
+                ld += it.kb;
+                if (!is_cut(it)) continue;
+                const uint32_t s = (ld - 1) % Cfg::STAGES;
+                if (!bounded_wait(&cut[s], (seen >> s) & 1, abort_flag, limit, p.status)) break;
+                seen ^= 1u << s;
+                // rows [first, end of its MMA step) of both operands, both
+                // 64-column chunks: a row is 128 bytes of each chunk
+                const int first = last_rows(it);
+                const int count = (first + Cfg::MMA_K - 1) / Cfg::MMA_K * Cfg::MMA_K - first;
+                const uint32_t a = smem_u32(smA + s * Cfg::A_STAGE + first * 128);
+                const uint32_t b = smem_u32(smB + s * Cfg::B_STAGE + first * 128);
+                for (int r = 0; r < 2; ++r) {
+                    const uint32_t ar = mapa_shared(a, r), br = mapa_shared(b, r);
+                    for (int i = lane; i < count * 8; i += 32) {
+                        clear_cluster(ar + i * 16);
+                        clear_cluster(ar + Cfg::BK * 128 + i * 16);
+                        clear_cluster(br + i * 16);
+                        clear_cluster(br + Cfg::BK * 128 + i * 16);
+                    }
+                }
+                // The zeros, the peer's too, come from the CTA whose thread issues
+                // the MMA over both CTAs' shared memory: the proxy fence and an
+                // arrival within the CTA order them.  Where each CTA clears its
+                // own, the peer's arrival has to release at cluster scope, which
+                // waits for a memory barrier: 32 groups of 1001 and 1047 rows then
+                // take 444 us, so 415.
+                fence_proxy_async_cluster();
+                __syncwarp();
+                if (lane == 0) mbar_arrive_two(&full[s]);
+            }
         }
     }
 

@@ -195,11 +195,6 @@ TG_HD void grp_rows(const int* offsets, int e, int ng, int M, int& r0, int& r1) 
     r1 = e < ng ? sched_min(sched_max(offsets[e + 1], r0), M) : M;
 }
 
-// Weight gradient, whose k blocks are `bk` rows of the group: the rows of
-// zeros that stand before the group's rows in block kb (the last block only
-// has any).
-TG_HD int grp_zero_rows(int rows, int kb, int bk) { return sched_max((kb + 1) * bk - rows, 0); }
-
 // ------------------------------------------------------- fp32 split-K
 // Number of k ranges per output tile: 1 when the tiles already fill the SMs;
 // otherwise enough to fill them, with at most 8 ranges and no more ranges than
