@@ -47,9 +47,10 @@
 //
 // What bounds it: the MMAs where groups are large (32 groups of 1024 rows,
 // 4096 x 2048 bf16: 352 us forward, 1560 TFLOP/s, 521 clocks a block of 512 MMA
-// clocks; its weight gradient 354, 374 with groups of 1000 rows; 8-bit 4096 x 8192 x 8192 141 to 159 us, 3450 to
-// 3900 TOP/s), the weight stream where they are small (64 groups of one row, 1024
-// x 2048: 47 us, 5.7 TB/s), and in long runs the power limit, at 1.1 to 1.7 GHz.
+// clocks; its weight gradient 354, 374 with groups of 1000 rows; 8-bit 4096 x
+// 8192 x 8192 141 to 159 us, 3450 to 3900 TOP/s), the weight stream where they are
+// small (64 groups of one row, 1024 x 2048: 47 us, 5.7 TB/s), and in long runs the
+// power limit, at 1.1 to 1.7 GHz.
 #pragma once
 #include "gemm_tc.cuh"
 
