@@ -392,6 +392,94 @@ TG_API tg_status tg_expert_combine_grad(int64_t tokens, int topk, int64_t H, int
                                         float *dweights, void *stream);
 
 /*
+ * Microscaled 4-bit floating point (the MXFP4 format of the OCP Microscaling
+ * Formats specification v1.0, as tg_gemm_wfp4's weights, but packed along k).
+ *
+ * A row of K values is ceil(K / 2) bytes of E2M1 codes, value k in the low half
+ * of byte k / 2 for even k and in the high half for odd k, and ceil(K / 32) E8M0
+ * bytes: value k is e2m1(code) * 2^(E[k / 32] - 127), E = 255 meaning NaN.  Rows
+ * of codes and of scales are 16-byte aligned and a multiple of 16 bytes apart.
+ *
+ * tg_quant_mxfp4 -- rows of 16-bit values to that format.  For each block of 32
+ *   with largest magnitude top: E = floor(log2(top)) - 2 + 127, at least 0; the
+ *   codes are x * 2^(127 - E) rounded to the nearest E2M1 value, ties to the even
+ *   code, magnitudes above 6 to 6.  They are exactly what the formula gives in
+ *   real arithmetic.  A block of zeros gets E = 0; one that holds an infinity or
+ *   a NaN gets E = 255 and codes 0.  An odd K's last half byte is 0.  X: M x K of
+ *   `type` (TG_TYPE_F16 or TG_TYPE_BF16), row pitch ldx (elements, % 8 == 0);  Q, scales: M
+ *   rows, pitches ldq and lds in bytes.
+ * tg_dequant_mxfp4 -- back to 16-bit values, each rounded once to `type` (for bfloat16 and
+ *   for what tg_quant_mxfp4 made of fp16 they are exact).
+ * tg_expert_quant_mxfp4 -- tg_expert_gather of quantised rows: row pos[i] of Q and
+ *   scales is X[i / topk] quantised; the rows of dropped choices are zero.  Each
+ *   token is read and quantised once.  pos and kept as in tg_expert_gather.
+ *
+ * tg_gemm_mxfp4 -- C[m][n] = epi( sum_k A[m][k] * W[n][k] ), both operands in the
+ *   format: A has M rows, the weights W have N (they are stored N x K).  Products with
+ *   their scales accumulate in fp32; rounded once to C's type (type, ldc as
+ *   tg_gemm_w8a8).  A NaN stays a NaN, also under TG_EPI_RELU.  Any K >= 0; for odd K
+ *   the last half byte must be 0 in A's rows or in W's.
+ * tg_gemm_grouped_mxfp4 -- the same over groups of rows (offsets as in
+ *   tg_gemm_grouped_w8a8): W_e at B + e * plane_b bytes, its scales at b_scales + e *
+ *   plane_s bytes (both % 16 == 0, not 0 unless E is 1).  Rows behind the last
+ *   group are written as zero.
+ * Neither uses a workspace.  Larger products run on CTA pairs; a refused cluster
+ * launch returns TG_ERR_UNSUPPORTED, as does M or N above 2^31 - 1025.
+ */
+TG_API tg_status tg_quant_mxfp4(int64_t M, int64_t K, const void *X, int64_t ldx, int type,
+                                uint8_t *Q, int64_t ldq, uint8_t *scales, int64_t lds, void *stream);
+TG_API tg_status tg_dequant_mxfp4(int64_t M, int64_t K, const uint8_t *Q, int64_t ldq,
+                                  const uint8_t *scales, int64_t lds, void *Y, int64_t ldy, int type,
+                                  void *stream);
+TG_API tg_status tg_expert_quant_mxfp4(int64_t tokens, int topk, int64_t K, const void *X, int64_t ldx,
+                                       int type, const int32_t *pos, const int32_t *kept,
+                                       uint8_t *Q, int64_t ldq, uint8_t *scales, int64_t lds, void *stream);
+TG_API tg_status tg_gemm_mxfp4(int64_t M, int64_t N, int64_t K,
+                               const uint8_t *A, int64_t lda, const uint8_t *a_scales, int64_t ldas,
+                               const uint8_t *B, int64_t ldb, const uint8_t *b_scales, int64_t ldbs,
+                               void *C, int64_t ldc, int type, int epilogue, void *stream);
+TG_API tg_status tg_gemm_grouped_mxfp4(int64_t M, int64_t N, int64_t K, int E,
+                                       const uint8_t *A, int64_t lda, const uint8_t *a_scales, int64_t ldas,
+                                       const int32_t *offsets,
+                                       const uint8_t *B, int64_t ldb, int64_t plane_b,
+                                       const uint8_t *b_scales, int64_t ldbs, int64_t plane_s,
+                                       void *C, int64_t ldc, int type, int epilogue, void *stream);
+
+/*
+ * Routing: the experts of each token, and their weights.
+ *
+ * tg_expert_route -- for each row x of logits (tokens x E of `type`, TG_TYPE_F16,
+ *   TG_TYPE_BF16 or TG_TYPE_F32, aligned to its elements, any row pitch ldl >= E):
+ *     score   p = softmax(x) (TG_SCORE_SOFTMAX) or sigmoid(x) (TG_SCORE_SIGMOID)
+ *     choice  the topk experts of largest x, or with a bias (E floats, not NULL) of
+ *             largest p + bias, in falling order, ties to the lower number.  With
+ *             groups > 1 (each E / groups consecutive experts) only from the
+ *             keep_groups groups of largest sum of their two largest p (+ bias), ties
+ *             to the lower group.
+ *     weight  scale * p, or with renorm = 1 scale * p over the sum of the chosen p.
+ *   ids (int32) and weights (float) are tokens x topk, dense.  An expert whose
+ *   logit is minus infinity is never chosen (nor counted in its group's sum); where fewer than topk are left
+ *   the rest are ids of -1 (a dropped choice for tg_expert_sort) with weight 0.  A
+ *   logit that is NaN or plus infinity is chosen first and makes its row's weights NaN.
+ *   Choices are those of 64-bit arithmetic on the given logits.
+ * tg_expert_route_grad -- dlogits (tokens x E of `type`, row pitch ldd) for the
+ *   gradient dweights of the weights (tokens x topk floats, dense), from the same logits and the
+ *   ids that the call above gave; ids of one row must differ, those outside 0..E-1
+ *   count as dropped.  The choice has no gradient, so the bias has none.
+ * 1 <= topk <= keep_groups * E / groups, groups a divisor of E, 1 <= keep_groups <= groups;
+ * topk or groups above 32, E above 1024, or 2^31 tokens and more -> TG_ERR_UNSUPPORTED.
+ */
+enum { TG_TYPE_F32 = 2 };
+enum { TG_SCORE_SOFTMAX = 0, TG_SCORE_SIGMOID = 1 };
+
+TG_API tg_status tg_expert_route(int64_t tokens, int E, const void *logits, int64_t ldl, int type,
+                                 const float *bias, int score, int groups, int keep_groups, int topk,
+                                 int renorm, float scale, int32_t *ids, float *weights, void *stream);
+TG_API tg_status tg_expert_route_grad(int64_t tokens, int E, const void *logits, int64_t ldl, int type,
+                                      int score, int topk, int renorm, float scale, const int32_t *ids,
+                                      const float *dweights, void *dlogits, int64_t ldd, void *stream);
+
+/*
  * tg_gemm_bf16_small_m_static -- tg_gemm_bf16 for M <= 128 that never
  * allocates device memory.  The pages have no counterpart: this entry point
  * exists for callers that may not call cudaMalloc / cudaFree where they run

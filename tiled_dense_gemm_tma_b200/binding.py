@@ -27,6 +27,8 @@ EXPORTS = ("tg_gemm_f32", "tg_gemm_f16", "tg_gemm_bf16", "tg_gemm_w4a16", "tg_ge
            "tg_gemm_grouped_wgrad_f16", "tg_gemm_grouped_wgrad_bf16", "tg_gemm_grouped_w8a8",
            "tg_expert_sort_scratch", "tg_expert_sort", "tg_expert_gather", "tg_expert_combine",
            "tg_expert_combine_grad",
+           "tg_quant_mxfp4", "tg_dequant_mxfp4", "tg_expert_quant_mxfp4", "tg_gemm_mxfp4",
+           "tg_gemm_grouped_mxfp4", "tg_expert_route", "tg_expert_route_grad",
            "tg_tune_set", "tg_tune_builtin", "tg_tune_query",
            "tg_status_string", "tg_last_device_status", "tg_num_sms")
 
@@ -102,6 +104,18 @@ def load_library():
         lib.tg_expert_combine.argtypes = [i64, ci, i64, ci, vp, i64, vp, vp, vp, vp, i64, vp]
         lib.tg_expert_combine_grad.argtypes = [i64, ci, i64, ci, vp, i64, vp, i64, vp, vp, vp,
                                                vp, i64, vp, vp]
+        lib.tg_quant_mxfp4.argtypes = [i64, i64, vp, i64, ci, vp, i64, vp, i64, vp]
+        lib.tg_dequant_mxfp4.argtypes = [i64, i64, vp, i64, vp, i64, vp, i64, ci, vp]
+        lib.tg_expert_quant_mxfp4.argtypes = [i64, ci, i64, vp, i64, ci, vp, vp, vp, i64, vp, i64, vp]
+        lib.tg_gemm_mxfp4.argtypes = [i64, i64, i64, vp, i64, vp, i64, vp, i64, vp, i64, vp, i64, ci, ci, vp]
+        lib.tg_gemm_grouped_mxfp4.argtypes = [i64, i64, i64, ci, vp, i64, vp, i64, vp, vp, i64, i64,
+                                              vp, i64, i64, vp, i64, ci, ci, vp]
+        cf = ctypes.c_float
+        lib.tg_expert_route.argtypes = [i64, ci, vp, i64, ci, vp, ci, ci, ci, ci, ci, cf, vp, vp, vp]
+        lib.tg_expert_route_grad.argtypes = [i64, ci, vp, i64, ci, ci, ci, ci, cf, vp, vp, vp, i64, vp]
+        for name in ("tg_quant_mxfp4", "tg_dequant_mxfp4", "tg_expert_quant_mxfp4", "tg_gemm_mxfp4",
+                     "tg_gemm_grouped_mxfp4", "tg_expert_route", "tg_expert_route_grad"):
+            getattr(lib, name).restype = ci
         for name in ("tg_quant_i8", "tg_gemm_w8a8", "tg_gemm_grouped_f16", "tg_gemm_grouped_bf16",
                      "tg_gemm_grouped_wgrad_f16", "tg_gemm_grouped_wgrad_bf16",
                      "tg_gemm_grouped_w8a8", "tg_expert_sort", "tg_expert_gather",
@@ -426,7 +440,7 @@ def gemm_bf16_small_m_static(A, B, C=None, relu=False, stream=None):
 
 # ------------------------------------------------------ 8-bit linear layers
 
-TYPE_F16, TYPE_BF16 = 0, 1
+TYPE_F16, TYPE_BF16, TYPE_F32 = 0, 1, 2
 
 
 def _type16(dtype, name):
@@ -1066,6 +1080,246 @@ def expert_matmul(Xs, W, groups):
     ones of widths that are no multiple of 8; the results here have padded rows)
     are copied first, in backward again; gemm_grouped refuses them."""
     return _expert(2).apply(Xs, W, _offsets_of(groups))
+
+
+# ------------------------------------------- microscaled 4-bit floating point
+
+def _blocks(q, scales, name):
+    """(rows, K in pairs) of row-major codes and their scales: uint8 rows x
+    K / 2 and rows x ceil(K / 32); for stacks of matrices, of one of them."""
+    import torch
+    if q.dtype != torch.uint8 or scales.dtype != torch.uint8:
+        raise TypeError(f"{name} and its scales must be uint8")
+    if q.dim() != scales.dim() or q.shape[:-1] != scales.shape[:-1]:
+        raise ValueError(f"{name} and its scales must have the same rows")
+    if scales.shape[-1] != -(-q.shape[-1] // 16):
+        raise ValueError(f"{name} needs one scale for every 16 bytes of a row")
+    return q.shape[-2], q.shape[-1]
+
+
+def quant_mxfp4(X, plan=None, Q=None, scales=None, stream=None):
+    """Rows of X (M x K, float16 / bfloat16) to microscaled 4-bit floating
+    point (MXFP4): E2M1 codes, two to a byte along the row, and an E8M0 scale for
+    every 32 values, 2^(floor(log2(max|x|)) - 2); round to nearest even, above 6
+    scales 6.  Returns (Q, scales), uint8 M x ceil(K / 2) and M x ceil(K / 32).  A
+    block with an infinity or a NaN gets scale 255, which stands for NaN.
+
+    With a plan of expert_sort the rows are sorted by expert on the way, as
+    expert_gather does: row plan.pos[t, j] of the results is X[t], the rows of
+    dropped choices are zero.  Rows of X that do not start on 16-byte boundaries
+    are copied to such ones first."""
+    import torch
+    if X.dim() != 2:
+        raise ValueError("X must be 2-D")
+    kind = _type16(X.dtype, "X")
+    M, K = X.shape
+    device = X.device
+    rows = M
+    if plan is not None:
+        T, k = plan._pos.shape
+        if M != T:
+            raise ValueError("X must have one row per token of the plan")
+        rows = T * k
+        _one_device(device, (plan._pos,), "the plan")
+    with contextlib.nullcontext() if stream is None else _memory_of(stream, device):
+        X = _aligned_rows(X)
+        Q, ldq = _bytes_out(Q, rows, -(-K // 2), device, "Q")
+        scales, lds = _bytes_out(scales, rows, -(-K // 32), device, "scales")
+    _one_device(device, (Q, scales), "Q, scales")
+    if plan is None:
+        _launch("tg_quant_mxfp4", device, stream, M, K, X.data_ptr(), _pitch(X, "X"), kind,
+                Q.data_ptr(), ldq, scales.data_ptr(), lds)
+    else:
+        _launch("tg_expert_quant_mxfp4", device, stream, T, k, K, X.data_ptr(), _pitch(X, "X"), kind,
+                plan._pos.data_ptr(), plan._kept(), Q.data_ptr(), ldq, scales.data_ptr(), lds)
+    return Q, scales
+
+
+def _bytes_out(t, M, N, device, name):
+    """(t, its row pitch), a new M x N matrix of bytes where it is None."""
+    import torch
+    if t is None:
+        return _rows_out(M, N, torch.uint8, device)
+    if t.shape != (M, N) or t.dtype != torch.uint8:
+        raise ValueError(f"{name} has the wrong shape or dtype")
+    return t, _pitch(t, name)
+
+
+def dequant_mxfp4(Q, scales, K=None, C=None, out_dtype=None, stream=None):
+    """The M x K values of codes and scales as quant_mxfp4 gives them, each
+    rounded once to out_dtype (float16 or bfloat16, by default C's or bfloat16).
+    K defaults to all that Q holds."""
+    import torch
+    if Q.dim() != 2:
+        raise ValueError("Q must be 2-D")
+    M, pairs = _blocks(Q, scales, "Q")
+    if K is None:
+        K = 2 * pairs
+    elif (K + 1) // 2 != pairs:
+        raise ValueError("Q must have ceil(K / 2) bytes a row")
+    if out_dtype is None:
+        out_dtype = torch.bfloat16 if C is None else C.dtype
+    kind = _type16(out_dtype, "C")
+    device = Q.device
+    C, ldc = _out(C, M, K, out_dtype, device, stream)
+    _one_device(device, (scales, C), "scales, C")
+    _launch("tg_dequant_mxfp4", device, stream, M, K, Q.data_ptr(), _pitch(Q, "Q"), scales.data_ptr(),
+            _pitch(scales, "scales"), C.data_ptr(), ldc, kind)
+    return C
+
+
+def gemm_mxfp4(A, a_scales, B, b_scales, C=None, out_dtype=None, relu=False, stream=None):
+    """C = epi(A @ W.T) for A (M x K) and the weights W (N x K), both microscaled
+    4-bit floating point as quant_mxfp4 gives it: codes uint8 M x K/2 and N x
+    K/2, scales uint8 M x ceil(K / 32) and N x ceil(K / 32).  fp32 accumulation; C
+    is float16 or bfloat16 (out_dtype, by default C's or bfloat16).  A NaN (of a
+    scale) stays one, also with relu.  Quantised rows of odd length end in a zero
+    half byte, which adds nothing."""
+    import torch
+    if A.dim() != 2 or B.dim() != 2:
+        raise ValueError("A and B must be 2-D")
+    (M, pairs), (N, pairs2) = _blocks(A, a_scales, "A"), _blocks(B, b_scales, "B")
+    if pairs != pairs2:
+        raise ValueError(f"inner dimensions differ: {2 * pairs} vs {2 * pairs2}")
+    if out_dtype is None:
+        out_dtype = torch.bfloat16 if C is None else C.dtype
+    kind = _type16(out_dtype, "C")
+    device = A.device
+    C, ldc = _out(C, M, N, out_dtype, device, stream)
+    _one_device(device, (a_scales, B, b_scales, C), "a_scales, B, b_scales, C")
+    _launch("tg_gemm_mxfp4", device, stream, M, N, 2 * pairs, A.data_ptr(), _pitch(A, "A"),
+            a_scales.data_ptr(), _pitch(a_scales, "a_scales"), B.data_ptr(), _pitch(B, "B"),
+            b_scales.data_ptr(), _pitch(b_scales, "b_scales"), C.data_ptr(), ldc, kind,
+            EPI_RELU if relu else EPI_NONE)
+    return C
+
+
+def gemm_grouped_mxfp4(A, a_scales, groups, B, b_scales, C=None, out_dtype=None, relu=False,
+                       stream=None):
+    """gemm_mxfp4 over groups of rows: row r of group e times W[e].T, the weights
+    B uint8 E x N x K/2 with scales E x N x ceil(K / 32); groups is an ExpertPlan
+    or its offsets.  Rows behind the last group are zero."""
+    import torch
+    offsets = _offsets_of(groups)
+    E = offsets.shape[0] - 1
+    if A.dim() != 2 or B.dim() != 3 or B.shape[0] != E:
+        raise ValueError("A must be 2-D and B one matrix per group")
+    (M, pairs), (N, pairs2) = _blocks(A, a_scales, "A"), _blocks(B, b_scales, "B")
+    if pairs != pairs2:
+        raise ValueError(f"inner dimensions differ: {2 * pairs} vs {2 * pairs2}")
+    if out_dtype is None:
+        out_dtype = torch.bfloat16 if C is None else C.dtype
+    kind = _type16(out_dtype, "C")
+    device = A.device
+    C, ldc = _out(C, M, N, out_dtype, device, stream)
+    _one_device(device, (a_scales, B, b_scales, offsets, C), "a_scales, B, b_scales, offsets, C")
+    _launch("tg_gemm_grouped_mxfp4", device, stream, M, N, 2 * pairs, E, A.data_ptr(), _pitch(A, "A"),
+            a_scales.data_ptr(), _pitch(a_scales, "a_scales"), offsets.data_ptr(),
+            B.data_ptr(), _pitch(B, "B"), _plane(B), b_scales.data_ptr(), _pitch(b_scales, "b_scales"),
+            _plane(b_scales), C.data_ptr(), ldc, kind, EPI_RELU if relu else EPI_NONE)
+    return C
+
+
+# ------------------------------------------------------------------ routing
+
+SCORES = {"softmax": 0, "sigmoid": 1}
+
+
+def _route_args(logits):
+    """(type, row pitch) of the router's logits, copied where they are not
+    row-major."""
+    import torch
+    kind = TYPE_F32 if logits.dtype == torch.float32 else _type16(logits.dtype, "logits other than float32")
+    T, E = logits.shape
+    down, across = logits.stride()
+    if (across != 1 and E > 1) or (T > 1 and down < E):
+        logits = logits.contiguous()
+        down = E
+    return logits, kind, down if T > 1 else E
+
+
+def _route(logits, topk, bias, score, groups, keep, renorm, scale):
+    import torch
+    T, E = logits.shape
+    device = logits.device
+    x, kind, ldl = _route_args(logits)
+    ids = torch.empty_strided((T, topk), (topk, 1), dtype=torch.int32, device=device)
+    weights = torch.empty_strided((T, topk), (topk, 1), dtype=torch.float32, device=device)
+    if bias is not None:
+        _vector(bias, E, torch.float32, "bias")
+        _one_device(device, (bias,), "bias")
+    _one_device(device, (x,), "logits")
+    _launch("tg_expert_route", device, None, T, E, x.data_ptr(), ldl, kind,
+            None if bias is None else bias.data_ptr(), score, groups, keep, topk, renorm, scale,
+            ids.data_ptr(), weights.data_ptr())
+    return ids, weights
+
+
+def _route_function():
+    import torch
+
+    class _Route(torch.autograd.Function):
+        """Experts and weights of each token; the weights' gradient reaches the
+        logits, the choice has none."""
+
+        @staticmethod
+        def forward(ctx, logits, *args):
+            ids, weights = _route(logits, *args)
+            topk, _, score, _, _, renorm, scale = args
+            ctx.args = score, topk, renorm, scale
+            ctx.save_for_backward(logits, ids)
+            ctx.mark_non_differentiable(ids)
+            return ids, weights
+
+        @staticmethod
+        def backward(ctx, _, g):
+            if torch.is_grad_enabled():
+                raise RuntimeError("the experts' operators are differentiable once")
+            logits, ids = ctx.saved_tensors
+            score, topk, renorm, scale = ctx.args
+            T, E = logits.shape
+            x, kind, ldl = _route_args(logits)
+            g = g.contiguous()
+            device = x.device
+            _one_device(device, (g,), "the gradient")
+            d = torch.empty_strided((T, E), (E, 1), dtype=logits.dtype, device=device)
+            _launch("tg_expert_route_grad", device, None, T, E, x.data_ptr(), ldl, kind, score, topk, renorm,
+                    scale, ids.data_ptr(), g.data_ptr(), d.data_ptr(), E)
+            return (d,) + (None,) * 7
+
+    return _Route
+
+
+_ROUTE = None
+
+
+def expert_route(logits, topk, *, bias=None, score="softmax", groups=1, topk_groups=None,
+                 renorm=True, scale=1.0):
+    """The experts of each token and their weights from the router's logits
+    (tokens x E, float32, float16 or bfloat16): (ids, weights), int32 and float32
+    tokens x topk, as expert_sort and expert_combine take them.
+
+    The scores are softmax(logits) or sigmoid(logits).  The topk highest are
+    chosen in falling order, ties to the lower number; a bias (float32, E) is
+    added to the scores for the choice alone.  With groups (of E / groups
+    consecutive experts) the choice is made in the topk_groups groups (by default all) whose two
+    highest (biased) scores sum highest.  Weights are scale times the chosen scores,
+    divided by their sum with renorm.  Minus infinity is never chosen; where fewer than topk
+    are left, the rest are -1 (dropped choices) and weigh 0.  A NaN or plus infinity
+    makes its row's weights NaN.  Differentiable in the logits."""
+    global _ROUTE
+    import torch
+    if logits.dim() != 2:
+        raise ValueError("logits must be 2-D (tokens x experts)")
+    if score not in SCORES:
+        raise ValueError("score must be 'softmax' or 'sigmoid'")
+    args = (topk, bias, SCORES[score], groups, groups if topk_groups is None else topk_groups,
+            1 if renorm else 0, scale)
+    if not (logits.requires_grad and torch.is_grad_enabled()):
+        return _route(logits, *args)
+    if _ROUTE is None:
+        _ROUTE = _route_function()
+    return _ROUTE.apply(logits, *args)
 
 
 def last_device_status(stream=None):

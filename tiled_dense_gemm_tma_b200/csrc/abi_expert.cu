@@ -1,5 +1,5 @@
-// abi_expert.cu -- the C ABI of the 8-bit linear layers and the experts'
-// operators: argument validation and dispatch.  As in abi.cu every check runs
+// abi_expert.cu -- the C ABI of the 8-bit and microscaled 4-bit linear layers and
+// the experts' operators: argument validation and dispatch.  As in abi.cu every check runs
 // before any CUDA call.
 #include "../../include/tg_gemm.h"
 #include "launch.h"
@@ -267,6 +267,141 @@ tg_status tg_expert_combine_grad(int64_t tokens, int topk, int64_t H, int type, 
     if (s != TG_OK) return s;
     return static_cast<tg_status>(tg::launch_expert_combine_grad(tokens, topk, H, type == TG_TYPE_BF16, Y, ldy, dout,
                                                                  ldd, pos, kept, weights, dY, lddy, dweights, stream));
+}
+
+namespace {
+
+// Codes and scales of `rows` rows of K values.
+tg_status check_blocks(const void* q, int64_t ldq, const void* scales, int64_t lds, int64_t K) {
+    return worst({check_matrix(q, ldq, (K + 1) / 2, 1), check_matrix(scales, lds, (K + 31) / 32, 1)});
+}
+
+tg_status mxfp4(int64_t M, int64_t N, int64_t K, int E, const uint8_t* A, int64_t lda, const uint8_t* a_scales,
+                int64_t ldas, const int32_t* offsets, const uint8_t* B, int64_t ldb, int64_t plane_b,
+                const uint8_t* b_scales, int64_t ldbs, int64_t plane_s, void* C, int64_t ldc, int type,
+                int epilogue, void* stream) {
+    if (M < 0 || N < 0 || K < 0 || E < 1 || bad_type(type)) return TG_ERR_INVALID_ARG;
+    if (epilogue != TG_EPI_NONE && epilogue != TG_EPI_RELU) return TG_ERR_INVALID_ARG;
+    if (M == 0 || N == 0) return TG_OK;
+    const tg_status s = worst({check_matrix(C, ldc, N, 2), K > 0 ? check_blocks(A, lda, a_scales, ldas, K) : TG_OK,
+                               K > 0 ? check_blocks(B, ldb, b_scales, ldbs, K) : TG_OK,
+                               K > 0 ? check_plane(plane_b, E, 1) : TG_OK, K > 0 ? check_plane(plane_s, E, 1) : TG_OK,
+                               (M > kMaxTiled || N > kMaxTiled || K > kMaxTiled || E > kMaxExperts) ? TG_ERR_UNSUPPORTED : TG_OK});
+    if (s != TG_OK) return s;
+    if (K == 0) return zero_rows(C, ldc, M, N, stream);
+    tg::GroupArgs a = group_args(M, N, (K + 1) / 2, E, A, lda, offsets, B, ldb, plane_b, 1, C, ldc, epilogue, stream);
+    a.row_blocks = a_scales;
+    a.block_lda = ldas;
+    a.col_blocks = b_scales;
+    a.block_ldb = ldbs;
+    a.block_plane = plane_s;
+    a.blocks = (K + 31) / 32;
+    const int bf16 = type == TG_TYPE_BF16;
+    return static_cast<tg_status>(offsets ? tg::launch_group_mx4(a, bf16) : tg::launch_mx4(a, bf16));
+}
+
+// Logits or their gradient: any pitch, the elements' own alignment.
+tg_status check_logits(const void* p, int64_t ld, int E, int type) {
+    const int eb = type == TG_TYPE_F32 ? 4 : 2;
+    if (!p || ld < E) return TG_ERR_INVALID_ARG;
+    if (ld >= (1ll << 40) / eb) return TG_ERR_UNSUPPORTED;
+    return aligned(p, eb) ? TG_OK : TG_ERR_ALIGNMENT;
+}
+
+// What both directions of the routing check.
+tg_status check_route(int64_t tokens, int E, const void* logits, int64_t ldl, int type, int score, int topk, int renorm,
+                      const void* ids, const void* weights) {
+    if (tokens < 0 || E < 1 || topk < 1 || topk > E) return TG_ERR_INVALID_ARG;
+    if (type != TG_TYPE_F16 && type != TG_TYPE_BF16 && type != TG_TYPE_F32) return TG_ERR_INVALID_ARG;
+    if ((score != TG_SCORE_SOFTMAX && score != TG_SCORE_SIGMOID) || (renorm != 0 && renorm != 1)) return TG_ERR_INVALID_ARG;
+    if (tokens == 0) return E > kMaxExperts || topk > 32 ? TG_ERR_UNSUPPORTED : TG_OK;
+    return worst({check_logits(logits, ldl, E, type), float_ptr(ids), float_ptr(weights),
+                  (tokens > kMaxDim || E > kMaxExperts || topk > 32) ? TG_ERR_UNSUPPORTED : TG_OK});
+}
+
+}  // namespace
+
+tg_status tg_quant_mxfp4(int64_t M, int64_t K, const void* X, int64_t ldx, int type, uint8_t* Q, int64_t ldq,
+                         uint8_t* scales, int64_t lds, void* stream) {
+    if (M < 0 || K < 0 || bad_type(type)) return TG_ERR_INVALID_ARG;
+    if (M == 0 || K == 0) return TG_OK;
+    const tg_status s = worst({check_matrix(X, ldx, K, 2), check_blocks(Q, ldq, scales, lds, K),
+                               (M > kMaxDim || K > kMaxTiled) ? TG_ERR_UNSUPPORTED : TG_OK});
+    if (s != TG_OK) return s;
+    return static_cast<tg_status>(tg::launch_quant_mxfp4(M, K, X, ldx, type == TG_TYPE_BF16, 1, nullptr, nullptr, Q, ldq,
+                                                         scales, lds, stream));
+}
+
+tg_status tg_dequant_mxfp4(int64_t M, int64_t K, const uint8_t* Q, int64_t ldq, const uint8_t* scales, int64_t lds,
+                           void* Y, int64_t ldy, int type, void* stream) {
+    if (M < 0 || K < 0 || bad_type(type)) return TG_ERR_INVALID_ARG;
+    if (M == 0 || K == 0) return TG_OK;
+    const tg_status s = worst({check_matrix(Y, ldy, K, 2), check_blocks(Q, ldq, scales, lds, K),
+                               (M > kMaxDim || K > kMaxTiled) ? TG_ERR_UNSUPPORTED : TG_OK});
+    if (s != TG_OK) return s;
+    return static_cast<tg_status>(tg::launch_dequant_mxfp4(M, K, Q, ldq, scales, lds, Y, ldy, type == TG_TYPE_BF16, stream));
+}
+
+tg_status tg_expert_quant_mxfp4(int64_t tokens, int topk, int64_t K, const void* X, int64_t ldx, int type,
+                                const int32_t* pos, const int32_t* kept, uint8_t* Q, int64_t ldq, uint8_t* scales,
+                                int64_t lds, void* stream) {
+    if (K < 0 || bad_type(type)) return TG_ERR_INVALID_ARG;
+    tg_status s = check_choices(tokens, topk);
+    if (s != TG_OK || tokens == 0 || K == 0) return s;
+    s = worst({check_matrix(X, ldx, K, 2), check_blocks(Q, ldq, scales, lds, K), float_ptr(pos), float_ptr(kept),
+               K > kMaxTiled ? TG_ERR_UNSUPPORTED : TG_OK});
+    if (s != TG_OK) return s;
+    return static_cast<tg_status>(tg::launch_quant_mxfp4(tokens, K, X, ldx, type == TG_TYPE_BF16, topk, pos, kept, Q, ldq,
+                                                         scales, lds, stream));
+}
+
+tg_status tg_gemm_mxfp4(int64_t M, int64_t N, int64_t K, const uint8_t* A, int64_t lda, const uint8_t* a_scales,
+                        int64_t ldas, const uint8_t* B, int64_t ldb, const uint8_t* b_scales, int64_t ldbs, void* C,
+                        int64_t ldc, int type, int epilogue, void* stream) {
+    return mxfp4(M, N, K, 1, A, lda, a_scales, ldas, nullptr, B, ldb, 0, b_scales, ldbs, 0, C, ldc, type, epilogue, stream);
+}
+
+tg_status tg_gemm_grouped_mxfp4(int64_t M, int64_t N, int64_t K, int E, const uint8_t* A, int64_t lda,
+                                const uint8_t* a_scales, int64_t ldas, const int32_t* offsets, const uint8_t* B,
+                                int64_t ldb, int64_t plane_b, const uint8_t* b_scales, int64_t ldbs, int64_t plane_s,
+                                void* C, int64_t ldc, int type, int epilogue, void* stream) {
+    if (M > 0 && N > 0 && float_ptr(offsets) != TG_OK) return float_ptr(offsets);
+    return mxfp4(M, N, K, E, A, lda, a_scales, ldas, offsets, B, ldb, plane_b, b_scales, ldbs, plane_s, C, ldc, type,
+                 epilogue, stream);
+}
+
+tg_status tg_expert_route(int64_t tokens, int E, const void* logits, int64_t ldl, int type, const float* bias, int score,
+                          int groups, int keep_groups, int topk, int renorm, float scale, int32_t* ids, float* weights,
+                          void* stream) {
+    if (groups < 1 || E < 1 || groups > E || E % groups != 0 || keep_groups < 1 || keep_groups > groups) return TG_ERR_INVALID_ARG;
+    if (topk > keep_groups * static_cast<int64_t>(E / groups)) return TG_ERR_INVALID_ARG;
+    tg_status s = check_route(tokens, E, logits, ldl, type, score, topk, renorm, ids, weights);
+    if (s == TG_ERR_INVALID_ARG) return s;
+    s = worst({s, groups > 32 ? TG_ERR_UNSUPPORTED : TG_OK,
+               bias && tokens > 0 ? float_ptr(bias) : TG_OK});
+    if (s != TG_OK || tokens == 0) return s;
+    tg::RouteArgs a = {};
+    a.tokens = tokens; a.E = E; a.groups = groups; a.keep = keep_groups; a.topk = topk;
+    a.type = type; a.sigmoid = score == TG_SCORE_SIGMOID; a.renorm = renorm; a.scale = scale;
+    a.logits = logits; a.ldl = ldl; a.bias = bias; a.ids = ids; a.weights = weights;
+    a.stream = stream;
+    return static_cast<tg_status>(tg::launch_route(a));
+}
+
+tg_status tg_expert_route_grad(int64_t tokens, int E, const void* logits, int64_t ldl, int type, int score, int topk,
+                               int renorm, float scale, const int32_t* ids, const float* dweights, void* dlogits,
+                               int64_t ldd, void* stream) {
+    tg_status s = check_route(tokens, E, logits, ldl, type, score, topk, renorm, ids, dweights);
+    if (s == TG_ERR_INVALID_ARG || tokens == 0) return s;
+    s = worst({s, check_logits(dlogits, ldd, E, type)});
+    if (s != TG_OK) return s;
+    tg::RouteArgs a = {};
+    a.tokens = tokens; a.E = E; a.groups = 1; a.keep = 1; a.topk = topk;
+    a.type = type; a.sigmoid = score == TG_SCORE_SIGMOID; a.renorm = renorm; a.scale = scale;
+    a.logits = logits; a.ldl = ldl; a.ids = const_cast<int32_t*>(ids); a.dweights = dweights;
+    a.dlogits = dlogits; a.ldd = ldd;
+    a.stream = stream;
+    return static_cast<tg_status>(tg::launch_route_grad(a));
 }
 
 }  // extern "C"

@@ -27,14 +27,20 @@ GrpParams params(const GroupArgs& a) {
     p.row_scale = a.row_scale;
     p.col_scale = a.col_scale;
     p.scale_plane = a.scale_plane;
+    p.row_blocks = a.row_blocks;
+    p.col_blocks = a.col_blocks;
+    p.block_lda = a.block_lda;
+    p.block_ldb = a.block_ldb;
+    p.block_plane = a.E > 1 ? a.block_plane : 0;
+    p.blocks = static_cast<int>(a.blocks);
     return p;
 }
 
-// At most one item per 256 rows and one more per group with rows (the rows
+// At most one item per `rows` rows and one more per group with rows (the rows
 // behind the last group included), times the 256-column tiles.
-long long max_items(const GroupArgs& a) {
+long long max_items(const GroupArgs& a, int rows) {
     const long long groups = a.offsets ? (a.E + 1 < a.g.M ? a.E + 1 : a.g.M) : 1;
-    return (a.g.M / 256 + groups) * ((a.g.N - 1) / 256 + 1);
+    return (a.g.M / rows + groups) * ((a.g.N - 1) / 256 + 1);
 }
 
 template <class Cfg>
@@ -69,7 +75,7 @@ int run_product(const GroupArgs& a, CUtensorMapDataType dt, int slot) {
     if (pair_kernels_disabled()) return kUnsupported;
     const DeviceInfo* di = current_device(nullptr);
     if (!di) return kNoDevice;
-    const long long items = max_items(a);
+    const long long items = max_items(a, Cfg::ROWS);
     if (items > 0x7fffffffll) return kUnsupported;
     constexpr int eb = Cfg::EB;
     const GemmArgs& g = a.g;
@@ -127,6 +133,11 @@ int launch_group_grad(const GroupArgs& a, int bf16) {
     if (a.g.M < 256ll * a.E)
         return bf16 ? run_grad<GrpCfg<1, OutT::BF16, 1, 1, 8>>(a, tb, 74) : run_grad<GrpCfg<0, OutT::F16, 1, 1, 8>>(a, th, 75);
     return bf16 ? run_grad<GrpCfg<1, OutT::BF16, 1, 1, 4>>(a, tb, 80) : run_grad<GrpCfg<0, OutT::F16, 1, 1, 4>>(a, th, 81);
+}
+
+int launch_group_mx4(const GroupArgs& a, int bf16) {
+    constexpr CUtensorMapDataType dt = CU_TENSOR_MAP_DATA_TYPE_UINT8;
+    return bf16 ? run_product<GrpCfg<4, OutT::BF16, 0>>(a, dt, 98) : run_product<GrpCfg<4, OutT::F16, 0>>(a, dt, 99);
 }
 
 int launch_group_i8(const GroupArgs& a, int bf16) {

@@ -8,6 +8,9 @@
 //   product (WG = 0):          C[r][n]    = epi( sum_k A[r][k] * W_e[k][n] )
 //   weight gradient (WG = 1):  C_e[k][n]  = sum_{r in group e} A[r][k] * G[r][n]
 //
+// 4-bit operands (E2M1 in blocks of 32 k with E8M0 scales): the tensor cores
+// multiply by the scales (kind::mxf4), sums are fp32.
+//
 // 8-bit operands: the sum is an exact 32-bit integer, and
 // C[r][n] = epi( (sum * row_scale[r]) * col_scale_e[n] ), in fp32, rounded once.
 //
@@ -53,6 +56,7 @@
 // power limit, at 1.1 to 1.7 GHz.
 #pragma once
 #include "gemm_tc.cuh"
+#include "block_scales.cuh"
 
 namespace tg {
 
@@ -73,9 +77,15 @@ struct GrpParams {
     const float* row_scale;   // 8-bit: one per row of A
     const float* col_scale;   // 8-bit: one per column, scale_plane apart per group
     long long scale_plane;
+    // 4-bit (K in bytes, two values each): a row's scale bytes, one per 32 values
+    const uint8_t* row_blocks;  // M rows of A, block_lda bytes apart
+    const uint8_t* col_blocks;  // N rows of W_e, block_ldb apart, block_plane per group
+    long long block_lda, block_ldb, block_plane;
+    int blocks;               // scale bytes in a row
 };
 
-// TYPE: 0 f16, 1 bf16 (idesc formats), 3 signed 8-bit.  W_MN = 1: the weights
+// TYPE: 0 f16, 1 bf16 (idesc formats), 3 signed 8-bit, 4 4-bit floating point
+// with block scales (only K-major; k counts bytes, two values each).  W_MN = 1: the weights
 // are stored K x N, their tiles MN-major; 0: N x K, K-major.  WG: the weight
 // gradient (16-bit; both operands MN-major).  EPI: epilogue warps, one or two
 // to each quarter of the lanes.
@@ -86,12 +96,20 @@ struct GrpCfg {
     static constexpr int W_MN = W_MN_;
     static constexpr int WG = WG_;
     static constexpr bool I8 = TYPE_ == 3;
-    static constexpr int EB = I8 ? 1 : 2;               // operand bytes
+    static constexpr bool MX = TYPE_ == 4;
+    static constexpr int EB = I8 || MX ? 1 : 2;         // operand bytes
     static constexpr int BK = 128 / EB;                 // k per stage: one 128-byte swizzle row
     static constexpr int MMA_K = 32 / EB;               // k per MMA: 16 or 32
     static constexpr int STEPS = BK / MMA_K;            // MMAs per stage
     static constexpr int CHUNK = 128 / EB;              // columns per MN-major box row
-    static constexpr int STAGES = 6;
+    static constexpr int STAGES = MX ? 5 : 6;
+    // 4-bit: a chunk is 512 k, 16 scale bytes of every row and two stages.  Four
+    // warps take the chunks in turn, each with a slot of its own: the scales of
+    // 128 lanes and of up to 256 rows, four words of four blocks a row.
+    static constexpr int SF_WARPS = MX ? 4 : 0;
+    static constexpr int SF_WORDS = 3 * 512;            // one word of every row
+    static constexpr int SF_SLOT = 4 * SF_WORDS;
+    static constexpr int SF_COLS = 24;                  // tensor memory of a stage's scales
     static constexpr int A_STAGE = 128 * 128;           // 128 lanes' operand, either major-ness
     static constexpr int B_STAGE = 128 * 128;           // up to 128 of the N side
     static constexpr int EPI_WARPS = EPI_;
@@ -99,16 +117,19 @@ struct GrpCfg {
     static_assert(EPI_ == 4 || EPI_ == 8, "epilogue warps");
     static constexpr int FIX_WARPS = WG_ ? 1 : 0;
     static constexpr int PRODUCERS = 2;                 // warp 0, and the first behind the epilogue
-    static_assert(STAGES % PRODUCERS == 0, "a producer keeps its own ring slots");
-    static constexpr int THREADS = 32 * (1 + PRODUCERS + EPI_WARPS + FIX_WARPS);
+    static constexpr int THREADS = 32 * (1 + PRODUCERS + EPI_WARPS + FIX_WARPS + SF_WARPS);
     static constexpr int STG_BUF = WG_ ? 4096 : 2048;   // a warp's [32 rows][128 bytes] or [32 rows][32 columns]
     static constexpr int NBUF = WG_ ? 8 / EPI_ : 1;     // staging tiles a warp
-    static constexpr int TMEM_COLS = 512;               // two accumulators of 256 columns
+    static constexpr int TMEM_COLS = 512;               // two accumulators of ROWS columns
+    static constexpr int ROWS = MX ? 224 : 256;         // most rows a tile: 4-bit scales take 48 columns
+    static constexpr int TMEM_SF = 2 * ROWS;
+    static_assert(!MX || TMEM_SF + 2 * SF_COLS <= TMEM_COLS, "tensor memory");
     static constexpr int TABLE = WG_ ? 0 : (4 * (kMaxGroups + 2)) * 4;
-    static constexpr int SMEM_DATA = STAGES * (A_STAGE + B_STAGE) + EPI_WARPS * NBUF * STG_BUF;
+    static constexpr int SMEM_DATA = STAGES * (A_STAGE + B_STAGE) + EPI_WARPS * NBUF * STG_BUF + SF_WARPS * SF_SLOT;
     static constexpr int SMEM_BYTES = SMEM_DATA + 512 + TABLE + 1024;
     static_assert(SMEM_BYTES <= 227 * 1024, "shared memory per CTA");
-    static_assert(!(I8 && WG_), "the 8-bit product has no gradient");
+    static_assert(!(EB == 1 && WG_), "the 8-bit and 4-bit products have no gradient");
+    static_assert(!(MX && W_MN_), "4-bit operands are K-major");
 };
 
 // 16 bytes of zeros at a shared::cluster address, possibly in the peer CTA.
@@ -158,6 +179,9 @@ __device__ __forceinline__ void grp_store_rows(const GrpParams& p, const GrpItem
             // a NaN (of the row's scale) stays one under ReLU; fmaxf would hide it,
             // and a comparison takes 2048 x 8192 x 1024 from 22.6 to 23.8 us
             const float x = (__int2float_rn(static_cast<int>(v)) * rs) * c;
+            return p.relu ? max_nan(x, 0.f) : x;
+        } else if constexpr (Cfg::MX) {
+            const float x = __uint_as_float(v);
             return p.relu ? max_nan(x, 0.f) : x;
         } else {
             const float x = __uint_as_float(v);
@@ -293,13 +317,16 @@ grp_gemm_kernel(const __grid_constant__ CUtensorMap tmA,
     uint8_t* smA = smem;
     uint8_t* smB = smA + Cfg::STAGES * Cfg::A_STAGE;
     uint8_t* smStg = smB + Cfg::STAGES * Cfg::B_STAGE;
-    uint64_t* full = reinterpret_cast<uint64_t*>(smStg + Cfg::EPI_WARPS * Cfg::NBUF * Cfg::STG_BUF);
+    uint8_t* smSf = smStg + Cfg::EPI_WARPS * Cfg::NBUF * Cfg::STG_BUF;
+    uint64_t* full = reinterpret_cast<uint64_t*>(smSf + Cfg::SF_WARPS * Cfg::SF_SLOT);
     uint64_t* empty = full + Cfg::STAGES;
     uint64_t* cut = empty + Cfg::STAGES;        // WG: a block that ends inside an MMA step has landed
     uint64_t* tfull = cut + Cfg::STAGES;
     uint64_t* tempty = tfull + 2;
     uint64_t* drain = tempty + 2;
-    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
+    uint64_t* sfull = drain + 1;                // 4-bit: a chunk's scales are there, in both CTAs
+    uint64_t* sempty = sfull + Cfg::SF_WARPS;
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(sempty + Cfg::SF_WARPS);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
     int* gcount = const_cast<int*>(abort_flag) + 1;
     int* gstart = gcount + 1;                   // product: first item of each group that has rows
@@ -325,6 +352,7 @@ grp_gemm_kernel(const __grid_constant__ CUtensorMap tmA,
             mbar_init(&cut[s], 2);
         }
         for (int a = 0; a < 2; ++a) { mbar_init(&tfull[a], 1); mbar_init(&tempty[a], 2 * Cfg::EPI_WARPS); }
+        for (int i = 0; i < Cfg::SF_WARPS; ++i) { mbar_init(&sfull[i], 2); mbar_init(&sempty[i], 1); }
         mbar_init(drain, 1);
         *abort_flag = 0;
         fence_mbar_init();
@@ -366,7 +394,7 @@ grp_gemm_kernel(const __grid_constant__ CUtensorMap tmA,
                 reached = __shfl_sync(0xffffffffu, low, 31);
                 r0 = low;
                 r1 = max(r1, r0);
-                if (r1 > r0) cnt = grp_tiles(r1 - r0) * ntl;
+                if (r1 > r0) cnt = grp_tiles(r1 - r0, Cfg::ROWS) * ntl;
                 int sum = cnt;
 #pragma unroll
                 for (int d = 1; d < 32; d <<= 1) {
@@ -426,8 +454,8 @@ grp_gemm_kernel(const __grid_constant__ CUtensorMap tmA,
             it.r0 = grow[g];
             it.rows = r1 - it.r0;
             int tl, tt, at;
-            tile_coords(w - gstart[g], ntl, grp_tiles(it.rows), p.group_m, tl, tt);
-            grp_tile(it.rows, tt, at, it.width);
+            tile_coords(w - gstart[g], ntl, grp_tiles(it.rows, Cfg::ROWS), p.group_m, tl, tt);
+            grp_tile(it.rows, tt, at, it.width, Cfg::ROWS);
             it.n0 = tl * 256;
             it.m0 = it.r0 + at;
             it.m1 = min(r1, it.m0 + it.width);
@@ -540,8 +568,9 @@ grp_gemm_kernel(const __grid_constant__ CUtensorMap tmA,
         if (rank == 0 && elect_one()) {
             constexpr int A_MN = Cfg::WG || Cfg::W_MN;
             constexpr uint32_t idesc0 = Cfg::I8 ? make_idesc_i8(256, 0, A_MN, 0)
+                                      : Cfg::MX ? make_idesc_mx4(256, 0)
                                                 : make_idesc(Cfg::TYPE, 256, 0, A_MN, Cfg::WG);
-            uint32_t ld = 0, tl = 0;
+            uint32_t ld = 0, tl = 0, chunk = 0;
             bool ok = true;
             int g = 0;
             for (int w = pair; w < num_items && ok; w += npairs) {
@@ -552,7 +581,7 @@ grp_gemm_kernel(const __grid_constant__ CUtensorMap tmA,
                 ++tl;
                 if (!bounded_wait(&tempty[acc], aph ^ 1, abort_flag, limit, p.status)) { ok = false; break; }
                 tc_fence_after();
-                const uint32_t d_tmem = tmem_base + acc * 256;
+                const uint32_t d_tmem = tmem_base + acc * Cfg::ROWS;
                 const uint32_t idesc = idesc0 | (static_cast<uint32_t>(it.width >> 3) << 17);
                 for (int kb = 0; kb < it.kb; ++kb, ++ld) {
                     const uint32_t s = ld % Cfg::STAGES;
@@ -561,6 +590,28 @@ grp_gemm_kernel(const __grid_constant__ CUtensorMap tmA,
                     tc_fence_after();
                     const uint32_t a_addr = smem_u32(smA + s * Cfg::A_STAGE);
                     const uint32_t b_addr = smem_u32(smB + s * Cfg::B_STAGE);
+                    uint32_t sf = 0;                             // this stage's scales in tensor memory
+                    if constexpr (Cfg::MX) {
+                        const uint32_t slot = chunk % Cfg::SF_WARPS;
+                        if (!(kb & 1)) {
+                            if (!bounded_wait_cluster(&sfull[slot], (chunk / Cfg::SF_WARPS) & 1, abort_flag, limit, p.status)) {
+                                ok = false;
+                                break;
+                            }
+                            tc_fence_after();
+                        }
+                        // two sets of columns in turn: a stage's copies do not wait for
+                        // the MMAs of the one before
+                        sf = tmem_base + Cfg::TMEM_SF + (ld & 1) * Cfg::SF_COLS;
+                        const uint32_t src = smem_u32(smSf + slot * Cfg::SF_SLOT) + (kb & 1) * 2 * Cfg::SF_WORDS;
+#pragma unroll
+                        for (int j = 0; j < 2; ++j) {
+                            tmem_cp_scales_pair(sf + 4 * j, scale_desc(src + j * Cfg::SF_WORDS));
+                            tmem_cp_scales_pair(sf + 8 + 8 * j, scale_desc(src + j * Cfg::SF_WORDS + 512));
+                            if (it.width > 128)
+                                tmem_cp_scales_pair(sf + 12 + 8 * j, scale_desc(src + j * Cfg::SF_WORDS + 1024));
+                        }
+                    }
                     const int steps = Cfg::WG && kb == it.kb - 1
                         ? (last_rows(it) + Cfg::MMA_K - 1) / Cfg::MMA_K : Cfg::STEPS;
 #pragma unroll
@@ -575,11 +626,22 @@ grp_gemm_kernel(const __grid_constant__ CUtensorMap tmA,
                             ? sw128_desc(b_addr + k * Cfg::MMA_K * 128, Cfg::BK * 128, 1024)
                             : sw128_desc(b_addr + k * 32, 16, 1024);
                         if constexpr (Cfg::I8) mma_i8_pair(d_tmem, ad, bd, idesc, kb != 0 || k != 0);
+                        else if constexpr (Cfg::MX)
+                            mma_mx4_pair(d_tmem, ad, bd, idesc | mx4_scale_id(k & 1), kb != 0 || k != 0,
+                                         sf + 4 * (k >> 1), sf + 8 + 8 * (k >> 1));
                         else mma_f16_pair(d_tmem, ad, bd, idesc, kb != 0 || k != 0);
                     }
                     const uint32_t e_loc = smem_u32(&empty[s]);
                     mma_commit_pair(mapa_shared(e_loc, 0));      // both CTAs' slots
                     mma_commit_pair(mapa_shared(e_loc, 1));
+                    if constexpr (Cfg::MX) {
+                        if ((kb & 1) || kb == it.kb - 1) {
+                            const uint32_t s_loc = smem_u32(&sempty[chunk % Cfg::SF_WARPS]);
+                            mma_commit_pair(mapa_shared(s_loc, 0));
+                            mma_commit_pair(mapa_shared(s_loc, 1));
+                            ++chunk;
+                        }
+                    }
                 }
                 if (!ok) break;
                 const uint32_t f_loc = smem_u32(&tfull[acc]);
@@ -609,7 +671,7 @@ grp_gemm_kernel(const __grid_constant__ CUtensorMap tmA,
                 if (!bounded_wait(&tfull[acc], aph, abort_flag, limit + it.kb * 4096ull, p.status)) break;
                 tc_fence_after();
             }
-            const uint32_t taddr = tmem_base + acc * 256 + (static_cast<uint32_t>(q * 32) << 16);
+            const uint32_t taddr = tmem_base + acc * Cfg::ROWS + (static_cast<uint32_t>(q * 32) << 16);
             const int l0 = it.n0 + static_cast<int>(rank) * 128 + q * 32;
             if constexpr (Cfg::WG) grp_store_grad<Cfg>(&tmC, p, it, taddr, l0, half, lane, stg, nstore);
             else grp_store_rows<Cfg>(p, it, taddr, l0, half, lane, stg);
@@ -624,6 +686,52 @@ grp_gemm_kernel(const __grid_constant__ CUtensorMap tmA,
             __syncwarp();
         }
     } else {
+        if constexpr (Cfg::MX) {
+            // ---------------------------------------- block scales (4-bit, both)
+            // Row r's word w (four blocks) goes to 16 * (r % 32) + 4 * (r / 32 % 4) of
+            // the 512 bytes that become columns of tensor memory.  Plain loads take
+            // rows from any place in a row-major matrix, and bytes past a row's last
+            // block become 0: the copy engine's zeros beside them must not meet a NaN.
+            const int turn = warp - (3 + Cfg::EPI_WARPS);
+            uint8_t* slot = smSf + turn * Cfg::SF_SLOT + lane * 16;
+            uint32_t chunk = 0, uses = 0;
+            bool ok = true;
+            int g = 0;
+            for (int w = pair; w < num_items && ok; w += npairs) {
+                const GrpItem it = item(w, g);
+                const int chunks = (it.kb + 1) / 2;
+                for (int c = 0; c < chunks; ++c, ++chunk) {
+                    if (static_cast<int>(chunk % Cfg::SF_WARPS) != turn) continue;
+                    const int n0 = it.n0 + static_cast<int>(rank) * 128 + lane;
+                    const uint8_t* cols = p.col_blocks + it.e * p.block_plane + 16ll * c;
+                    const uint8_t* rows = p.row_blocks + 16ll * c;
+                    const int left = p.blocks - 16 * c;
+                    uint4 v[12];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        v[i] = load_blocks(cols + (n0 + 32 * i) * p.block_ldb, left, p.N - (n0 + 32 * i));
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        const int m = it.m0 + 32 * i + lane;
+                        v[4 + i] = load_blocks(rows + m * p.block_lda, left, m < it.m1 ? p.M - m : 0);
+                    }
+                    if (!bounded_wait(&sempty[turn], (uses & 1) ^ 1, abort_flag, limit, p.status)) { ok = false; break; }
+                    ++uses;
+#pragma unroll
+                    for (int i = 0; i < 12; ++i) {
+                        uint8_t* dst = slot + (i / 4) * 512 + (i % 4) * 4;
+                        *reinterpret_cast<uint32_t*>(dst) = v[i].x;
+                        *reinterpret_cast<uint32_t*>(dst + Cfg::SF_WORDS) = v[i].y;
+                        *reinterpret_cast<uint32_t*>(dst + 2 * Cfg::SF_WORDS) = v[i].z;
+                        *reinterpret_cast<uint32_t*>(dst + 3 * Cfg::SF_WORDS) = v[i].w;
+                    }
+                    // the copies into both CTAs' tensor memory are issued by the leader
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive_release_cluster(mapa_shared(smem_u32(&sfull[turn]), 0));
+                }
+            }
+        }
         // ------------------------------------------ fix-up (WG, leader only)
         if constexpr (Cfg::WG) {
             uint32_t ld = 0, seen = 0;                  // seen: parity of each slot's cut barrier

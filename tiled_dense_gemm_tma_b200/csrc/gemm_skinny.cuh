@@ -44,9 +44,14 @@
 //   and its column's scale.  They never take stream-K: no workspace.  Bound by
 //   the weight stream: 1 x 8192 x 8192 16.4 us cold, 4.1 TB/s on 128 CTAs (the
 //   CTA-pair kernel of gemm_group.cuh, 32 pairs there: 23.4).
+// * 4-bit weights and activations with block scales (kind::mxf4, both K-major):
+//   a 128-byte row holds 256 k, a unit is 512 k and 16 scale bytes of each row,
+//   which four more warps bring into the slot, already in the order of tensor
+//   memory; the MMA thread copies them there.  Never stream-K either.
 #pragma once
 #include "ptx.cuh"
 #include "dequant.cuh"
+#include "block_scales.cuh"
 #include "tile_sched.h"     // sk_begin / sk_owner / cl_begin / cl_split
 #include "host.cuh"         // max_active_clusters
 #include <cuda_bf16.h>
@@ -57,8 +62,9 @@ namespace tg {
 // Weight kinds: 16-bit weights, signed 4-bit integers with fp16 group scales
 // (fp16 activations and output), FP4 E2M1 codes with E8M0 block scales
 // (bf16 activations and output), signed 8-bit weights and activations with a
-// scale per row and column (f16 or bf16 output, SkParams::out_bf16).
-enum class WKind { F16 = 0, BF16 = 1, INT4 = 2, FP4 = 3, I8 = 4 };
+// scale per row and column (f16 or bf16 output, SkParams::out_bf16), E2M1 weights
+// and activations with a scale per 32 k (the same outputs).
+enum class WKind { F16 = 0, BF16 = 1, INT4 = 2, FP4 = 3, I8 = 4, MX4 = 5 };
 
 // WK_ = 1: 16-bit weights stored transposed (B is N x K row-major, the
 // op(B) = B^T of a transposed-operand call): each weight tile arrives as
@@ -73,20 +79,22 @@ struct SkCfg {
     static constexpr bool Q4 = W_ == WKind::INT4 || W_ == WKind::FP4;   // packed 4-bit weights
     static constexpr bool FP4 = W_ == WKind::FP4;
     static constexpr bool I8 = W_ == WKind::I8;
+    static constexpr bool MX = W_ == WKind::MX4;        // k below counts bytes, two values each
+    static constexpr bool BYTES = I8 || MX;
     // activation, MMA operand and output type
     static constexpr WKind OUTW = (W_ == WKind::BF16 || W_ == WKind::FP4) ? WKind::BF16 : WKind::F16;
     // k rows per unit: 16-bit weights come in 128-row boxes (taller TMA
     // copies stream faster; 8-bit: 256 rows), 4-bit weights in 64-row slices
-    static constexpr int BK = Q4 ? 64 : I8 ? 256 : 128;
-    static constexpr int KW = I8 ? 128 : 64;            // k in a 128-byte activation row
+    static constexpr int BK = Q4 ? 64 : BYTES ? 256 : 128;
+    static constexpr int KW = BYTES ? 128 : 64;         // k in a 128-byte activation row
     static constexpr int KSL = BK / KW;                 // activation k-slices per unit
-    static constexpr int MMA_K = I8 ? 32 : 16;          // k per MMA
+    static constexpr int MMA_K = BYTES ? 32 : 16;       // k per MMA
     // 4-bit units span two 128-column sub-tiles so packed rows arrive as
     // 128-byte runs (narrower rows stream markedly slower from HBM)
     static constexpr int NSUB = Q4 ? 2 : 1;
     static constexpr int GN = NSUB * TN;                // weight columns per unit
     static constexpr int W_CHUNK = BK * 128;            // 64 (8-bit: 128) columns x BK rows, bytes
-    static constexpr int W_BYTES = (I8 ? 1 : NSUB * 2) * W_CHUNK;   // weight tile of one unit
+    static constexpr int W_BYTES = (BYTES ? 1 : NSUB * 2) * W_CHUNK;   // weight tile of one unit
     static constexpr int X_SLICE = MPAD * 128;          // MPAD rows x 64 fp16
     static constexpr int X_BYTES = KSL * X_SLICE;
     static constexpr int Q_BYTES = Q4 ? BK * GN / 2 : 0;   // 8 KB packed
@@ -97,7 +105,12 @@ struct SkCfg {
     // 4-bit weights: [Q | S], released by the converters as soon as they have
     // expanded it into a second ring of fp16 tiles; the activations then
     // travel in a ring of their own, released by the MMA.
-    static constexpr int RAW_SLOT_USED = Q4 ? (Q_BYTES + S_BYTES) : (X_BYTES + W_BYTES);
+    // block scales of a unit: four words of four blocks, each 512 bytes for the
+    // 128 columns and 512 for the activation rows
+    static constexpr int SF_WORDS = 1024;
+    static constexpr int SF_BYTES = MX ? 4 * SF_WORDS : 0;
+    static constexpr int SF_WARPS = MX ? 4 : 0;
+    static constexpr int RAW_SLOT_USED = Q4 ? (Q_BYTES + S_BYTES) : (X_BYTES + W_BYTES + SF_BYTES);
     static constexpr int RAW_SLOT = (RAW_SLOT_USED + 1023) / 1024 * 1024;   // swizzle alignment
     // the fp16 tiles only bridge converters and MMA (on-chip latency): two
     // suffice, which leaves the shared memory to packed weights in flight
@@ -111,7 +124,7 @@ struct SkCfg {
     // rows per warp the reducer sums per round (registers allow more with the
     // 6-warp 16-bit kernel than beside the 4-bit converters)
     static constexpr int RED_ROWS = Q4 ? 2 : 8;
-    static constexpr int THREADS = 32 * (2 + EPI_WARPS + CONV_WARPS);
+    static constexpr int THREADS = 32 * (2 + EPI_WARPS + CONV_WARPS + SF_WARPS);
     // Split-K inside a cluster: a CTA's ring, idle once its accumulator is
     // final, receives the partials of the columns it owns from every rank
     // ([rank][MPAD rows][GN/S columns] fp32, MPAD x GN floats in all).
@@ -120,9 +133,11 @@ struct SkCfg {
     // Independent accumulator sets: k-step kk of a unit accumulates into set
     // kk % R, so consecutive small MMAs do not wait on each other's result;
     // the epilogue adds the R sets in a fixed order.
-    static constexpr int R = (2 * NSUB * MPAD * 4 <= 512) ? 4 : (2 * NSUB * MPAD * 2 <= 512) ? 2 : 1;
+    static constexpr int R = MX ? 1 : (2 * NSUB * MPAD * 4 <= 512) ? 4 : (2 * NSUB * MPAD * 2 <= 512) ? 2 : 1;
     static constexpr int ACC_COLS = R * NSUB * MPAD;          // one accumulator buffer
-    static constexpr int TMEM_USED = 2 * ACC_COLS;
+    // two units' scales in turn, 4 columns for each word of the columns and rows
+    static constexpr int SF_COLS = MX ? 32 : 0;
+    static constexpr int TMEM_USED = 2 * ACC_COLS + 2 * SF_COLS;
     static constexpr int TMEM_COLS = TMEM_USED <= 32 ? 32 : TMEM_USED <= 64 ? 64 :
                                      TMEM_USED <= 128 ? 128 : TMEM_USED <= 256 ? 256 : 512;
     static_assert(TMEM_USED <= 512, "TMEM");
@@ -158,7 +173,11 @@ struct SkParams {
     int* tickets;             // [T], zero between calls
     const float* row_scale;   // 8-bit: M
     const float* col_scale;   // 8-bit: N
-    int out_bf16;             // 8-bit: C's type
+    int out_bf16;             // 8-bit, 4-bit blocks: C's type
+    const uint8_t* row_blocks;  // 4-bit blocks: scale bytes of the M rows, of the N weight rows
+    const uint8_t* col_blocks;
+    long long block_lda, block_ldb;
+    int blocks;               // in a row
 };
 
 template <WKind W>
@@ -217,6 +236,21 @@ __device__ __forceinline__ void store_scaled4(const SkParams& p, int m, int n, c
     else store_out4<WKind::F16>(p.C, p.ldc, m, n, p.N, o);
 }
 
+// 4-bit blocks: one output, or four neighbouring ones.  A NaN stays one under ReLU.
+__device__ __forceinline__ void store_blocks(const SkParams& p, int m, int n, float x) {
+    if (p.relu) x = max_nan(x, 0.f);
+    if (p.out_bf16) store_out<WKind::BF16>(p.C, p.ldc, m, n, x);
+    else store_out<WKind::F16>(p.C, p.ldc, m, n, x);
+}
+
+__device__ __forceinline__ void store_blocks4(const SkParams& p, int m, int n, float (&o)[4]) {
+    if (p.relu)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) o[e] = max_nan(o[e], 0.f);
+    if (p.out_bf16) store_out4<WKind::BF16>(p.C, p.ldc, m, n, p.N, o);
+    else store_out4<WKind::F16>(p.C, p.ldc, m, n, p.N, o);
+}
+
 // tmW: fp16/bf16 weights (N x K view: 64-column boxes of BK rows), or the
 //      packed 4-bit weights (64-byte boxes of BK rows) for INT4;
 // tmS: scales (INT4 only); tmX: activations, K-major boxes of 64 x MPAD.
@@ -253,6 +287,7 @@ skinny_kernel(const __grid_constant__ CUtensorMap tmW,
     // slot layout: 16-bit weights [W | X]; 4-bit weights [Q | S] (X in xring)
     auto slot_x = [&](int s) { return ring + s * Cfg::RAW_SLOT + Cfg::W_BYTES; };
     auto slot_w = [&](int s) { return ring + s * Cfg::RAW_SLOT; };
+    auto slot_sf = [&](int s) { return ring + s * Cfg::RAW_SLOT + Cfg::W_BYTES + Cfg::X_BYTES; };
     auto slot_q = [&](int s) { return ring + s * Cfg::RAW_SLOT; };
     auto slot_s = [&](int s) { return ring + s * Cfg::RAW_SLOT + Cfg::Q_BYTES; };
 
@@ -277,7 +312,7 @@ skinny_kernel(const __grid_constant__ CUtensorMap tmW,
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < Cfg::RAW_STAGES; ++s) {
-            mbar_init(&full[s], 1);
+            mbar_init(&full[s], Cfg::MX ? 2 : 1);        // block scales come from a warp of their own
             mbar_init(&rempty[s], Cfg::Q4 ? Cfg::CONV_WARPS : 1);
         }
         for (int s = 0; s < Cfg::W_STAGES; ++s) {
@@ -395,6 +430,7 @@ skinny_kernel(const __grid_constant__ CUtensorMap tmW,
         if (elect_one()) {
             constexpr uint32_t fmt = Cfg::OUTW == WKind::BF16 ? 1u : 0u;
             constexpr uint32_t idesc = Cfg::I8 ? make_idesc_i8(Cfg::TN, Cfg::MPAD, Cfg::WK ? 0 : 1, 0)
+                                     : Cfg::MX ? make_idesc_mx4(Cfg::TN, Cfg::MPAD)
                                                : make_idesc(fmt, Cfg::TN, Cfg::MPAD, Cfg::WK ? 0 : 1, 0);
             bool ok = true;
             int it = 0, seg = 0;
@@ -432,6 +468,15 @@ skinny_kernel(const __grid_constant__ CUtensorMap tmW,
                     x_addr = smem_u32(slot_x(s));
                 }
                 tc_fence_after();
+                const uint32_t sf = tmem_base + 2 * Cfg::ACC_COLS + (it & 1) * Cfg::SF_COLS;
+                if constexpr (Cfg::MX) {
+                    const uint32_t src = smem_u32(slot_sf(s));
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        tmem_cp_scales(sf + 8 * j, scale_desc(src + j * Cfg::SF_WORDS));
+                        tmem_cp_scales(sf + 8 * j + 4, scale_desc(src + j * Cfg::SF_WORDS + 512));
+                    }
+                }
 #pragma unroll
                 for (int j = 0; j < Cfg::NSUB; ++j) {
 #pragma unroll
@@ -447,6 +492,9 @@ skinny_kernel(const __grid_constant__ CUtensorMap tmW,
                         const int set = k % Cfg::R;
                         if constexpr (Cfg::I8)
                             mma_i8(d_tmem + set * Cfg::MPAD, ad, bd, idesc, (first && k < Cfg::R) ? 0u : 1u);
+                        else if constexpr (Cfg::MX)
+                            mma_mx4(d_tmem, ad, bd, idesc | mx4_scale_id(k & 1), (first && k == 0) ? 0u : 1u,
+                                    sf + 8 * (k >> 1), sf + 8 * (k >> 1) + 4);
                         else
                             mma_f16(d_tmem + (set * Cfg::NSUB + j) * Cfg::MPAD, ad, bd, idesc,
                                     (first && k < Cfg::R) ? 0u : 1u);
@@ -546,6 +594,10 @@ skinny_kernel(const __grid_constant__ CUtensorMap tmW,
                                 continue;
                             }
                             const float x = __uint_as_float(v[i]);
+                            if constexpr (Cfg::MX) {
+                                if (n < p.N) store_blocks(p, m, n, x);
+                                continue;
+                            }
                             if (n < p.N) store_out<Cfg::OUTW>(p.C, p.ldc, m, n, p.relu ? fmaxf(x, 0.f) : x);
                         }
                     } else if (cl) {
@@ -609,6 +661,10 @@ skinny_kernel(const __grid_constant__ CUtensorMap tmW,
                             x.x += v4.x; x.y += v4.y; x.z += v4.z; x.w += v4.w;
                         }
                     float o[4] = {x.x, x.y, x.z, x.w};
+                    if constexpr (Cfg::MX) {
+                        store_blocks4(p, m, n, o);
+                        continue;
+                    }
                     if (p.relu)
 #pragma unroll
                         for (int e = 0; e < 4; ++e) o[e] = fmaxf(o[e], 0.f);
@@ -616,7 +672,7 @@ skinny_kernel(const __grid_constant__ CUtensorMap tmW,
                 }
                 continue;
             }
-            if constexpr (Cfg::I8) break;                     // whole groups or cluster splits only
+            if constexpr (Cfg::BYTES) break;                     // whole groups or cluster splits only
             // Publish the partial, take a ticket; the tile's last contributor
             // reduces.  The epilogue warps meet on mbarriers with bounded waits
             // (never an unbounded bar.sync, which a warp that gave up would hang).
@@ -696,6 +752,45 @@ skinny_kernel(const __grid_constant__ CUtensorMap tmW,
             }
         }
     } else {
+        // ----------------------------------- block scales (4-bit blocks only)
+        // Row r's word w goes to 16 * (r % 32) + 4 * (r / 32) of its 512 bytes;
+        // bytes past a row's last block become 0 (as in gemm_group.cuh).
+        if constexpr (Cfg::MX) {
+            constexpr int XR = (Cfg::MPAD + 31) / 32;
+            const int turn = warp - (2 + Cfg::EPI_WARPS);
+            int it = 0;
+            for (int u = u0; u < u1; ++u, ++it) {
+                if (it % Cfg::SF_WARPS != turn) continue;
+                const int t = u / KB, kb = u - (u / KB) * KB;
+                const int s = it % Cfg::RAW_STAGES;
+                const uint32_t ph = (it / Cfg::RAW_STAGES) & 1;
+                const int left = p.blocks - 16 * kb;
+                uint4 v[4 + XR];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int n = t * Cfg::TN + 32 * i + lane;
+                    v[i] = load_blocks(p.col_blocks + n * p.block_ldb + 16ll * kb, left, p.N - n);
+                }
+#pragma unroll
+                for (int i = 0; i < XR; ++i) {
+                    const int m = 32 * i + lane;
+                    v[4 + i] = load_blocks(p.row_blocks + m * p.block_lda + 16ll * kb, left, p.M - m);
+                }
+                if (!bounded_wait(&rempty[s], ph ^ 1, abort_flag, limit, p.status)) break;
+                uint8_t* slot = slot_sf(s) + lane * 16;
+#pragma unroll
+                for (int i = 0; i < 4 + XR; ++i) {
+                    uint8_t* dst = slot + i * 4 + (i < 4 ? 0 : 512 - 16);
+                    *reinterpret_cast<uint32_t*>(dst) = v[i].x;
+                    *reinterpret_cast<uint32_t*>(dst + Cfg::SF_WORDS) = v[i].y;
+                    *reinterpret_cast<uint32_t*>(dst + 2 * Cfg::SF_WORDS) = v[i].z;
+                    *reinterpret_cast<uint32_t*>(dst + 3 * Cfg::SF_WORDS) = v[i].w;
+                }
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&full[s]);
+            }
+        }
         // ---------------------------------------------- converters (4-bit only)
         if constexpr (Cfg::Q4) {
             const int ctid = threadIdx.x - 32 * (2 + Cfg::EPI_WARPS);
@@ -759,6 +854,22 @@ inline int skinny_cluster_split(long long T, long long KB, long long cap, int nu
             max_s = S / 2;
         }
     }
+}
+
+// The split for the kinds that never ask for stream-K, whose partials would
+// need a workspace: the most of 4, 2, 1 CTAs to a 128-column group that leave
+// every CTA k-units of its own and all groups on the device at once; 1 where
+// the groups alone fill it.  8192 x 8192 8-bit weights take 64 x 2 CTAs either way.
+template <class Cfg>
+int skinny_whole_split(long long T, long long KB, int num_sms, int slot) {
+    static_assert(Cfg::CL_OK, "partials fit the ring");
+    for (int S = 4; S > 1; S >>= 1) {
+        if (S > KB || T * S > num_sms) continue;
+        if (max_active_clusters(reinterpret_cast<const void*>(skinny_kernel<Cfg>), slot, S, Cfg::THREADS,
+                                Cfg::SMEM_BYTES) >= T)
+            return S;
+    }
+    return 1;
 }
 
 // Launch G CTAs; clusters of S CTAs when S > 1 (p.S == S).

@@ -8,23 +8,6 @@ namespace tg {
 
 namespace {
 
-// CTAs a 128-column group is split over: the most of 4, 2, 1 that leave every
-// CTA k-units of its own and all groups on the device at once; 1 where the
-// groups alone fill it.  Unlike skinny_cluster_split it never asks for
-// stream-K, whose partials would need a workspace: 8192 x 8192 weights take
-// 64 x 2 CTAs either way.
-template <class Cfg>
-int split(long long T, long long KB, int num_sms, int slot) {
-    static_assert(Cfg::CL_OK, "partials fit the ring");
-    for (int S = 4; S > 1; S >>= 1) {
-        if (S > KB || T * S > num_sms) continue;
-        if (max_active_clusters(reinterpret_cast<const void*>(skinny_kernel<Cfg>), slot, S, Cfg::THREADS,
-                                Cfg::SMEM_BYTES) >= T)
-            return S;
-    }
-    return 1;
-}
-
 template <int MPAD, int WK>
 int run(const GroupArgs& a, int bf16, int slot) {
     using Cfg = SkCfg<WKind::I8, MPAD, WK>;
@@ -35,7 +18,7 @@ int run(const GroupArgs& a, int bf16, int slot) {
     if (T * KB > 0x7fffffffll) return kUnsupported;
     auto kern = skinny_kernel<Cfg>;
     if (set_smem_attr(reinterpret_cast<const void*>(kern), Cfg::SMEM_BYTES, slot) != cudaSuccess) return kCudaError;
-    const int S = split<Cfg>(T, KB, di->num_sms, slot);
+    const int S = skinny_whole_split<Cfg>(T, KB, di->num_sms, slot);
     CUtensorMap tW, tX;
     constexpr CUtensorMapDataType dt = CU_TENSOR_MAP_DATA_TYPE_UINT8;
     if (WK ? !tensor_map_2d(&tW, g.B, dt, 1, g.K, g.N, g.ldb, 128, Cfg::TN, SWZ_128)

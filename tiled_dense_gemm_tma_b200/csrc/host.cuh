@@ -71,6 +71,8 @@ int* device_status_ptr();
 //   70-81  gemm_group.cu     experts' products and 8-bit products
 //   82-89  expert.cu         sort by expert
 //   90-97  gemm_skinny_i8.cu
+//   98-99  gemm_group.cu     4-bit products
+//  100-103 gemm_skinny_mx4.cu
 constexpr int kMaxSlots = 128;
 cudaError_t set_smem_attr(const void* func, int bytes, int slot);
 

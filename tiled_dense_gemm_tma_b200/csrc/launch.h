@@ -57,16 +57,47 @@ struct GroupArgs {
     const float* row_scale;          // 8-bit only: g.M
     const float* col_scale;          // 8-bit only: N per group, scale_plane apart
     int64_t scale_plane;
+    // 4-bit only (g.K, leading dimensions and planes in bytes): a scale byte for
+    // every 32 values of a row of A and of a row of the weights
+    const uint8_t* row_blocks; int64_t block_lda;
+    const uint8_t* col_blocks; int64_t block_ldb, block_plane;
+    int64_t blocks;                  // scale bytes in a row
 };
 int launch_group(const GroupArgs& a, int bf16);
 int launch_group_grad(const GroupArgs& a, int bf16);
 int launch_group_i8(const GroupArgs& a, int bf16);
 // One group of all rows: the weight-streaming or the CTA-pair kernel.
 int launch_w8a8(const GroupArgs& a, int bf16);
+// The same with 4-bit operands, both K-major.
+int launch_group_mx4(const GroupArgs& a, int bf16);
+int launch_mx4(const GroupArgs& a, int bf16);
 
 // Rows of 16-bit values to 8-bit integers with one scale per row.
 int launch_quant_i8(int64_t M, int64_t K, const void* X, int64_t ldx, int bf16, int8_t* Q,
                     int64_t ldq, float* scales, void* stream);
+// Rows of 16-bit values to microscaled 4-bit ones and back; with pos, topk rows
+// of the output for each row of X, those from *kept on zero.
+int launch_quant_mxfp4(int64_t M, int64_t K, const void* X, int64_t ldx, int bf16, int topk, const int* pos,
+                       const int* kept, uint8_t* Q, int64_t ldq, uint8_t* scales, int64_t lds, void* stream);
+int launch_dequant_mxfp4(int64_t M, int64_t K, const uint8_t* Q, int64_t ldq, const uint8_t* scales, int64_t lds,
+                         void* Y, int64_t ldy, int bf16, void* stream);
+// Routing (route.cu): the experts of each token and their weights.
+struct RouteArgs {
+    int64_t tokens;
+    int E, groups, keep, topk;
+    int type;                        // of the logits: 0 f16, 1 bf16, 2 f32
+    int sigmoid, renorm;
+    float scale;
+    const void* logits; int64_t ldl;
+    const float* bias;               // null: none
+    int* ids;                        // tokens x topk
+    float* weights;
+    const float* dweights;           // gradient only
+    void* dlogits; int64_t ldd;
+    void* stream;
+};
+int launch_route(const RouteArgs& a);
+int launch_route_grad(const RouteArgs& a);
 // Tokens sorted by expert, and back (expert.cu).
 int64_t expert_sort_scratch(int64_t n, int E);
 int launch_expert_sort(int64_t tokens, int topk, int E, const void* ids, int id_bytes, int* offsets,

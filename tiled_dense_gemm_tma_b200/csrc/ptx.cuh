@@ -391,6 +391,47 @@ __host__ __device__ constexpr uint32_t make_idesc_i8(uint32_t m, uint32_t n, uin
          | (a_mn << 15) | (b_mn << 16) | ((n >> 3) << 17) | ((m >> 4) << 24);
 }
 
+// The same for kind::mxf4: E2M1 A and B, both K-major, with E8M0 scales for
+// blocks of 32 k, fp32 sums.  The scale selectors (which bytes of the scales'
+// 32-bit columns an MMA's 64 k take) are 0 here; mx4_scale_id gives them.
+__host__ __device__ constexpr uint32_t make_idesc_mx4(uint32_t m, uint32_t n) {
+    return (1u << 7)              // A format: E2M1
+         | (1u << 10)             // B format: E2M1
+         | (1u << 23)             // scale format: E8M0
+         | ((n >> 3) << 17) | ((m >> 4) << 24);
+}
+
+// A column of scale bytes holds four blocks, so the scales of two MMAs (64 k,
+// two blocks each): bytes 0 and 1, or 2 and 3.
+__host__ __device__ constexpr uint32_t mx4_scale_id(uint32_t odd) {
+    return odd ? (2u << 4) | (2u << 29) : 0u;      // of B, of A
+}
+
+// D(tmem) (+)= A x B, kind::mxf4 (4-bit operands in 32-byte k steps of 64), each
+// block of 32 k times the scales of A's row and B's row in tensor memory.
+__device__ __forceinline__ void mma_mx4(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                                        uint32_t accumulate, uint32_t sa_tmem, uint32_t sb_tmem) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%5], [%6], p;\n\t}"
+        ::"r"(d_tmem), "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate), "r"(sa_tmem), "r"(sb_tmem)
+        : "memory");
+}
+
+// 32 rows of 16 bytes from shared memory into 4 columns of tensor memory, the
+// same in the lanes of all four warps: how the scales of 128 rows (row 32c + i
+// in lane i, column c) reach the MMA.  `desc` as scale_desc.
+__device__ __forceinline__ void tmem_cp_scales(uint32_t taddr, uint64_t desc) {
+    asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(desc) : "memory");
+}
+
+// Descriptor of 512 contiguous bytes as 32 rows of 16: no swizzle, groups of
+// eight rows 128 bytes apart.
+__device__ __forceinline__ uint64_t scale_desc(uint32_t smem_addr) {
+    return static_cast<uint64_t>((smem_addr >> 4) & 0x3FFFu) | (static_cast<uint64_t>(128 >> 4) << 32) | (1ull << 46);
+}
+
 }  // namespace tg
 
 namespace tg {
@@ -424,6 +465,12 @@ __device__ __forceinline__ void mbar_arrive_expect_tx_cluster(uint32_t cl_addr, 
 
 __device__ __forceinline__ void mbar_arrive_cluster(uint32_t cl_addr) {
     asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(cl_addr) : "memory");
+}
+
+// The same, publishing this thread's earlier writes (and those it has been told
+// of within its warp) to the peer CTA.
+__device__ __forceinline__ void mbar_arrive_release_cluster(uint32_t cl_addr) {
+    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cl_addr) : "memory");
 }
 
 // ------------------------------------------- split-K reduction in a cluster
@@ -579,6 +626,23 @@ __device__ __forceinline__ void mma_f16_sp_pair(uint32_t d_tmem, uint64_t a_desc
         "tcgen05.mma.sp.cta_group::2.kind::f16 [%0], %1, %2, [%5], %3, p;\n\t}"
         ::"r"(d_tmem), "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate), "r"(e_tmem)
         : "memory");
+}
+
+// The same with kind::mxf4: each CTA holds the scales of its own rows of A and
+// of all rows of B in its tensor memory, at the same addresses.
+__device__ __forceinline__ void mma_mx4_pair(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                                             uint32_t accumulate, uint32_t sa_tmem, uint32_t sb_tmem) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%5], [%6], p;\n\t}"
+        ::"r"(d_tmem), "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate), "r"(sa_tmem), "r"(sb_tmem)
+        : "memory");
+}
+
+// tmem_cp_scales in both CTAs, each from its own shared memory.
+__device__ __forceinline__ void tmem_cp_scales_pair(uint32_t taddr, uint64_t desc) {
+    asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(desc) : "memory");
 }
 
 // Arrive once on the mbarrier at shared::cluster address `bar_cl` (this CTA

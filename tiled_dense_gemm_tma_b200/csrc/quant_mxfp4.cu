@@ -1,0 +1,243 @@
+// quant_mxfp4.cu -- rows of 16-bit values to microscaled 4-bit floating point
+// and back: the operands of the 4-bit products.
+//
+// 32 consecutive values of a row are a block.  With top its largest magnitude,
+//
+//   E = floor(log2(top)) - 2 + 127 (at least 0),   q[k] = E2M1(x[k] * 2^(127 - E))
+//
+// rounded to the nearest of 0, 0.5, 1, 1.5, 2, 3, 4, 6, ties to the even code,
+// magnitudes above 6 (they are below 8) to 6.  A block of zeros gets E = 0; one
+// that holds an infinity or a NaN gets E = 255, the format's NaN, and codes 0.
+//
+// floor(log2(top)) + 127 is the exponent field of top in fp32, where top is
+// normal; a subnormal top (bfloat16 only) has field 0 and is below 2^-126, so
+// that E is 0 either way.  The product with a power of two is exact (it can
+// only underflow where the result rounds to 0 all the same), so the one rounding
+// is that to E2M1, by the conversion instruction: the code is the one that the
+// formula gives in real arithmetic.
+//
+// A warp takes UNROLL x 256 consecutive values of a row, a lane eight at a
+// time; four neighbouring lanes hold a block, and its maximum takes two
+// shuffles.
+#include "host.cuh"
+#include "launch.h"
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+namespace tg {
+
+namespace {
+
+template <bool BF16>
+__device__ __forceinline__ float2 widen2(uint32_t w) {
+    if constexpr (BF16)
+        return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
+    else
+        return __half22float2(*reinterpret_cast<const __half2*>(&w));
+}
+
+// Eight values to eight codes, the first in the lowest bits.
+__device__ __forceinline__ uint32_t codes8(const float2 (&x)[4]) {
+    uint32_t r;
+    asm("{\n\t.reg .b8 a, b, c, d;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 a, %2, %1;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 b, %4, %3;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 c, %6, %5;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 d, %8, %7;\n\t"
+        "mov.b32 %0, {a, b, c, d};\n\t}"
+        : "=r"(r) : "f"(x[0].x), "f"(x[0].y), "f"(x[1].x), "f"(x[1].y), "f"(x[2].x), "f"(x[2].y), "f"(x[3].x), "f"(x[3].y));
+    return r;
+}
+
+// Eight codes to four pairs of fp16 values (exact).
+__device__ __forceinline__ void values8(uint32_t q, __half2 (&h)[4]) {
+    uint32_t r[4];
+    asm("{\n\t.reg .b8 a, b, c, d;\n\t"
+        "mov.b32 {a, b, c, d}, %4;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %0, a;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %1, b;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %2, c;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %3, d;\n\t}"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(q));
+#pragma unroll
+    for (int i = 0; i < 4; ++i) h[i] = *reinterpret_cast<const __half2*>(&r[i]);
+}
+
+// 16-byte vector v of a row of K values, zero past its end.
+__device__ __forceinline__ uint4 load_vec(const uint16_t* row, int v, int K) {
+    const int left = K - 8 * v;
+    if (left >= 8) return __ldg(reinterpret_cast<const uint4*>(row) + v);
+    uint32_t w[4] = {0, 0, 0, 0};
+#pragma unroll
+    for (int j = 0; j < 7; ++j)
+        if (j < left) w[j >> 1] |= static_cast<uint32_t>(__ldg(row + 8ll * v + j)) << (16 * (j & 1));
+    return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// PLACES: each row goes to the rows pos[row * topk ..] of the output, as zeros
+// to those from *kept on; else to its own.
+template <bool BF16, bool PLACES, int UNROLL>
+__global__ void __launch_bounds__(256)
+quant_mxfp4_kernel(long long units, int per_row, int K, const uint16_t* __restrict__ X, long long ldx, int topk,
+                   long long rows_out, const int* __restrict__ pos, const int* __restrict__ kept,
+                   uint8_t* __restrict__ Q, long long ldq, uint8_t* __restrict__ S, long long lds) {
+    const int lane = threadIdx.x & 31;
+    const long long unit = blockIdx.x * 8ll + (threadIdx.x >> 5);
+    if (unit >= units) return;
+    const long long row = unit / per_row;
+    const int v0 = static_cast<int>(unit - row * per_row) * (32 * UNROLL) + lane;
+    const int nvec = (K + 7) >> 3;
+    const uint16_t* x = X + row * ldx;
+    uint4 v[UNROLL];
+#pragma unroll
+    for (int i = 0; i < UNROLL; ++i)
+        v[i] = v0 + 32 * i < nvec ? load_vec(x, v0 + 32 * i, K) : make_uint4(0, 0, 0, 0);
+    uint32_t code[UNROLL], exps[UNROLL];
+#pragma unroll
+    for (int i = 0; i < UNROLL; ++i) {
+        // largest magnitude as a bit pattern, infinity and NaN above all values
+        uint32_t top2 = __vimax3_u16x2(v[i].x & 0x7fff7fffu, v[i].y & 0x7fff7fffu, v[i].z & 0x7fff7fffu);
+        top2 = __vmaxu2(top2, v[i].w & 0x7fff7fffu);
+        top2 = __vmaxu2(top2, __shfl_xor_sync(0xffffffffu, top2, 1));
+        top2 = __vmaxu2(top2, __shfl_xor_sync(0xffffffffu, top2, 2));
+        const uint32_t top = max(top2 & 0xffffu, top2 >> 16);
+        const bool bad = top >= (BF16 ? 0x7f80u : 0x7c00u);
+        const int field = static_cast<int>(__float_as_uint(widen2<BF16>(top).x) >> 23);
+        const int E = max(field - 2, 0);
+        const float up = __uint_as_float(static_cast<uint32_t>(254 - E) << 23);
+        const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+        float2 f[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            f[j] = widen2<BF16>(w[j]);
+            f[j].x *= up;
+            f[j].y *= up;
+        }
+        code[i] = bad ? 0u : codes8(f);
+        exps[i] = bad ? 255u : static_cast<uint32_t>(E);
+    }
+    const int bytes = (K + 1) >> 1;
+    auto write = [&](long long r, bool live) {
+        uint8_t* q = Q + r * ldq;
+        uint8_t* s = S + r * lds;
+#pragma unroll
+        for (int i = 0; i < UNROLL; ++i) {
+            const int vi = v0 + 32 * i;
+            const uint32_t c = live ? code[i] : 0u;
+            const int left = bytes - 4 * vi;
+            if (left >= 4) {
+                reinterpret_cast<uint32_t*>(q)[vi] = c;
+            } else {
+#pragma unroll
+                for (int j = 0; j < 3; ++j)
+                    if (j < left) q[4ll * vi + j] = static_cast<uint8_t>(c >> (8 * j));
+            }
+            if ((lane & 3) == 0 && left > 0) s[vi >> 2] = static_cast<uint8_t>(live ? exps[i] : 0u);
+        }
+    };
+    if constexpr (PLACES) {
+        const int live = __ldg(kept);
+        for (int j = 0; j < topk; ++j) {
+            const int r = __ldg(pos + row * topk + j);
+            if (r >= 0 && r < rows_out) write(r, r < live);
+        }
+    } else {
+        write(row, true);
+    }
+}
+
+template <bool BF16>
+__global__ void __launch_bounds__(256)
+dequant_mxfp4_kernel(long long vecs, int per_row, int K, const uint8_t* __restrict__ Q, long long ldq,
+                     const uint8_t* __restrict__ S, long long lds, uint16_t* __restrict__ Y, long long ldy) {
+    const long long t = blockIdx.x * 256ll + threadIdx.x;
+    if (t >= vecs) return;
+    const long long row = t / per_row;
+    const int v = static_cast<int>(t - row * per_row);
+    const uint8_t* q = Q + row * ldq + 4ll * v;
+    const int left = K - 8 * v;
+    uint32_t c = 0;
+    if (left >= 8) {
+        c = __ldg(reinterpret_cast<const uint32_t*>(q));
+    } else {
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            if (2 * j < left) c |= static_cast<uint32_t>(__ldg(q + j)) << (8 * j);
+    }
+    const uint32_t E = __ldg(S + row * lds + (v >> 2));
+    const float up = __uint_as_float(E == 0 ? 0x00400000u : E == 255 ? 0x7fc00000u : E << 23);
+    __half2 h[4];
+    values8(c, h);
+    uint32_t o[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        const float2 f = __half22float2(h[j]);
+        if constexpr (BF16) {
+            const __nv_bfloat162 b = __floats2bfloat162_rn(f.x * up, f.y * up);
+            o[j] = *reinterpret_cast<const uint32_t*>(&b);
+        } else {
+            const __half2 b = __floats2half2_rn(f.x * up, f.y * up);
+            o[j] = *reinterpret_cast<const uint32_t*>(&b);
+        }
+    }
+    uint16_t* y = Y + row * ldy + 8ll * v;
+    if (left >= 8) {
+        *reinterpret_cast<uint4*>(y) = make_uint4(o[0], o[1], o[2], o[3]);
+    } else {
+#pragma unroll
+        for (int j = 0; j < 7; ++j)
+            if (j < left) y[j] = static_cast<uint16_t>(o[j >> 1] >> (16 * (j & 1)));
+    }
+}
+
+constexpr long long kMaxBlocks = 0x7fffffffll;
+
+template <bool BF16, bool PLACES, int UNROLL>
+int start(int64_t M, int64_t K, const void* X, int64_t ldx, int topk, const int* pos, const int* kept, uint8_t* Q,
+          int64_t ldq, uint8_t* scales, int64_t lds, cudaStream_t s) {
+    const long long per_row = (K + 256 * UNROLL - 1) / (256 * UNROLL), units = M * per_row;
+    if ((units + 7) / 8 > kMaxBlocks) return kUnsupported;
+    quant_mxfp4_kernel<BF16, PLACES, UNROLL><<<static_cast<unsigned>((units + 7) / 8), 256, 0, s>>>(
+        units, static_cast<int>(per_row), static_cast<int>(K), static_cast<const uint16_t*>(X), ldx, topk,
+        M * topk, pos, kept, Q, ldq, scales, lds);
+    return cudaGetLastError() == cudaSuccess ? kOk : kCudaError;
+}
+
+template <bool BF16, bool PLACES>
+int pick(int64_t M, int64_t K, const void* X, int64_t ldx, int topk, const int* pos, const int* kept, uint8_t* Q,
+         int64_t ldq, uint8_t* scales, int64_t lds, cudaStream_t s) {
+    // few values: more warps, each with less to wait for
+    if (K <= 256 || M * ((K + 1023) / 1024) < 148 * 16)
+        return start<BF16, PLACES, 1>(M, K, X, ldx, topk, pos, kept, Q, ldq, scales, lds, s);
+    return start<BF16, PLACES, 4>(M, K, X, ldx, topk, pos, kept, Q, ldq, scales, lds, s);
+}
+
+}  // namespace
+
+int launch_quant_mxfp4(int64_t M, int64_t K, const void* X, int64_t ldx, int bf16, int topk, const int* pos,
+                       const int* kept, uint8_t* Q, int64_t ldq, uint8_t* scales, int64_t lds, void* stream) {
+    if (!current_device(nullptr)) return kNoDevice;
+    const cudaStream_t s = static_cast<cudaStream_t>(stream);
+    if (pos)
+        return bf16 ? pick<true, true>(M, K, X, ldx, topk, pos, kept, Q, ldq, scales, lds, s)
+                    : pick<false, true>(M, K, X, ldx, topk, pos, kept, Q, ldq, scales, lds, s);
+    return bf16 ? pick<true, false>(M, K, X, ldx, 1, nullptr, nullptr, Q, ldq, scales, lds, s)
+                : pick<false, false>(M, K, X, ldx, 1, nullptr, nullptr, Q, ldq, scales, lds, s);
+}
+
+int launch_dequant_mxfp4(int64_t M, int64_t K, const uint8_t* Q, int64_t ldq, const uint8_t* scales, int64_t lds,
+                         void* Y, int64_t ldy, int bf16, void* stream) {
+    if (!current_device(nullptr)) return kNoDevice;
+    const long long per_row = (K + 7) / 8, vecs = M * per_row, blocks = (vecs + 255) / 256;
+    if (blocks > kMaxBlocks) return kUnsupported;
+    const cudaStream_t s = static_cast<cudaStream_t>(stream);
+    uint16_t* y = static_cast<uint16_t*>(Y);
+    if (bf16)
+        dequant_mxfp4_kernel<true><<<static_cast<unsigned>(blocks), 256, 0, s>>>(vecs, static_cast<int>(per_row), static_cast<int>(K), Q, ldq, scales, lds, y, ldy);
+    else
+        dequant_mxfp4_kernel<false><<<static_cast<unsigned>(blocks), 256, 0, s>>>(vecs, static_cast<int>(per_row), static_cast<int>(K), Q, ldq, scales, lds, y, ldy);
+    return cudaGetLastError() == cudaSuccess ? kOk : kCudaError;
+}
+
+}  // namespace tg
