@@ -77,11 +77,6 @@ struct GrpParams {
     const float* row_scale;   // 8-bit: one per row of A
     const float* col_scale;   // 8-bit: one per column, scale_plane apart per group
     long long scale_plane;
-    // 4-bit (K in bytes, two values each): a row's scale bytes, one per 32 values
-    const uint8_t* row_blocks;  // M rows of A, block_lda bytes apart
-    const uint8_t* col_blocks;  // N rows of W_e, block_ldb apart, block_plane per group
-    long long block_lda, block_ldb, block_plane;
-    int blocks;               // scale bytes in a row
 };
 
 // TYPE: 0 f16, 1 bf16 (idesc formats), 3 signed 8-bit, 4 4-bit floating point
@@ -103,12 +98,12 @@ struct GrpCfg {
     static constexpr int STEPS = BK / MMA_K;            // MMAs per stage
     static constexpr int CHUNK = 128 / EB;              // columns per MN-major box row
     static constexpr int STAGES = MX ? 5 : 6;
-    // 4-bit: a chunk is 512 k, 16 scale bytes of every row and two stages.  Four
-    // warps take the chunks in turn, each with a slot of its own: the scales of
-    // 128 lanes and of up to 256 rows, four words of four blocks a row.
+    // 4-bit: a chunk is 512 k, 16 scale bytes of every row and two stages, in a slot
+    // of 128 lanes' and up to 256 rows' scales.  One warp loads chunks, three put
+    // them in the order of tensor memory in turn.
     static constexpr int SF_WARPS = MX ? 4 : 0;
-    static constexpr int SF_WORDS = 3 * 512;            // one word of every row
-    static constexpr int SF_SLOT = 4 * SF_WORDS;
+    static constexpr int SF_SLOTS = MX ? 4 : 0;
+    static constexpr int SF_SLOT = 3 * kScaleTile;
     static constexpr int SF_COLS = 24;                  // tensor memory of a stage's scales
     static constexpr int A_STAGE = 128 * 128;           // 128 lanes' operand, either major-ness
     static constexpr int B_STAGE = 128 * 128;           // up to 128 of the N side
@@ -125,7 +120,7 @@ struct GrpCfg {
     static constexpr int TMEM_SF = 2 * ROWS;
     static_assert(!MX || TMEM_SF + 2 * SF_COLS <= TMEM_COLS, "tensor memory");
     static constexpr int TABLE = WG_ ? 0 : (4 * (kMaxGroups + 2)) * 4;
-    static constexpr int SMEM_DATA = STAGES * (A_STAGE + B_STAGE) + EPI_WARPS * NBUF * STG_BUF + SF_WARPS * SF_SLOT;
+    static constexpr int SMEM_DATA = STAGES * (A_STAGE + B_STAGE) + EPI_WARPS * NBUF * STG_BUF + SF_SLOTS * SF_SLOT;
     static constexpr int SMEM_BYTES = SMEM_DATA + 512 + TABLE + 1024;
     static_assert(SMEM_BYTES <= 227 * 1024, "shared memory per CTA");
     static_assert(!(EB == 1 && WG_), "the 8-bit and 4-bit products have no gradient");
@@ -301,7 +296,8 @@ __device__ __forceinline__ void grp_store_grad(const CUtensorMap* tmC, const Grp
 
 // tmA: the 256-lane operand (product: weights, 3-D; WG: A).  tmB .. tmB16:
 // the N-side operand (product: rows of A in boxes of 128, 64, 32 and 16 rows;
-// WG: G in tmB).  tmC: C (WG only).
+// WG: G in tmB).  tmC: C (WG only).  tmSA, tmSB: the scales of the lanes and of
+// the rows in boxes of 16 bytes by 128 rows (4-bit only).
 template <class Cfg>
 __global__ void __launch_bounds__(Cfg::THREADS, 1)
 grp_gemm_kernel(const __grid_constant__ CUtensorMap tmA,
@@ -310,6 +306,8 @@ grp_gemm_kernel(const __grid_constant__ CUtensorMap tmA,
                 const __grid_constant__ CUtensorMap tmB32,
                 const __grid_constant__ CUtensorMap tmB16,
                 const __grid_constant__ CUtensorMap tmC,
+                const __grid_constant__ CUtensorMap tmSA,
+                const __grid_constant__ CUtensorMap tmSB,
                 const GrpParams p) {
     extern __shared__ uint8_t smem_raw[];
     const uint32_t raw = smem_u32(smem_raw);
@@ -318,15 +316,16 @@ grp_gemm_kernel(const __grid_constant__ CUtensorMap tmA,
     uint8_t* smB = smA + Cfg::STAGES * Cfg::A_STAGE;
     uint8_t* smStg = smB + Cfg::STAGES * Cfg::B_STAGE;
     uint8_t* smSf = smStg + Cfg::EPI_WARPS * Cfg::NBUF * Cfg::STG_BUF;
-    uint64_t* full = reinterpret_cast<uint64_t*>(smSf + Cfg::SF_WARPS * Cfg::SF_SLOT);
+    uint64_t* full = reinterpret_cast<uint64_t*>(smSf + Cfg::SF_SLOTS * Cfg::SF_SLOT);
     uint64_t* empty = full + Cfg::STAGES;
     uint64_t* cut = empty + Cfg::STAGES;        // WG: a block that ends inside an MMA step has landed
     uint64_t* tfull = cut + Cfg::STAGES;
     uint64_t* tempty = tfull + 2;
     uint64_t* drain = tempty + 2;
     uint64_t* sfull = drain + 1;                // 4-bit: a chunk's scales are there, in both CTAs
-    uint64_t* sempty = sfull + Cfg::SF_WARPS;
-    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(sempty + Cfg::SF_WARPS);
+    uint64_t* sempty = sfull + Cfg::SF_SLOTS;
+    uint64_t* sraw = sempty + Cfg::SF_SLOTS;    // 4-bit: a chunk has landed in this CTA
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(sraw + Cfg::SF_SLOTS);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
     int* gcount = const_cast<int*>(abort_flag) + 1;
     int* gstart = gcount + 1;                   // product: first item of each group that has rows
@@ -352,7 +351,11 @@ grp_gemm_kernel(const __grid_constant__ CUtensorMap tmA,
             mbar_init(&cut[s], 2);
         }
         for (int a = 0; a < 2; ++a) { mbar_init(&tfull[a], 1); mbar_init(&tempty[a], 2 * Cfg::EPI_WARPS); }
-        for (int i = 0; i < Cfg::SF_WARPS; ++i) { mbar_init(&sfull[i], 2); mbar_init(&sempty[i], 1); }
+        for (int i = 0; i < Cfg::SF_SLOTS; ++i) {
+            mbar_init(&sfull[i], 2);
+            mbar_init(&sempty[i], 1);
+            mbar_init(&sraw[i], 1);
+        }
         mbar_init(drain, 1);
         *abort_flag = 0;
         fence_mbar_init();
@@ -592,9 +595,9 @@ grp_gemm_kernel(const __grid_constant__ CUtensorMap tmA,
                     const uint32_t b_addr = smem_u32(smB + s * Cfg::B_STAGE);
                     uint32_t sf = 0;                             // this stage's scales in tensor memory
                     if constexpr (Cfg::MX) {
-                        const uint32_t slot = chunk % Cfg::SF_WARPS;
+                        const uint32_t slot = chunk % Cfg::SF_SLOTS;
                         if (!(kb & 1)) {
-                            if (!bounded_wait_cluster(&sfull[slot], (chunk / Cfg::SF_WARPS) & 1, abort_flag, limit, p.status)) {
+                            if (!bounded_wait_cluster(&sfull[slot], (chunk / Cfg::SF_SLOTS) & 1, abort_flag, limit, p.status)) {
                                 ok = false;
                                 break;
                             }
@@ -603,13 +606,13 @@ grp_gemm_kernel(const __grid_constant__ CUtensorMap tmA,
                         // two sets of columns in turn: a stage's copies do not wait for
                         // the MMAs of the one before
                         sf = tmem_base + Cfg::TMEM_SF + (ld & 1) * Cfg::SF_COLS;
-                        const uint32_t src = smem_u32(smSf + slot * Cfg::SF_SLOT) + (kb & 1) * 2 * Cfg::SF_WORDS;
+                        const uint32_t src = smem_u32(smSf + slot * Cfg::SF_SLOT) + (kb & 1) * 1024;
 #pragma unroll
                         for (int j = 0; j < 2; ++j) {
-                            tmem_cp_scales_pair(sf + 4 * j, scale_desc(src + j * Cfg::SF_WORDS));
-                            tmem_cp_scales_pair(sf + 8 + 8 * j, scale_desc(src + j * Cfg::SF_WORDS + 512));
+                            tmem_cp_scales_pair(sf + 4 * j, scale_desc(src + j * 512));
+                            tmem_cp_scales_pair(sf + 8 + 8 * j, scale_desc(src + kScaleTile + j * 512));
                             if (it.width > 128)
-                                tmem_cp_scales_pair(sf + 12 + 8 * j, scale_desc(src + j * Cfg::SF_WORDS + 1024));
+                                tmem_cp_scales_pair(sf + 12 + 8 * j, scale_desc(src + 2 * kScaleTile + j * 512));
                         }
                     }
                     const int steps = Cfg::WG && kb == it.kb - 1
@@ -636,7 +639,7 @@ grp_gemm_kernel(const __grid_constant__ CUtensorMap tmA,
                     mma_commit_pair(mapa_shared(e_loc, 1));
                     if constexpr (Cfg::MX) {
                         if ((kb & 1) || kb == it.kb - 1) {
-                            const uint32_t s_loc = smem_u32(&sempty[chunk % Cfg::SF_WARPS]);
+                            const uint32_t s_loc = smem_u32(&sempty[chunk % Cfg::SF_SLOTS]);
                             mma_commit_pair(mapa_shared(s_loc, 0));
                             mma_commit_pair(mapa_shared(s_loc, 1));
                             ++chunk;
@@ -688,47 +691,64 @@ grp_gemm_kernel(const __grid_constant__ CUtensorMap tmA,
     } else {
         if constexpr (Cfg::MX) {
             // ---------------------------------------- block scales (4-bit, both)
-            // Row r's word w (four blocks) goes to 16 * (r % 32) + 4 * (r / 32 % 4) of
-            // the 512 bytes that become columns of tensor memory.  Plain loads take
-            // rows from any place in a row-major matrix, and bytes past a row's last
-            // block become 0: the copy engine's zeros beside them must not meet a NaN.
+            // Each CTA brings the scales of its own lanes and of all the tile's rows;
+            // rows may start anywhere.  Plain 16-byte loads of 384 rows a chunk took
+            // longer than its MMAs (8192 x 8192 x 8192 354 us, so 200).
             const int turn = warp - (3 + Cfg::EPI_WARPS);
-            uint8_t* slot = smSf + turn * Cfg::SF_SLOT + lane * 16;
-            uint32_t chunk = 0, uses = 0;
+            uint32_t chunk = 0, armed = 0;
             bool ok = true;
             int g = 0;
-            for (int w = pair; w < num_items && ok; w += npairs) {
-                const GrpItem it = item(w, g);
-                const int chunks = (it.kb + 1) / 2;
-                for (int c = 0; c < chunks; ++c, ++chunk) {
-                    if (static_cast<int>(chunk % Cfg::SF_WARPS) != turn) continue;
-                    const int n0 = it.n0 + static_cast<int>(rank) * 128 + lane;
-                    const uint8_t* cols = p.col_blocks + it.e * p.block_plane + 16ll * c;
-                    const uint8_t* rows = p.row_blocks + 16ll * c;
-                    const int left = p.blocks - 16 * c;
-                    uint4 v[12];
-#pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        v[i] = load_blocks(cols + (n0 + 32 * i) * p.block_ldb, left, p.N - (n0 + 32 * i));
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        const int m = it.m0 + 32 * i + lane;
-                        v[4 + i] = load_blocks(rows + m * p.block_lda, left, m < it.m1 ? p.M - m : 0);
+            if (turn == Cfg::SF_WARPS - 1) {
+                if (elect_one()) {
+                    tma_prefetch_desc(&tmSA);
+                    tma_prefetch_desc(&tmSB);
+                    for (int w = pair; w < num_items && ok; w += npairs) {
+                        const GrpItem it = item(w, g);
+                        const int n0 = it.n0 + static_cast<int>(rank) * 128;
+                        const bool a_live = n0 < p.N, b_two = it.width > 128 && it.m0 + 128 < p.M;
+                        const uint32_t bytes = (1 + a_live + b_two) * kScaleTile;
+                        for (int c = 0; c < (it.kb + 1) / 2; ++c, ++chunk) {
+                            const uint32_t i = chunk % Cfg::SF_SLOTS;
+                            if (!bounded_wait(&sempty[i], ((chunk / Cfg::SF_SLOTS) & 1) ^ 1, abort_flag, limit, p.status)) {
+                                ok = false;
+                                break;
+                            }
+                            uint8_t* slot = smSf + i * Cfg::SF_SLOT;
+                            mbar_arrive_expect_tx(&sraw[i], bytes);
+                            armed |= 1u << i;
+                            if (a_live) tma_load_3d(slot, &tmSA, &sraw[i], 16 * c, n0, it.e);
+                            tma_load_2d(slot + kScaleTile, &tmSB, &sraw[i], 16 * c, it.m0);
+                            if (b_two) tma_load_2d(slot + 2 * kScaleTile, &tmSB, &sraw[i], 16 * c, it.m0 + 128);
+                        }
                     }
-                    if (!bounded_wait(&sempty[turn], (uses & 1) ^ 1, abort_flag, limit, p.status)) { ok = false; break; }
-                    ++uses;
-#pragma unroll
-                    for (int i = 0; i < 12; ++i) {
-                        uint8_t* dst = slot + (i / 4) * 512 + (i % 4) * 4;
-                        *reinterpret_cast<uint32_t*>(dst) = v[i].x;
-                        *reinterpret_cast<uint32_t*>(dst + Cfg::SF_WORDS) = v[i].y;
-                        *reinterpret_cast<uint32_t*>(dst + 2 * Cfg::SF_WORDS) = v[i].z;
-                        *reinterpret_cast<uint32_t*>(dst + 3 * Cfg::SF_WORDS) = v[i].w;
+                    // loads that nobody waits for any more
+                    for (uint32_t i = 0; i < Cfg::SF_SLOTS && !ok; ++i)
+                        if (armed & (1u << i)) {
+                            const uint32_t last = (chunk - 1 - i) / Cfg::SF_SLOTS;     // uses of the slot before its last
+                            volatile int never = 0;
+                            bounded_wait(&sraw[i], last & 1, &never, limit, p.status);
+                        }
+                }
+                __syncwarp();
+            } else {
+                for (int w = pair; w < num_items && ok; w += npairs) {
+                    const GrpItem it = item(w, g);
+                    for (int c = 0; c < (it.kb + 1) / 2; ++c, ++chunk) {
+                        if (static_cast<int>(chunk % (Cfg::SF_WARPS - 1)) != turn) continue;
+                        const uint32_t i = chunk % Cfg::SF_SLOTS;
+                        if (!bounded_wait(&sraw[i], (chunk / Cfg::SF_SLOTS) & 1, abort_flag, limit, p.status)) {
+                            ok = false;
+                            break;
+                        }
+                        const uint32_t slot = smem_u32(smSf + i * Cfg::SF_SLOT);
+                        order_scales(slot, lane);
+                        order_scales(slot + kScaleTile, lane);
+                        if (it.width > 128) order_scales(slot + 2 * kScaleTile, lane);
+                        // the copies into both CTAs' tensor memory are issued by the leader
+                        fence_proxy_async_smem();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive_release_cluster(mapa_shared(smem_u32(&sfull[i]), 0));
                     }
-                    // the copies into both CTAs' tensor memory are issued by the leader
-                    fence_proxy_async_smem();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive_release_cluster(mapa_shared(smem_u32(&sfull[turn]), 0));
                 }
             }
         }

@@ -87,7 +87,7 @@ int run(const GemmArgs& a) {
     p.ws = ws;
     p.tickets = tickets;
     if (!p.status) return kCudaError;
-    return skinny_launch<Cfg>(G, S, static_cast<cudaStream_t>(a.stream), tW, tS, tX, p) == cudaSuccess
+    return skinny_launch<Cfg>(G, S, static_cast<cudaStream_t>(a.stream), tW, tS, tX, tX, p) == cudaSuccess
                ? kOk : kCudaError;
 }
 

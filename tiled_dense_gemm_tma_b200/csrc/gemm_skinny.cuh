@@ -46,8 +46,8 @@
 //   CTA-pair kernel of gemm_group.cuh, 32 pairs there: 23.4).
 // * 4-bit weights and activations with block scales (kind::mxf4, both K-major):
 //   a 128-byte row holds 256 k, a unit is 512 k and 16 scale bytes of each row,
-//   which four more warps bring into the slot, already in the order of tensor
-//   memory; the MMA thread copies them there.  Never stream-K either.
+//   which one more warp puts in the order of tensor memory before the MMA
+//   thread copies them there.  Never stream-K either.
 #pragma once
 #include "ptx.cuh"
 #include "dequant.cuh"
@@ -105,11 +105,9 @@ struct SkCfg {
     // 4-bit weights: [Q | S], released by the converters as soon as they have
     // expanded it into a second ring of fp16 tiles; the activations then
     // travel in a ring of their own, released by the MMA.
-    // block scales of a unit: four words of four blocks, each 512 bytes for the
-    // 128 columns and 512 for the activation rows
-    static constexpr int SF_WORDS = 1024;
-    static constexpr int SF_BYTES = MX ? 4 * SF_WORDS : 0;
-    static constexpr int SF_WARPS = MX ? 4 : 0;
+    // block scales of a unit: 16 bytes of each column and of each activation row
+    static constexpr int SF_BYTES = MX ? 2 * kScaleTile : 0;
+    static constexpr int SF_WARPS = MX ? 1 : 0;
     static constexpr int RAW_SLOT_USED = Q4 ? (Q_BYTES + S_BYTES) : (X_BYTES + W_BYTES + SF_BYTES);
     static constexpr int RAW_SLOT = (RAW_SLOT_USED + 1023) / 1024 * 1024;   // swizzle alignment
     // the fp16 tiles only bridge converters and MMA (on-chip latency): two
@@ -174,10 +172,6 @@ struct SkParams {
     const float* row_scale;   // 8-bit: M
     const float* col_scale;   // 8-bit: N
     int out_bf16;             // 8-bit, 4-bit blocks: C's type
-    const uint8_t* row_blocks;  // 4-bit blocks: scale bytes of the M rows, of the N weight rows
-    const uint8_t* col_blocks;
-    long long block_lda, block_ldb;
-    int blocks;               // in a row
 };
 
 template <WKind W>
@@ -253,12 +247,14 @@ __device__ __forceinline__ void store_blocks4(const SkParams& p, int m, int n, f
 
 // tmW: fp16/bf16 weights (N x K view: 64-column boxes of BK rows), or the
 //      packed 4-bit weights (64-byte boxes of BK rows) for INT4;
-// tmS: scales (INT4 only); tmX: activations, K-major boxes of 64 x MPAD.
+// tmS: scales (4-bit weights); tmX: activations, K-major boxes of 64 x MPAD;
+// tmSX: the activations' scales (4-bit blocks only).
 template <class Cfg>
 __global__ void __launch_bounds__(Cfg::THREADS, 1)
 skinny_kernel(const __grid_constant__ CUtensorMap tmW,
               const __grid_constant__ CUtensorMap tmS,
               const __grid_constant__ CUtensorMap tmX,
+              const __grid_constant__ CUtensorMap tmSX,
               const SkParams p) {
     extern __shared__ uint8_t smem_raw[];
     const uint32_t raw_addr = smem_u32(smem_raw);
@@ -280,7 +276,8 @@ skinny_kernel(const __grid_constant__ CUtensorMap tmW,
     uint64_t* flag_bar = epi_bar + 1;                                // ticket result published
     uint64_t* cl_ready = flag_bar + 1;                               // peers' rings may receive
     uint64_t* cl_full = cl_ready + 1;                                // this CTA's columns arrived
-    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(cl_full + 1);
+    uint64_t* sraw = cl_full + 1;                                    // [RAW_STAGES], block scales landed
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(sraw + (Cfg::MX ? Cfg::RAW_STAGES : 0));
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
     volatile int* last_flag = abort_flag + 1;
 
@@ -312,7 +309,8 @@ skinny_kernel(const __grid_constant__ CUtensorMap tmW,
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < Cfg::RAW_STAGES; ++s) {
-            mbar_init(&full[s], Cfg::MX ? 2 : 1);        // block scales come from a warp of their own
+            mbar_init(&full[s], Cfg::MX ? 2 : 1);        // the block scales are in order, too
+            if constexpr (Cfg::MX) mbar_init(&sraw[s], 1);
             mbar_init(&rempty[s], Cfg::Q4 ? Cfg::CONV_WARPS : 1);
         }
         for (int s = 0; s < Cfg::W_STAGES; ++s) {
@@ -378,6 +376,11 @@ skinny_kernel(const __grid_constant__ CUtensorMap tmW,
                     xarmed_par = (xarmed_par & ~(1u << xs)) | (xph << xs);
                 } else if constexpr (Cfg::WK) {
                     if (p.inject == 1 && it == 0 && c == 0) continue;   // debug: never arm slot 0
+                    if constexpr (Cfg::MX) {
+                        mbar_arrive_expect_tx(&sraw[s], kScaleTile + 16 * Cfg::MPAD);
+                        tma_load_2d(slot_sf(s), &tmS, &sraw[s], 16 * kb, t * Cfg::TN);
+                        tma_load_2d(slot_sf(s) + kScaleTile, &tmSX, &sraw[s], 16 * kb, 0);
+                    }
                     // B stored N x K: BK/64 boxes of the tile's 128 n rows x 64 k
                     // (rows past N read the copy engine's zero fill)
                     mbar_arrive_expect_tx(&full[s], Cfg::X_BYTES + Cfg::W_BYTES);
@@ -473,8 +476,8 @@ skinny_kernel(const __grid_constant__ CUtensorMap tmW,
                     const uint32_t src = smem_u32(slot_sf(s));
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
-                        tmem_cp_scales(sf + 8 * j, scale_desc(src + j * Cfg::SF_WORDS));
-                        tmem_cp_scales(sf + 8 * j + 4, scale_desc(src + j * Cfg::SF_WORDS + 512));
+                        tmem_cp_scales(sf + 8 * j, scale_desc(src + j * 512));
+                        tmem_cp_scales(sf + 8 * j + 4, scale_desc(src + kScaleTile + j * 512));
                     }
                 }
 #pragma unroll
@@ -753,39 +756,14 @@ skinny_kernel(const __grid_constant__ CUtensorMap tmW,
         }
     } else {
         // ----------------------------------- block scales (4-bit blocks only)
-        // Row r's word w goes to 16 * (r % 32) + 4 * (r / 32) of its 512 bytes;
-        // bytes past a row's last block become 0 (as in gemm_group.cuh).
         if constexpr (Cfg::MX) {
-            constexpr int XR = (Cfg::MPAD + 31) / 32;
-            const int turn = warp - (2 + Cfg::EPI_WARPS);
             int it = 0;
             for (int u = u0; u < u1; ++u, ++it) {
-                if (it % Cfg::SF_WARPS != turn) continue;
-                const int t = u / KB, kb = u - (u / KB) * KB;
                 const int s = it % Cfg::RAW_STAGES;
-                const uint32_t ph = (it / Cfg::RAW_STAGES) & 1;
-                const int left = p.blocks - 16 * kb;
-                uint4 v[4 + XR];
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const int n = t * Cfg::TN + 32 * i + lane;
-                    v[i] = load_blocks(p.col_blocks + n * p.block_ldb + 16ll * kb, left, p.N - n);
-                }
-#pragma unroll
-                for (int i = 0; i < XR; ++i) {
-                    const int m = 32 * i + lane;
-                    v[4 + i] = load_blocks(p.row_blocks + m * p.block_lda + 16ll * kb, left, p.M - m);
-                }
-                if (!bounded_wait(&rempty[s], ph ^ 1, abort_flag, limit, p.status)) break;
-                uint8_t* slot = slot_sf(s) + lane * 16;
-#pragma unroll
-                for (int i = 0; i < 4 + XR; ++i) {
-                    uint8_t* dst = slot + i * 4 + (i < 4 ? 0 : 512 - 16);
-                    *reinterpret_cast<uint32_t*>(dst) = v[i].x;
-                    *reinterpret_cast<uint32_t*>(dst + Cfg::SF_WORDS) = v[i].y;
-                    *reinterpret_cast<uint32_t*>(dst + 2 * Cfg::SF_WORDS) = v[i].z;
-                    *reinterpret_cast<uint32_t*>(dst + 3 * Cfg::SF_WORDS) = v[i].w;
-                }
+                if (!bounded_wait(&sraw[s], (it / Cfg::RAW_STAGES) & 1, abort_flag, limit, p.status)) break;
+                const uint32_t at = smem_u32(slot_sf(s));
+                order_scales(at, lane);
+                order_scales(at + kScaleTile, lane);       // places past the MPAD rows hold what they will
                 fence_proxy_async_smem();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&full[s]);
@@ -872,10 +850,11 @@ int skinny_whole_split(long long T, long long KB, int num_sms, int slot) {
     return 1;
 }
 
-// Launch G CTAs; clusters of S CTAs when S > 1 (p.S == S).
+// Launch G CTAs; clusters of S CTAs when S > 1 (p.S == S).  tS and tSX only where
+// the weights have scales, else any map.
 template <class Cfg>
 inline cudaError_t skinny_launch(long long G, int S, cudaStream_t stream, const CUtensorMap& tW,
-                                 const CUtensorMap& tS, const CUtensorMap& tX, const SkParams& p) {
+                                 const CUtensorMap& tS, const CUtensorMap& tX, const CUtensorMap& tSX, const SkParams& p) {
     if (S > 1) {
         cudaLaunchConfig_t cfg = {};
         cfg.gridDim = dim3(static_cast<unsigned>(G), 1, 1);
@@ -889,9 +868,9 @@ inline cudaError_t skinny_launch(long long G, int S, cudaStream_t stream, const 
         attr[0].val.clusterDim.z = 1;
         cfg.attrs = attr;
         cfg.numAttrs = 1;
-        return cudaLaunchKernelEx(&cfg, skinny_kernel<Cfg>, tW, tS, tX, p);
+        return cudaLaunchKernelEx(&cfg, skinny_kernel<Cfg>, tW, tS, tX, tSX, p);
     }
-    skinny_kernel<Cfg><<<static_cast<unsigned>(G), Cfg::THREADS, Cfg::SMEM_BYTES, stream>>>(tW, tS, tX, p);
+    skinny_kernel<Cfg><<<static_cast<unsigned>(G), Cfg::THREADS, Cfg::SMEM_BYTES, stream>>>(tW, tS, tX, tSX, p);
     return cudaGetLastError();
 }
 

@@ -44,7 +44,7 @@ int run(const GroupArgs& a, int bf16, int slot) {
     p.col_scale = a.col_scale;
     p.out_bf16 = bf16;
     if (!p.status) return kCudaError;
-    return skinny_launch<Cfg>(T * S, S, static_cast<cudaStream_t>(g.stream), tW, tW, tX, p) == cudaSuccess
+    return skinny_launch<Cfg>(T * S, S, static_cast<cudaStream_t>(g.stream), tW, tW, tX, tX, p) == cudaSuccess
                ? kOk : kCudaError;
 }
 

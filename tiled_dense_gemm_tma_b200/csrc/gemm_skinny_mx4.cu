@@ -19,10 +19,12 @@ int run(const GroupArgs& a, int bf16, int slot) {
     auto kern = skinny_kernel<Cfg>;
     if (set_smem_attr(reinterpret_cast<const void*>(kern), Cfg::SMEM_BYTES, slot) != cudaSuccess) return kCudaError;
     const int S = skinny_whole_split<Cfg>(T, KB, di->num_sms, slot);
-    CUtensorMap tW, tX;
+    CUtensorMap tW, tX, tS, tSX;
     constexpr CUtensorMapDataType dt = CU_TENSOR_MAP_DATA_TYPE_UINT8;
     if (!tensor_map_2d(&tW, g.B, dt, 1, g.K, g.N, g.ldb, 128, Cfg::TN, SWZ_128) ||
-        !tensor_map_2d(&tX, g.A, dt, 1, g.K, g.M, g.lda, 128, MPAD, SWZ_128))
+        !tensor_map_2d(&tX, g.A, dt, 1, g.K, g.M, g.lda, 128, MPAD, SWZ_128) ||
+        !tensor_map_2d(&tS, a.col_blocks, dt, 1, a.blocks, g.N, a.block_ldb, 16, Cfg::TN, SWZ_NONE) ||
+        !tensor_map_2d(&tSX, a.row_blocks, dt, 1, a.blocks, g.M, a.block_lda, 16, MPAD, SWZ_NONE))
         return kCudaError;
     SkParams p = {};
     p.M = static_cast<int>(g.M);
@@ -40,13 +42,8 @@ int run(const GroupArgs& a, int bf16, int slot) {
     p.C = g.C;
     p.ldc = g.ldc;
     p.out_bf16 = bf16;
-    p.row_blocks = a.row_blocks;
-    p.col_blocks = a.col_blocks;
-    p.block_lda = a.block_lda;
-    p.block_ldb = a.block_ldb;
-    p.blocks = static_cast<int>(a.blocks);
     if (!p.status) return kCudaError;
-    return skinny_launch<Cfg>(T * S, S, static_cast<cudaStream_t>(g.stream), tW, tW, tX, p) == cudaSuccess
+    return skinny_launch<Cfg>(T * S, S, static_cast<cudaStream_t>(g.stream), tW, tS, tX, tSX, p) == cudaSuccess
                ? kOk : kCudaError;
 }
 

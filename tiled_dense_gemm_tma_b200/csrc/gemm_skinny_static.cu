@@ -144,7 +144,7 @@ tg_status run_static(int64_t M, int64_t N, int64_t K, const void* A, int64_t lda
     p.ws = part;
     p.tickets = tick;
     if (!p.status) return TG_ERR_CUDA;
-    return skinny_launch<Cfg>(G, S, s, tW, tW, tX, p) == cudaSuccess ? TG_OK : TG_ERR_CUDA;
+    return skinny_launch<Cfg>(G, S, s, tW, tW, tX, tX, p) == cudaSuccess ? TG_OK : TG_ERR_CUDA;
 }
 
 }  // namespace
