@@ -30,11 +30,11 @@ GrpParams params(const GroupArgs& a) {
     return p;
 }
 
-// At most one item per `rows` rows and one more per group with rows (the rows
+// At most one item per 256 rows and one more per group with rows (the rows
 // behind the last group included), times the 256-column tiles.
-long long max_items(const GroupArgs& a, int rows) {
+long long max_items(const GroupArgs& a) {
     const long long groups = a.offsets ? (a.E + 1 < a.g.M ? a.E + 1 : a.g.M) : 1;
-    return (a.g.M / rows + groups) * ((a.g.N - 1) / 256 + 1);
+    return (a.g.M / 256 + groups) * ((a.g.N - 1) / 256 + 1);
 }
 
 template <class Cfg>
@@ -69,7 +69,7 @@ int run_product(const GroupArgs& a, CUtensorMapDataType dt, int slot) {
     if (pair_kernels_disabled()) return kUnsupported;
     const DeviceInfo* di = current_device(nullptr);
     if (!di) return kNoDevice;
-    const long long items = max_items(a, Cfg::ROWS);
+    const long long items = max_items(a);
     if (items > 0x7fffffffll) return kUnsupported;
     constexpr int eb = Cfg::EB;
     const GemmArgs& g = a.g;
@@ -87,8 +87,8 @@ int run_product(const GroupArgs& a, CUtensorMapDataType dt, int slot) {
         return kCudaError;
     if constexpr (Cfg::MX) {
         const uint64_t s_plane = static_cast<uint64_t>(a.E > 1 ? a.block_plane : a.block_ldb);
-        if (!tensor_map_3d(&tSA, a.col_blocks, dt, a.blocks, g.N, a.block_ldb, a.E, s_plane, 16, 128, SWZ_NONE) ||
-            !tensor_map_2d(&tSB, a.row_blocks, dt, 1, a.blocks, g.M, a.block_lda, 16, 128, SWZ_NONE))
+        if (!tensor_map_3d(&tSA, a.col_blocks, dt, a.blocks, g.N, a.block_ldb, a.E, s_plane, 32, 128, SWZ_NONE) ||
+            !tensor_map_2d(&tSB, a.row_blocks, dt, 1, a.blocks, g.M, a.block_lda, 32, 128, SWZ_NONE))
             return kCudaError;
         return launch<Cfg>(a, items, tA, tB, tA, tSA, tSB, di->num_sms);
     }

@@ -98,12 +98,13 @@ struct GrpCfg {
     static constexpr int STEPS = BK / MMA_K;            // MMAs per stage
     static constexpr int CHUNK = 128 / EB;              // columns per MN-major box row
     static constexpr int STAGES = MX ? 5 : 6;
-    // 4-bit: a chunk is 512 k, 16 scale bytes of every row and two stages, in a slot
-    // of 128 lanes' and up to 256 rows' scales.  One warp loads chunks, three put
-    // them in the order of tensor memory in turn.
+    // 4-bit: a chunk is 1024 k, 32 scale bytes of every row and four stages, in a
+    // slot of 128 lanes' and up to 256 rows' scales.  One warp loads chunks, three
+    // put them in the order of tensor memory in turn.
     static constexpr int SF_WARPS = MX ? 4 : 0;
-    static constexpr int SF_SLOTS = MX ? 4 : 0;
-    static constexpr int SF_SLOT = 3 * kScaleTile;
+    static constexpr int SF_SLOTS = MX ? 3 : 0;
+    static constexpr int SF_TILE = 128 * 32;
+    static constexpr int SF_SLOT = 3 * SF_TILE;
     static constexpr int SF_COLS = 24;                  // tensor memory of a stage's scales
     static constexpr int A_STAGE = 128 * 128;           // 128 lanes' operand, either major-ness
     static constexpr int B_STAGE = 128 * 128;           // up to 128 of the N side
@@ -115,17 +116,26 @@ struct GrpCfg {
     static constexpr int THREADS = 32 * (1 + PRODUCERS + EPI_WARPS + FIX_WARPS + SF_WARPS);
     static constexpr int STG_BUF = WG_ ? 4096 : 2048;   // a warp's [32 rows][128 bytes] or [32 rows][32 columns]
     static constexpr int NBUF = WG_ ? 8 / EPI_ : 1;     // staging tiles a warp
-    static constexpr int TMEM_COLS = 512;               // two accumulators of ROWS columns
-    static constexpr int ROWS = MX ? 224 : 256;         // most rows a tile: 4-bit scales take 48 columns
-    static constexpr int TMEM_SF = 2 * ROWS;
-    static_assert(!MX || TMEM_SF + 2 * SF_COLS <= TMEM_COLS, "tensor memory");
-    static constexpr int TABLE = WG_ ? 0 : (4 * (kMaxGroups + 2)) * 4;
+    // Two accumulators of up to 256 columns, the first from the left, the second up
+    // to ACC_END.  4-bit scales take the last 48 columns, so that two accumulators of
+    // together more than 464 rows share some in the middle: the second waits until
+    // those have been read.  (Tiles of at most 224 rows never would: 8192 x 8192 x
+    // 8192 220 us.)
+    static constexpr int TMEM_COLS = 512;
+    static constexpr int ACC_END = MX ? TMEM_COLS - 2 * SF_COLS : TMEM_COLS;
+    static constexpr int TABLE = WG_ ? 0 : ((MX ? 3 : 4) * (kMaxGroups + 2)) * 4;
     static constexpr int SMEM_DATA = STAGES * (A_STAGE + B_STAGE) + EPI_WARPS * NBUF * STG_BUF + SF_SLOTS * SF_SLOT;
     static constexpr int SMEM_BYTES = SMEM_DATA + 512 + TABLE + 1024;
     static_assert(SMEM_BYTES <= 227 * 1024, "shared memory per CTA");
     static_assert(!(EB == 1 && WG_), "the 8-bit and 4-bit products have no gradient");
     static_assert(!(MX && W_MN_), "4-bit operands are K-major");
 };
+
+// First column of an accumulator of `width` columns.
+template <class Cfg>
+__device__ __forceinline__ uint32_t grp_acc_col(uint32_t acc, int width) {
+    return !acc ? 0 : Cfg::MX ? Cfg::ACC_END - width : 256;
+}
 
 // 16 bytes of zeros at a shared::cluster address, possibly in the peer CTA.
 __device__ __forceinline__ void clear_cluster(uint32_t cl_addr) {
@@ -157,8 +167,22 @@ struct GrpItem {
 // of the tile's rows, 32 at a time (half: which of HALVES warps).
 template <class Cfg>
 __device__ __forceinline__ void grp_store_rows(const GrpParams& p, const GrpItem& it, uint32_t taddr,
-                                               int nw, int half, int lane, uint8_t* stg) {
-    if (nw >= p.N) return;                                  // warp-uniform
+                                               int nw, int half, int lane, uint8_t* stg, uint32_t acc, uint64_t* tpart) {
+    // 4-bit: the columns that two accumulators may share come first, the last ones
+    // of the first accumulator, the first of the second
+    bool parted = !(Cfg::MX && it.kb);
+    auto part = [&] {
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_leader(tpart);
+        parted = true;
+    };
+    if (nw >= p.N) {                                        // warp-uniform
+        if (!parted) part();
+        return;
+    }
+    const int chunks = (it.m1 - it.m0 - 32 * half + 32 * Cfg::HALVES - 1) / (32 * Cfg::HALVES);
+    const bool down = Cfg::MX && acc == 0;
     float cs[4] = {0.f, 0.f, 0.f, 0.f};
     if constexpr (Cfg::I8) {
         if (it.kb) {
@@ -196,7 +220,8 @@ __device__ __forceinline__ void grp_store_rows(const GrpParams& p, const GrpItem
     const int mj = lane >> 3, mc = lane & 7;                // stmatrix: this lane's matrix and column
     const int rr = lane >> 2, ch = lane & 3;                // row store: row and 16-byte chunk
 #pragma unroll 1
-    for (int m = it.m0 + 32 * half; m < it.m1; m += 32 * Cfg::HALVES) {
+    for (int i = 0; i < chunks; ++i) {
+        const int m = it.m0 + 32 * (half + Cfg::HALVES * (down ? chunks - 1 - i : i));
         uint32_t v0[16], v1[16];
         if (it.kb) {
             tmem_ld_16x256b_x4(taddr + (m - it.m0), v0);
@@ -214,7 +239,8 @@ __device__ __forceinline__ void grp_store_rows(const GrpParams& p, const GrpItem
             }
         }
         if (it.kb) tmem_ld_wait();
-        __syncwarp();                                       // the last chunk's rows are read
+        if (!parted) part();
+        else __syncwarp();                                  // the last chunk's rows are read
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             const float ra = Cfg::I8 ? rs[2 * i] : 0.f, rb = Cfg::I8 ? rs[2 * i + 1] : 0.f;
@@ -246,6 +272,7 @@ __device__ __forceinline__ void grp_store_rows(const GrpParams& p, const GrpItem
             }
         }
     }
+    if (!parted) part();                                    // no rows of this warp's
 }
 
 // Epilogue of a weight-gradient tile: this warp's 32 rows k from kr of C_e,
@@ -297,7 +324,7 @@ __device__ __forceinline__ void grp_store_grad(const CUtensorMap* tmC, const Grp
 // tmA: the 256-lane operand (product: weights, 3-D; WG: A).  tmB .. tmB16:
 // the N-side operand (product: rows of A in boxes of 128, 64, 32 and 16 rows;
 // WG: G in tmB).  tmC: C (WG only).  tmSA, tmSB: the scales of the lanes and of
-// the rows in boxes of 16 bytes by 128 rows (4-bit only).
+// the rows in boxes of 32 bytes by 128 rows (4-bit only).
 template <class Cfg>
 __global__ void __launch_bounds__(Cfg::THREADS, 1)
 grp_gemm_kernel(const __grid_constant__ CUtensorMap tmA,
@@ -325,7 +352,8 @@ grp_gemm_kernel(const __grid_constant__ CUtensorMap tmA,
     uint64_t* sfull = drain + 1;                // 4-bit: a chunk's scales are there, in both CTAs
     uint64_t* sempty = sfull + Cfg::SF_SLOTS;
     uint64_t* sraw = sempty + Cfg::SF_SLOTS;    // 4-bit: a chunk has landed in this CTA
-    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(sraw + Cfg::SF_SLOTS);
+    uint64_t* tpart = sraw + Cfg::SF_SLOTS;     // 4-bit: an accumulator's shared columns have been read
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(tpart + 2);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
     int* gcount = const_cast<int*>(abort_flag) + 1;
     int* gstart = gcount + 1;                   // product: first item of each group that has rows
@@ -350,7 +378,11 @@ grp_gemm_kernel(const __grid_constant__ CUtensorMap tmA,
             mbar_init(&empty[s], 1);
             mbar_init(&cut[s], 2);
         }
-        for (int a = 0; a < 2; ++a) { mbar_init(&tfull[a], 1); mbar_init(&tempty[a], 2 * Cfg::EPI_WARPS); }
+        for (int a = 0; a < 2; ++a) {
+            mbar_init(&tfull[a], 1);
+            mbar_init(&tempty[a], 2 * Cfg::EPI_WARPS);
+            if constexpr (Cfg::MX) mbar_init(&tpart[a], 2 * Cfg::EPI_WARPS);
+        }
         for (int i = 0; i < Cfg::SF_SLOTS; ++i) {
             mbar_init(&sfull[i], 2);
             mbar_init(&sempty[i], 1);
@@ -397,7 +429,7 @@ grp_gemm_kernel(const __grid_constant__ CUtensorMap tmA,
                 reached = __shfl_sync(0xffffffffu, low, 31);
                 r0 = low;
                 r1 = max(r1, r0);
-                if (r1 > r0) cnt = grp_tiles(r1 - r0, Cfg::ROWS) * ntl;
+                if (r1 > r0) cnt = grp_tiles(r1 - r0) * ntl;
                 int sum = cnt;
 #pragma unroll
                 for (int d = 1; d < 32; d <<= 1) {
@@ -410,12 +442,13 @@ grp_gemm_kernel(const __grid_constant__ CUtensorMap tmA,
                     gstart[i] = base + sum - cnt;
                     gexp[i] = e;
                     grow[i] = r0;
-                    gend[i] = r1;
+                    if constexpr (!Cfg::MX) gend[i] = r1;
                 }
                 n += __popc(live);
                 base += __shfl_sync(0xffffffffu, sum, 31);
             }
             if (lane == 0) {
+                if constexpr (Cfg::MX) grow[n] = p.M;
                 gstart[n] = base;
                 *gcount = n;
             }
@@ -453,12 +486,12 @@ grp_gemm_kernel(const __grid_constant__ CUtensorMap tmA,
         } else {
             while (w >= gstart[g + 1]) ++g;
             it.e = gexp[g];
-            const int r1 = gend[g];
+            const int r1 = Cfg::MX ? grow[g + 1] : gend[g];     // groups lie one behind the other
             it.r0 = grow[g];
             it.rows = r1 - it.r0;
             int tl, tt, at;
-            tile_coords(w - gstart[g], ntl, grp_tiles(it.rows, Cfg::ROWS), p.group_m, tl, tt);
-            grp_tile(it.rows, tt, at, it.width, Cfg::ROWS);
+            tile_coords(w - gstart[g], ntl, grp_tiles(it.rows), p.group_m, tl, tt);
+            grp_tile(it.rows, tt, at, it.width);
             it.n0 = tl * 256;
             it.m0 = it.r0 + at;
             it.m1 = min(r1, it.m0 + it.width);
@@ -574,6 +607,7 @@ grp_gemm_kernel(const __grid_constant__ CUtensorMap tmA,
                                       : Cfg::MX ? make_idesc_mx4(256, 0)
                                                 : make_idesc(Cfg::TYPE, 256, 0, A_MN, Cfg::WG);
             uint32_t ld = 0, tl = 0, chunk = 0;
+            int last_width = 0;
             bool ok = true;
             int g = 0;
             for (int w = pair; w < num_items && ok; w += npairs) {
@@ -581,10 +615,19 @@ grp_gemm_kernel(const __grid_constant__ CUtensorMap tmA,
                 if (it.kb == 0) continue;
                 const uint32_t acc = tl & 1;
                 const uint32_t aph = (tl >> 1) & 1;
-                ++tl;
                 if (!bounded_wait(&tempty[acc], aph ^ 1, abort_flag, limit, p.status)) { ok = false; break; }
+                if constexpr (Cfg::MX) {
+                    // (tl - 1) / 2: the last tile's use of the other accumulator
+                    if (last_width + it.width > Cfg::ACC_END &&
+                        !bounded_wait(&tpart[acc ^ 1], ((tl - 1) >> 1) & 1, abort_flag, limit, p.status)) {
+                        ok = false;
+                        break;
+                    }
+                    last_width = it.width;
+                }
+                ++tl;
                 tc_fence_after();
-                const uint32_t d_tmem = tmem_base + acc * Cfg::ROWS;
+                const uint32_t d_tmem = tmem_base + grp_acc_col<Cfg>(acc, it.width);
                 const uint32_t idesc = idesc0 | (static_cast<uint32_t>(it.width >> 3) << 17);
                 for (int kb = 0; kb < it.kb; ++kb, ++ld) {
                     const uint32_t s = ld % Cfg::STAGES;
@@ -596,7 +639,7 @@ grp_gemm_kernel(const __grid_constant__ CUtensorMap tmA,
                     uint32_t sf = 0;                             // this stage's scales in tensor memory
                     if constexpr (Cfg::MX) {
                         const uint32_t slot = chunk % Cfg::SF_SLOTS;
-                        if (!(kb & 1)) {
+                        if (!(kb & 3)) {
                             if (!bounded_wait_cluster(&sfull[slot], (chunk / Cfg::SF_SLOTS) & 1, abort_flag, limit, p.status)) {
                                 ok = false;
                                 break;
@@ -605,14 +648,14 @@ grp_gemm_kernel(const __grid_constant__ CUtensorMap tmA,
                         }
                         // two sets of columns in turn: a stage's copies do not wait for
                         // the MMAs of the one before
-                        sf = tmem_base + Cfg::TMEM_SF + (ld & 1) * Cfg::SF_COLS;
-                        const uint32_t src = smem_u32(smSf + slot * Cfg::SF_SLOT) + (kb & 1) * 1024;
+                        sf = tmem_base + Cfg::ACC_END + (ld & 1) * Cfg::SF_COLS;
+                        const uint32_t src = smem_u32(smSf + slot * Cfg::SF_SLOT) + (kb & 3) * 1024;
 #pragma unroll
                         for (int j = 0; j < 2; ++j) {
                             tmem_cp_scales_pair(sf + 4 * j, scale_desc(src + j * 512));
-                            tmem_cp_scales_pair(sf + 8 + 8 * j, scale_desc(src + kScaleTile + j * 512));
+                            tmem_cp_scales_pair(sf + 8 + 8 * j, scale_desc(src + Cfg::SF_TILE + j * 512));
                             if (it.width > 128)
-                                tmem_cp_scales_pair(sf + 12 + 8 * j, scale_desc(src + 2 * kScaleTile + j * 512));
+                                tmem_cp_scales_pair(sf + 12 + 8 * j, scale_desc(src + 2 * Cfg::SF_TILE + j * 512));
                         }
                     }
                     const int steps = Cfg::WG && kb == it.kb - 1
@@ -638,7 +681,7 @@ grp_gemm_kernel(const __grid_constant__ CUtensorMap tmA,
                     mma_commit_pair(mapa_shared(e_loc, 0));      // both CTAs' slots
                     mma_commit_pair(mapa_shared(e_loc, 1));
                     if constexpr (Cfg::MX) {
-                        if ((kb & 1) || kb == it.kb - 1) {
+                        if ((kb & 3) == 3 || kb == it.kb - 1) {
                             const uint32_t s_loc = smem_u32(&sempty[chunk % Cfg::SF_SLOTS]);
                             mma_commit_pair(mapa_shared(s_loc, 0));
                             mma_commit_pair(mapa_shared(s_loc, 1));
@@ -674,10 +717,10 @@ grp_gemm_kernel(const __grid_constant__ CUtensorMap tmA,
                 if (!bounded_wait(&tfull[acc], aph, abort_flag, limit + it.kb * 4096ull, p.status)) break;
                 tc_fence_after();
             }
-            const uint32_t taddr = tmem_base + acc * Cfg::ROWS + (static_cast<uint32_t>(q * 32) << 16);
+            const uint32_t taddr = tmem_base + grp_acc_col<Cfg>(acc, it.width) + (static_cast<uint32_t>(q * 32) << 16);
             const int l0 = it.n0 + static_cast<int>(rank) * 128 + q * 32;
             if constexpr (Cfg::WG) grp_store_grad<Cfg>(&tmC, p, it, taddr, l0, half, lane, stg, nstore);
-            else grp_store_rows<Cfg>(p, it, taddr, l0, half, lane, stg);
+            else grp_store_rows<Cfg>(p, it, taddr, l0, half, lane, stg, acc, &tpart[acc]);
             if (it.kb) {
                 tc_fence_before();
                 __syncwarp();
@@ -692,8 +735,9 @@ grp_gemm_kernel(const __grid_constant__ CUtensorMap tmA,
         if constexpr (Cfg::MX) {
             // ---------------------------------------- block scales (4-bit, both)
             // Each CTA brings the scales of its own lanes and of all the tile's rows;
-            // rows may start anywhere.  Plain 16-byte loads of 384 rows a chunk took
-            // longer than its MMAs (8192 x 8192 x 8192 354 us, so 200).
+            // rows may start anywhere.  Plain 16-byte loads of 384 rows for 512 k took
+            // longer than the MMAs, and a row costs the copy engine about the same for
+            // 16 bytes as for 32.
             const int turn = warp - (3 + Cfg::EPI_WARPS);
             uint32_t chunk = 0, armed = 0;
             bool ok = true;
@@ -706,8 +750,8 @@ grp_gemm_kernel(const __grid_constant__ CUtensorMap tmA,
                         const GrpItem it = item(w, g);
                         const int n0 = it.n0 + static_cast<int>(rank) * 128;
                         const bool a_live = n0 < p.N, b_two = it.width > 128 && it.m0 + 128 < p.M;
-                        const uint32_t bytes = (1 + a_live + b_two) * kScaleTile;
-                        for (int c = 0; c < (it.kb + 1) / 2; ++c, ++chunk) {
+                        const uint32_t bytes = (1 + a_live + b_two) * Cfg::SF_TILE;
+                        for (int c = 0; c < (it.kb + 3) / 4; ++c, ++chunk) {
                             const uint32_t i = chunk % Cfg::SF_SLOTS;
                             if (!bounded_wait(&sempty[i], ((chunk / Cfg::SF_SLOTS) & 1) ^ 1, abort_flag, limit, p.status)) {
                                 ok = false;
@@ -716,9 +760,9 @@ grp_gemm_kernel(const __grid_constant__ CUtensorMap tmA,
                             uint8_t* slot = smSf + i * Cfg::SF_SLOT;
                             mbar_arrive_expect_tx(&sraw[i], bytes);
                             armed |= 1u << i;
-                            if (a_live) tma_load_3d(slot, &tmSA, &sraw[i], 16 * c, n0, it.e);
-                            tma_load_2d(slot + kScaleTile, &tmSB, &sraw[i], 16 * c, it.m0);
-                            if (b_two) tma_load_2d(slot + 2 * kScaleTile, &tmSB, &sraw[i], 16 * c, it.m0 + 128);
+                            if (a_live) tma_load_3d(slot, &tmSA, &sraw[i], 32 * c, n0, it.e);
+                            tma_load_2d(slot + Cfg::SF_TILE, &tmSB, &sraw[i], 32 * c, it.m0);
+                            if (b_two) tma_load_2d(slot + 2 * Cfg::SF_TILE, &tmSB, &sraw[i], 32 * c, it.m0 + 128);
                         }
                     }
                     // loads that nobody waits for any more
@@ -733,7 +777,7 @@ grp_gemm_kernel(const __grid_constant__ CUtensorMap tmA,
             } else {
                 for (int w = pair; w < num_items && ok; w += npairs) {
                     const GrpItem it = item(w, g);
-                    for (int c = 0; c < (it.kb + 1) / 2; ++c, ++chunk) {
+                    for (int c = 0; c < (it.kb + 3) / 4; ++c, ++chunk) {
                         if (static_cast<int>(chunk % (Cfg::SF_WARPS - 1)) != turn) continue;
                         const uint32_t i = chunk % Cfg::SF_SLOTS;
                         if (!bounded_wait(&sraw[i], (chunk / Cfg::SF_SLOTS) & 1, abort_flag, limit, p.status)) {
@@ -741,9 +785,9 @@ grp_gemm_kernel(const __grid_constant__ CUtensorMap tmA,
                             break;
                         }
                         const uint32_t slot = smem_u32(smSf + i * Cfg::SF_SLOT);
-                        order_scales(slot, lane);
-                        order_scales(slot + kScaleTile, lane);
-                        if (it.width > 128) order_scales(slot + 2 * kScaleTile, lane);
+                        order_scales<2>(slot, lane);
+                        order_scales<2>(slot + Cfg::SF_TILE, lane);
+                        if (it.width > 128) order_scales<2>(slot + 2 * Cfg::SF_TILE, lane);
                         // the copies into both CTAs' tensor memory are issued by the leader
                         fence_proxy_async_smem();
                         __syncwarp();

@@ -106,7 +106,8 @@ struct SkCfg {
     // expanded it into a second ring of fp16 tiles; the activations then
     // travel in a ring of their own, released by the MMA.
     // block scales of a unit: 16 bytes of each column and of each activation row
-    static constexpr int SF_BYTES = MX ? 2 * kScaleTile : 0;
+    static constexpr int SF_TILE = 128 * 16;
+    static constexpr int SF_BYTES = MX ? 2 * SF_TILE : 0;
     static constexpr int SF_WARPS = MX ? 1 : 0;
     static constexpr int RAW_SLOT_USED = Q4 ? (Q_BYTES + S_BYTES) : (X_BYTES + W_BYTES + SF_BYTES);
     static constexpr int RAW_SLOT = (RAW_SLOT_USED + 1023) / 1024 * 1024;   // swizzle alignment
@@ -377,9 +378,9 @@ skinny_kernel(const __grid_constant__ CUtensorMap tmW,
                 } else if constexpr (Cfg::WK) {
                     if (p.inject == 1 && it == 0 && c == 0) continue;   // debug: never arm slot 0
                     if constexpr (Cfg::MX) {
-                        mbar_arrive_expect_tx(&sraw[s], kScaleTile + 16 * Cfg::MPAD);
+                        mbar_arrive_expect_tx(&sraw[s], Cfg::SF_TILE + 16 * Cfg::MPAD);
                         tma_load_2d(slot_sf(s), &tmS, &sraw[s], 16 * kb, t * Cfg::TN);
-                        tma_load_2d(slot_sf(s) + kScaleTile, &tmSX, &sraw[s], 16 * kb, 0);
+                        tma_load_2d(slot_sf(s) + Cfg::SF_TILE, &tmSX, &sraw[s], 16 * kb, 0);
                     }
                     // B stored N x K: BK/64 boxes of the tile's 128 n rows x 64 k
                     // (rows past N read the copy engine's zero fill)
@@ -477,7 +478,7 @@ skinny_kernel(const __grid_constant__ CUtensorMap tmW,
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
                         tmem_cp_scales(sf + 8 * j, scale_desc(src + j * 512));
-                        tmem_cp_scales(sf + 8 * j + 4, scale_desc(src + kScaleTile + j * 512));
+                        tmem_cp_scales(sf + 8 * j + 4, scale_desc(src + Cfg::SF_TILE + j * 512));
                     }
                 }
 #pragma unroll
@@ -762,8 +763,8 @@ skinny_kernel(const __grid_constant__ CUtensorMap tmW,
                 const int s = it % Cfg::RAW_STAGES;
                 if (!bounded_wait(&sraw[s], (it / Cfg::RAW_STAGES) & 1, abort_flag, limit, p.status)) break;
                 const uint32_t at = smem_u32(slot_sf(s));
-                order_scales(at, lane);
-                order_scales(at + kScaleTile, lane);       // places past the MPAD rows hold what they will
+                order_scales<1>(at, lane);
+                order_scales<1>(at + Cfg::SF_TILE, lane);       // places past the MPAD rows hold what they will
                 fence_proxy_async_smem();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&full[s]);

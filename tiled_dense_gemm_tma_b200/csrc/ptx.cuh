@@ -477,7 +477,13 @@ __device__ __forceinline__ void mbar_arrive_cluster(uint32_t cl_addr) {
     asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(cl_addr) : "memory");
 }
 
-// The same, publishing this thread's earlier writes (and those it has been told
+// A signal to the first CTA of the cluster that orders nothing but what this
+// thread's own CTA has been told (frees what the tensor cores may overwrite).
+__device__ __forceinline__ void mbar_arrive_leader(uint64_t* bar) {
+    mbar_arrive_cluster(mapa_shared(smem_u32(bar), 0));
+}
+
+// As mbar_arrive_cluster, publishing this thread's earlier writes (and those it has been told
 // of within its warp) to the peer CTA.
 __device__ __forceinline__ void mbar_arrive_release_cluster(uint32_t cl_addr) {
     asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cl_addr) : "memory");

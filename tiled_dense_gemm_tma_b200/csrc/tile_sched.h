@@ -154,15 +154,14 @@ TG_HD void tile_coords(int t, int ntm, int ntn, int group_m, int& tm, int& tn) {
 // grp_tiles(rows) tiles, as few as 256 rows a tile allow.  An MMA takes
 // widths in units of 32 rows: the group's units are dealt out evenly, so that
 // no more than the last unit is padding (1348 rows are 256 + 5 x 224, not
-// 6 x 256, nor 5 x 256 + 96).  `most` is a narrower limit on a tile's rows (a
-// multiple of 32) where tensor memory holds other things as well.
+// 6 x 256, nor 5 x 256 + 96).
 
-TG_HD int grp_tiles(int rows, int most = 256) { return (rows - 1) / most + 1; }
+TG_HD int grp_tiles(int rows) { return (rows - 1) / 256 + 1; }
 
 // Tile i of the group: its first row in the group and its MMA width (a
-// multiple of 32, at most `most`; the last tile may hold fewer rows).
-TG_HD void grp_tile(int rows, int i, int& at, int& width, int most = 256) {
-    const int nt = grp_tiles(rows, most), units = (rows - 1) / 32 + 1;
+// multiple of 32, at most 256; the last tile may hold fewer rows).
+TG_HD void grp_tile(int rows, int i, int& at, int& width) {
+    const int nt = grp_tiles(rows), units = (rows - 1) / 32 + 1;
     const int each = units / nt, more = units - each * nt;     // the first `more` tiles take one more
     at = 32 * (i * each + sched_min(i, more));
     width = 32 * (each + (i < more ? 1 : 0));
