@@ -3,9 +3,9 @@
 //
 // A row's scales lie in memory along k, 4 bytes (a word) for 128 k.  An MMA
 // takes a word of each row from four columns of tensor memory: row 32c + i in lane
-// i, column c.  The copy engine brings 4 or 8 words of 128 rows, row behind row
-// (zeros past a row's last block and past the last row: the zeros beside them
-// must not meet a NaN); a warp puts word w of row 32c + i at word c of lane i of
+// i, column c.  4 or 8 words of 128 rows are brought row behind row (zeros past a
+// row's last block and past the last row: the zeros beside them must not meet a
+// NaN); a warp puts word w of row 32c + i at word c of lane i of
 // the w-th 512 bytes, which tmem_cp_scales then copies as they are.
 #pragma once
 #include "ptx.cuh"
@@ -35,6 +35,28 @@ __device__ __forceinline__ void order_scales(uint32_t tile, int lane) {
         put(4 * h + 1, v[0][h].y, v[1][h].y, v[2][h].y, v[3][h].y);
         put(4 * h + 2, v[0][h].z, v[1][h].z, v[2][h].z, v[3][h].z);
         put(4 * h + 3, v[0][h].w, v[1][h].w, v[2][h].w, v[3][h].w);
+    }
+}
+
+// 16 bytes from global to shared memory, the first `bytes` (0..16) of them read
+// and the rest zero, completing at cp_async_wait of the same thread.
+__device__ __forceinline__ void cp_async_16(uint32_t dst, const void* src, int bytes) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+
+__device__ __forceinline__ void cp_async_wait() { asm volatile("cp.async.wait_all;" ::: "memory"); }
+
+// Start bringing 32 bytes from byte k on of the rows row0 .. row0 + 127 of
+// `rows` rows of `blocks` bytes, `ld` apart.
+__device__ __forceinline__ void load_scales(uint32_t tile, const uint8_t* base, int row0, int rows, long long ld,
+                                            int k, int blocks, int lane) {
+    const int at = k + 16 * (lane & 1);
+    const int bytes = min(16, max(0, blocks - at));
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const int r = row0 + 16 * i + (lane >> 1);
+        const bool in = r < rows && bytes > 0;
+        cp_async_16(tile + (16 * i * 32 + lane * 16), in ? base + r * ld + at : base, in ? bytes : 0);
     }
 }
 

@@ -27,6 +27,12 @@ GrpParams params(const GroupArgs& a) {
     p.row_scale = a.row_scale;
     p.col_scale = a.col_scale;
     p.scale_plane = a.scale_plane;
+    p.row_blocks = a.row_blocks;
+    p.col_blocks = a.col_blocks;
+    p.block_lda = a.block_lda;
+    p.block_ldb = a.block_ldb;
+    p.block_plane = a.block_plane;
+    p.blocks = static_cast<int>(a.blocks);
     return p;
 }
 
@@ -39,7 +45,7 @@ long long max_items(const GroupArgs& a) {
 
 template <class Cfg>
 int launch(const GroupArgs& a, long long items, const CUtensorMap& tA, const CUtensorMap (&tB)[4],
-           const CUtensorMap& tC, const CUtensorMap& tSA, const CUtensorMap& tSB, int num_sms) {
+           const CUtensorMap& tC, int num_sms) {
     const GrpParams p = params(a);
     if (!p.status) return kCudaError;
     // a tile of a thin wave runs as up to four pieces (WG: two)
@@ -56,7 +62,7 @@ int launch(const GroupArgs& a, long long items, const CUtensorMap& tA, const CUt
     attr[0].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    const cudaError_t e = cudaLaunchKernelEx(&cfg, grp_gemm_kernel<Cfg>, tA, tB[0], tB[1], tB[2], tB[3], tC, tSA, tSB, p);
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, grp_gemm_kernel<Cfg>, tA, tB[0], tB[1], tB[2], tB[3], tC, p);
     if (e != cudaSuccess) {
         cudaGetLastError();                       // clear
         return kUnsupported;
@@ -74,7 +80,7 @@ int run_product(const GroupArgs& a, CUtensorMapDataType dt, int slot) {
     constexpr int eb = Cfg::EB;
     const GemmArgs& g = a.g;
     const uint64_t plane = static_cast<uint64_t>(a.E > 1 ? a.plane_b : g.ldb) * eb;   // one group: any legal stride
-    CUtensorMap tA, tB[4], tSA, tSB;
+    CUtensorMap tA, tB[4];
     // weights: K x N -> boxes of 128 bytes of columns x BK rows; N x K ->
     // boxes of BK x 128 columns
     if (Cfg::W_MN ? !tensor_map_3d(&tA, g.B, dt, g.N, g.K, g.ldb * eb, a.E, plane, Cfg::CHUNK, Cfg::BK, SWZ_128)
@@ -85,14 +91,7 @@ int run_product(const GroupArgs& a, CUtensorMapDataType dt, int slot) {
             return kCudaError;
     if (set_smem_attr(reinterpret_cast<const void*>(grp_gemm_kernel<Cfg>), Cfg::SMEM_BYTES, slot) != cudaSuccess)
         return kCudaError;
-    if constexpr (Cfg::MX) {
-        const uint64_t s_plane = static_cast<uint64_t>(a.E > 1 ? a.block_plane : a.block_ldb);
-        if (!tensor_map_3d(&tSA, a.col_blocks, dt, a.blocks, g.N, a.block_ldb, a.E, s_plane, 32, 128, SWZ_NONE) ||
-            !tensor_map_2d(&tSB, a.row_blocks, dt, 1, a.blocks, g.M, a.block_lda, 32, 128, SWZ_NONE))
-            return kCudaError;
-        return launch<Cfg>(a, items, tA, tB, tA, tSA, tSB, di->num_sms);
-    }
-    return launch<Cfg>(a, items, tA, tB, tA, tA, tA, di->num_sms);
+    return launch<Cfg>(a, items, tA, tB, tA, di->num_sms);
 }
 
 template <class Cfg>
@@ -112,7 +111,7 @@ int run_grad(const GroupArgs& a, CUtensorMapDataType dt, int slot) {
     tB[1] = tB[2] = tB[3] = tB[0];
     if (set_smem_attr(reinterpret_cast<const void*>(grp_gemm_kernel<Cfg>), Cfg::SMEM_BYTES, slot) != cudaSuccess)
         return kCudaError;
-    return launch<Cfg>(a, per * a.E, tA, tB, tC, tC, tC, di->num_sms);
+    return launch<Cfg>(a, per * a.E, tA, tB, tC, di->num_sms);
 }
 
 }  // namespace

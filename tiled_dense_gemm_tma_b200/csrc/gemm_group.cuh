@@ -77,6 +77,11 @@ struct GrpParams {
     const float* row_scale;   // 8-bit: one per row of A
     const float* col_scale;   // 8-bit: one per column, scale_plane apart per group
     long long scale_plane;
+    // 4-bit (K in bytes, two values each): a row's scale bytes, one per 32 values
+    const uint8_t* row_blocks;  // M rows of A, block_lda bytes apart
+    const uint8_t* col_blocks;  // N rows of W_e, block_ldb apart, block_plane per group
+    long long block_lda, block_ldb, block_plane;
+    int blocks;               // scale bytes in a row
 };
 
 // TYPE: 0 f16, 1 bf16 (idesc formats), 3 signed 8-bit, 4 4-bit floating point
@@ -99,10 +104,9 @@ struct GrpCfg {
     static constexpr int CHUNK = 128 / EB;              // columns per MN-major box row
     static constexpr int STAGES = MX ? 5 : 6;
     // 4-bit: a chunk is 1024 k, 32 scale bytes of every row and four stages, in a
-    // slot of 128 lanes' and up to 256 rows' scales.  One warp loads chunks, three
-    // put them in the order of tensor memory in turn.
-    static constexpr int SF_WARPS = MX ? 4 : 0;
-    static constexpr int SF_SLOTS = MX ? 3 : 0;
+    // slot of 128 lanes' and up to 256 rows' scales.  Three warps take the chunks
+    // in turn, each with a slot of its own.
+    static constexpr int SF_WARPS = MX ? 3 : 0;
     static constexpr int SF_TILE = 128 * 32;
     static constexpr int SF_SLOT = 3 * SF_TILE;
     static constexpr int SF_COLS = 24;                  // tensor memory of a stage's scales
@@ -124,7 +128,7 @@ struct GrpCfg {
     static constexpr int TMEM_COLS = 512;
     static constexpr int ACC_END = MX ? TMEM_COLS - 2 * SF_COLS : TMEM_COLS;
     static constexpr int TABLE = WG_ ? 0 : ((MX ? 3 : 4) * (kMaxGroups + 2)) * 4;
-    static constexpr int SMEM_DATA = STAGES * (A_STAGE + B_STAGE) + EPI_WARPS * NBUF * STG_BUF + SF_SLOTS * SF_SLOT;
+    static constexpr int SMEM_DATA = STAGES * (A_STAGE + B_STAGE) + EPI_WARPS * NBUF * STG_BUF + SF_WARPS * SF_SLOT;
     static constexpr int SMEM_BYTES = SMEM_DATA + 512 + TABLE + 1024;
     static_assert(SMEM_BYTES <= 227 * 1024, "shared memory per CTA");
     static_assert(!(EB == 1 && WG_), "the 8-bit and 4-bit products have no gradient");
@@ -323,8 +327,7 @@ __device__ __forceinline__ void grp_store_grad(const CUtensorMap* tmC, const Grp
 
 // tmA: the 256-lane operand (product: weights, 3-D; WG: A).  tmB .. tmB16:
 // the N-side operand (product: rows of A in boxes of 128, 64, 32 and 16 rows;
-// WG: G in tmB).  tmC: C (WG only).  tmSA, tmSB: the scales of the lanes and of
-// the rows in boxes of 32 bytes by 128 rows (4-bit only).
+// WG: G in tmB).  tmC: C (WG only).
 template <class Cfg>
 __global__ void __launch_bounds__(Cfg::THREADS, 1)
 grp_gemm_kernel(const __grid_constant__ CUtensorMap tmA,
@@ -333,8 +336,6 @@ grp_gemm_kernel(const __grid_constant__ CUtensorMap tmA,
                 const __grid_constant__ CUtensorMap tmB32,
                 const __grid_constant__ CUtensorMap tmB16,
                 const __grid_constant__ CUtensorMap tmC,
-                const __grid_constant__ CUtensorMap tmSA,
-                const __grid_constant__ CUtensorMap tmSB,
                 const GrpParams p) {
     extern __shared__ uint8_t smem_raw[];
     const uint32_t raw = smem_u32(smem_raw);
@@ -343,16 +344,15 @@ grp_gemm_kernel(const __grid_constant__ CUtensorMap tmA,
     uint8_t* smB = smA + Cfg::STAGES * Cfg::A_STAGE;
     uint8_t* smStg = smB + Cfg::STAGES * Cfg::B_STAGE;
     uint8_t* smSf = smStg + Cfg::EPI_WARPS * Cfg::NBUF * Cfg::STG_BUF;
-    uint64_t* full = reinterpret_cast<uint64_t*>(smSf + Cfg::SF_SLOTS * Cfg::SF_SLOT);
+    uint64_t* full = reinterpret_cast<uint64_t*>(smSf + Cfg::SF_WARPS * Cfg::SF_SLOT);
     uint64_t* empty = full + Cfg::STAGES;
     uint64_t* cut = empty + Cfg::STAGES;        // WG: a block that ends inside an MMA step has landed
     uint64_t* tfull = cut + Cfg::STAGES;
     uint64_t* tempty = tfull + 2;
     uint64_t* drain = tempty + 2;
     uint64_t* sfull = drain + 1;                // 4-bit: a chunk's scales are there, in both CTAs
-    uint64_t* sempty = sfull + Cfg::SF_SLOTS;
-    uint64_t* sraw = sempty + Cfg::SF_SLOTS;    // 4-bit: a chunk has landed in this CTA
-    uint64_t* tpart = sraw + Cfg::SF_SLOTS;     // 4-bit: an accumulator's shared columns have been read
+    uint64_t* sempty = sfull + Cfg::SF_WARPS;
+    uint64_t* tpart = sempty + Cfg::SF_WARPS;    // 4-bit: an accumulator's shared columns have been read
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(tpart + 2);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
     int* gcount = const_cast<int*>(abort_flag) + 1;
@@ -383,10 +383,9 @@ grp_gemm_kernel(const __grid_constant__ CUtensorMap tmA,
             mbar_init(&tempty[a], 2 * Cfg::EPI_WARPS);
             if constexpr (Cfg::MX) mbar_init(&tpart[a], 2 * Cfg::EPI_WARPS);
         }
-        for (int i = 0; i < Cfg::SF_SLOTS; ++i) {
+        for (int i = 0; i < Cfg::SF_WARPS; ++i) {
             mbar_init(&sfull[i], 2);
             mbar_init(&sempty[i], 1);
-            mbar_init(&sraw[i], 1);
         }
         mbar_init(drain, 1);
         *abort_flag = 0;
@@ -638,9 +637,9 @@ grp_gemm_kernel(const __grid_constant__ CUtensorMap tmA,
                     const uint32_t b_addr = smem_u32(smB + s * Cfg::B_STAGE);
                     uint32_t sf = 0;                             // this stage's scales in tensor memory
                     if constexpr (Cfg::MX) {
-                        const uint32_t slot = chunk % Cfg::SF_SLOTS;
+                        const uint32_t slot = chunk % Cfg::SF_WARPS;
                         if (!(kb & 3)) {
-                            if (!bounded_wait_cluster(&sfull[slot], (chunk / Cfg::SF_SLOTS) & 1, abort_flag, limit, p.status)) {
+                            if (!bounded_wait_cluster(&sfull[slot], (chunk / Cfg::SF_WARPS) & 1, abort_flag, limit, p.status)) {
                                 ok = false;
                                 break;
                             }
@@ -682,7 +681,7 @@ grp_gemm_kernel(const __grid_constant__ CUtensorMap tmA,
                     mma_commit_pair(mapa_shared(e_loc, 1));
                     if constexpr (Cfg::MX) {
                         if ((kb & 3) == 3 || kb == it.kb - 1) {
-                            const uint32_t s_loc = smem_u32(&sempty[chunk % Cfg::SF_SLOTS]);
+                            const uint32_t s_loc = smem_u32(&sempty[chunk % Cfg::SF_WARPS]);
                             mma_commit_pair(mapa_shared(s_loc, 0));
                             mma_commit_pair(mapa_shared(s_loc, 1));
                             ++chunk;
@@ -734,65 +733,36 @@ grp_gemm_kernel(const __grid_constant__ CUtensorMap tmA,
     } else {
         if constexpr (Cfg::MX) {
             // ---------------------------------------- block scales (4-bit, both)
-            // Each CTA brings the scales of its own lanes and of all the tile's rows;
-            // rows may start anywhere.  Plain 16-byte loads of 384 rows for 512 k took
-            // longer than the MMAs, and a row costs the copy engine about the same for
-            // 16 bytes as for 32.
+            // Each CTA brings the scales of its own lanes and of all the tile's rows,
+            // which may start anywhere, in asynchronous 16-byte copies: two lanes to a
+            // row, a sector.  (8192 x 8192 x 8192: plain loads 376 us with 16 bytes of a
+            // row at a time, their lines thrash what shared memory leaves of L1; boxes
+            // of the copy engine 220, of 32 bytes 191: a chunk's 384 rows land late.)
             const int turn = warp - (3 + Cfg::EPI_WARPS);
-            uint32_t chunk = 0, armed = 0;
+            const uint32_t slot = smem_u32(smSf + turn * Cfg::SF_SLOT);
+            uint32_t chunk = 0, uses = 0;
             bool ok = true;
             int g = 0;
-            if (turn == Cfg::SF_WARPS - 1) {
-                if (elect_one()) {
-                    tma_prefetch_desc(&tmSA);
-                    tma_prefetch_desc(&tmSB);
-                    for (int w = pair; w < num_items && ok; w += npairs) {
-                        const GrpItem it = item(w, g);
-                        const int n0 = it.n0 + static_cast<int>(rank) * 128;
-                        const bool a_live = n0 < p.N, b_two = it.width > 128 && it.m0 + 128 < p.M;
-                        const uint32_t bytes = (1 + a_live + b_two) * Cfg::SF_TILE;
-                        for (int c = 0; c < (it.kb + 3) / 4; ++c, ++chunk) {
-                            const uint32_t i = chunk % Cfg::SF_SLOTS;
-                            if (!bounded_wait(&sempty[i], ((chunk / Cfg::SF_SLOTS) & 1) ^ 1, abort_flag, limit, p.status)) {
-                                ok = false;
-                                break;
-                            }
-                            uint8_t* slot = smSf + i * Cfg::SF_SLOT;
-                            mbar_arrive_expect_tx(&sraw[i], bytes);
-                            armed |= 1u << i;
-                            if (a_live) tma_load_3d(slot, &tmSA, &sraw[i], 32 * c, n0, it.e);
-                            tma_load_2d(slot + Cfg::SF_TILE, &tmSB, &sraw[i], 32 * c, it.m0);
-                            if (b_two) tma_load_2d(slot + 2 * Cfg::SF_TILE, &tmSB, &sraw[i], 32 * c, it.m0 + 128);
-                        }
-                    }
-                    // loads that nobody waits for any more
-                    for (uint32_t i = 0; i < Cfg::SF_SLOTS && !ok; ++i)
-                        if (armed & (1u << i)) {
-                            const uint32_t last = (chunk - 1 - i) / Cfg::SF_SLOTS;     // uses of the slot before its last
-                            volatile int never = 0;
-                            bounded_wait(&sraw[i], last & 1, &never, limit, p.status);
-                        }
-                }
-                __syncwarp();
-            } else {
-                for (int w = pair; w < num_items && ok; w += npairs) {
-                    const GrpItem it = item(w, g);
-                    for (int c = 0; c < (it.kb + 3) / 4; ++c, ++chunk) {
-                        if (static_cast<int>(chunk % (Cfg::SF_WARPS - 1)) != turn) continue;
-                        const uint32_t i = chunk % Cfg::SF_SLOTS;
-                        if (!bounded_wait(&sraw[i], (chunk / Cfg::SF_SLOTS) & 1, abort_flag, limit, p.status)) {
-                            ok = false;
-                            break;
-                        }
-                        const uint32_t slot = smem_u32(smSf + i * Cfg::SF_SLOT);
-                        order_scales<2>(slot, lane);
-                        order_scales<2>(slot + Cfg::SF_TILE, lane);
-                        if (it.width > 128) order_scales<2>(slot + 2 * Cfg::SF_TILE, lane);
-                        // the copies into both CTAs' tensor memory are issued by the leader
-                        fence_proxy_async_smem();
-                        __syncwarp();
-                        if (lane == 0) mbar_arrive_release_cluster(mapa_shared(smem_u32(&sfull[i]), 0));
-                    }
+            for (int w = pair; w < num_items && ok; w += npairs) {
+                const GrpItem it = item(w, g);
+                const int n0 = it.n0 + static_cast<int>(rank) * 128;
+                const uint8_t* cols = p.col_blocks + it.e * p.block_plane;
+                const int tiles = it.width > 128 ? 3 : 2;
+                for (int c = 0; c < (it.kb + 3) / 4; ++c, ++chunk) {
+                    if (static_cast<int>(chunk % Cfg::SF_WARPS) != turn) continue;
+                    if (!bounded_wait(&sempty[turn], (uses & 1) ^ 1, abort_flag, limit, p.status)) { ok = false; break; }
+                    ++uses;
+                    load_scales(slot, cols, n0, p.N, p.block_ldb, 32 * c, p.blocks, lane);
+                    load_scales(slot + Cfg::SF_TILE, p.row_blocks, it.m0, p.M, p.block_lda, 32 * c, p.blocks, lane);
+                    if (tiles > 2)
+                        load_scales(slot + 2 * Cfg::SF_TILE, p.row_blocks, it.m0 + 128, p.M, p.block_lda, 32 * c, p.blocks, lane);
+                    cp_async_wait();
+                    __syncwarp();
+                    for (int i = 0; i < tiles; ++i) order_scales<2>(slot + i * Cfg::SF_TILE, lane);
+                    // the copies into both CTAs' tensor memory are issued by the leader
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive_release_cluster(mapa_shared(smem_u32(&sfull[turn]), 0));
                 }
             }
         }
