@@ -1084,17 +1084,31 @@ def expert_matmul(Xs, W, groups):
 
 # ------------------------------------------- microscaled 4-bit floating point
 
-def _blocks(q, scales, name):
-    """(rows, K in pairs) of row-major codes and their scales: uint8 rows x
-    K / 2 and rows x ceil(K / 32); for stacks of matrices, of one of them."""
+def _row_pitch(t, name):
+    """_pitch of a 2-D tensor, quickly where it has more than one row."""
+    down, across = t.stride()
+    return down if across == 1 and t.shape[0] > 1 else _pitch(t, name)
+
+
+def _check_blocks(q, scales, dims, name):
+    """Codes and their scales: uint8, `dims` dimensions, the same rows, one scale
+    for every 16 bytes."""
     import torch
     if q.dtype != torch.uint8 or scales.dtype != torch.uint8:
         raise TypeError(f"{name} and its scales must be uint8")
-    if q.dim() != scales.dim() or q.shape[:-1] != scales.shape[:-1]:
+    if q.dim() != dims:
+        raise ValueError(f"{name} must be {dims}-D")
+    if q.shape[:-1] != scales.shape[:-1]:
         raise ValueError(f"{name} and its scales must have the same rows")
-    if scales.shape[-1] != -(-q.shape[-1] // 16):
-        raise ValueError(f"{name} needs one scale for every 16 bytes of a row")
-    return q.shape[-2], q.shape[-1]
+    raise ValueError(f"{name} needs one scale for every 16 bytes of a row")
+
+
+def _bytes_out(t, M, N, name):
+    """The row pitch of t, a given M x N matrix of bytes."""
+    import torch
+    if t.shape != (M, N) or t.dtype != torch.uint8:
+        raise ValueError(f"{name} has the wrong shape or dtype")
+    return _pitch(t, name)
 
 
 def quant_mxfp4(X, plan=None, Q=None, scales=None, stream=None):
@@ -1108,6 +1122,13 @@ def quant_mxfp4(X, plan=None, Q=None, scales=None, stream=None):
     expert_gather does: row plan.pos[t, j] of the results is X[t], the rows of
     dropped choices are zero.  Rows of X that do not start on 16-byte boundaries
     are copied to such ones first."""
+    if stream is not None:
+        with _memory_of(stream, X.device):
+            return _quant_mxfp4(X, plan, Q, scales, stream)
+    return _quant_mxfp4(X, plan, Q, scales, None)
+
+
+def _quant_mxfp4(X, plan, Q, scales, stream):
     import torch
     if X.dim() != 2:
         raise ValueError("X must be 2-D")
@@ -1121,28 +1142,30 @@ def quant_mxfp4(X, plan=None, Q=None, scales=None, stream=None):
             raise ValueError("X must have one row per token of the plan")
         rows = T * k
         _one_device(device, (plan._pos,), "the plan")
-    with contextlib.nullcontext() if stream is None else _memory_of(stream, device):
-        X = _aligned_rows(X)
-        Q, ldq = _bytes_out(Q, rows, -(-K // 2), device, "Q")
-        scales, lds = _bytes_out(scales, rows, -(-K // 32), device, "scales")
-    _one_device(device, (Q, scales), "Q, scales")
+    X = _aligned_rows(X)
+    wide, blocks = (K + 1) // 2, (K + 31) // 32
+    u8 = torch.uint8
+    if Q is None:
+        ldq = (wide + 15) // 16 * 16 or 16
+        Q = torch.empty_strided((rows, wide), (ldq, 1), dtype=u8, device=device)
+    else:
+        ldq = _bytes_out(Q, rows, wide, "Q")
+        _one_device(device, (Q,), "Q")
+    if scales is None:
+        lds = (blocks + 15) // 16 * 16 or 16
+        scales = torch.empty_strided((rows, blocks), (lds, 1), dtype=u8, device=device)
+    else:
+        lds = _bytes_out(scales, rows, blocks, "scales")
+        _one_device(device, (scales,), "scales")
+    if not X.is_cuda:
+        _require_cuda(device, (X, "X"))
     if plan is None:
-        _launch("tg_quant_mxfp4", device, stream, M, K, X.data_ptr(), _pitch(X, "X"), kind,
+        _launch("tg_quant_mxfp4", device, stream, M, K, X.data_ptr(), _row_pitch(X, "X"), kind,
                 Q.data_ptr(), ldq, scales.data_ptr(), lds)
     else:
-        _launch("tg_expert_quant_mxfp4", device, stream, T, k, K, X.data_ptr(), _pitch(X, "X"), kind,
+        _launch("tg_expert_quant_mxfp4", device, stream, T, k, K, X.data_ptr(), _row_pitch(X, "X"), kind,
                 plan._pos.data_ptr(), plan._kept(), Q.data_ptr(), ldq, scales.data_ptr(), lds)
     return Q, scales
-
-
-def _bytes_out(t, M, N, device, name):
-    """(t, its row pitch), a new M x N matrix of bytes where it is None."""
-    import torch
-    if t is None:
-        return _rows_out(M, N, torch.uint8, device)
-    if t.shape != (M, N) or t.dtype != torch.uint8:
-        raise ValueError(f"{name} has the wrong shape or dtype")
-    return t, _pitch(t, name)
 
 
 def dequant_mxfp4(Q, scales, K=None, C=None, out_dtype=None, stream=None):
@@ -1150,9 +1173,10 @@ def dequant_mxfp4(Q, scales, K=None, C=None, out_dtype=None, stream=None):
     rounded once to out_dtype (float16 or bfloat16, by default C's or bfloat16).
     K defaults to all that Q holds."""
     import torch
-    if Q.dim() != 2:
-        raise ValueError("Q must be 2-D")
-    M, pairs = _blocks(Q, scales, "Q")
+    u8 = torch.uint8
+    if Q.dtype != u8 or scales.dtype != u8 or Q.dim() != 2 or scales.shape != (Q.shape[0], (Q.shape[1] + 15) // 16):
+        _check_blocks(Q, scales, 2, "Q")
+    M, pairs = Q.shape
     if K is None:
         K = 2 * pairs
     elif (K + 1) // 2 != pairs:
@@ -1163,8 +1187,8 @@ def dequant_mxfp4(Q, scales, K=None, C=None, out_dtype=None, stream=None):
     device = Q.device
     C, ldc = _out(C, M, K, out_dtype, device, stream)
     _one_device(device, (scales, C), "scales, C")
-    _launch("tg_dequant_mxfp4", device, stream, M, K, Q.data_ptr(), _pitch(Q, "Q"), scales.data_ptr(),
-            _pitch(scales, "scales"), C.data_ptr(), ldc, kind)
+    _launch("tg_dequant_mxfp4", device, stream, M, K, Q.data_ptr(), _row_pitch(Q, "Q"), scales.data_ptr(),
+            _row_pitch(scales, "scales"), C.data_ptr(), ldc, kind)
     return C
 
 
@@ -1176,9 +1200,14 @@ def gemm_mxfp4(A, a_scales, B, b_scales, C=None, out_dtype=None, relu=False, str
     scale) stays one, also with relu.  Quantised rows of odd length end in a zero
     half byte, which adds nothing."""
     import torch
-    if A.dim() != 2 or B.dim() != 2:
-        raise ValueError("A and B must be 2-D")
-    (M, pairs), (N, pairs2) = _blocks(A, a_scales, "A"), _blocks(B, b_scales, "B")
+    u8 = torch.uint8
+    if A.dtype != u8 or a_scales.dtype != u8 or A.dim() != 2 or \
+            a_scales.shape != (A.shape[0], (A.shape[1] + 15) // 16):
+        _check_blocks(A, a_scales, 2, "A")
+    if B.dtype != u8 or b_scales.dtype != u8 or B.dim() != 2 or \
+            b_scales.shape != (B.shape[0], (B.shape[1] + 15) // 16):
+        _check_blocks(B, b_scales, 2, "B")
+    (M, pairs), (N, pairs2) = A.shape, B.shape
     if pairs != pairs2:
         raise ValueError(f"inner dimensions differ: {2 * pairs} vs {2 * pairs2}")
     if out_dtype is None:
@@ -1187,9 +1216,9 @@ def gemm_mxfp4(A, a_scales, B, b_scales, C=None, out_dtype=None, relu=False, str
     device = A.device
     C, ldc = _out(C, M, N, out_dtype, device, stream)
     _one_device(device, (a_scales, B, b_scales, C), "a_scales, B, b_scales, C")
-    _launch("tg_gemm_mxfp4", device, stream, M, N, 2 * pairs, A.data_ptr(), _pitch(A, "A"),
-            a_scales.data_ptr(), _pitch(a_scales, "a_scales"), B.data_ptr(), _pitch(B, "B"),
-            b_scales.data_ptr(), _pitch(b_scales, "b_scales"), C.data_ptr(), ldc, kind,
+    _launch("tg_gemm_mxfp4", device, stream, M, N, 2 * pairs, A.data_ptr(), _row_pitch(A, "A"),
+            a_scales.data_ptr(), _row_pitch(a_scales, "a_scales"), B.data_ptr(), _row_pitch(B, "B"),
+            b_scales.data_ptr(), _row_pitch(b_scales, "b_scales"), C.data_ptr(), ldc, kind,
             EPI_RELU if relu else EPI_NONE)
     return C
 
@@ -1200,11 +1229,18 @@ def gemm_grouped_mxfp4(A, a_scales, groups, B, b_scales, C=None, out_dtype=None,
     B uint8 E x N x K/2 with scales E x N x ceil(K / 32); groups is an ExpertPlan
     or its offsets.  Rows behind the last group are zero."""
     import torch
+    u8 = torch.uint8
     offsets = _offsets_of(groups)
     E = offsets.shape[0] - 1
-    if A.dim() != 2 or B.dim() != 3 or B.shape[0] != E:
-        raise ValueError("A must be 2-D and B one matrix per group")
-    (M, pairs), (N, pairs2) = _blocks(A, a_scales, "A"), _blocks(B, b_scales, "B")
+    if A.dtype != u8 or a_scales.dtype != u8 or A.dim() != 2 or \
+            a_scales.shape != (A.shape[0], (A.shape[1] + 15) // 16):
+        _check_blocks(A, a_scales, 2, "A")
+    if B.dtype != u8 or b_scales.dtype != u8 or B.dim() != 3 or \
+            b_scales.shape != (B.shape[0], B.shape[1], (B.shape[2] + 15) // 16):
+        _check_blocks(B, b_scales, 3, "B")
+    (M, pairs), (E2, N, pairs2) = A.shape, B.shape
+    if E2 != E:
+        raise ValueError("B must hold one matrix per group")
     if pairs != pairs2:
         raise ValueError(f"inner dimensions differ: {2 * pairs} vs {2 * pairs2}")
     if out_dtype is None:
@@ -1213,8 +1249,8 @@ def gemm_grouped_mxfp4(A, a_scales, groups, B, b_scales, C=None, out_dtype=None,
     device = A.device
     C, ldc = _out(C, M, N, out_dtype, device, stream)
     _one_device(device, (a_scales, B, b_scales, offsets, C), "a_scales, B, b_scales, offsets, C")
-    _launch("tg_gemm_grouped_mxfp4", device, stream, M, N, 2 * pairs, E, A.data_ptr(), _pitch(A, "A"),
-            a_scales.data_ptr(), _pitch(a_scales, "a_scales"), offsets.data_ptr(),
+    _launch("tg_gemm_grouped_mxfp4", device, stream, M, N, 2 * pairs, E, A.data_ptr(), _row_pitch(A, "A"),
+            a_scales.data_ptr(), _row_pitch(a_scales, "a_scales"), offsets.data_ptr(),
             B.data_ptr(), _pitch(B, "B"), _plane(B), b_scales.data_ptr(), _pitch(b_scales, "b_scales"),
             _plane(b_scales), C.data_ptr(), ldc, kind, EPI_RELU if relu else EPI_NONE)
     return C
@@ -1225,69 +1261,75 @@ def gemm_grouped_mxfp4(A, a_scales, groups, B, b_scales, C=None, out_dtype=None,
 SCORES = {"softmax": 0, "sigmoid": 1}
 
 
-def _route_args(logits):
-    """(type, row pitch) of the router's logits, copied where they are not
-    row-major."""
+def _logits(x):
+    """(x, its type, its row pitch), x copied where it is not row-major."""
     import torch
-    kind = TYPE_F32 if logits.dtype == torch.float32 else _type16(logits.dtype, "logits other than float32")
-    T, E = logits.shape
-    down, across = logits.stride()
-    if (across != 1 and E > 1) or (T > 1 and down < E):
-        logits = logits.contiguous()
+    dtype = x.dtype
+    kind = TYPE_F32 if dtype == torch.float32 else _type16(dtype, "logits other than float32")
+    (T, E), (down, across) = x.shape, x.stride()
+    if T <= 1 or E <= 1 or across != 1 or down < E:
+        x = x.contiguous()
         down = E
-    return logits, kind, down if T > 1 else E
+    return x, kind, down
 
 
 def _route(logits, topk, bias, score, groups, keep, renorm, scale):
     import torch
     T, E = logits.shape
     device = logits.device
-    x, kind, ldl = _route_args(logits)
+    x, kind, ldl = _logits(logits)
     ids = torch.empty_strided((T, topk), (topk, 1), dtype=torch.int32, device=device)
     weights = torch.empty_strided((T, topk), (topk, 1), dtype=torch.float32, device=device)
+    at_bias = None
     if bias is not None:
         _vector(bias, E, torch.float32, "bias")
         _one_device(device, (bias,), "bias")
-    _one_device(device, (x,), "logits")
-    _launch("tg_expert_route", device, None, T, E, x.data_ptr(), ldl, kind,
-            None if bias is None else bias.data_ptr(), score, groups, keep, topk, renorm, scale,
-            ids.data_ptr(), weights.data_ptr())
+        at_bias = bias.data_ptr()
+    if not x.is_cuda:
+        _require_cuda(device, (x, "logits"))
+    _launch("tg_expert_route", device, None, T, E, x.data_ptr(), ldl, kind, at_bias, score, groups, keep,
+            topk, renorm, scale, ids.data_ptr(), weights.data_ptr())
     return ids, weights
 
 
 def _route_function():
     import torch
+    grad_enabled = torch.is_grad_enabled
 
     class _Route(torch.autograd.Function):
         """Experts and weights of each token; the weights' gradient reaches the
         logits, the choice has none."""
 
         @staticmethod
-        def forward(ctx, logits, *args):
+        def forward(ctx, logits, args):
             ids, weights = _route(logits, *args)
-            topk, _, score, _, _, renorm, scale = args
-            ctx.args = score, topk, renorm, scale
+            ctx.args = args
             ctx.save_for_backward(logits, ids)
             ctx.mark_non_differentiable(ids)
+            ctx.set_materialize_grads(False)
             return ids, weights
 
         @staticmethod
         def backward(ctx, _, g):
-            if torch.is_grad_enabled():
+            if grad_enabled():
                 raise RuntimeError("the experts' operators are differentiable once")
+            if g is None:
+                return None, None
             logits, ids = ctx.saved_tensors
-            score, topk, renorm, scale = ctx.args
+            topk, _, score, _, _, renorm, scale = ctx.args
             T, E = logits.shape
-            x, kind, ldl = _route_args(logits)
-            g = g.contiguous()
+            x, kind, ldl = _logits(logits)
+            if not g.is_contiguous():
+                g = g.contiguous()
             device = x.device
-            _one_device(device, (g,), "the gradient")
-            d = torch.empty_strided((T, E), (E, 1), dtype=logits.dtype, device=device)
+            if g.device != device:
+                _one_device(device, (g,), "the gradient")
+            d = torch.empty_strided((T, E), (E, 1), dtype=x.dtype, device=device)
             _launch("tg_expert_route_grad", device, None, T, E, x.data_ptr(), ldl, kind, score, topk, renorm,
                     scale, ids.data_ptr(), g.data_ptr(), d.data_ptr(), E)
-            return (d,) + (None,) * 7
+            return d, None
 
-    return _Route
+    return _Route.apply
 
 
 _ROUTE = None
@@ -1302,24 +1344,27 @@ def expert_route(logits, topk, *, bias=None, score="softmax", groups=1, topk_gro
     The scores are softmax(logits) or sigmoid(logits).  The topk highest are
     chosen in falling order, ties to the lower number; a bias (float32, E) is
     added to the scores for the choice alone.  With groups (of E / groups
-    consecutive experts) the choice is made in the topk_groups groups (by default all) whose two
-    highest (biased) scores sum highest.  Weights are scale times the chosen scores,
-    divided by their sum with renorm.  Minus infinity is never chosen; where fewer than topk
-    are left, the rest are -1 (dropped choices) and weigh 0.  A NaN or plus infinity
-    makes its row's weights NaN.  Differentiable in the logits."""
+    consecutive experts) the choice is made in the topk_groups of them (by default
+    all) whose two highest (biased) scores sum highest.  Weights are scale times the
+    chosen scores, divided by their sum with renorm.  Minus infinity is never
+    chosen; where fewer than topk are left, the rest are -1 (dropped choices) and
+    weigh 0.  A NaN or plus infinity makes its row's weights NaN.  Differentiable in
+    the logits."""
     global _ROUTE
     import torch
     if logits.dim() != 2:
         raise ValueError("logits must be 2-D (tokens x experts)")
-    if score not in SCORES:
+    kind = SCORES.get(score)
+    if kind is None:
         raise ValueError("score must be 'softmax' or 'sigmoid'")
-    args = (topk, bias, SCORES[score], groups, groups if topk_groups is None else topk_groups,
-            1 if renorm else 0, scale)
+    if topk < 1:
+        raise ValueError("topk must be at least 1")
+    args = (topk, bias, kind, groups, groups if topk_groups is None else topk_groups, 1 if renorm else 0, scale)
     if not (logits.requires_grad and torch.is_grad_enabled()):
         return _route(logits, *args)
     if _ROUTE is None:
         _ROUTE = _route_function()
-    return _ROUTE.apply(logits, *args)
+    return _ROUTE(logits, args)
 
 
 def last_device_status(stream=None):
