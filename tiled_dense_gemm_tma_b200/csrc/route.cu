@@ -11,21 +11,25 @@
 // are -1 and weigh 0.  A NaN or plus infinity is chosen before all else, and makes
 // every weight of its row NaN.
 //
-// The order is that of 64-bit arithmetic.  Without bias and groups it is the
-// order of the logits, which is exact.  Otherwise keys are formed in 32 bits and a
-// row is done again in 64 where two keys that decide something are closer
-// than their errors could reach: neighbours among the topk + 1 first of
-// different logit or bias, or the last kept and the first dropped group.  (In
-// 64 bits throughout, the exponentials alone cost more than reading the logits.)
-// Errors: a sigmoid is off by less than 2^-21, e^(x - top) / sum by less than
-// 2^-19 of the row's largest score (the difference, rounded, shifts it by
-// |x - top| 2^-24 of itself, and y e^-y < 1), the sum with the bias by 2^-24 of
-// itself; a group's sum by twice that.
+// The order is that of 64-bit arithmetic.  Keys are 32-bit: a value in the order of
+// its bits, the lowest ones given to the lane's number of the expert, so that one
+// comparison moves both.  A row is done again in 64 bits where two keys that decide
+// something are closer than their errors could reach: neighbours among the topk +
+// 1 first of different logit or bias, or the last kept and the first dropped
+// group.  (In 64 bits throughout, the exponentials alone cost more than reading
+// the logits.)  Errors: a key that is a logit has lost its lowest bits only, so that
+// equal ones are in question; 16-bit logits lose nothing.  An exponential is off by
+// (2 + 1.5 |v|) 2^-23 of itself; a sigmoid by less than 2^-22 then (s (1 - s) |v| <
+// 1/4), e^(x - top) / sum by less than 2^-18 of the row's largest score (y e^-y <
+// 1/2, and a sum of E terms), the sum with the bias by 2^-24 of itself; a group's
+// sum by twice that.
 //
 // A warp takes a token.  The row is dealt out so that a group lies in 32 /
 // (groups, up to a power of two) neighbouring lanes, V consecutive experts a
 // lane: what is found by lane order is in the order of the experts' numbers.
-// The chosen sit one in each of the first topk lanes.
+// Each lane sorts its keys (two instructions a comparison), and each choice is the
+// largest of the lanes' first, which that lane drops.  The chosen sit one in each
+// of the first topk lanes.
 #include "host.cuh"
 #include "launch.h"
 #include "route.h"
@@ -50,6 +54,19 @@ __device__ __forceinline__ float warp_sum(float v) {
     return v;
 }
 
+constexpr float kLog2e = 1.44269504f;
+
+__device__ __forceinline__ float exp2_of(float v) {
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
+    return r;
+}
+__device__ __forceinline__ float reciprocal(float v) {
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
+    return r;
+}
+
 // A 32-bit key in the order of the value: 0 is below all, ~0 above all.
 __device__ __forceinline__ uint32_t ordered(float v) {
     const uint32_t u = __float_as_uint(v + 0.f);           // -0 is 0
@@ -59,9 +76,27 @@ __device__ __forceinline__ float value_of(uint32_t key) {
     return __uint_as_float(key ^ (key >> 31 ? 0x80000000u : 0xffffffffu));
 }
 
+// Falling order (odd-even merge sort; V a power of two).
+template <int V>
+__device__ __forceinline__ void sort_keys(uint32_t (&k)[V]) {
+#pragma unroll
+    for (int p = 1; p < V; p *= 2)
+#pragma unroll
+        for (int q = p; q >= 1; q /= 2)
+#pragma unroll
+            for (int j = q % p; j + q < V; j += 2 * q)
+#pragma unroll
+                for (int i = 0; i < q; ++i)
+                    if (i + j + q < V && (i + j) / (2 * p) == (i + j + q) / (2 * p)) {
+                        const uint32_t a = k[i + j], b = k[i + j + q];
+                        k[i + j] = max(a, b);
+                        k[i + j + q] = min(a, b);
+                    }
+}
+
 struct RouteParams {
     int tokens, E, groups, keep, topk, per;      // per: experts to a group
-    int lanes;                                   // lanes to a group (a power of two)
+    int lanes, shift;                            // lanes to a group, 1 << shift
     int sigmoid, renorm;
     float scale;
     const void* logits;
@@ -98,16 +133,40 @@ template <class F>
 __device__ __forceinline__ int group_rank(F score, int group, const RouteParams& p) {
     int before = 0;
     for (int g = 0; g < p.groups; ++g) {
-        const F other = __shfl_sync(kAll, score, g * p.lanes);
+        const F other = __shfl_sync(kAll, score, g << p.shift);
         before += other > score || (other == score && g < group);
     }
     return before;
 }
 
-// A row in 64 bits: choices only.  `x` are the lane's logits, dead ones
-// (minus infinity, or past the group's end) as -inf; all are below +inf.
-template <int V>
-__device__ __noinline__ int choose_exact(const RouteParams& p, const float (&x)[V], int first, int live, float top, int lane) {
+// V values of a row for a lane, `none` from the live-th on; as 16-byte vectors
+// where `vec`.
+template <int V, class T>
+__device__ __forceinline__ void load_row(const T* row, int live, bool vec, float none, float (&x)[V]) {
+    constexpr int N = 16 / sizeof(T);
+    if constexpr (V % N == 0) {
+        if (vec) {
+#pragma unroll
+            for (int i = 0; i < V; i += N) {
+                uint4 v = make_uint4(0, 0, 0, 0);
+                if (i < live) v = __ldg(reinterpret_cast<const uint4*>(row + i));
+                const T* e = reinterpret_cast<const T*>(&v);
+#pragma unroll
+                for (int j = 0; j < N; ++j) x[i + j] = i < live ? to_float(e[j]) : none;
+            }
+            return;
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < V; ++i) x[i] = i < live ? to_float(row[i]) : none;
+}
+
+// A row in 64 bits: choices only, of logits below plus infinity.  It reads them
+// again: an array handed to it would live in memory in every row.
+template <int V, class T>
+__device__ __noinline__ int choose_exact(const RouteParams& p, const T* row, int first, int live, float top, int lane) {
+    float x[V];
+    load_row<V>(row + first, live, false, -kInf, x);
     double s[V];
     double sum = 0.0;
     if (!p.sigmoid) {
@@ -134,7 +193,7 @@ __device__ __noinline__ int choose_exact(const RouteParams& p, const float (&x)[
             b = lo > b ? lo : b;
         }
         group_top2(a, b, p.lanes);
-        in = group_rank(group_score(a, b), lane / p.lanes, p) < p.keep;
+        in = group_rank(group_score(a, b), lane >> p.shift, p) < p.keep;
     }
     // without a bias the logits have the scores' order, and keep it where scores saturate
     if (!p.bias) {
@@ -164,130 +223,165 @@ __device__ __noinline__ int choose_exact(const RouteParams& p, const float (&x)[
     return mine;
 }
 
+// vec: the rows, the groups and the bias allow 16-byte loads.
 template <int V, class T>
 __global__ void __launch_bounds__(256)
-route_kernel(const RouteParams p) {
+route_kernel(const RouteParams p, const bool vec) {
+    constexpr uint32_t kLow = V - 1;                          // a key's bits that number the lane's experts
+    constexpr uint32_t kNone = 0x007fffffu, kOver = 0xff800000u;    // the infinities, ordered
     const int lane = threadIdx.x & 31;
-    const long long t = blockIdx.x * 8ll + (threadIdx.x >> 5);
+    const int t = blockIdx.x * 8 + (threadIdx.x >> 5);
     if (t >= p.tokens) return;
     const T* row = static_cast<const T*>(p.logits) + t * p.ldl;
-    const int group = lane / p.lanes, off = (lane % p.lanes) * V;
-    const int first = group * p.per + off;                    // this lane's experts: first .. first + live - 1
-    const int live = group < p.groups ? min(V, p.per - off) : 0;
-    float x[V];
-    bool bad = false;
-    float top = -kInf;
+    const int group = lane >> p.shift, part = lane & (p.lanes - 1);
+    const int first = group * p.per + part * V;               // this lane's experts: first .. first + live - 1
+    const int live = group < p.groups ? min(V, p.per - part * V) : 0;
+    const bool keyed = p.bias != nullptr;                     // keys are scores, not logits
+    float x[V], s[V];
+    load_row<V>(row + first, live, vec, -kInf, x);
+    if (keyed) load_row<V>(p.bias + first, live, vec, 0.f, s);
+    uint32_t key[V];
+    uint32_t most = 0, least = ~0u;
 #pragma unroll
     for (int i = 0; i < V; ++i) {
-        x[i] = i < live ? to_float(row[first + i]) : -kInf;
-        bad |= !(x[i] < kInf);
-        top = fmaxf(top, x[i]);
+        key[i] = ordered(x[i]);
+        most = max(most, key[i]);
+        least = min(least, key[i]);
     }
-    const bool bad_row = __any_sync(kAll, bad);
-    const bool keyed = p.bias != nullptr;                     // keys are scores, not logits
-    const bool sums = !p.sigmoid && (keyed || p.groups > 1 || !p.renorm);
-    float sum = 1.f;
-    top = value_of(__reduce_max_sync(kAll, ordered(top)));
-    if (sums) {
-        sum = 0.f;
+    most = __reduce_max_sync(kAll, most);
+    // masked experts, lanes that are not full; NaNs (those with a sign lie below
+    // minus infinity) and plus infinity
+    const bool odd = __any_sync(kAll, least <= kNone) || most >= kOver;
+    bool bad_row = false;
+    if (odd) {
+        bool bad = false;
+#pragma unroll
+        for (int i = 0; i < V; ++i) bad |= !(x[i] < kInf);
+        bad_row = __any_sync(kAll, bad);
+    }
+    const float top = value_of(most);                         // where it matters the row is not a bad one
+    float inv = 1.f;
+    if (!p.sigmoid && (keyed || p.groups > 1 || !p.renorm)) {
+        float sum = 0.f;
 #pragma unroll
         for (int i = 0; i < V; ++i) sum += x[i] > -kInf ? expf(x[i] - top) : 0.f;
-        sum = warp_sum(sum);
+        inv = 1.f / warp_sum(sum);
     }
-    const float inv = 1.f / sum;
-    uint32_t key[V];
-    bool close = false;
-    if (keyed || p.groups > 1) {
-        float a = -kInf, b = -kInf, s[V];
+    auto score_of = [&](float v) {
+        return p.sigmoid ? reciprocal(1.f + exp2_of(v * -kLog2e)) : exp2_of((v - top) * kLog2e) * inv;
+    };
+    if (!odd) {
+        if (keyed)
 #pragma unroll
-        for (int i = 0; i < V; ++i) {
-            const float score = bad_row ? 0.f : p.sigmoid ? 1.f / (1.f + expf(-x[i])) : expf(x[i] - top) * inv;
-            s[i] = !(x[i] < kInf) ? kInf : x[i] == -kInf ? -kInf : keyed ? score + __ldg(p.bias + first + i) : score;
-            const float lo = fminf(s[i], a);
-            a = fmaxf(s[i], a);
-            b = fmaxf(b, lo);
-        }
-        bool in = true;
-        if (p.groups > 1) {
-            group_top2(a, b, p.lanes);
-            const float score = group < p.groups ? group_score(a, b) : -kInf;
-            const int rank = group_rank(score, group, p);
-            in = rank < p.keep;
-            // the first of the dropped groups, the last of the kept ones
-            const bool head = group < p.groups && lane % p.lanes == 0;
-            const unsigned out_at = __ballot_sync(kAll, head && rank == p.keep);
-            const unsigned in_at = __ballot_sync(kAll, head && rank == p.keep - 1);
-            if (out_at && in_at) {
-                const float hi = __shfl_sync(kAll, score, __ffs(in_at) - 1), lo = __shfl_sync(kAll, score, __ffs(out_at) - 1);
-                close = lo > -kInf && hi - lo <= 2.f * route_slack(p.sigmoid ? 1.f : inv, fmaxf(fabsf(hi), fabsf(lo)));
-            }
-        }
+            for (int i = 0; i < V; ++i) key[i] = ordered(score_of(x[i]) + s[i]);
 #pragma unroll
-        for (int i = 0; i < V; ++i) {
-            const float v = keyed ? s[i] : x[i];
-            key[i] = !in || x[i] == -kInf ? 0u : !(x[i] < kInf) ? ~0u : ordered(v);
-        }
+        for (int i = 0; i < V; ++i) key[i] = (key[i] & ~kLow) | (kLow - i);
     } else {
 #pragma unroll
-        for (int i = 0; i < V; ++i) key[i] = x[i] == -kInf ? 0u : !(x[i] < kInf) ? ~0u : ordered(x[i]);
+        for (int i = 0; i < V; ++i) {
+            uint32_t k = key[i];
+            // a NaN or plus infinity takes the other scores of its row with it
+            if (keyed) k = ordered((bad_row ? 0.f : score_of(x[i])) + s[i]);
+            if (!(x[i] < kInf)) k = ~0u;
+            key[i] = x[i] == -kInf ? 0u : (k & ~kLow) | (kLow - i);
+        }
     }
-    // the topk largest, and with keys that are rounded the next one
-    const int picks = min(32, p.topk + (keyed ? 1 : 0));
-    uint32_t best = 0;
-    int at = 0;
-    auto scan = [&] {
-        best = 0;
-        at = 0;
+    sort_keys(key);
+    bool close = false, in = true;
+    if (p.groups > 1) {
+        auto best_score = [&](uint32_t k) -> float {
+            if (k == 0) return -kInf;
+            if (keyed) return value_of(k & ~kLow);
+            float v = x[0];
 #pragma unroll
-        for (int i = 0; i < V; ++i)
-            if (key[i] > best) { best = key[i]; at = i; }
-    };
-    scan();
-    int mine = -1;                                            // lane j: the j-th choice, its key
+            for (int i = 1; i < V; ++i) v = kLow - (k & kLow) == i ? x[i] : v;
+            return !(v < kInf) ? kInf : bad_row ? 0.f : score_of(v);
+        };
+        float a = best_score(key[0]), b = V > 1 ? best_score(key[V > 1 ? 1 : 0]) : -kInf;
+        if (bad_row) {                                        // truncated NaNs
+            if (!(a <= kInf)) a = kInf;
+            if (!(b <= kInf)) b = kInf;
+        }
+        group_top2(a, b, p.lanes);
+        const float score = group < p.groups ? group_score(a, b) : -kInf;
+        const int rank = group_rank(score, group, p);
+        in = rank < p.keep;
+        // the first of the dropped groups, the last of the kept ones
+        const bool head = group < p.groups && part == 0;
+        const unsigned out_at = __ballot_sync(kAll, head && rank == p.keep);
+        const unsigned in_at = __ballot_sync(kAll, head && rank == p.keep - 1);
+        if (out_at && in_at) {
+            const int hi_at = __ffs(in_at) - 1, lo_at = __ffs(out_at) - 1;
+            const float size = fabsf(a) + (b > -kInf ? fabsf(b) : 0.f);      // terms may cancel in the sum
+            const float hi = __shfl_sync(kAll, score, hi_at), lo = __shfl_sync(kAll, score, lo_at);
+            const float larger = fmaxf(__shfl_sync(kAll, size, hi_at), __shfl_sync(kAll, size, lo_at));
+            close = lo > -kInf && hi - lo <= 2.f * route_slack(p.sigmoid, inv, larger, V);
+        }
+    }
+    // the topk largest.  Lanes are compared without the bits that number their
+    // experts: of equal values the lowest lane's is the lowest expert.
+    uint32_t best = in && key[0] ? key[0] | kLow : 0u;
+    int mine = -1;                                            // lane j: the j-th choice
     uint32_t mkey = 0;
-    for (int j = 0; j < picks; ++j) {
+    for (int j = 0; j < p.topk; ++j) {
         const uint32_t m = __reduce_max_sync(kAll, best);
         if (m == 0) break;
         const int win = __ffs(__ballot_sync(kAll, best == m)) - 1;
-        const int e = __shfl_sync(kAll, first + at, win);
+        const int e = __shfl_sync(kAll, first + static_cast<int>(kLow - (key[0] & kLow)), win);
         if (lane == j) { mine = e; mkey = m; }
         if (lane == win) {
 #pragma unroll
-            for (int i = 0; i < V; ++i)
-                if (i == at) key[i] = 0;
-            scan();
+            for (int i = 0; i + 1 < V; ++i) key[i] = key[i + 1];
+            key[V - 1] = 0;
+            best = key[0] ? key[0] | kLow : 0u;
         }
     }
-    float mx = mine >= 0 ? to_float(row[mine]) : -kInf;
-    if (keyed && !bad_row) {
-        // neighbours whose order the keys' rounding could have changed
-        const float v = mkey ? value_of(mkey) : -kInf, next = __shfl_down_sync(kAll, v, 1);
-        const float bias = mine >= 0 ? __ldg(p.bias + mine) : 0.f;
-        const float nx = __shfl_down_sync(kAll, mx, 1), nb = __shfl_down_sync(kAll, bias, 1);
-        const bool near = lane < 31 && next > -kInf && (mx != nx || bias != nb) &&
-                          v - next <= route_slack(p.sigmoid ? 1.f : inv, fmaxf(fabsf(v), fabsf(next)));
-        close = close || __any_sync(kAll, near) || p.topk == 32;
+    if (!bad_row && (keyed || (sizeof(T) == 4 && V > 1))) {
+        // neighbours whose order the keys could have got wrong, the next key after
+        // the choices among them
+        const uint32_t lkey = __reduce_max_sync(kAll, best);
+        uint32_t nkey = __shfl_down_sync(kAll, mkey, 1);
+        if (lane == p.topk - 1) nkey = lkey;
+        bool near = lane < p.topk && mkey && nkey && mkey == nkey;
+        if (keyed) {
+            const float v = value_of(mkey & ~kLow), next = value_of(nkey & ~kLow);
+            near = lane < p.topk && mkey && nkey &&
+                   v - next <= route_slack(p.sigmoid, inv, fmaxf(fabsf(v), fabsf(next)), V);
+        }
+        if (__any_sync(kAll, near)) {
+            // the same logit and bias are a tie, and ties are in order
+            const int win = __ffs(__ballot_sync(kAll, best == lkey)) - 1;
+            const int last = __shfl_sync(kAll, first + static_cast<int>(kLow - (key[0] & kLow)), win);
+            int next = __shfl_down_sync(kAll, mine, 1);
+            if (lane == p.topk - 1) next = last;
+            near = near && (to_float(row[mine]) != to_float(row[next]) ||
+                            (keyed && __ldg(p.bias + mine) != __ldg(p.bias + next)));
+            close = close || __any_sync(kAll, near);
+        }
     }
-    if (close && !bad_row) {
-        mine = choose_exact<V>(p, x, first, live, top, lane);
-        mx = mine >= 0 ? to_float(row[mine]) : -kInf;
-    }
+    if (close && !bad_row) mine = choose_exact<V>(p, row, first, live, top, lane);
     if (lane >= p.topk) mine = -1;
     const bool has = mine >= 0;
+    const float mx = has ? to_float(row[mine]) : -kInf;
     float w;
     if (p.renorm) {
-        // the chosen scores over their sum, from their logarithms: no sum vanishes
-        const float l = !has ? -kInf : p.sigmoid ? fminf(mx, 0.f) - log1pf(expf(-fabsf(mx))) : mx;
-        const float lt = value_of(__reduce_max_sync(kAll, ordered(l)));
-        w = has ? expf(l - lt) : 0.f;
-        w /= warp_sum(w);
+        // the chosen scores over their sum; where they could vanish, from their logarithms
+        if (p.sigmoid && !__any_sync(kAll, has && !(mx > -60.f))) {
+            w = has ? reciprocal(1.f + expf(-mx)) : 0.f;
+        } else {
+            const float l = !has ? -kInf : p.sigmoid ? fminf(mx, 0.f) - log1pf(expf(-fabsf(mx))) : mx;
+            const float lt = value_of(__reduce_max_sync(kAll, ordered(l)));
+            w = has ? expf(l - lt) : 0.f;
+        }
+        w *= reciprocal(warp_sum(w));
     } else {
         w = p.sigmoid ? 1.f / (1.f + expf(-mx)) : expf(mx - top) * inv;
     }
     w = bad_row ? __uint_as_float(0x7fc00000u) : has ? w * p.scale : 0.f;
     if (lane < p.topk) {
-        p.ids[t * p.topk + lane] = mine;
-        p.weights[t * p.topk + lane] = w;
+        const long long at = static_cast<long long>(t) * p.topk + lane;
+        p.ids[at] = mine;
+        p.weights[at] = w;
     }
 }
 
@@ -360,6 +454,7 @@ RouteParams params(const RouteArgs& a) {
     p.topk = a.topk;
     p.per = a.E / a.groups;
     p.lanes = route_lanes(a.groups);
+    while (1 << p.shift < p.lanes) ++p.shift;
     p.sigmoid = a.sigmoid;
     p.renorm = a.renorm;
     p.scale = a.scale;
@@ -378,13 +473,17 @@ template <class T>
 void start(const RouteParams& p, cudaStream_t s) {
     const unsigned blocks = static_cast<unsigned>((p.tokens + 7ll) / 8);
     const int v = route_values(p.E, p.groups);
-    if (v <= 1) route_kernel<1, T><<<blocks, 256, 0, s>>>(p);
-    else if (v <= 2) route_kernel<2, T><<<blocks, 256, 0, s>>>(p);
-    else if (v <= 4) route_kernel<4, T><<<blocks, 256, 0, s>>>(p);
-    else if (v <= 8) route_kernel<8, T><<<blocks, 256, 0, s>>>(p);
-    else if (v <= 16) route_kernel<16, T><<<blocks, 256, 0, s>>>(p);
-    else if (v <= 32) route_kernel<32, T><<<blocks, 256, 0, s>>>(p);
-    else route_kernel<64, T><<<blocks, 256, 0, s>>>(p);
+    // whole vectors a lane, in every row and group
+    constexpr int N = 16 / sizeof(T);
+    const bool vec = p.per % N == 0 && (p.tokens == 1 || p.ldl % N == 0) && reinterpret_cast<uintptr_t>(p.logits) % 16 == 0 &&
+                     p.per % 4 == 0 && reinterpret_cast<uintptr_t>(p.bias) % 16 == 0;
+    if (v <= 1) route_kernel<1, T><<<blocks, 256, 0, s>>>(p, vec);
+    else if (v <= 2) route_kernel<2, T><<<blocks, 256, 0, s>>>(p, vec);
+    else if (v <= 4) route_kernel<4, T><<<blocks, 256, 0, s>>>(p, vec);
+    else if (v <= 8) route_kernel<8, T><<<blocks, 256, 0, s>>>(p, vec);
+    else if (v <= 16) route_kernel<16, T><<<blocks, 256, 0, s>>>(p, vec);
+    else if (v <= 32) route_kernel<32, T><<<blocks, 256, 0, s>>>(p, vec);
+    else route_kernel<64, T><<<blocks, 256, 0, s>>>(p, vec);
 }
 
 }  // namespace

@@ -23,11 +23,12 @@ TG_HD_ROUTE int route_values(int E, int groups) {
     return (E / groups + route_lanes(groups) - 1) / route_lanes(groups);
 }
 
-// What the difference of two keys of at most `size`, sums of a score of at most
-// `score` and a bias, may be off by: twice 2^-19 of the score and 2^-24 of
-// the sum, with as much again to spare.
-TG_HD_ROUTE float route_slack(float score, float size) {
-    return score * 0x1p-17f + size * 0x1p-22f;
+// What the difference of two keys of at most `size` may be off by, sums of a
+// score (a sigmoid, or one of a softmax of at most `highest`) and a bias: the
+// errors of both scores and of both sums (2^-24 each), twice over, and the bits that
+// number a lane's `values` experts.
+TG_HD_ROUTE float route_slack(int sigmoid, float highest, float size, int values) {
+    return (sigmoid ? 0x1p-20f : highest * 0x1p-16f) + size * (0x1p-22f + 0x1p-23f * static_cast<float>(values));
 }
 
 }  // namespace tg
