@@ -147,51 +147,75 @@ quant_mxfp4_kernel(long long units, int per_row, int K, const uint16_t* __restri
     }
 }
 
-template <bool BF16>
+// The same units of a row a warp, back.
+template <bool BF16, int UNROLL>
 __global__ void __launch_bounds__(256)
-dequant_mxfp4_kernel(long long vecs, int per_row, int K, const uint8_t* __restrict__ Q, long long ldq,
+dequant_mxfp4_kernel(long long units, int per_row, int K, const uint8_t* __restrict__ Q, long long ldq,
                      const uint8_t* __restrict__ S, long long lds, uint16_t* __restrict__ Y, long long ldy) {
-    const long long t = blockIdx.x * 256ll + threadIdx.x;
-    if (t >= vecs) return;
-    const long long row = t / per_row;
-    const int v = static_cast<int>(t - row * per_row);
-    const uint8_t* q = Q + row * ldq + 4ll * v;
-    const int left = K - 8 * v;
-    uint32_t c = 0;
-    if (left >= 8) {
-        c = __ldg(reinterpret_cast<const uint32_t*>(q));
-    } else {
+    const int lane = threadIdx.x & 31;
+    const long long unit = blockIdx.x * 8ll + (threadIdx.x >> 5);
+    if (unit >= units) return;
+    const long long row = unit / per_row;
+    const int v0 = static_cast<int>(unit - row * per_row) * (32 * UNROLL) + lane;
+    const uint8_t* q = Q + row * ldq;
+    const uint8_t* s = S + row * lds;
+    uint32_t c[UNROLL], E[UNROLL];
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
-            if (2 * j < left) c |= static_cast<uint32_t>(__ldg(q + j)) << (8 * j);
-    }
-    const uint32_t E = __ldg(S + row * lds + (v >> 2));
-    const float up = __uint_as_float(E == 0 ? 0x00400000u : E == 255 ? 0x7fc00000u : E << 23);
-    __half2 h[4];
-    values8(c, h);
-    uint32_t o[4];
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-        const float2 f = __half22float2(h[j]);
-        if constexpr (BF16) {
-            const __nv_bfloat162 b = __floats2bfloat162_rn(f.x * up, f.y * up);
-            o[j] = *reinterpret_cast<const uint32_t*>(&b);
+    for (int i = 0; i < UNROLL; ++i) {
+        const int v = v0 + 32 * i, left = K - 8 * v;
+        c[i] = E[i] = 0;
+        if (left > 0) E[i] = __ldg(s + (v >> 2));
+        if (left >= 8) {
+            c[i] = __ldg(reinterpret_cast<const uint32_t*>(q) + v);
         } else {
-            const __half2 b = __floats2half2_rn(f.x * up, f.y * up);
-            o[j] = *reinterpret_cast<const uint32_t*>(&b);
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                if (2 * j < left) c[i] |= static_cast<uint32_t>(__ldg(q + 4ll * v + j)) << (8 * j);
         }
     }
-    uint16_t* y = Y + row * ldy + 8ll * v;
-    if (left >= 8) {
-        *reinterpret_cast<uint4*>(y) = make_uint4(o[0], o[1], o[2], o[3]);
-    } else {
 #pragma unroll
-        for (int j = 0; j < 7; ++j)
-            if (j < left) y[j] = static_cast<uint16_t>(o[j >> 1] >> (16 * (j & 1)));
+    for (int i = 0; i < UNROLL; ++i) {
+        const int v = v0 + 32 * i, left = K - 8 * v;
+        const float up = __uint_as_float(E[i] == 0 ? 0x00400000u : E[i] == 255 ? 0x7fc00000u : E[i] << 23);
+        __half2 h[4];
+        values8(c[i], h);
+        uint32_t o[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const float2 f = __half22float2(h[j]);
+            if constexpr (BF16) {
+                const __nv_bfloat162 b = __floats2bfloat162_rn(f.x * up, f.y * up);
+                o[j] = *reinterpret_cast<const uint32_t*>(&b);
+            } else {
+                const __half2 b = __floats2half2_rn(f.x * up, f.y * up);
+                o[j] = *reinterpret_cast<const uint32_t*>(&b);
+            }
+        }
+        uint16_t* y = Y + row * ldy + 8ll * v;
+        if (left >= 8) {
+            *reinterpret_cast<uint4*>(y) = make_uint4(o[0], o[1], o[2], o[3]);
+        } else {
+#pragma unroll
+            for (int j = 0; j < 7; ++j)
+                if (j < left) y[j] = static_cast<uint16_t>(o[j >> 1] >> (16 * (j & 1)));
+        }
     }
 }
 
 constexpr long long kMaxBlocks = 0x7fffffffll;
+
+// Few values, or short rows: more warps, each with less to wait for.
+bool few_values(int64_t M, int64_t K) { return K <= 256 || M * ((K + 1023) / 1024) < 148 * 16; }
+
+template <bool BF16, int UNROLL>
+int back(int64_t M, int64_t K, const uint8_t* Q, int64_t ldq, const uint8_t* scales, int64_t lds, void* Y, int64_t ldy,
+         cudaStream_t s) {
+    const long long per_row = (K + 256 * UNROLL - 1) / (256 * UNROLL), units = M * per_row;
+    if ((units + 7) / 8 > kMaxBlocks) return kUnsupported;
+    dequant_mxfp4_kernel<BF16, UNROLL><<<static_cast<unsigned>((units + 7) / 8), 256, 0, s>>>(
+        units, static_cast<int>(per_row), static_cast<int>(K), Q, ldq, scales, lds, static_cast<uint16_t*>(Y), ldy);
+    return cudaGetLastError() == cudaSuccess ? kOk : kCudaError;
+}
 
 template <bool BF16, bool PLACES, int UNROLL>
 int start(int64_t M, int64_t K, const void* X, int64_t ldx, int topk, const int* pos, const int* kept, uint8_t* Q,
@@ -207,8 +231,7 @@ int start(int64_t M, int64_t K, const void* X, int64_t ldx, int topk, const int*
 template <bool BF16, bool PLACES>
 int pick(int64_t M, int64_t K, const void* X, int64_t ldx, int topk, const int* pos, const int* kept, uint8_t* Q,
          int64_t ldq, uint8_t* scales, int64_t lds, cudaStream_t s) {
-    // few values: more warps, each with less to wait for
-    if (K <= 256 || M * ((K + 1023) / 1024) < 148 * 16)
+    if (few_values(M, K))
         return start<BF16, PLACES, 1>(M, K, X, ldx, topk, pos, kept, Q, ldq, scales, lds, s);
     return start<BF16, PLACES, 4>(M, K, X, ldx, topk, pos, kept, Q, ldq, scales, lds, s);
 }
@@ -229,15 +252,10 @@ int launch_quant_mxfp4(int64_t M, int64_t K, const void* X, int64_t ldx, int bf1
 int launch_dequant_mxfp4(int64_t M, int64_t K, const uint8_t* Q, int64_t ldq, const uint8_t* scales, int64_t lds,
                          void* Y, int64_t ldy, int bf16, void* stream) {
     if (!current_device(nullptr)) return kNoDevice;
-    const long long per_row = (K + 7) / 8, vecs = M * per_row, blocks = (vecs + 255) / 256;
-    if (blocks > kMaxBlocks) return kUnsupported;
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
-    uint16_t* y = static_cast<uint16_t*>(Y);
-    if (bf16)
-        dequant_mxfp4_kernel<true><<<static_cast<unsigned>(blocks), 256, 0, s>>>(vecs, static_cast<int>(per_row), static_cast<int>(K), Q, ldq, scales, lds, y, ldy);
-    else
-        dequant_mxfp4_kernel<false><<<static_cast<unsigned>(blocks), 256, 0, s>>>(vecs, static_cast<int>(per_row), static_cast<int>(K), Q, ldq, scales, lds, y, ldy);
-    return cudaGetLastError() == cudaSuccess ? kOk : kCudaError;
+    if (few_values(M, K))
+        return bf16 ? back<true, 1>(M, K, Q, ldq, scales, lds, Y, ldy, s) : back<false, 1>(M, K, Q, ldq, scales, lds, Y, ldy, s);
+    return bf16 ? back<true, 4>(M, K, Q, ldq, scales, lds, Y, ldy, s) : back<false, 4>(M, K, Q, ldq, scales, lds, Y, ldy, s);
 }
 
 }  // namespace tg
