@@ -1145,14 +1145,16 @@ def _quant_mxfp4(X, plan, Q, scales, stream):
     X = _aligned_rows(X)
     wide, blocks = (K + 1) // 2, (K + 31) // 32
     u8 = torch.uint8
+    # rows of codes on 128-byte lines, of scales on 32-byte sectors, where that adds
+    # little: 3000 x 5000 x 4000 takes 41 us so, 45 with rows 2000 bytes apart
     if Q is None:
-        ldq = (wide + 15) // 16 * 16 or 16
+        ldq = (wide + 127) // 128 * 128 if wide > 512 else (wide + 15) // 16 * 16 or 16
         Q = torch.empty_strided((rows, wide), (ldq, 1), dtype=u8, device=device)
     else:
         ldq = _bytes_out(Q, rows, wide, "Q")
         _one_device(device, (Q,), "Q")
     if scales is None:
-        lds = (blocks + 15) // 16 * 16 or 16
+        lds = (blocks + 31) // 32 * 32 if blocks > 32 else (blocks + 15) // 16 * 16 or 16
         scales = torch.empty_strided((rows, blocks), (lds, 1), dtype=u8, device=device)
     else:
         lds = _bytes_out(scales, rows, blocks, "scales")

@@ -44,9 +44,10 @@ long long max_items(const GroupArgs& a) {
 }
 
 template <class Cfg>
-int launch(const GroupArgs& a, long long items, const CUtensorMap& tA, const CUtensorMap (&tB)[4],
+int launch(const GroupArgs& a, long long items, int tiles, const CUtensorMap& tA, const CUtensorMap (&tB)[4],
            const CUtensorMap& tC, int num_sms) {
-    const GrpParams p = params(a);
+    GrpParams p = params(a);
+    p.tiles = tiles;
     if (!p.status) return kCudaError;
     // a tile of a thin wave runs as up to four pieces (WG: two)
     const long long npairs = persistent_grid(items * (Cfg::WG ? 2 : 4), num_sms / 2, 0);
@@ -75,7 +76,13 @@ int run_product(const GroupArgs& a, CUtensorMapDataType dt, int slot) {
     if (pair_kernels_disabled()) return kUnsupported;
     const DeviceInfo* di = current_device(nullptr);
     if (!di) return kNoDevice;
-    const long long items = max_items(a);
+    long long items = max_items(a);
+    int tiles = 0;
+    if (Cfg::MX && !a.offsets) {
+        const long long ntl = (a.g.N - 1) / 256 + 1;
+        tiles = mx4_even_tiles(a.g.M, ntl, di->num_sms / 2);
+        items = tiles * ntl;
+    }
     if (items > 0x7fffffffll) return kUnsupported;
     constexpr int eb = Cfg::EB;
     const GemmArgs& g = a.g;
@@ -91,7 +98,7 @@ int run_product(const GroupArgs& a, CUtensorMapDataType dt, int slot) {
             return kCudaError;
     if (set_smem_attr(reinterpret_cast<const void*>(grp_gemm_kernel<Cfg>), Cfg::SMEM_BYTES, slot) != cudaSuccess)
         return kCudaError;
-    return launch<Cfg>(a, items, tA, tB, tA, di->num_sms);
+    return launch<Cfg>(a, items, tiles, tA, tB, tA, di->num_sms);
 }
 
 template <class Cfg>
@@ -111,7 +118,7 @@ int run_grad(const GroupArgs& a, CUtensorMapDataType dt, int slot) {
     tB[1] = tB[2] = tB[3] = tB[0];
     if (set_smem_attr(reinterpret_cast<const void*>(grp_gemm_kernel<Cfg>), Cfg::SMEM_BYTES, slot) != cudaSuccess)
         return kCudaError;
-    return launch<Cfg>(a, per * a.E, tA, tB, tC, di->num_sms);
+    return launch<Cfg>(a, per * a.E, 0, tA, tB, tC, di->num_sms);
 }
 
 }  // namespace

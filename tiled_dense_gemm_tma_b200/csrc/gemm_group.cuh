@@ -82,6 +82,7 @@ struct GrpParams {
     const uint8_t* col_blocks;  // N rows of W_e, block_ldb apart, block_plane per group
     long long block_lda, block_ldb, block_plane;
     int blocks;               // scale bytes in a row
+    int tiles;                // row tiles where one group holds all rows; 0: as its rows ask for
 };
 
 // TYPE: 0 f16, 1 bf16 (idesc formats), 3 signed 8-bit, 4 4-bit floating point
@@ -371,6 +372,7 @@ grp_gemm_kernel(const __grid_constant__ CUtensorMap tmA,
     const int lanes_total = Cfg::WG ? p.K : p.N;
     const int ntl = (lanes_total - 1) / 256 + 1;
     const int ntg = Cfg::WG ? (p.N - 1) / 256 + 1 : 0;      // WG: tiles of G's columns
+    auto tiles_of = [&](int rows) { return Cfg::MX && p.tiles ? p.tiles : grp_tiles(rows); };
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < Cfg::STAGES; ++s) {
@@ -428,7 +430,7 @@ grp_gemm_kernel(const __grid_constant__ CUtensorMap tmA,
                 reached = __shfl_sync(0xffffffffu, low, 31);
                 r0 = low;
                 r1 = max(r1, r0);
-                if (r1 > r0) cnt = grp_tiles(r1 - r0) * ntl;
+                if (r1 > r0) cnt = tiles_of(r1 - r0) * ntl;
                 int sum = cnt;
 #pragma unroll
                 for (int d = 1; d < 32; d <<= 1) {
@@ -489,8 +491,8 @@ grp_gemm_kernel(const __grid_constant__ CUtensorMap tmA,
             it.r0 = grow[g];
             it.rows = r1 - it.r0;
             int tl, tt, at;
-            tile_coords(w - gstart[g], ntl, grp_tiles(it.rows), p.group_m, tl, tt);
-            grp_tile(it.rows, tt, at, it.width);
+            tile_coords(w - gstart[g], ntl, tiles_of(it.rows), p.group_m, tl, tt);
+            grp_tile(it.rows, tt, at, it.width, tiles_of(it.rows));
             it.n0 = tl * 256;
             it.m0 = it.r0 + at;
             it.m1 = min(r1, it.m0 + it.width);
