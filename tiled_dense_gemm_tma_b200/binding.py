@@ -1084,15 +1084,28 @@ def expert_matmul(Xs, W, groups):
 
 # ------------------------------------------- microscaled 4-bit floating point
 
-def _row_pitch(t, name):
-    """_pitch of a 2-D tensor, quickly where it has more than one row."""
-    down, across = t.stride()
-    return down if across == 1 and t.shape[0] > 1 else _pitch(t, name)
+# These calls are made several times a layer and token step, so that their checks
+# read each property once, and say what is wrong only where something is.
+
+_torch = None
+
+
+def _get_torch():
+    global _torch
+    import torch
+    _torch = torch
+    return torch
+
+
+def _row_pitch(t, rows, cols, name):
+    """_pitch of a matrix (of the last two dimensions), quickly where it is dense
+    and has more than one row."""
+    return cols if rows > 1 and t.is_contiguous() else _pitch(t, name)
 
 
 def _check_blocks(q, scales, dims, name):
-    """Codes and their scales: uint8, `dims` dimensions, the same rows, one scale
-    for every 16 bytes."""
+    """What is wrong with codes and their scales: uint8, `dims` dimensions, the
+    same rows, one scale for every 16 bytes."""
     import torch
     if q.dtype != torch.uint8 or scales.dtype != torch.uint8:
         raise TypeError(f"{name} and its scales must be uint8")
@@ -1100,15 +1113,33 @@ def _check_blocks(q, scales, dims, name):
         raise ValueError(f"{name} must be {dims}-D")
     if q.shape[:-1] != scales.shape[:-1]:
         raise ValueError(f"{name} and its scales must have the same rows")
-    raise ValueError(f"{name} needs one scale for every 16 bytes of a row")
+    if scales.shape[-1] != (q.shape[-1] + 15) // 16:
+        raise ValueError(f"{name} needs one scale for every 16 bytes of a row")
 
 
-def _bytes_out(t, M, N, name):
+def _bytes_out(t, M, N, device, name):
     """The row pitch of t, a given M x N matrix of bytes."""
     import torch
     if t.shape != (M, N) or t.dtype != torch.uint8:
         raise ValueError(f"{name} has the wrong shape or dtype")
+    _one_device(device, (t,), name)
     return _pitch(t, name)
+
+
+def _values_out(C, M, N, out_dtype, device, stream):
+    """(C, its type, its row pitch): C made where it is None, of out_dtype, by
+    default bfloat16."""
+    torch = _torch or _get_torch()
+    if C is None and stream is None:
+        dtype = torch.bfloat16 if out_dtype is None else out_dtype
+        kind = TYPE_BF16 if dtype is torch.bfloat16 else _type16(dtype, "C")
+        ldc = (N + 7) // 8 * 8 or 8
+        return torch.empty_strided((M, N), (ldc, 1), dtype=dtype, device=device), kind, ldc
+    if out_dtype is None:
+        out_dtype = torch.bfloat16 if C is None else C.dtype
+    kind = _type16(out_dtype, "C")
+    C, ldc = _out(C, M, N, out_dtype, device, stream)
+    return C, kind, ldc
 
 
 def quant_mxfp4(X, plan=None, Q=None, scales=None, stream=None):
@@ -1129,10 +1160,11 @@ def quant_mxfp4(X, plan=None, Q=None, scales=None, stream=None):
 
 
 def _quant_mxfp4(X, plan, Q, scales, stream):
-    import torch
+    torch = _torch or _get_torch()
+    dtype = X.dtype
+    kind = TYPE_BF16 if dtype is torch.bfloat16 else _type16(dtype, "X")
     if X.dim() != 2:
         raise ValueError("X must be 2-D")
-    kind = _type16(X.dtype, "X")
     M, K = X.shape
     device = X.device
     rows = M
@@ -1142,31 +1174,32 @@ def _quant_mxfp4(X, plan, Q, scales, stream):
             raise ValueError("X must have one row per token of the plan")
         rows = T * k
         _one_device(device, (plan._pos,), "the plan")
-    X = _aligned_rows(X)
+    if not X.is_cuda:
+        _require_cuda(device, (X, "X"))
+    at = X.data_ptr()
+    if K % 8 == 0 and M > 1 and at % 16 == 0 and X.is_contiguous():
+        ldx = K
+    else:
+        X = _aligned_rows(X)
+        at, ldx = X.data_ptr(), _pitch(X, "X")
     wide, blocks = (K + 1) // 2, (K + 31) // 32
-    u8 = torch.uint8
     # rows of codes on 128-byte lines, of scales on 32-byte sectors, where that adds
     # little: 3000 x 5000 x 4000 takes 41 us so, 45 with rows 2000 bytes apart
     if Q is None:
         ldq = (wide + 127) // 128 * 128 if wide > 512 else (wide + 15) // 16 * 16 or 16
-        Q = torch.empty_strided((rows, wide), (ldq, 1), dtype=u8, device=device)
+        Q = torch.empty_strided((rows, wide), (ldq, 1), dtype=torch.uint8, device=device)
     else:
-        ldq = _bytes_out(Q, rows, wide, "Q")
-        _one_device(device, (Q,), "Q")
+        ldq = _bytes_out(Q, rows, wide, device, "Q")
     if scales is None:
         lds = (blocks + 31) // 32 * 32 if blocks > 32 else (blocks + 15) // 16 * 16 or 16
-        scales = torch.empty_strided((rows, blocks), (lds, 1), dtype=u8, device=device)
+        scales = torch.empty_strided((rows, blocks), (lds, 1), dtype=torch.uint8, device=device)
     else:
-        lds = _bytes_out(scales, rows, blocks, "scales")
-        _one_device(device, (scales,), "scales")
-    if not X.is_cuda:
-        _require_cuda(device, (X, "X"))
+        lds = _bytes_out(scales, rows, blocks, device, "scales")
     if plan is None:
-        _launch("tg_quant_mxfp4", device, stream, M, K, X.data_ptr(), _row_pitch(X, "X"), kind,
-                Q.data_ptr(), ldq, scales.data_ptr(), lds)
+        _launch("tg_quant_mxfp4", device, stream, M, K, at, ldx, kind, Q.data_ptr(), ldq, scales.data_ptr(), lds)
     else:
-        _launch("tg_expert_quant_mxfp4", device, stream, T, k, K, X.data_ptr(), _row_pitch(X, "X"), kind,
-                plan._pos.data_ptr(), plan._kept(), Q.data_ptr(), ldq, scales.data_ptr(), lds)
+        _launch("tg_expert_quant_mxfp4", device, stream, T, k, K, at, ldx, kind, plan._pos.data_ptr(),
+                plan._kept(), Q.data_ptr(), ldq, scales.data_ptr(), lds)
     return Q, scales
 
 
@@ -1174,23 +1207,23 @@ def dequant_mxfp4(Q, scales, K=None, C=None, out_dtype=None, stream=None):
     """The M x K values of codes and scales as quant_mxfp4 gives them, each
     rounded once to out_dtype (float16 or bfloat16, by default C's or bfloat16).
     K defaults to all that Q holds."""
-    import torch
+    torch = _torch or _get_torch()
     u8 = torch.uint8
-    if Q.dtype != u8 or scales.dtype != u8 or Q.dim() != 2 or scales.shape != (Q.shape[0], (Q.shape[1] + 15) // 16):
+    if Q.dim() != 2 or Q.dtype is not u8 or scales.dtype is not u8:
         _check_blocks(Q, scales, 2, "Q")
     M, pairs = Q.shape
+    blocks = (pairs + 15) // 16
+    if scales.shape != (M, blocks):
+        _check_blocks(Q, scales, 2, "Q")
     if K is None:
         K = 2 * pairs
     elif (K + 1) // 2 != pairs:
         raise ValueError("Q must have ceil(K / 2) bytes a row")
-    if out_dtype is None:
-        out_dtype = torch.bfloat16 if C is None else C.dtype
-    kind = _type16(out_dtype, "C")
     device = Q.device
-    C, ldc = _out(C, M, K, out_dtype, device, stream)
+    C, kind, ldc = _values_out(C, M, K, out_dtype, device, stream)
     _one_device(device, (scales, C), "scales, C")
-    _launch("tg_dequant_mxfp4", device, stream, M, K, Q.data_ptr(), _row_pitch(Q, "Q"), scales.data_ptr(),
-            _row_pitch(scales, "scales"), C.data_ptr(), ldc, kind)
+    _launch("tg_dequant_mxfp4", device, stream, M, K, Q.data_ptr(), _row_pitch(Q, M, pairs, "Q"),
+            scales.data_ptr(), _row_pitch(scales, M, blocks, "scales"), C.data_ptr(), ldc, kind)
     return C
 
 
@@ -1201,27 +1234,26 @@ def gemm_mxfp4(A, a_scales, B, b_scales, C=None, out_dtype=None, relu=False, str
     is float16 or bfloat16 (out_dtype, by default C's or bfloat16).  A NaN (of a
     scale) stays one, also with relu.  Quantised rows of odd length end in a zero
     half byte, which adds nothing."""
-    import torch
+    torch = _torch or _get_torch()
     u8 = torch.uint8
-    if A.dtype != u8 or a_scales.dtype != u8 or A.dim() != 2 or \
-            a_scales.shape != (A.shape[0], (A.shape[1] + 15) // 16):
+    if A.dim() != 2 or B.dim() != 2 or A.dtype is not u8 or a_scales.dtype is not u8 or \
+            B.dtype is not u8 or b_scales.dtype is not u8:
         _check_blocks(A, a_scales, 2, "A")
-    if B.dtype != u8 or b_scales.dtype != u8 or B.dim() != 2 or \
-            b_scales.shape != (B.shape[0], (B.shape[1] + 15) // 16):
         _check_blocks(B, b_scales, 2, "B")
     (M, pairs), (N, pairs2) = A.shape, B.shape
     if pairs != pairs2:
         raise ValueError(f"inner dimensions differ: {2 * pairs} vs {2 * pairs2}")
-    if out_dtype is None:
-        out_dtype = torch.bfloat16 if C is None else C.dtype
-    kind = _type16(out_dtype, "C")
+    blocks = (pairs + 15) // 16
+    if a_scales.shape != (M, blocks) or b_scales.shape != (N, blocks):
+        _check_blocks(A, a_scales, 2, "A")
+        _check_blocks(B, b_scales, 2, "B")
     device = A.device
-    C, ldc = _out(C, M, N, out_dtype, device, stream)
-    _one_device(device, (a_scales, B, b_scales, C), "a_scales, B, b_scales, C")
-    _launch("tg_gemm_mxfp4", device, stream, M, N, 2 * pairs, A.data_ptr(), _row_pitch(A, "A"),
-            a_scales.data_ptr(), _row_pitch(a_scales, "a_scales"), B.data_ptr(), _row_pitch(B, "B"),
-            b_scales.data_ptr(), _row_pitch(b_scales, "b_scales"), C.data_ptr(), ldc, kind,
-            EPI_RELU if relu else EPI_NONE)
+    C, kind, ldc = _values_out(C, M, N, out_dtype, device, stream)
+    _same_gpu(A, a_scales, B, b_scales, C, "A, a_scales, B, b_scales, C")
+    _launch("tg_gemm_mxfp4", device, stream, M, N, 2 * pairs, A.data_ptr(), _row_pitch(A, M, pairs, "A"),
+            a_scales.data_ptr(), _row_pitch(a_scales, M, blocks, "a_scales"),
+            B.data_ptr(), _row_pitch(B, N, pairs, "B"), b_scales.data_ptr(),
+            _row_pitch(b_scales, N, blocks, "b_scales"), C.data_ptr(), ldc, kind, EPI_RELU if relu else EPI_NONE)
     return C
 
 
@@ -1230,32 +1262,41 @@ def gemm_grouped_mxfp4(A, a_scales, groups, B, b_scales, C=None, out_dtype=None,
     """gemm_mxfp4 over groups of rows: row r of group e times W[e].T, the weights
     B uint8 E x N x K/2 with scales E x N x ceil(K / 32); groups is an ExpertPlan
     or its offsets.  Rows behind the last group are zero."""
-    import torch
+    torch = _torch or _get_torch()
     u8 = torch.uint8
     offsets = _offsets_of(groups)
     E = offsets.shape[0] - 1
-    if A.dtype != u8 or a_scales.dtype != u8 or A.dim() != 2 or \
-            a_scales.shape != (A.shape[0], (A.shape[1] + 15) // 16):
+    if A.dim() != 2 or B.dim() != 3 or b_scales.dim() != 3 or A.dtype is not u8 or a_scales.dtype is not u8 or \
+            B.dtype is not u8 or b_scales.dtype is not u8:
         _check_blocks(A, a_scales, 2, "A")
-    if B.dtype != u8 or b_scales.dtype != u8 or B.dim() != 3 or \
-            b_scales.shape != (B.shape[0], B.shape[1], (B.shape[2] + 15) // 16):
         _check_blocks(B, b_scales, 3, "B")
     (M, pairs), (E2, N, pairs2) = A.shape, B.shape
     if E2 != E:
         raise ValueError("B must hold one matrix per group")
     if pairs != pairs2:
         raise ValueError(f"inner dimensions differ: {2 * pairs} vs {2 * pairs2}")
-    if out_dtype is None:
-        out_dtype = torch.bfloat16 if C is None else C.dtype
-    kind = _type16(out_dtype, "C")
+    blocks = (pairs + 15) // 16
+    if a_scales.shape != (M, blocks) or b_scales.shape != (E, N, blocks):
+        _check_blocks(A, a_scales, 2, "A")
+        _check_blocks(B, b_scales, 3, "B")
     device = A.device
-    C, ldc = _out(C, M, N, out_dtype, device, stream)
-    _one_device(device, (a_scales, B, b_scales, offsets, C), "a_scales, B, b_scales, offsets, C")
-    _launch("tg_gemm_grouped_mxfp4", device, stream, M, N, 2 * pairs, E, A.data_ptr(), _row_pitch(A, "A"),
-            a_scales.data_ptr(), _row_pitch(a_scales, "a_scales"), offsets.data_ptr(),
-            B.data_ptr(), _pitch(B, "B"), _plane(B), b_scales.data_ptr(), _pitch(b_scales, "b_scales"),
-            _plane(b_scales), C.data_ptr(), ldc, kind, EPI_RELU if relu else EPI_NONE)
+    C, kind, ldc = _values_out(C, M, N, out_dtype, device, stream)
+    _one_device(device, (offsets,), "offsets")
+    _same_gpu(A, a_scales, B, b_scales, C, "A, a_scales, B, b_scales, C")
+    _launch("tg_gemm_grouped_mxfp4", device, stream, M, N, 2 * pairs, E, A.data_ptr(),
+            _row_pitch(A, M, pairs, "A"), a_scales.data_ptr(), _row_pitch(a_scales, M, blocks, "a_scales"),
+            offsets.data_ptr(), B.data_ptr(), _row_pitch(B, N, pairs, "B"), _plane(B), b_scales.data_ptr(),
+            _row_pitch(b_scales, N, blocks, "b_scales"), _plane(b_scales), C.data_ptr(), ldc, kind,
+            EPI_RELU if relu else EPI_NONE)
     return C
+
+
+def _same_gpu(a, b, c, d, e, names):
+    """All five on a's device, a GPU."""
+    index = a.get_device()
+    if b.get_device() != index or c.get_device() != index or d.get_device() != index or \
+            e.get_device() != index or index < 0:
+        _require_cuda(a.device, *zip((a, b, c, d, e), names.split(", ")))
 
 
 # ------------------------------------------------------------------ routing
@@ -1263,12 +1304,14 @@ def gemm_grouped_mxfp4(A, a_scales, groups, B, b_scales, C=None, out_dtype=None,
 SCORES = {"softmax": 0, "sigmoid": 1}
 
 
-def _logits(x):
+def _logits(x, T, E):
     """(x, its type, its row pitch), x copied where it is not row-major."""
-    import torch
+    torch = _torch or _get_torch()
     dtype = x.dtype
-    kind = TYPE_F32 if dtype == torch.float32 else _type16(dtype, "logits other than float32")
-    (T, E), (down, across) = x.shape, x.stride()
+    kind = TYPE_F32 if dtype is torch.float32 else _type16(dtype, "logits other than float32")
+    if x.is_contiguous():
+        return x, kind, E
+    down, across = x.stride()
     if T <= 1 or E <= 1 or across != 1 or down < E:
         x = x.contiguous()
         down = E
@@ -1276,10 +1319,10 @@ def _logits(x):
 
 
 def _route(logits, topk, bias, score, groups, keep, renorm, scale):
-    import torch
+    torch = _torch or _get_torch()
     T, E = logits.shape
     device = logits.device
-    x, kind, ldl = _logits(logits)
+    x, kind, ldl = _logits(logits, T, E)
     ids = torch.empty_strided((T, topk), (topk, 1), dtype=torch.int32, device=device)
     weights = torch.empty_strided((T, topk), (topk, 1), dtype=torch.float32, device=device)
     at_bias = None
@@ -1320,7 +1363,7 @@ def _route_function():
             logits, ids = ctx.saved_tensors
             topk, _, score, _, _, renorm, scale = ctx.args
             T, E = logits.shape
-            x, kind, ldl = _logits(logits)
+            x, kind, ldl = _logits(logits, T, E)
             if not g.is_contiguous():
                 g = g.contiguous()
             device = x.device
@@ -1353,7 +1396,7 @@ def expert_route(logits, topk, *, bias=None, score="softmax", groups=1, topk_gro
     weigh 0.  A NaN or plus infinity makes its row's weights NaN.  Differentiable in
     the logits."""
     global _ROUTE
-    import torch
+    torch = _torch or _get_torch()
     if logits.dim() != 2:
         raise ValueError("logits must be 2-D (tokens x experts)")
     kind = SCORES.get(score)
