@@ -474,6 +474,13 @@ skinny_kernel(const __grid_constant__ CUtensorMap tmW,
                 tc_fence_after();
                 const uint32_t sf = tmem_base + 2 * Cfg::ACC_COLS + (it & 1) * Cfg::SF_COLS;
                 if constexpr (Cfg::MX) {
+                    // the MMAs that read these columns, of the unit before the last, are done
+                    const int u2 = it - 2;
+                    if (u2 >= 0 && !bounded_wait(&rempty[u2 % Cfg::RAW_STAGES], (u2 / Cfg::RAW_STAGES) & 1, abort_flag, limit, p.status)) {
+                        ok = false;
+                        break;
+                    }
+                    tc_fence_after();
                     const uint32_t src = smem_u32(slot_sf(s));
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {

@@ -533,6 +533,7 @@ __device__ __forceinline__ bool mbar_try_wait_acq_cluster(uint64_t* bar, uint32_
 __device__ __forceinline__ bool bounded_wait_cluster(uint64_t* bar, uint32_t parity,
                                                      volatile int* abort, uint64_t limit_ns,
                                                      int* status) {
+    if (mbar_try_wait_acq_cluster(bar, parity, 1000000u)) return true;
     const uint64_t t0 = globaltimer_ns();
     for (;;) {
         if (mbar_try_wait_acq_cluster(bar, parity, 1000000u)) return true;
