@@ -172,22 +172,8 @@ struct GrpItem {
 // of the tile's rows, 32 at a time (half: which of HALVES warps).
 template <class Cfg>
 __device__ __forceinline__ void grp_store_rows(const GrpParams& p, const GrpItem& it, uint32_t taddr,
-                                               int nw, int half, int lane, uint8_t* stg, uint32_t acc, uint64_t* tpart) {
-    // 4-bit: the columns that two accumulators may share come first, the last ones
-    // of the first accumulator, the first of the second
-    bool parted = !(Cfg::MX && it.kb);
-    auto part = [&] {
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive_leader(tpart);
-        parted = true;
-    };
-    if (nw >= p.N) {                                        // warp-uniform
-        if (!parted) part();
-        return;
-    }
-    const int chunks = (it.m1 - it.m0 - 32 * half + 32 * Cfg::HALVES - 1) / (32 * Cfg::HALVES);
-    const bool down = Cfg::MX && acc == 0;
+                                               int nw, int half, int lane, uint8_t* stg) {
+    if (nw >= p.N) return;                                  // warp-uniform
     float cs[4] = {0.f, 0.f, 0.f, 0.f};
     if constexpr (Cfg::I8) {
         if (it.kb) {
@@ -203,9 +189,6 @@ __device__ __forceinline__ void grp_store_rows(const GrpParams& p, const GrpItem
             // a NaN (of the row's scale) stays one under ReLU; fmaxf would hide it,
             // and a comparison takes 2048 x 8192 x 1024 from 22.6 to 23.8 us
             const float x = (__int2float_rn(static_cast<int>(v)) * rs) * c;
-            return p.relu ? max_nan(x, 0.f) : x;
-        } else if constexpr (Cfg::MX) {
-            const float x = __uint_as_float(v);
             return p.relu ? max_nan(x, 0.f) : x;
         } else {
             const float x = __uint_as_float(v);
@@ -225,8 +208,7 @@ __device__ __forceinline__ void grp_store_rows(const GrpParams& p, const GrpItem
     const int mj = lane >> 3, mc = lane & 7;                // stmatrix: this lane's matrix and column
     const int rr = lane >> 2, ch = lane & 3;                // row store: row and 16-byte chunk
 #pragma unroll 1
-    for (int i = 0; i < chunks; ++i) {
-        const int m = it.m0 + 32 * (half + Cfg::HALVES * (down ? chunks - 1 - i : i));
+    for (int m = it.m0 + 32 * half; m < it.m1; m += 32 * Cfg::HALVES) {
         uint32_t v0[16], v1[16];
         if (it.kb) {
             tmem_ld_16x256b_x4(taddr + (m - it.m0), v0);
@@ -244,8 +226,7 @@ __device__ __forceinline__ void grp_store_rows(const GrpParams& p, const GrpItem
             }
         }
         if (it.kb) tmem_ld_wait();
-        if (!parted) part();
-        else __syncwarp();                                  // the last chunk's rows are read
+        __syncwarp();                                       // the last chunk's rows are read
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             const float ra = Cfg::I8 ? rs[2 * i] : 0.f, rb = Cfg::I8 ? rs[2 * i + 1] : 0.f;
@@ -277,7 +258,80 @@ __device__ __forceinline__ void grp_store_rows(const GrpParams& p, const GrpItem
             }
         }
     }
-    if (!parted) part();                                    // no rows of this warp's
+}
+
+// The same for a 4-bit product.  (Loading the next 32 rows before these are
+// written costs time: 8192 x 8192 x 1024 68 us, so 55.)  Columns that two accumulators may share come first, the last ones of the first
+// accumulator, the first of the second; tpart hears when they have been read.
+template <class Cfg>
+__device__ __forceinline__ void grp_store_values(const GrpParams& p, const GrpItem& it, uint32_t taddr, int nw,
+                                                 int half, int lane, uint8_t* stg, uint32_t acc, uint64_t* tpart) {
+    auto part = [&] {
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_leader(tpart);
+    };
+    const int rows = it.m1 - it.m0 - 32 * half;             // from this warp's first on
+    const int chunks = nw < p.N && rows > 0 ? (rows - 1) / (32 * Cfg::HALVES) + 1 : 0;
+    if (chunks == 0) {                                      // warp-uniform
+        if (it.kb) part();
+        return;
+    }
+    const float floor = p.relu ? 0.f : -__builtin_huge_valf();
+    auto pack = [&](uint32_t va, uint32_t vb) -> uint32_t {
+        // a NaN (of a scale) stays one
+        const float a = max_nan(__uint_as_float(va), floor), b = max_nan(__uint_as_float(vb), floor);
+        if constexpr (Cfg::OUT == OutT::BF16) {
+            __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+            return *reinterpret_cast<uint32_t*>(&h);
+        } else {
+            __half2 h = __floats2half2_rn(a, b);
+            return *reinterpret_cast<uint32_t*>(&h);
+        }
+    };
+    const uint32_t stg_a = smem_u32(stg);
+    const int mj = lane >> 3, mc = lane & 7;                // as above
+    const int rr = lane >> 2, ch = lane & 3;
+    const int left = p.N - (nw + ch * 8);
+    uint16_t* dst0 = static_cast<uint16_t*>(p.C) + nw + ch * 8;
+    const bool down = acc == 0;
+    uint32_t v0[16], v1[16];
+#pragma unroll 1
+    for (int i = 0; i < chunks; ++i) {
+        const int m = it.m0 + 32 * (half + Cfg::HALVES * (down ? chunks - 1 - i : i));
+        if (it.kb) {
+            tmem_ld_16x256b_x4(taddr + (m - it.m0), v0);
+            tmem_ld_16x256b_x4(taddr + (16u << 16) + (m - it.m0), v1);
+            tmem_ld_wait_for(v0, v1);
+            if (i == 0) part();
+        } else {
+#pragma unroll
+            for (int j = 0; j < 16; ++j) v0[j] = v1[j] = 0;
+        }
+        __syncwarp();                                       // the last chunk's rows are read
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            stmatrix_x4_trans(stg_a + (8 * j + mc) * 64 + ((mj ^ ((mc >> 1) & 3)) << 4), pack(v0[4 * j], v0[4 * j + 1]),
+                              pack(v0[4 * j + 2], v0[4 * j + 3]), pack(v1[4 * j], v1[4 * j + 1]),
+                              pack(v1[4 * j + 2], v1[4 * j + 3]));
+        __syncwarp();
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const int r = 8 * j + rr;
+            const uint4 x = *reinterpret_cast<const uint4*>(stg + r * 64 + ((ch ^ ((r >> 1) & 3)) << 4));
+            if (m + r < it.m1) {
+                uint16_t* dst = dst0 + static_cast<long long>(m + r) * p.ldc;
+                if (left >= 8) {
+                    *reinterpret_cast<uint4*>(dst) = x;
+                } else {
+                    const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+                    for (int k = 0; k < 7; ++k)
+                        if (k < left) dst[k] = static_cast<uint16_t>(w[k >> 1] >> (16 * (k & 1)));
+                }
+            }
+        }
+    }
 }
 
 // Epilogue of a weight-gradient tile: this warp's 32 rows k from kr of C_e,
@@ -730,7 +784,8 @@ grp_gemm_kernel(const __grid_constant__ CUtensorMap tmA,
             const uint32_t taddr = tmem_base + grp_acc_col<Cfg>(acc, it.width) + (static_cast<uint32_t>(q * 32) << 16);
             const int l0 = it.n0 + static_cast<int>(rank) * 128 + q * 32;
             if constexpr (Cfg::WG) grp_store_grad<Cfg>(&tmC, p, it, taddr, l0, half, lane, stg, nstore);
-            else grp_store_rows<Cfg>(p, it, taddr, l0, half, lane, stg, acc, &tpart[acc]);
+            else if constexpr (Cfg::MX) grp_store_values<Cfg>(p, it, taddr, l0, half, lane, stg, acc, &tpart[acc]);
+            else grp_store_rows<Cfg>(p, it, taddr, l0, half, lane, stg);
             if (it.kb) {
                 tc_fence_before();
                 __syncwarp();
