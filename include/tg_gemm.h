@@ -413,6 +413,8 @@ TG_API tg_status tg_expert_combine_grad(int64_t tokens, int topk, int64_t H, int
  * tg_expert_quant_mxfp4 -- tg_expert_gather of quantised rows: row pos[i] of Q and
  *   scales is X[i / topk] quantised; the rows of dropped choices are zero.  Each
  *   token is read and quantised once.  pos and kept as in tg_expert_gather.
+ * Outputs of these must not overlap their inputs.  Rows of codes on 128-byte
+ * lines are read fastest by the products.
  *
  * tg_gemm_mxfp4 -- C[m][n] = epi( sum_k A[m][k] * W[n][k] ), both operands in the
  *   format: A has M rows, the weights W have N (they are stored N x K).  Products with
@@ -451,7 +453,7 @@ TG_API tg_status tg_gemm_grouped_mxfp4(int64_t M, int64_t N, int64_t K, int E,
  * tg_expert_route -- for each row x of logits (tokens x E of `type`, TG_TYPE_F16,
  *   TG_TYPE_BF16 or TG_TYPE_F32, aligned to its elements, any row pitch ldl >= E):
  *     score   p = softmax(x) (TG_SCORE_SOFTMAX) or sigmoid(x) (TG_SCORE_SIGMOID)
- *     choice  the topk experts of largest x, or with a bias (E floats, not NULL) of
+ *     choice  the topk experts of largest x, or with a bias (E finite floats, not NULL) of
  *             largest p + bias, in falling order, ties to the lower number.  With
  *             groups > 1 (each E / groups consecutive experts) only from the
  *             keep_groups groups of largest sum of their two largest p (+ bias), ties

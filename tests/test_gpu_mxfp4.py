@@ -286,3 +286,16 @@ def test_grouped_equals_dense_rows():
     C = tg.gemm_grouped_mxfp4(a, sa, offsets_of([300]), w, sw)
     assert torch.equal(C, tg.gemm_mxfp4(a, sa, w[0], sw[0]))
     assert torch.equal(C, tg.gemm_grouped_mxfp4(a, sa, offsets_of([300]), w, sw))
+
+
+@pytest.mark.parametrize("M", [3, 200])
+def test_scales_at_the_ends_of_their_range(M):
+    """Scales of 2^-127 to 2^127 whose product is moderate are exact together."""
+    N, K = 140, 64
+    a = bytes_like(torch.full((M, K // 2), 0x22, dtype=torch.uint8).cuda())             # ones
+    w = bytes_like(torch.full((N, K // 2), 0x22, dtype=torch.uint8).cuda())
+    for ea, ew in ((0, 254), (254, 0), (1, 250), (3, 240), (127, 127), (0, 200), (200, 0), (64, 190)):
+        sa = bytes_like(torch.full((M, 2), ea, dtype=torch.uint8).cuda())
+        sw = bytes_like(torch.full((N, 2), ew, dtype=torch.uint8).cuda())
+        C = tg.gemm_mxfp4(a, sa, w, sw)
+        assert bool((C.double() == 64.0 * 2.0 ** (ea + ew - 254)).all()), (ea, ew, C[0, 0].item())

@@ -1,6 +1,6 @@
 // gemm_group.cuh -- products over groups of rows on CTA pairs: the experts'
-// products of a mixture-of-experts layer (16-bit and 8-bit), their weight
-// gradient, and, as one group of all rows, the dense 8-bit product.
+// products of a mixture-of-experts layer (16-bit, 8-bit and microscaled 4-bit), their
+// weight gradient, and, as one group of all rows, the dense 8-bit and 4-bit products.
 //
 // The rows of A (R x K) are sorted into groups: group e is the rows
 // [offsets[e], offsets[e + 1]), known on the device only.
@@ -9,7 +9,9 @@
 //   weight gradient (WG = 1):  C_e[k][n]  = sum_{r in group e} A[r][k] * G[r][n]
 //
 // 4-bit operands (E2M1 in blocks of 32 k with E8M0 scales): the tensor cores
-// multiply by the scales (kind::mxf4), sums are fp32.
+// multiply by the scales (kind::mxf4), which they read from tensor memory; sums
+// are fp32.  Three more warps of each CTA bring the scales of its weight columns
+// and of all the tile's rows (block_scales.cuh).
 //
 // 8-bit operands: the sum is an exact 32-bit integer, and
 // C[r][n] = epi( (sum * row_scale[r]) * col_scale_e[n] ), in fp32, rounded once.
@@ -53,7 +55,13 @@
 // clocks; its weight gradient 354, 374 with groups of 1000 rows; 8-bit 4096 x
 // 8192 x 8192 141 to 159 us, 3450 to 3900 TOP/s), the weight stream where they are
 // small (64 groups of one row, 1024 x 2048: 47 us, 5.7 TB/s), and in long runs the
-// power limit, at 1.1 to 1.7 GHz.
+// power limit, at 1.1 to 1.7 GHz.  4-bit: a block of 256 k takes 512 clocks of MMAs
+// and 600 in all, with five stages (six do not fit beside the scales) and shared memory
+// that MMAs, copies and scales contend for; about 900 more a tile pass between
+// its last MMA and the next one's first where their accumulators share columns.
+// 8192 x 8192 x 8192 202 us (5450 TFLOP/s), 64 groups of 256 rows, 4096 x 4096, 138
+// (5.4 TB/s), of 64 rows 112 (5.3 TB/s).  With few blocks (1024 k) the epilogue
+// bounds it: 8192 x 8192 x 1024 55 us.
 #pragma once
 #include "gemm_tc.cuh"
 #include "block_scales.cuh"
@@ -261,8 +269,9 @@ __device__ __forceinline__ void grp_store_rows(const GrpParams& p, const GrpItem
 }
 
 // The same for a 4-bit product.  (Loading the next 32 rows before these are
-// written costs time: 8192 x 8192 x 1024 68 us, so 55.)  Columns that two accumulators may share come first, the last ones of the first
-// accumulator, the first of the second; tpart hears when they have been read.
+// written costs time: 8192 x 8192 x 1024 68 us, so 55.)  Columns that two
+// accumulators may share come first, the last ones of the first accumulator, the
+// first of the second; tpart hears when they have been read.
 template <class Cfg>
 __device__ __forceinline__ void grp_store_values(const GrpParams& p, const GrpItem& it, uint32_t taddr, int nw,
                                                  int half, int lane, uint8_t* stg, uint32_t acc, uint64_t* tpart) {

@@ -416,11 +416,17 @@ skinny_kernel(const __grid_constant__ CUtensorMap tmW,
                 armed_par = (armed_par & ~(1u << s)) | (ph << s);
             }
             if (!ok) {
+                // (4-bit blocks: `full` also waits for the warp that orders the scales,
+                // which may have given up; the other copies of the slot get a fixed 1 ms)
                 for (int s = 0; s < Cfg::RAW_STAGES; ++s)
                     if (armed & (1u << s)) {
                         volatile int never = 0;
-                        bounded_wait(&full[s], (armed_par >> s) & 1, &never, limit, p.status);
+                        bounded_wait(Cfg::MX ? &sraw[s] : &full[s], (armed_par >> s) & 1, &never, limit, p.status);
                     }
+                if constexpr (Cfg::MX) {
+                    const uint64_t t0 = globaltimer_ns();
+                    while (globaltimer_ns() - t0 < 1000000ull) __nanosleep(10000);
+                }
                 for (int s = 0; s < Cfg::X_STAGES; ++s)
                     if (xarmed & (1u << s)) {
                         volatile int never = 0;
@@ -683,7 +689,7 @@ skinny_kernel(const __grid_constant__ CUtensorMap tmW,
                 }
                 continue;
             }
-            if constexpr (Cfg::BYTES) break;                     // whole groups or cluster splits only
+            if constexpr (Cfg::BYTES) break;                  // whole groups or cluster splits only
             // Publish the partial, take a ticket; the tile's last contributor
             // reduces.  The epilogue warps meet on mbarriers with bounded waits
             // (never an unbounded bar.sync, which a warp that gave up would hang).

@@ -230,7 +230,7 @@ route_kernel(const RouteParams p, const bool vec) {
     constexpr uint32_t kLow = V - 1;                          // a key's bits that number the lane's experts
     constexpr uint32_t kNone = 0x007fffffu, kOver = 0xff800000u;    // the infinities, ordered
     const int lane = threadIdx.x & 31;
-    const int t = blockIdx.x * 8 + (threadIdx.x >> 5);
+    const long long t = blockIdx.x * 8ll + (threadIdx.x >> 5);
     if (t >= p.tokens) return;
     const T* row = static_cast<const T*>(p.logits) + t * p.ldl;
     const int group = lane >> p.shift, part = lane & (p.lanes - 1);
@@ -379,7 +379,7 @@ route_kernel(const RouteParams p, const bool vec) {
     }
     w = bad_row ? __uint_as_float(0x7fc00000u) : has ? w * p.scale : 0.f;
     if (lane < p.topk) {
-        const long long at = static_cast<long long>(t) * p.topk + lane;
+        const long long at = t * p.topk + lane;
         p.ids[at] = mine;
         p.weights[at] = w;
     }

@@ -196,6 +196,7 @@ TG_HD int mx4_stage_clocks(int width) { return sched_max(2 * width + 70, sched_m
 inline int mx4_even_tiles(long long rows, long long ntl, int npairs) {
     const long long least = (rows - 1) / 256 + 1, units = (rows - 1) / 32 + 1;
     long long best = least, cost = -1;
+    if (least * ntl >= 16ll * npairs) return static_cast<int>(least);     // one wave of many
     for (long long nt = least; nt <= least + least / 3 + 1 && nt <= units; ++nt) {
         const int width = static_cast<int>(32 * ((units - 1) / nt + 1));
         const long long tiles = nt * ntl, rest = tiles % npairs;
