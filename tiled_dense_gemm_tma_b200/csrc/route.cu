@@ -427,7 +427,11 @@ route_grad_kernel(const RouteParams p) {
         for (int i = lane; i < p.E; i += 32) out[i] = from_float<T>(-total * (expf(to_float(row[i]) - base) * inv));
         d = prob * (g - total);
     } else {
-        for (int i = lane; i < p.E; i += 32) out[i] = from_float<T>(0.f);
+        constexpr int N = 16 / sizeof(T);
+        if (p.E % N == 0 && reinterpret_cast<uintptr_t>(out) % 16 == 0)
+            for (int i = lane * N; i < p.E; i += 32 * N) *reinterpret_cast<uint4*>(out + i) = make_uint4(0, 0, 0, 0);
+        else
+            for (int i = lane; i < p.E; i += 32) out[i] = from_float<T>(0.f);
         const float rest = p.sigmoid ? 1.f / (1.f + expf(x)) : 1.f;          // 1 - sigmoid
         if (p.renorm) {
             const float l = !has ? -kInf : p.sigmoid ? fminf(x, 0.f) - log1pf(expf(-fabsf(x))) : x;
