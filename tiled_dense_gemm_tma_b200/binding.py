@@ -1,4 +1,5 @@
-"""ctypes binding of the C ABI declared in include/tg_gemm.h.
+"""Binding of the C ABI declared in include/tg_gemm.h, through ctypes and, for
+what a layer calls several times a step, through csrc/calls.c.
 
 Argument marshalling only: every step of the GEMM runs in the CUDA kernels
 of ``libtg_gemm.so``.  Torch is used for device memory and streams.  If the
@@ -455,6 +456,17 @@ def _type16(dtype, name):
 _fns = {}
 
 
+def _calls():
+    """The module that calls the entry points of the sections below: a call
+    through ctypes converts its 10 to 20 arguments in 1.5 us, this one in 0.2."""
+    load_library()
+    try:
+        from . import _tg_calls
+    except ImportError as e:
+        raise ImportError(f"_tg_calls is not built ({e}); run tiled_dense_gemm_tma_b200/build.py") from e
+    return _tg_calls
+
+
 def _launch(name, device, stream, *args):
     """Call the entry point on `device` (made current where it is not) and on
     `stream`, by default that device's current stream; raise on an error.  The
@@ -464,7 +476,7 @@ def _launch(name, device, stream, *args):
     if fn is None:
         import torch
         _fns["stream"], _fns["device"] = torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice
-        fn = _fns[name] = getattr(load_library(), name)
+        fn = _fns[name] = getattr(_calls(), name)
     index = device.index
     if stream is None:
         stream = _fns["stream"](index)

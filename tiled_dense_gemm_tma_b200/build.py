@@ -1,4 +1,5 @@
-"""Build libtg_gemm.so in-tree from csrc/*.cu for sm_100a.
+"""Build libtg_gemm.so in-tree from csrc/*.cu for sm_100a, and beside it the
+Python module _tg_calls from csrc/calls.c, which calls it.
 
     python tiled_dense_gemm_tma_b200/build.py [--force] [--verbose]
 
@@ -13,10 +14,12 @@ import glob
 import os
 import subprocess
 import sys
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 OUT = os.path.join(HERE, "libtg_gemm.so")
+CALLS = os.path.join(HERE, "_tg_calls.so")
 BUILD = os.path.join(HERE, "_build")
 INCLUDE = os.path.join(os.path.dirname(HERE), "include")
 NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")
@@ -54,11 +57,29 @@ def _compile(src, verbose):
     return obj
 
 
+def _build_calls(force):
+    """The module finds the library beside itself, wherever both are moved."""
+    src = os.path.join(CSRC, "calls.c")
+    if not force and not _stale(CALLS, [src, os.path.join(INCLUDE, "tg_gemm.h")]):
+        return
+    tmp = CALLS + f".tmp{os.getpid()}"
+    subprocess.run(["gcc", "-O2", "-std=c11", "-shared", "-fPIC", "-fvisibility=hidden", "-I", INCLUDE, "-I",
+                    sysconfig.get_path("include"), src, "-o", tmp, "-L", HERE, "-l:libtg_gemm.so",
+                    "-Wl,-rpath,$ORIGIN"], check=True)
+    os.replace(tmp, CALLS)
+
+
 def build(force: bool = False, verbose: bool = False) -> str:
+    _build_library(force, verbose)
+    _build_calls(force)
+    return OUT
+
+
+def _build_library(force, verbose):
     os.makedirs(BUILD, exist_ok=True)
     srcs = _sources()
     if not force and not _stale(OUT, srcs + _deps()):
-        return OUT
+        return
     if force:
         for o in glob.glob(os.path.join(BUILD, "*.o")):
             os.remove(o)
@@ -68,7 +89,6 @@ def build(force: bool = False, verbose: bool = False) -> str:
     cmd = [NVCC] + ARCH + ["-shared", "-cudart", "static", "-o", tmp] + objs
     subprocess.run(cmd, check=True)
     os.replace(tmp, OUT)
-    return OUT
 
 
 if __name__ == "__main__":
