@@ -319,3 +319,49 @@ def test_second_device_is_named():
         tg.quant_mxfp4(normal((4, 64), torch.bfloat16, 1), Q=q.cpu())
     with pytest.raises(ValueError):
         tg.expert_route(torch.zeros(4, 8, device="cuda"), 2, bias=torch.zeros(8))
+
+
+def test_nothing_to_do():
+    """No rows, no columns, no tokens: results of the right shapes, no launch
+    that would fail."""
+    bf = torch.bfloat16
+    for M, K in ((0, 64), (5, 0), (0, 0)):
+        q, s = tg.quant_mxfp4(torch.zeros(M, K, dtype=bf, device="cuda"))
+        assert q.shape == (M, K // 2) and s.shape == (M, K // 32)
+        assert tg.dequant_mxfp4(q, s).shape == (M, K)
+    ids, w = tg.expert_route(torch.zeros(0, 8, device="cuda"), 2)
+    plan = tg.expert_sort(ids, 8)
+    q, s = tg.quant_mxfp4(torch.zeros(0, 64, dtype=bf, device="cuda"), plan)
+    W, S = random_blocks((8, 40, 64), 1)
+    y = tg.gemm_grouped_mxfp4(q, s, plan, W, S)
+    assert y.shape == (0, 40) and tg.expert_combine(y, plan, w).shape == (0, 40)
+    # no k: zeros, groups or not
+    none, nos = torch.zeros(6, 0, dtype=torch.uint8, device="cuda"), torch.zeros(6, 0, dtype=torch.uint8, device="cuda")
+    W0 = torch.zeros(2, 40, 0, dtype=torch.uint8, device="cuda")
+    C = tg.gemm_grouped_mxfp4(none, nos, offsets_of([2, 4]), W0, W0)
+    assert C.shape == (6, 40) and not C.any()
+    # every choice dropped
+    plan = tg.expert_sort(torch.full((5, 2), -1, dtype=torch.int32, device="cuda"), 8)
+    q, s = tg.quant_mxfp4(normal((5, 64), bf, 1), plan)
+    assert not q.any() and not s.any()
+    assert not tg.gemm_grouped_mxfp4(q, s, plan, W, S).any()
+    assert tg.last_device_status() == 0
+
+
+def test_refusals_of_the_library():
+    """Limits and alignment that only the entry points check."""
+    q, s = random_blocks((4, 64), 1)
+    odd = torch.zeros(4 * 40 + 8, dtype=torch.uint8, device="cuda")
+    for call, code in [
+            (lambda: tg.expert_route(torch.zeros(4, 64, device="cuda"), 33), 3),
+            (lambda: tg.expert_route(torch.zeros(4, 1025, device="cuda"), 2), 3),
+            (lambda: tg.expert_route(torch.zeros(4, 64, device="cuda"), 65), 1),
+            (lambda: tg.expert_route(torch.zeros(4, 64, device="cuda"), 9, groups=8, topk_groups=1), 1),
+            (lambda: tg.expert_route(torch.zeros(4, 64, device="cuda"), 2, groups=5), 1),
+            (lambda: tg.gemm_mxfp4(odd[8:].view(4, 40)[:, :32], s, q, s), 2),
+            (lambda: tg.gemm_mxfp4(odd[:160].view(4, 40)[:, :32], s, q, s), 2),
+            (lambda: tg.dequant_mxfp4(q, s, C=torch.zeros(4, 68, dtype=torch.bfloat16, device="cuda")[:, :64]), 2),
+            (lambda: tg.quant_mxfp4(normal((4, 64), torch.bfloat16, 1), Q=odd[:160].view(4, 40)[:, :32]), 2)]:
+        with pytest.raises(tg.TgError) as e:
+            call()
+        assert e.value.code == code

@@ -303,23 +303,40 @@ route_kernel(const RouteParams p, const bool vec) {
             if (!(b <= kInf)) b = kInf;
         }
         group_top2(a, b, p.lanes);
+        // the highest groups one by one, a group's number (falling, so that ties go to
+        // the lowest) in its key's lowest bits
         const float score = group < p.groups ? group_score(a, b) : -kInf;
-        const int rank = group_rank(score, group, p);
-        in = rank < p.keep;
-        // the first of the dropped groups, the last of the kept ones
-        const bool head = group < p.groups && part == 0;
-        const unsigned out_at = __ballot_sync(kAll, head && rank == p.keep);
-        const unsigned in_at = __ballot_sync(kAll, head && rank == p.keep - 1);
-        if (out_at && in_at) {
-            const int hi_at = __ffs(in_at) - 1, lo_at = __ffs(out_at) - 1;
-            const float size = fabsf(a) + (b > -kInf ? fabsf(b) : 0.f);      // terms may cancel in the sum
-            const float hi = __shfl_sync(kAll, score, hi_at), lo = __shfl_sync(kAll, score, lo_at);
-            const float larger = fmaxf(__shfl_sync(kAll, size, hi_at), __shfl_sync(kAll, size, lo_at));
-            close = lo > -kInf && hi - lo <= 2.f * route_slack(p.sigmoid, inv, larger, V);
+        uint32_t gkey = score > -kInf ? (ordered(score) & ~31u) | (31 - group) : 0u, last = 0;
+        in = false;
+        for (int g = 0; g < p.keep; ++g) {
+            last = __reduce_max_sync(kAll, gkey);
+            if (last == 0) break;
+            if (gkey == last) {
+                in = true;
+                gkey = 0;
+            }
+        }
+        const uint32_t next = __reduce_max_sync(kAll, gkey);  // the first of the dropped ones
+        if (next) {
+            const float size = score > -kInf ? fabsf(a) + (b > -kInf ? fabsf(b) : 0.f) : 0.f;   // terms may cancel in the sum
+            const float larger = __uint_as_float(__reduce_max_sync(kAll, __float_as_uint(size)));
+            close = value_of(last & ~31u) - value_of(next & ~31u) <=
+                    2.f * route_slack(p.sigmoid, inv, larger, V) + 0x1p-18f * larger;
         }
     }
     // the topk largest.  Lanes are compared without the bits that number their
     // experts: of equal values the lowest lane's is the lowest expert.
+    // A lane's keys behind its first wait in shared memory (up to 16; more are
+    // moved up in registers): one load a choice and not V moves.
+    constexpr bool kListed = V > 1 && V <= 16;
+    __shared__ uint32_t lists[kListed ? 8 * V * 32 : 1];
+    const int base = kListed ? (threadIdx.x >> 5) * V * 32 + lane : 0;
+    if constexpr (kListed) {
+#pragma unroll
+        for (int i = 1; i < V; ++i) lists[base + 32 * (i - 1)] = key[i];
+        lists[base + 32 * (V - 1)] = 0;
+    }
+    int at = base;
     uint32_t best = in && key[0] ? key[0] | kLow : 0u;
     int mine = -1;                                            // lane j: the j-th choice
     uint32_t mkey = 0;
@@ -330,9 +347,14 @@ route_kernel(const RouteParams p, const bool vec) {
         const int e = __shfl_sync(kAll, first + static_cast<int>(kLow - (key[0] & kLow)), win);
         if (lane == j) { mine = e; mkey = m; }
         if (lane == win) {
+            if constexpr (kListed) {
+                key[0] = lists[at];
+                at += 32;
+            } else {
 #pragma unroll
-            for (int i = 0; i + 1 < V; ++i) key[i] = key[i + 1];
-            key[V - 1] = 0;
+                for (int i = 0; i + 1 < V; ++i) key[i] = key[i + 1];
+                key[V - 1] = 0;
+            }
             best = key[0] ? key[0] | kLow : 0u;
         }
     }
