@@ -136,9 +136,10 @@ struct GrpCfg {
     // 8192 220 us.)
     static constexpr int TMEM_COLS = 512;
     static constexpr int ACC_END = MX ? TMEM_COLS - 2 * SF_COLS : TMEM_COLS;
-    static constexpr int TABLE = WG_ ? 0 : ((MX ? 3 : 4) * (kMaxGroups + 2)) * 4;
+    static constexpr int TABLE = WG_ ? 0 : ((MX ? 3 : 4) * (kMaxGroups + 2) * 4 + 15) / 16 * 16;
+    static constexpr int ITEMS = MX ? 64 : 0;           // a pair's first items, ready in shared memory
     static constexpr int SMEM_DATA = STAGES * (A_STAGE + B_STAGE) + EPI_WARPS * NBUF * STG_BUF + SF_WARPS * SF_SLOT;
-    static constexpr int SMEM_BYTES = SMEM_DATA + 512 + TABLE + 1024;
+    static constexpr int SMEM_BYTES = SMEM_DATA + 512 + TABLE + ITEMS * 16 + 1024;
     static_assert(SMEM_BYTES <= 227 * 1024, "shared memory per CTA");
     static_assert(!(EB == 1 && WG_), "the 8-bit and 4-bit products have no gradient");
     static_assert(!(MX && W_MN_), "4-bit operands are K-major");
@@ -174,6 +175,12 @@ struct GrpItem {
     int width;                // MMA N
     int kb;                   // k blocks; 0: the tile is zero
     int r0, rows;             // WG: the group's rows
+};
+
+// Where a role stands in its pair's items.
+struct GrpWalk {
+    int i = 0;                // 4-bit: next entry of the table
+    int g = 0;                // group
 };
 
 // Epilogue of a product tile: this warp's 32 weight columns from nw, its share
@@ -303,6 +310,7 @@ __device__ __forceinline__ void grp_store_values(const GrpParams& p, const GrpIt
     const int rr = lane >> 2, ch = lane & 3;
     const int left = p.N - (nw + ch * 8);
     uint16_t* dst0 = static_cast<uint16_t*>(p.C) + nw + ch * 8;
+    const bool whole = nw + 32 <= p.N;
     const bool down = acc == 0;
     uint32_t v0[16], v1[16];
 #pragma unroll 1
@@ -324,6 +332,14 @@ __device__ __forceinline__ void grp_store_values(const GrpParams& p, const GrpIt
                               pack(v0[4 * j + 2], v0[4 * j + 3]), pack(v1[4 * j], v1[4 * j + 1]),
                               pack(v1[4 * j + 2], v1[4 * j + 3]));
         __syncwarp();
+        if (whole && m + 32 <= it.m1) {                     // as below, without a branch to each row
+            uint16_t* dst = dst0 + static_cast<long long>(m + rr) * p.ldc;
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                *reinterpret_cast<uint4*>(dst + j * 8 * p.ldc) =
+                    *reinterpret_cast<const uint4*>(stg + (8 * j + rr) * 64 + ((ch ^ ((rr >> 1) & 3)) << 4));
+            continue;
+        }
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
             const int r = 8 * j + rr;
@@ -424,6 +440,7 @@ grp_gemm_kernel(const __grid_constant__ CUtensorMap tmA,
     int* gexp = gstart + kMaxGroups + 2;        // product: which group that is
     int* grow = gexp + kMaxGroups + 2;          // product: its first row
     int* gend = grow + kMaxGroups + 2;          // product: the row after its last
+    int4* gitem = reinterpret_cast<int4*>(reinterpret_cast<uint8_t*>(full) + 512 + Cfg::TABLE);
 
     const int warp = threadIdx.x >> 5;
     const int lane = threadIdx.x & 31;
@@ -569,6 +586,42 @@ grp_gemm_kernel(const __grid_constant__ CUtensorMap tmA,
         }
         return it;
     };
+    // The next item.  Six divisions take 900 clocks: of 4-bit products, whose tiles can be
+    // as short as that, a thread works out each of the pair's first ITEMS, before the roles
+    // part (8192 x 8192 x 1024 5X -> 5X us).
+    if constexpr (Cfg::ITEMS > 0) {
+        const long long w = pair + static_cast<long long>(threadIdx.x) * npairs;
+        if (threadIdx.x < Cfg::ITEMS && w < num_items) {
+            const int i = static_cast<int>(w), t = i < dp ? i : dp + (i - dp) / pieces;
+            int g = 0, after = *gcount;                     // gstart[g] <= t < gstart[after]
+            while (after - g > 1) {
+                const int mid = (g + after) >> 1;
+                if (gstart[mid] <= t) g = mid;
+                else after = mid;
+            }
+            const GrpItem it = item(i, g);
+            gitem[threadIdx.x] = make_int4(it.m0, it.n0, it.width | max(it.m1 - it.m0, 0) << 16,
+                                           it.kb ? it.e : it.e | 1 << 16);
+        }
+        __syncthreads();
+    }
+    auto next = [&](int w, GrpWalk& at) -> GrpItem {
+        if constexpr (Cfg::ITEMS > 0) {
+            if (at.i < Cfg::ITEMS) {
+                const int4 v = gitem[at.i++];
+                GrpItem it;
+                it.m0 = v.x;
+                it.n0 = v.y;
+                it.width = v.z & 0xffff;
+                it.m1 = v.x + (v.z >> 16);
+                it.e = v.w & 0xffff;
+                it.kb = v.w >> 16 ? 0 : (p.K - 1) / Cfg::BK + 1;
+                it.r0 = it.rows = 0;                        // WG's
+                return it;
+            }
+        }
+        return item(w, at.g);
+    };
     // WG: rows of the group in its last block, and whether they end inside an
     // MMA step
     auto last_rows = [&](const GrpItem& it) { return it.rows - (it.kb - 1) * Cfg::BK; };
@@ -586,9 +639,9 @@ grp_gemm_kernel(const __grid_constant__ CUtensorMap tmA,
         if (elect_one()) {
             uint32_t armed = 0, armed_par = 0, ld = 0;
             bool ok = true;
-            int g = 0;
+            GrpWalk at;
             for (int w = pair; w < num_items && ok; w += npairs) {
-                const GrpItem it = item(w, g);
+                const GrpItem it = next(w, at);
                 const int n0 = it.n0 + static_cast<int>(rank) * 128;     // this CTA's lanes
                 const int left = lanes_total - n0;
                 const int hn = it.width >> 1;
@@ -666,21 +719,25 @@ grp_gemm_kernel(const __grid_constant__ CUtensorMap tmA,
     } else if (warp == 1) {
         // ------------------------------------------ MMA issuer (leader only)
         if (rank == 0 && elect_one()) {
-            constexpr int A_MN = Cfg::WG || Cfg::W_MN;
-            constexpr uint32_t idesc0 = Cfg::I8 ? make_idesc_i8(256, 0, A_MN, 0)
-                                      : Cfg::MX ? make_idesc_mx4(256, 0)
-                                                : make_idesc(Cfg::TYPE, 256, 0, A_MN, Cfg::WG);
-            uint32_t ld = 0, tl = 0, chunk = 0;
-            int last_width = 0;
-            bool ok = true;
-            int g = 0;
-            for (int w = pair; w < num_items && ok; w += npairs) {
-                const GrpItem it = item(w, g);
-                if (it.kb == 0) continue;
-                const uint32_t acc = tl & 1;
-                const uint32_t aph = (tl >> 1) & 1;
-                if (!bounded_wait(&tempty[acc], aph ^ 1, abort_flag, limit, p.status)) { ok = false; break; }
-                if constexpr (Cfg::MX) {
+            if constexpr (Cfg::MX) {
+                // A stage's MMAs take 512 clocks, and this thread not much less to issue
+                // them: positions in the rings are counted, descriptors added to
+                // (8192 x 8192 x 8192 20X us, with a division and descriptors from the start
+                // 200).
+                uint32_t tl = 0;
+                uint32_t s = 0, ph = 0;                              // this stage's slot and parity
+                uint32_t old = Cfg::STAGES - 2, old_ph = 1;          // of the stage before the last
+                uint32_t slot = 0, slot_ph = 0, set = 0;             // of the chunk; columns of its scales
+                const uint64_t a0 = sw128_desc(smem_u32(smA), 16, 1024), b0 = sw128_desc(smem_u32(smB), 16, 1024);
+                const uint64_t sf0 = scale_desc(smem_u32(smSf));
+                int last_width = 0;
+                bool ok = true;
+                GrpWalk at;
+                for (int w = pair; w < num_items && ok; w += npairs) {
+                    const GrpItem it = next(w, at);
+                    if (it.kb == 0) continue;
+                    const uint32_t acc = tl & 1;
+                    if (!bounded_wait(&tempty[acc], ((tl >> 1) & 1) ^ 1, abort_flag, limit, p.status)) { ok = false; break; }
                     // (tl - 1) / 2: the last tile's use of the other accumulator
                     if (last_width + it.width > Cfg::ACC_END &&
                         !bounded_wait(&tpart[acc ^ 1], ((tl - 1) >> 1) & 1, abort_flag, limit, p.status)) {
@@ -688,84 +745,97 @@ grp_gemm_kernel(const __grid_constant__ CUtensorMap tmA,
                         break;
                     }
                     last_width = it.width;
-                }
-                ++tl;
-                tc_fence_after();
-                const uint32_t d_tmem = tmem_base + grp_acc_col<Cfg>(acc, it.width);
-                const uint32_t idesc = idesc0 | (static_cast<uint32_t>(it.width >> 3) << 17);
-                for (int kb = 0; kb < it.kb; ++kb, ++ld) {
-                    const uint32_t s = ld % Cfg::STAGES;
-                    const uint32_t ph = (ld / Cfg::STAGES) & 1;
-                    if (!bounded_wait(&full[s], ph, abort_flag, limit, p.status)) { ok = false; break; }
-                    tc_fence_after();
-                    const uint32_t a_addr = smem_u32(smA + s * Cfg::A_STAGE);
-                    const uint32_t b_addr = smem_u32(smB + s * Cfg::B_STAGE);
-                    uint32_t sf = 0;                             // this stage's scales in tensor memory
-                    if constexpr (Cfg::MX) {
-                        const uint32_t slot = chunk % Cfg::SF_WARPS;
-                        if (!(kb & 3)) {
-                            if (!bounded_wait_cluster(&sfull[slot], (chunk / Cfg::SF_WARPS) & 1, abort_flag, limit, p.status)) {
-                                ok = false;
-                                break;
-                            }
-                            tc_fence_after();
+                    ++tl;
+                    const uint32_t d_tmem = tmem_base + grp_acc_col<Cfg>(acc, it.width);
+                    const uint32_t idesc = make_idesc_mx4(256, 0) | (static_cast<uint32_t>(it.width >> 3) << 17);
+                    for (int kb = 0; kb < it.kb; ++kb) {
+                        if (!(kb & 3) && !bounded_wait_cluster(&sfull[slot], slot_ph, abort_flag, limit, p.status)) {
+                            ok = false;
+                            break;
                         }
                         // two sets of columns in turn.  A copy runs before the MMAs issued
                         // after it, but its definition does not put it behind those issued
                         // before: the MMAs that read the set, of the stage before the last,
-                        // have to be done.  (8192 x 8192 x 8192 206 us, 189 without; sets of
+                        // have to be done.  (8192 x 8192 x 8192 20X us, 189 without; sets of
                         // half a stage, four of them, 226: MMAs wait for copies in between.)
-                        if (ld >= 2 && !bounded_wait(&empty[(ld - 2) % Cfg::STAGES], ((ld - 2) / Cfg::STAGES) & 1,
-                                                     abort_flag, limit, p.status)) {
-                            ok = false;
-                            break;
-                        }
+                        if (!bounded_wait(&empty[old], old_ph, abort_flag, limit, p.status)) { ok = false; break; }
                         tc_fence_after();
-                        sf = tmem_base + Cfg::ACC_END + (ld & 1) * Cfg::SF_COLS;
-                        const uint32_t src = smem_u32(smSf + slot * Cfg::SF_SLOT) + (kb & 3) * 1024;
+                        const uint32_t sf = tmem_base + Cfg::ACC_END + set;
+                        const uint64_t src = sf0 + ((slot * Cfg::SF_SLOT + (kb & 3) * 1024) >> 4);
 #pragma unroll
                         for (int j = 0; j < 2; ++j) {
-                            tmem_cp_scales_pair(sf + 4 * j, scale_desc(src + j * 512));
-                            tmem_cp_scales_pair(sf + 8 + 8 * j, scale_desc(src + Cfg::SF_TILE + j * 512));
+                            tmem_cp_scales_pair(sf + 4 * j, src + 32 * j);
+                            tmem_cp_scales_pair(sf + 8 + 8 * j, src + (Cfg::SF_TILE >> 4) + 32 * j);
                             if (it.width > 128)
-                                tmem_cp_scales_pair(sf + 12 + 8 * j, scale_desc(src + 2 * Cfg::SF_TILE + j * 512));
+                                tmem_cp_scales_pair(sf + 12 + 8 * j, src + (Cfg::SF_TILE >> 3) + 32 * j);
                         }
-                    }
-                    const int steps = Cfg::WG && kb == it.kb - 1
-                        ? (last_rows(it) + Cfg::MMA_K - 1) / Cfg::MMA_K : Cfg::STEPS;
+                        if (!bounded_wait(&full[s], ph, abort_flag, limit, p.status)) { ok = false; break; }
+                        tc_fence_after();
+                        const uint64_t ad = a0 + s * (Cfg::A_STAGE >> 4), bd = b0 + s * (Cfg::B_STAGE >> 4);
 #pragma unroll
-                    for (int k = 0; k < Cfg::STEPS; ++k) {
-                        if (Cfg::WG && k >= steps) break;
-                        // K-major: 32 bytes of k along the 128-byte rows; MN-major:
-                        // MMA_K rows of 128 bytes, 128-byte wide chunks LBO apart
-                        const uint64_t ad = A_MN
-                            ? sw128_desc(a_addr + k * Cfg::MMA_K * 128, Cfg::BK * 128, 1024)
-                            : sw128_desc(a_addr + k * 32, 16, 1024);
-                        const uint64_t bd = Cfg::WG
-                            ? sw128_desc(b_addr + k * Cfg::MMA_K * 128, Cfg::BK * 128, 1024)
-                            : sw128_desc(b_addr + k * 32, 16, 1024);
-                        if constexpr (Cfg::I8) mma_i8_pair(d_tmem, ad, bd, idesc, kb != 0 || k != 0);
-                        else if constexpr (Cfg::MX)
-                            mma_mx4_pair(d_tmem, ad, bd, idesc | mx4_scale_id(k & 1), kb != 0 || k != 0,
+                        for (int k = 0; k < Cfg::STEPS; ++k)         // 32 bytes of k along the 128-byte rows
+                            mma_mx4_pair(d_tmem, ad + 2 * k, bd + 2 * k, idesc | mx4_scale_id(k & 1), kb != 0 || k != 0,
                                          sf + 4 * (k >> 1), sf + 8 + 8 * (k >> 1));
-                        else mma_f16_pair(d_tmem, ad, bd, idesc, kb != 0 || k != 0);
-                    }
-                    const uint32_t e_loc = smem_u32(&empty[s]);
-                    mma_commit_pair(mapa_shared(e_loc, 0));      // both CTAs' slots
-                    mma_commit_pair(mapa_shared(e_loc, 1));
-                    if constexpr (Cfg::MX) {
+                        mma_commit_both(&empty[s]);                  // both CTAs' slots
                         if ((kb & 3) == 3 || kb == it.kb - 1) {
-                            const uint32_t s_loc = smem_u32(&sempty[chunk % Cfg::SF_WARPS]);
-                            mma_commit_pair(mapa_shared(s_loc, 0));
-                            mma_commit_pair(mapa_shared(s_loc, 1));
-                            ++chunk;
+                            mma_commit_both(&sempty[slot]);
+                            if (++slot == Cfg::SF_WARPS) slot = 0, slot_ph ^= 1;
                         }
+                        if (++s == Cfg::STAGES) s = 0, ph ^= 1;
+                        if (++old == Cfg::STAGES) old = 0, old_ph ^= 1;
+                        set = Cfg::SF_COLS - set;
                     }
+                    if (ok) mma_commit_both(&tfull[acc]);            // both CTAs' accumulators
                 }
-                if (!ok) break;
-                const uint32_t f_loc = smem_u32(&tfull[acc]);
-                mma_commit_pair(mapa_shared(f_loc, 0));          // both CTAs' accumulators
-                mma_commit_pair(mapa_shared(f_loc, 1));
+            } else {
+                constexpr int A_MN = Cfg::WG || Cfg::W_MN;
+                constexpr uint32_t idesc0 = Cfg::I8 ? make_idesc_i8(256, 0, A_MN, 0)
+                                          : make_idesc(Cfg::TYPE, 256, 0, A_MN, Cfg::WG);
+                uint32_t ld = 0, tl = 0;
+                bool ok = true;
+                GrpWalk at;
+                for (int w = pair; w < num_items && ok; w += npairs) {
+                    const GrpItem it = next(w, at);
+                    if (it.kb == 0) continue;
+                    const uint32_t acc = tl & 1;
+                    const uint32_t aph = (tl >> 1) & 1;
+                    if (!bounded_wait(&tempty[acc], aph ^ 1, abort_flag, limit, p.status)) { ok = false; break; }
+                    ++tl;
+                    tc_fence_after();
+                    const uint32_t d_tmem = tmem_base + grp_acc_col<Cfg>(acc, it.width);
+                    const uint32_t idesc = idesc0 | (static_cast<uint32_t>(it.width >> 3) << 17);
+                    for (int kb = 0; kb < it.kb; ++kb, ++ld) {
+                        const uint32_t s = ld % Cfg::STAGES;
+                        const uint32_t ph = (ld / Cfg::STAGES) & 1;
+                        if (!bounded_wait(&full[s], ph, abort_flag, limit, p.status)) { ok = false; break; }
+                        tc_fence_after();
+                        const uint32_t a_addr = smem_u32(smA + s * Cfg::A_STAGE);
+                        const uint32_t b_addr = smem_u32(smB + s * Cfg::B_STAGE);
+                        const int steps = Cfg::WG && kb == it.kb - 1
+                            ? (last_rows(it) + Cfg::MMA_K - 1) / Cfg::MMA_K : Cfg::STEPS;
+#pragma unroll
+                        for (int k = 0; k < Cfg::STEPS; ++k) {
+                            if (Cfg::WG && k >= steps) break;
+                            // K-major: 32 bytes of k along the 128-byte rows; MN-major:
+                            // MMA_K rows of 128 bytes, 128-byte wide chunks LBO apart
+                            const uint64_t ad = A_MN
+                                ? sw128_desc(a_addr + k * Cfg::MMA_K * 128, Cfg::BK * 128, 1024)
+                                : sw128_desc(a_addr + k * 32, 16, 1024);
+                            const uint64_t bd = Cfg::WG
+                                ? sw128_desc(b_addr + k * Cfg::MMA_K * 128, Cfg::BK * 128, 1024)
+                                : sw128_desc(b_addr + k * 32, 16, 1024);
+                            if constexpr (Cfg::I8) mma_i8_pair(d_tmem, ad, bd, idesc, kb != 0 || k != 0);
+                            else mma_f16_pair(d_tmem, ad, bd, idesc, kb != 0 || k != 0);
+                        }
+                        const uint32_t e_loc = smem_u32(&empty[s]);
+                        mma_commit_pair(mapa_shared(e_loc, 0));      // both CTAs' slots
+                        mma_commit_pair(mapa_shared(e_loc, 1));
+                    }
+                    if (!ok) break;
+                    const uint32_t f_loc = smem_u32(&tfull[acc]);
+                    mma_commit_pair(mapa_shared(f_loc, 0));          // both CTAs' accumulators
+                    mma_commit_pair(mapa_shared(f_loc, 1));
+                }
             }
             mma_commit_pair(mapa_shared(smem_u32(drain), 0));
             volatile int never = 0;
@@ -778,9 +848,9 @@ grp_gemm_kernel(const __grid_constant__ CUtensorMap tmA,
         const int half = (warp - 2) >> 2;
         uint8_t* stg = smStg + (warp - 2) * Cfg::NBUF * Cfg::STG_BUF;
         uint32_t tl = 0, nstore = 0;
-        int g = 0;
+        GrpWalk at;
         for (int w = pair; w < num_items; w += npairs) {
-            const GrpItem it = item(w, g);
+            const GrpItem it = next(w, at);
             const uint32_t acc = tl & 1;
             const uint32_t aph = (tl >> 1) & 1;
             if (it.kb) {
@@ -817,9 +887,9 @@ grp_gemm_kernel(const __grid_constant__ CUtensorMap tmA,
             const uint32_t slot = smem_u32(smSf + turn * Cfg::SF_SLOT);
             uint32_t chunk = 0, uses = 0;
             bool ok = true;
-            int g = 0;
+            GrpWalk at;
             for (int w = pair; w < num_items && ok; w += npairs) {
-                const GrpItem it = item(w, g);
+                const GrpItem it = next(w, at);
                 const int n0 = it.n0 + static_cast<int>(rank) * 128;
                 const uint8_t* cols = p.col_blocks + it.e * p.block_plane;
                 const int tiles = it.width > 128 ? 3 : 2;
@@ -844,9 +914,9 @@ grp_gemm_kernel(const __grid_constant__ CUtensorMap tmA,
         // ------------------------------------------ fix-up (WG, leader only)
         if constexpr (Cfg::WG) {
             uint32_t ld = 0, seen = 0;                  // seen: parity of each slot's cut barrier
-            int g = 0;
+            GrpWalk at;
             for (int w = pair; w < num_items && rank == 0; w += npairs) {
-                const GrpItem it = item(w, g);
+                const GrpItem it = next(w, at);
                 ld += it.kb;
                 if (!is_cut(it)) continue;
                 const uint32_t s = (ld - 1) % Cfg::STAGES;

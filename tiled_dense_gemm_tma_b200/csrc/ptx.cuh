@@ -681,4 +681,11 @@ __device__ __forceinline__ void mma_commit_pair(uint32_t bar_cl) {
         ::"r"(bar_cl) : "memory");
 }
 
+// On this barrier of either CTA.
+__device__ __forceinline__ void mma_commit_both(uint64_t* bar) {
+    asm volatile(
+        "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;"
+        ::"r"(smem_u32(bar)), "h"(static_cast<uint16_t>(3)) : "memory");
+}
+
 }  // namespace tg
