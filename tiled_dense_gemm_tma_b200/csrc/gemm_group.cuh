@@ -59,9 +59,10 @@
 // and 600 in all, with five stages (six do not fit beside the scales) and shared memory
 // that MMAs, copies and scales contend for; about 900 more a tile pass between
 // its last MMA and the next one's first where their accumulators share columns.
-// 8192 x 8192 x 8192 202 us (5450 TFLOP/s), 64 groups of 256 rows, 4096 x 4096, 138
-// (5.4 TB/s), of 64 rows 112 (5.3 TB/s).  With few blocks (1024 k) the epilogue
-// bounds it: 8192 x 8192 x 1024 55 us.
+// 8192 x 8192 x 8192 190 us (5780 TFLOP/s), 64 groups of 256 rows, 4096 x 4096, 133
+// (5.6 TB/s), of 64 rows 110 (5.6 TB/s).  With few blocks (1024 k) the epilogue
+// bounds it, some 150 clocks to read, 170 to pack and 300 to store 32 rows of a warp:
+// 8192 x 8192 x 1024 47 us.
 #pragma once
 #include "gemm_tc.cuh"
 #include "block_scales.cuh"
@@ -276,7 +277,7 @@ __device__ __forceinline__ void grp_store_rows(const GrpParams& p, const GrpItem
 }
 
 // The same for a 4-bit product.  (Loading the next 32 rows before these are
-// written costs time: 8192 x 8192 x 1024 68 us, so 55.)  Columns that two
+// written cost time: 8192 x 8192 x 1024 68 us where it took 55.)  Columns that two
 // accumulators may share come first, the last ones of the first accumulator, the
 // first of the second; tpart hears when they have been read.
 template <class Cfg>
@@ -757,8 +758,9 @@ grp_gemm_kernel(const __grid_constant__ CUtensorMap tmA,
                         // two sets of columns in turn.  A copy runs before the MMAs issued
                         // after it, but its definition does not put it behind those issued
                         // before: the MMAs that read the set, of the stage before the last,
-                        // have to be done.  (8192 x 8192 x 8192 202 us, 189 without; sets of
-                        // half a stage, four of them, 226: MMAs wait for copies in between.)
+                        // have to be done.  (The wait took 8192 x 8192 x 8192 from 189
+                        // to 202 us; sets of half a stage, four of them, 226: MMAs wait for
+                        // copies in between.)
                         if (!bounded_wait(&empty[old], old_ph, abort_flag, limit, p.status)) { ok = false; break; }
                         tc_fence_after();
                         const uint32_t sf = tmem_base + Cfg::ACC_END + set;
