@@ -310,6 +310,34 @@ def test_many_tiles_a_pair():
         at += n
 
 
+@pytest.mark.parametrize("M,most", [(1400, 1), (4000, 6)])
+def test_more_items_than_a_pair_lists(M, most):
+    """Items past those that a pair works out beforehand: groups of a few rows (some of
+    none, rows behind the last) on enough column tiles for more than 64 a pair."""
+    E, N, K = 1024, 1500, 96
+    counts = torch.randint(1, most + 1, (E,), generator=torch.Generator().manual_seed(M))
+    counts[::7] = 0
+    counts[5] = 300
+    off, live = offsets_of(counts.tolist()), int(counts.sum())
+    assert live < M
+    tiles = int(((counts + 255) // 256).sum()) + (M - live + 255) // 256
+    assert tiles * -(-N // 256) > 65 * (torch.cuda.get_device_properties(0).multi_processor_count // 2)
+    a, sa = random_blocks((M, K), 1)
+    w, sw = random_blocks((E, N, K), 2)
+    C = tg.gemm_grouped_mxfp4(a, sa, off, w, sw)
+    assert tg.last_device_status() == 0
+    group = torch.repeat_interleave(torch.arange(E), counts).cuda()
+    av, wv = values(a, sa), values(w, sw)
+    for r0 in range(0, live, 256):
+        rows = slice(r0, min(r0 + 256, live))
+        x, v = av[rows, None, :], wv[group[rows]]
+        ref = (v @ x.transpose(1, 2))[..., 0]
+        mags = (v.abs() @ x.abs().transpose(1, 2))[..., 0]
+        close(C[rows], ref, ref.abs() * 2.0 ** -8 * 1.01 + K * 2.0 ** -23 * mags + 2.0 ** -134)
+    assert not bool(C[live:].any())
+
+
+
 def test_second_device_is_named():
     """Operands on two devices, or on the host, are refused before any launch."""
     q, s = random_blocks((4, 64), 1)
