@@ -44,3 +44,14 @@ def test_arguments_are_checked_for_number_and_kind(calls):
         calls.tg_quant_mxfp4(1 << 70, 0, None, 0, 0, None, 0, None, 0, None)
     with pytest.raises(TypeError):
         calls.tg_expert_route(0, 8, None, 8, 2, None, 0, 1, 1, 2, 1, "x", None, None, None)
+
+
+def test_numbers_beyond_an_int_are_refused(calls):
+    """Not cut to their lowest 32 bits, which could be a number that is allowed."""
+    good = (0, 8, None, 8, 2, None, 0, 2, 1, 2, 1, 1.0, None, None, None)
+    assert calls.tg_expert_route(*good) == 0
+    for at in (1, 4, 6, 7, 8, 9, 10):
+        for far in (1 << 32, -(1 << 32)):
+            args = list(good)
+            args[at] += far
+            assert calls.tg_expert_route(*args) != 0, (at, far)

@@ -12,6 +12,7 @@
  */
 #define PY_SSIZE_T_CLEAN
 #include <Python.h>
+#include <limits.h>
 
 #include "tg_gemm.h"
 
@@ -34,9 +35,12 @@ static int read_args(PyObject *const *args, Py_ssize_t n, Py_ssize_t want, Py_ss
     return 1;
 }
 
+/* What does not fit an int becomes the nearest that does, which the library refuses. */
+static int narrow(int64_t x) { return x > INT_MAX ? INT_MAX : x < INT_MIN ? INT_MIN : (int)x; }
+
 #define P(i) ((void *)(intptr_t)v[i])
 #define I(i) v[i]
-#define N(i) ((int)v[i])
+#define N(i) narrow(v[i])
 
 #define CALL(name, want, ...)                                                              \
     static PyObject *py_##name(PyObject *self, PyObject *const *args, Py_ssize_t n) {      \
