@@ -1110,9 +1110,9 @@ def _get_torch():
 
 
 def _row_pitch(t, rows, cols, name):
-    """_pitch of a matrix (of the last two dimensions), quickly where it is dense
-    and has more than one row."""
-    return cols if rows > 1 and t.is_contiguous() else _pitch(t, name)
+    """_pitch of a matrix of bytes (of the last two dimensions), quickly where it is
+    dense and has more than one row, or one of whole 16 bytes."""
+    return cols if t.is_contiguous() and (rows > 1 or (cols and cols % 16 == 0)) else _pitch(t, name)
 
 
 def _check_blocks(q, scales, dims, name):
@@ -1189,7 +1189,7 @@ def _quant_mxfp4(X, plan, Q, scales, stream):
     if not X.is_cuda:
         _require_cuda(device, (X, "X"))
     at = X.data_ptr()
-    if K % 8 == 0 and M > 1 and at % 16 == 0 and X.is_contiguous():
+    if K % 8 == 0 and at % 16 == 0 and X.is_contiguous():
         ldx = K
     else:
         X = _aligned_rows(X)
