@@ -12,6 +12,7 @@ import torch
 import tiled_dense_gemm_tma_b200 as tg
 from expert_util import close, normal, offsets_of
 from mxfp4_util import product, quantised, random_blocks, values
+from test_gpu_mxfp4 import guarded, untouched
 
 pytestmark = pytest.mark.gpu
 ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
@@ -308,6 +309,29 @@ def test_many_tiles_a_pair():
     for e, n in enumerate(counts):
         close(C[at:at + n], *product(values(a[at:at + n], sa[at:at + n]), values(w[e], sw[e]), torch.bfloat16), f"group {e}")
         at += n
+
+
+@pytest.mark.parametrize("T,k,H", [(2400, 2, 1000), (1250, 3, 1090), (1250, 2, 1033), (1200, 2, 1279), (1200, 1, 2048),
+                                   (820, 2, 2051)])
+def test_quant_sorted_of_many_rows(T, k, H):
+    """Enough rows for four blocks of 256 values a warp, which writes the scales of
+    a place in words: whole ones, and parts of one at a row's end."""
+    ids = torch.randint(-1, 9, (T, k), generator=torch.Generator().manual_seed(T)).int().cuda()
+    plan = tg.expert_sort(ids, 8)
+    X = normal((T, H), torch.bfloat16, seed=H)
+    bq, Q = guarded(T * k, (H + 1) // 2)
+    bs, S = guarded(T * k, -(-H // 32))
+    tg.quant_mxfp4(X, plan, Q=Q, scales=S)
+    q, s = tg.quant_mxfp4(X)
+    want = quantised(X[:40])
+    assert torch.equal(q[:40].cpu(), want[0]) and torch.equal(s[:40].cpu(), want[1])
+    token, kept = plan.src.long() // k, int(plan.offsets[-1])
+    q, s = q[token], s[token]
+    q[kept:] = 0
+    s[kept:] = 0
+    assert 0 < kept < T * k and torch.equal(Q, q) and torch.equal(S, s)
+    untouched(bq, Q)
+    untouched(bs, S)
 
 
 @pytest.mark.parametrize("M,most", [(1400, 1), (4000, 6)])
