@@ -15,7 +15,8 @@
 // its bits, the lowest ones given to the lane's number of the expert, so that one
 // comparison moves both.  A row is done again in 64 bits where two keys that decide
 // something are closer than their errors could reach: neighbours among the topk +
-// 1 first of different logit or bias, or the last kept and the first dropped
+// 1 first of different logit or bias, where the last two of those are a tie any
+// further one of different logit or bias, or the last kept and the first dropped
 // group.  (In 64 bits throughout, the exponentials alone cost more than reading
 // the logits.)  Errors: a key that is a logit has lost its lowest bits only, so that
 // equal ones are in question; 16-bit logits lose nothing.  An exponential is off by
@@ -338,6 +339,17 @@ route_kernel(const RouteParams p, const bool vec) {
     }
     int at = base;
     uint32_t best = in && key[0] ? key[0] | kLow : 0u;
+    auto drop = [&] {                                         // this lane's first key
+        if constexpr (kListed) {
+            key[0] = lists[at];
+            at += 32;
+        } else {
+#pragma unroll
+            for (int i = 0; i + 1 < V; ++i) key[i] = key[i + 1];
+            key[V - 1] = 0;
+        }
+        best = key[0] ? key[0] | kLow : 0u;
+    };
     int mine = -1;                                            // lane j: the j-th choice
     uint32_t mkey = 0;
     for (int j = 0; j < p.topk; ++j) {
@@ -346,17 +358,7 @@ route_kernel(const RouteParams p, const bool vec) {
         const int win = __ffs(__ballot_sync(kAll, best == m)) - 1;
         const int e = __shfl_sync(kAll, first + static_cast<int>(kLow - (key[0] & kLow)), win);
         if (lane == j) { mine = e; mkey = m; }
-        if (lane == win) {
-            if constexpr (kListed) {
-                key[0] = lists[at];
-                at += 32;
-            } else {
-#pragma unroll
-                for (int i = 0; i + 1 < V; ++i) key[i] = key[i + 1];
-                key[V - 1] = 0;
-            }
-            best = key[0] ? key[0] | kLow : 0u;
-        }
+        if (lane == win) drop();
     }
     if (!bad_row && (keyed || (sizeof(T) == 4 && V > 1))) {
         // neighbours whose order the keys could have got wrong, the next key after
@@ -376,9 +378,29 @@ route_kernel(const RouteParams p, const bool vec) {
             const int last = __shfl_sync(kAll, first + static_cast<int>(kLow - (key[0] & kLow)), win);
             int next = __shfl_down_sync(kAll, mine, 1);
             if (lane == p.topk - 1) next = last;
-            near = near && (to_float(row[mine]) != to_float(row[next]) ||
-                            (keyed && __ldg(p.bias + mine) != __ldg(p.bias + next)));
-            close = close || __any_sync(kAll, near);
+            const bool differ = near && (to_float(row[mine]) != to_float(row[next]) ||
+                                         (keyed && __ldg(p.bias + mine) != __ldg(p.bias + next)));
+            close = close || __any_sync(kAll, differ);
+            // behind a tie of the last choice and the next key others may follow that the
+            // keys cannot tell from the two: each lane walks its own while they are near
+            if (!close && __any_sync(kAll, near && lane == p.topk - 1)) {
+                const int e0 = __shfl_sync(kAll, mine, p.topk - 1);
+                const uint32_t k0 = __shfl_sync(kAll, mkey, p.topk - 1);
+                const float x0 = to_float(row[e0]), b0 = keyed ? __ldg(p.bias + e0) : 0.f;
+                bool other = false;
+                while (best && !other) {
+                    other = best == k0;
+                    if (keyed) {
+                        const float v = value_of(k0 & ~kLow), w = value_of(best & ~kLow);
+                        other = v - w <= route_slack(p.sigmoid, inv, fmaxf(fabsf(v), fabsf(w)), V);
+                    }
+                    if (!other) break;                        // the lane's further keys are lower still
+                    const int e = first + static_cast<int>(kLow - (key[0] & kLow));
+                    other = to_float(row[e]) != x0 || (keyed && __ldg(p.bias + e) != b0);
+                    drop();
+                }
+                close = __any_sync(kAll, other);
+            }
         }
     }
     if (close && !bad_row) mine = choose_exact<V>(p, row, first, live, top, lane);
