@@ -290,15 +290,23 @@ route_kernel(const RouteParams p, const bool vec) {
     sort_keys(key);
     bool close = false, in = true;
     if (p.groups > 1) {
-        auto best_score = [&](uint32_t k) -> float {
-            if (k == 0) return -kInf;
-            if (keyed) return value_of(k & ~kLow);
-            float v = x[0];
+        float a = -kInf, b = -kInf;                           // this lane's two best
+        if (keyed) {
+            if (key[0]) a = value_of(key[0] & ~kLow);
+            if (V > 1 && key[V > 1 ? 1 : 0]) b = value_of(key[V > 1 ? 1 : 0] & ~kLow);
+        } else {
+            // Of the logits as they are: a key has lost up to V - 1 of a 32-bit logit's
+            // last units, and each is |x| 2^-23 of a softmax's score.
 #pragma unroll
-            for (int i = 1; i < V; ++i) v = kLow - (k & kLow) == i ? x[i] : v;
-            return !(v < kInf) ? kInf : bad_row ? 0.f : score_of(v);
-        };
-        float a = best_score(key[0]), b = V > 1 ? best_score(key[V > 1 ? 1 : 0]) : -kInf;
+            for (int i = 0; i < V; ++i) {
+                const float v = bad_row && !(x[i] < kInf) ? kInf : x[i];
+                b = fmaxf(b, fminf(a, v));
+                a = fmaxf(a, v);
+            }
+            auto scored = [&](float v) { return v == -kInf || v == kInf ? v : bad_row ? 0.f : score_of(v); };
+            a = scored(a);
+            b = scored(b);
+        }
         if (bad_row) {                                        // truncated NaNs
             if (!(a <= kInf)) a = kInf;
             if (!(b <= kInf)) b = kInf;
