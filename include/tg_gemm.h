@@ -453,16 +453,18 @@ TG_API tg_status tg_gemm_grouped_mxfp4(int64_t M, int64_t N, int64_t K, int E,
  * tg_expert_route -- for each row x of logits (tokens x E of `type`, TG_TYPE_F16,
  *   TG_TYPE_BF16 or TG_TYPE_F32, aligned to its elements, any row pitch ldl >= E):
  *     score   p = softmax(x) (TG_SCORE_SOFTMAX) or sigmoid(x) (TG_SCORE_SIGMOID)
- *     choice  the topk experts of largest x, or with a bias (E finite floats, not NULL) of
- *             largest p + bias, in falling order, ties to the lower number.  With
+ *     choice  the topk experts of largest x, or with a bias (E floats, not NULL; finite or
+ *             minus infinity) of largest p + bias, in falling order, ties to the lower number.  With
  *             groups > 1 (each E / groups consecutive experts) only from the
  *             keep_groups groups of largest sum of their two largest p (+ bias), ties
  *             to the lower group.
  *     weight  scale * p, or with renorm = 1 scale * p over the sum of the chosen p.
  *   ids (int32) and weights (float) are tokens x topk, dense.  An expert whose
- *   logit is minus infinity is never chosen (nor counted in its group's sum); where fewer than topk are left
- *   the rest are ids of -1 (a dropped choice for tg_expert_sort) with weight 0.  A
- *   logit that is NaN or plus infinity is chosen first and makes its row's weights NaN.
+ *   logit or bias is minus infinity is never chosen, nor counted in its group's
+ *   sum (one switched off by its bias stays in the softmax); where fewer than topk
+ *   are left the rest are ids of -1 (a dropped choice for tg_expert_sort) with
+ *   weight 0.  A logit that is NaN or plus infinity is chosen before all other live
+ *   ones and makes its row's weights NaN.
  *   Choices are those of 64-bit arithmetic on the given logits.
  * tg_expert_route_grad -- dlogits (tokens x E of `type`, row pitch ldd) for the
  *   gradient dweights of the weights (tokens x topk floats, dense), from the same logits and the

@@ -1399,14 +1399,14 @@ def expert_route(logits, topk, *, bias=None, score="softmax", groups=1, topk_gro
     tokens x topk, as expert_sort and expert_combine take them.
 
     The scores are softmax(logits) or sigmoid(logits).  The topk highest are
-    chosen in falling order, ties to the lower number; a bias (float32, E) is
-    added to the scores for the choice alone.  With groups (of E / groups
-    consecutive experts) the choice is made in the topk_groups of them (by default
-    all) whose two highest (biased) scores sum highest.  Weights are scale times the
-    chosen scores, divided by their sum with renorm.  Minus infinity is never
-    chosen; where fewer than topk are left, the rest are -1 (dropped choices) and
-    weigh 0.  A NaN or plus infinity makes its row's weights NaN.  Differentiable in
-    the logits."""
+    chosen in falling order, ties to the lower number; a bias (float32, E, finite
+    or minus infinity) is added to the scores for the choice alone.  With groups
+    (of E / groups consecutive experts) the choice is made in the topk_groups of
+    them (by default all) whose two highest (biased) scores sum highest.  Weights
+    are scale times the chosen scores, divided by their sum with renorm.  A logit
+    or bias of minus infinity is never chosen; where fewer than topk are left, the
+    rest are -1 (dropped choices) and weigh 0.  A logit of NaN or plus infinity
+    makes its row's weights NaN.  Differentiable in the logits."""
     global _ROUTE
     torch = _torch or _get_torch()
     if logits.dim() != 2:

@@ -7,8 +7,8 @@
 //             groups only from the `keep` groups whose two largest sum highest
 //   weight    w_j = scale * p_j, or with renorm scale * p_j / sum of the chosen p
 //
-// A logit of minus infinity is never chosen; choices that nothing is left for
-// are -1 and weigh 0.  A NaN or plus infinity is chosen before all else, and makes
+// A logit or a bias of minus infinity is never chosen; choices that nothing is left
+// for are -1 and weigh 0.  A NaN or plus infinity is chosen before all else, and makes
 // every weight of its row NaN.
 //
 // The order is that of 64-bit arithmetic.  Keys are 32-bit: a value in the order of
@@ -271,10 +271,13 @@ route_kernel(const RouteParams p, const bool vec) {
     auto score_of = [&](float v) {
         return p.sigmoid ? reciprocal(1.f + exp2_of(v * -kLog2e)) : exp2_of((v - top) * kLog2e) * inv;
     };
-    if (!odd) {
-        if (keyed)
+    if (!odd && keyed) {
 #pragma unroll
-            for (int i = 0; i < V; ++i) key[i] = ordered(score_of(x[i]) + s[i]);
+        for (int i = 0; i < V; ++i) {
+            const uint32_t k = ordered(score_of(x[i]) + s[i]);
+            key[i] = k <= kNone ? 0u : (k & ~kLow) | (kLow - i);
+        }
+    } else if (!odd) {
 #pragma unroll
         for (int i = 0; i < V; ++i) key[i] = (key[i] & ~kLow) | (kLow - i);
     } else {
@@ -283,8 +286,9 @@ route_kernel(const RouteParams p, const bool vec) {
             uint32_t k = key[i];
             // a NaN or plus infinity takes the other scores of its row with it
             if (keyed) k = ordered((bad_row ? 0.f : score_of(x[i])) + s[i]);
+            const bool off = x[i] == -kInf || (keyed && s[i] == -kInf);
             if (!(x[i] < kInf)) k = ~0u;
-            key[i] = x[i] == -kInf ? 0u : (k & ~kLow) | (kLow - i);
+            key[i] = off ? 0u : (k & ~kLow) | (kLow - i);
         }
     }
     sort_keys(key);
