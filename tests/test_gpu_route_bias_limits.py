@@ -1,4 +1,5 @@
-"""The router's bias at its limits: minus infinity switches an expert off."""
+"""The router's bias at its limits: minus infinity switches an expert off, the
+lowest finite value puts it last."""
 import math
 
 import pytest
@@ -6,9 +7,11 @@ import torch
 
 import tiled_dense_gemm_tma_b200 as tg
 from expert_util import close
-from route_util import relative, scores, weights_of
+from route_util import choose, relative, scores, weights_of
 
 pytestmark = pytest.mark.gpu
+
+LOWEST = torch.finfo(torch.float32).min
 
 
 def definition(x, topk, score, bias, groups, keep):
@@ -93,3 +96,20 @@ def test_a_bad_logit_and_a_bias_of_minus_infinity(score):
         ids, w = tg.expert_route(x.cuda(), 4, bias=bias.cuda(), score=score, groups=groups, topk_groups=keep)
         assert bool(w[:2].isnan().all()) and not bool(w[2].isnan().any())
         assert not ((ids >= 3) & (ids <= 5)).any() and bool((ids < 16).all())
+
+
+@pytest.mark.parametrize("low", [LOWEST, LOWEST / 2, -1e30])
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("E,groups,keep,topk", [(16, 1, 1, 8), (16, 4, 3, 10), (64, 8, 4, 20), (256, 8, 8, 32), (32, 32, 9, 9)])
+def test_the_lowest_value_comes_last(E, groups, keep, topk, score, low):
+    """A finite bias excludes nobody: its experts, and groups that hold no others,
+    are there when the rest is used up."""
+    x = logits(12, E, torch.float32, E)
+    x[3, E // 2:] = -math.inf
+    per = E // groups
+    bias = torch.zeros(E)
+    bias[torch.arange(E) // per != groups // 2] = low
+    if groups == 1:
+        bias[4:] = low
+    want = run(x, topk, bias, score, groups, keep, True)
+    assert choose(x[0].double().tolist(), topk, score, bias.double().tolist(), groups, keep) == want[0].tolist()

@@ -317,8 +317,11 @@ route_kernel(const RouteParams p, const bool vec) {
         }
         group_top2(a, b, p.lanes);
         // the highest groups one by one, a group's number (falling, so that ties go to
-        // the lowest) in its key's lowest bits
-        const float score = group < p.groups ? group_score(a, b) : -kInf;
+        // the lowest) in its key's lowest bits.  Two of the lowest values do not add up
+        // to minus infinity, which is a group of none (nor their sizes to infinity).
+        constexpr float kMost = 0x1.fffffep127f;
+        float score = group < p.groups ? group_score(a, b) : -kInf;
+        if (score == -kInf && a > -kInf) score = -kMost;
         uint32_t gkey = score > -kInf ? (ordered(score) & ~31u) | (31 - group) : 0u, last = 0;
         in = false;
         for (int g = 0; g < p.keep; ++g) {
@@ -329,12 +332,14 @@ route_kernel(const RouteParams p, const bool vec) {
                 gkey = 0;
             }
         }
-        const uint32_t next = __reduce_max_sync(kAll, gkey);  // the first of the dropped ones
-        if (next) {
-            const float size = score > -kInf ? fabsf(a) + (b > -kInf ? fabsf(b) : 0.f) : 0.f;   // terms may cancel in the sum
-            const float larger = __uint_as_float(__reduce_max_sync(kAll, __float_as_uint(size)));
-            close = value_of(last & ~31u) - value_of(next & ~31u) <=
-                    2.f * route_slack(p.sigmoid, inv, larger, V) + 0x1p-18f * larger;
+        if (__any_sync(kAll, gkey != 0)) {                    // groups that are dropped
+            // Of each group its own error: terms may cancel in its sum, and one of very
+            // low biases is far off but also far below.
+            const float size = fminf(fabsf(a) + (b > -kInf ? fabsf(b) : 0.f), kMost);
+            const float off = route_slack(p.sigmoid, inv, size, V);
+            const uint32_t low = __reduce_min_sync(kAll, in ? ordered(score - off) : ~0u);
+            const uint32_t high = __reduce_max_sync(kAll, gkey ? ordered(score + off) : 0u);
+            close = low <= high;
         }
     }
     // the topk largest.  Lanes are compared without the bits that number their
