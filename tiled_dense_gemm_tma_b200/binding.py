@@ -1417,7 +1417,9 @@ def expert_route(logits, topk, *, bias=None, score="softmax", groups=1, topk_gro
     if topk < 1:
         raise ValueError("topk must be at least 1")
     args = (topk, bias, kind, groups, groups if topk_groups is None else topk_groups, 1 if renorm else 0, scale)
-    if not (logits.requires_grad and torch.is_grad_enabled()):
+    # without a graph to record, the autograd function would only cost time; inside
+    # a level of forward mode it refuses a tensor that has a tangent
+    if not (logits.requires_grad and torch.is_grad_enabled()) and torch.autograd.forward_ad._current_level < 0:
         return _route(logits, *args)
     if _ROUTE is None:
         _ROUTE = _route_function()
