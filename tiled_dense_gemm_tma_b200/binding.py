@@ -1373,6 +1373,8 @@ def _route_function():
             if g is None:
                 return None, None
             logits, ids = ctx.saved_tensors
+            if not ids.is_contiguous():                 # from a saved-tensor hook
+                ids = ids.contiguous()
             topk, _, score, _, _, renorm, scale = ctx.args
             T, E = logits.shape
             x, kind, ldl = _logits(logits, T, E)
