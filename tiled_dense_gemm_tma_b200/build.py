@@ -19,7 +19,7 @@ import sysconfig
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 OUT = os.path.join(HERE, "libtg_gemm.so")
-CALLS = os.path.join(HERE, "_tg_calls.so")
+CALLS = os.path.join(HERE, "_tg_calls" + sysconfig.get_config_var("EXT_SUFFIX"))
 BUILD = os.path.join(HERE, "_build")
 INCLUDE = os.path.join(os.path.dirname(HERE), "include")
 NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")
@@ -58,7 +58,11 @@ def _compile(src, verbose):
 
 
 def _build_calls(force):
-    """The module finds the library beside itself, wherever both are moved."""
+    """The module finds the library beside itself, wherever both are moved.  Its
+    name carries the interpreter's tag: each Python builds and finds its own."""
+    untagged = os.path.join(HERE, "_tg_calls.so")      # what builds before the tag left: any Python finds it
+    if os.path.exists(untagged) and untagged != CALLS:
+        os.remove(untagged)
     src = os.path.join(CSRC, "calls.c")
     if not force and not _stale(CALLS, [src, os.path.join(INCLUDE, "tg_gemm.h")]):
         return
