@@ -1,5 +1,5 @@
 """Binding of the C ABI declared in include/tg_gemm.h, through ctypes and, for
-what a layer calls several times a step, through csrc/calls.c.
+what a layer calls several times a step, through csrc/calls.c where it was built.
 
 Argument marshalling only: every step of the GEMM runs in the CUDA kernels
 of ``libtg_gemm.so``.  Torch is used for device memory and streams.  If the
@@ -457,14 +457,33 @@ _fns = {}
 
 
 def _calls():
-    """The module that calls the entry points of the sections below: a call
-    through ctypes converts its 10 to 20 arguments in 1.5 us, this one in 0.2."""
-    load_library()
+    """What calls the entry points of the sections below: the module _tg_calls where
+    it was built (a call through ctypes converts its 10 to 20 arguments in 1.5 us,
+    this one in 0.2), else the library itself."""
+    lib = load_library()
     try:
         from . import _tg_calls
-    except ImportError as e:
-        raise ImportError(f"_tg_calls is not built ({e}); run tiled_dense_gemm_tma_b200/build.py") from e
+    except ImportError:
+        return _PlainCalls(lib)
     return _tg_calls
+
+
+class _PlainCalls:
+    """The entry points through ctypes.  What does not fit an int becomes the
+    nearest that does, as in _tg_calls: ctypes would cut it to its lowest 32 bits."""
+
+    def __init__(self, lib):
+        self._library = lib
+
+    def __getattr__(self, name):
+        fn = getattr(self._library, name)
+        narrow = [kind is ctypes.c_int for kind in fn.argtypes]
+
+        def call(*args):
+            return fn(*[max(-1 << 31, min((1 << 31) - 1, a)) if n else a for a, n in zip(args, narrow, strict=True)])
+
+        setattr(self, name, call)
+        return call
 
 
 def _launch(name, device, stream, *args):

@@ -1,5 +1,6 @@
 """Build libtg_gemm.so in-tree from csrc/*.cu for sm_100a, and beside it the
-Python module _tg_calls from csrc/calls.c, which calls it.
+Python module _tg_calls from csrc/calls.c, which calls it (where there is a C
+compiler and this Python's headers; without it those calls go through ctypes).
 
     python tiled_dense_gemm_tma_b200/build.py [--force] [--verbose]
 
@@ -67,10 +68,19 @@ def _build_calls(force):
     if not force and not _stale(CALLS, [src, os.path.join(INCLUDE, "tg_gemm.h")]):
         return
     tmp = CALLS + f".tmp{os.getpid()}"
-    subprocess.run(["gcc", "-O2", "-std=c11", "-shared", "-fPIC", "-fvisibility=hidden", "-I", INCLUDE, "-I",
-                    sysconfig.get_path("include"), src, "-o", tmp, "-L", HERE, "-l:libtg_gemm.so",
-                    "-Wl,-rpath,$ORIGIN"], check=True)
+    try:
+        _compile_calls(src, tmp)
+    except (OSError, subprocess.CalledProcessError) as e:
+        # no C compiler, or no headers of this Python: the library is all that a call needs
+        sys.stderr.write(f"_tg_calls is not built ({e}); its calls go through ctypes, 1.3 us more each\n")
+        return
     os.replace(tmp, CALLS)
+
+
+def _compile_calls(src, out):
+    subprocess.run(["gcc", "-O2", "-std=c11", "-shared", "-fPIC", "-fvisibility=hidden", "-I", INCLUDE, "-I",
+                    sysconfig.get_path("include"), src, "-o", out, "-L", HERE, "-l:libtg_gemm.so",
+                    "-Wl,-rpath,$ORIGIN"], check=True)
 
 
 def build(force: bool = False, verbose: bool = False) -> str:
