@@ -1427,7 +1427,8 @@ def expert_route(logits, topk, *, bias=None, score="softmax", groups=1, topk_gro
     are scale times the chosen scores, divided by their sum with renorm.  A logit
     or bias of minus infinity is never chosen; where fewer than topk are left, the
     rest are -1 (dropped choices) and weigh 0.  A logit of NaN or plus infinity
-    makes its row's weights NaN.  Differentiable in the logits."""
+    makes its row's weights NaN.  At most 1024 experts, 32 choices and 32 groups.
+    Differentiable in the logits."""
     global _ROUTE
     torch = _torch or _get_torch()
     if logits.dim() != 2:

@@ -49,7 +49,12 @@ int run(const GroupArgs& a, int bf16, int slot) {
 
 }  // namespace
 
-// The dense 4-bit product: the choice of the 8-bit one (launch_w8a8).
+// The dense 4-bit product: the choice of the 8-bit one (launch_w8a8).  This kernel
+// against that on CTA pairs, us in a graph: K = 8192, N = 8192, 1 row 12.0 / 16.8, 17
+// 12.4 / 16.9, 64 14.1 / 16.7, 128 17.3 / 17.5; N = 14336, 16 rows 15.8 / 19.2, 17 16.1 /
+// 19.3, 64 18.5 / 19.3, 128 22.9 / 20.4; K = 2048, N = 8192, 17 rows 7.8 / 9.4, 64 9.4
+// both, 128 12.0 / 10.1.  (So of 17 to 64 rows with more than 9472 columns the slower
+// one is taken, and of 65 to 128 with few k.)
 int launch_mx4(const GroupArgs& a, int bf16) {
     const DeviceInfo* di = current_device(nullptr);
     if (!di) return kNoDevice;
